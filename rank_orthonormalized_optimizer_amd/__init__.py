@@ -10,6 +10,10 @@ computation runs in the library's kernels.  1-D parameters (biases, norms) are
 not Dion's: ``group_matrices`` rejects them, and ``adamw_step_`` / ``lion_step_``
 (or ``MixedDion``, which routes every parameter) update them with the library's
 element-wise AdamW or Lion, as the page describes.
+
+``embedding_``, ``embedding_grad_``, ``linear_cross_entropy_`` and
+``linear_cross_entropy_grad_`` are the operators at the two ends of the model over its
+vocabulary matrices; they leave those matrices' gradients where the steps above read them.
 """
 from __future__ import annotations
 
@@ -19,3 +23,5 @@ from ._lib import (BF16, EXPORTS, F32, FLAG_F64, FLAG_HOUSEHOLDER, FLAG_NONFINIT
                    step_batched_raw, strerror, version, workspace_size)
 from .api import (DionStack, GraphedStep, MixedDion, StickyF64Hint, adamw_step_, group_matrices,  # noqa: F401
                   lambda_max_, lion_step_, step_)
+from .vocab import (embedding_, embedding_grad_, embedding_grad_workspace_for,  # noqa: F401
+                    linear_cross_entropy_, linear_cross_entropy_grad_, linear_cross_entropy_workspace_for)

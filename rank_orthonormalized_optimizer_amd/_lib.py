@@ -44,6 +44,12 @@ EXPORTS = ("dion_workspace_size", "dion_step_batched", "dion_step_batched_profil
            "dion_lion_step", "dion_lambda_max_workspace_size", "dion_lambda_max_batched", "dion_strerror",
            "dion_version")
 
+# include/dion_vocab.h
+I32, I64 = 0, 1
+VOCAB_MAX_TOKENS = 1 << 20
+VOCAB_EXPORTS = ("dion_embedding", "dion_embedding_grad_workspace_size", "dion_embedding_grad",
+                 "dion_linear_xent_workspace_size", "dion_linear_xent", "dion_linear_xent_grad")
+
 
 class StepOutputs(ctypes.Structure):
     """dion_step_outputs: optional phase events and the per-matrix momentum-change output."""
@@ -92,6 +98,20 @@ def load() -> ctypes.CDLL:
     lib.dion_lambda_max_workspace_size.argtypes = [i64, i64, i32]
     lib.dion_lambda_max_batched.restype = ctypes.c_int
     lib.dion_lambda_max_batched.argtypes = [vp, i64, i64, vp, i32, i32, vp, vp, ctypes.c_size_t, vp]
+    sz = ctypes.c_size_t
+    lib.dion_embedding.restype = ctypes.c_int
+    lib.dion_embedding.argtypes = [vp, vp, vp, i64, i64, i64, f32, i32, i32, i32, vp]
+    lib.dion_embedding_grad_workspace_size.restype = sz
+    lib.dion_embedding_grad_workspace_size.argtypes = [i64, i64, i64]
+    lib.dion_embedding_grad.restype = ctypes.c_int
+    lib.dion_embedding_grad.argtypes = [vp, vp, vp, i64, i64, i64, f32, i64, i32, i32, i32, i32, vp, sz, vp]
+    lib.dion_linear_xent_workspace_size.restype = sz
+    lib.dion_linear_xent_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
+    lib.dion_linear_xent.restype = ctypes.c_int
+    lib.dion_linear_xent.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, vp, sz, vp]
+    lib.dion_linear_xent_grad.restype = ctypes.c_int
+    lib.dion_linear_xent_grad.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, i32, i32, i32, vp, sz,
+                                          vp]
     lib.dion_strerror.restype = ctypes.c_char_p
     lib.dion_strerror.argtypes = [ctypes.c_int]
     lib.dion_version.restype = ctypes.c_int

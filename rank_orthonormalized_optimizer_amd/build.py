@@ -13,7 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libdion_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["dion_step.hip", "stream16.hip", "elementwise.hip", "spectral.hip", "noalloc.hip", "dion_api.cpp"]
+SOURCES = ["dion_step.hip", "stream16.hip", "elementwise.hip", "spectral.hip", "noalloc.hip", "dion_api.cpp",
+           "vocab/embedding.hip", "vocab/cross_entropy.hip", "vocab/vocab_api.cpp"]
 ARCH = "gfx950"
 
 
@@ -37,7 +38,7 @@ def build(verbose: bool = False) -> str:
     objs = []
     os.makedirs(os.path.join(HERE, "_build"), exist_ok=True)
     for src in SOURCES:
-        obj = os.path.join(HERE, "_build", src + ".o")
+        obj = os.path.join(HERE, "_build", src.replace("/", "_") + ".o")
         lang = [] if src.endswith(".hip") else ["-x", "hip"]
         cmd = [hipcc()] + compile_flags() + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:

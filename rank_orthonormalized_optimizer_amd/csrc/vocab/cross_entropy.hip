@@ -1,0 +1,580 @@
+// Softmax cross entropy of a linear head without stored logits, and its gradients.
+//
+//   z = H W^T (tokens x vocab);  lse = log sum_v exp z;  loss = lse - z[target]
+//   D = grad (exp(z - lse) - onehot(target));  dH = D W;  dW = D^T H
+//
+// The tokens whose target is not ignored are first gathered into H's planes in the workspace
+// (order kept, their number left in device memory), so ignored rows cost no products and whatever
+// they hold reaches nothing.  The loss: one tile product over W, whose epilogue reduces each tile
+// of logits to a maximum and a sum of exponentials per token (online softmax across tiles), then
+// one pass over these pairs.  The gradient: per piece of the vocabulary the logits are formed
+// again, turned into D (bf16, one part or an exact split in three) and multiplied from both sides.
+// Matrix-core bound: 2 tokens vocab width flops for the loss, four times that for loss and
+// gradients together, the recomputed logits included.
+//
+// In every product the vocabulary (or width) runs along the matrix core's rows and the tokens (or
+// vocabulary) along its columns: a lane then holds four consecutive elements of the contiguous
+// dimension of what it writes, and the softmax's reduction runs mostly inside a lane.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "dion_vocab.h"
+#include "mm16.hpp"
+#include "vocab_plan.h"
+
+namespace dion {
+
+namespace {
+
+using mm::f32x4;
+using mm::u32x2;
+using mm::u32x4;
+
+__device__ __forceinline__ float up16(uint32_t b) { return __uint_as_float(b << 16); }
+__device__ __forceinline__ uint32_t down16(float f) { return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f); }
+
+// a = h + m + l exactly: h = RN(a), m = RN(a - h), l = a - h - m
+__device__ __forceinline__ void split3(float a, uint32_t (&part)[3]) {
+    part[0] = down16(a);
+    const float r = a - up16(part[0]);
+    part[1] = down16(r);
+    part[2] = down16(r - up16(part[1]));
+}
+
+// exp(x) for x <= 0 to about an ulp: the rounding of x log2(e) is carried into the result.
+__device__ __forceinline__ float exp_exact(float x) {
+    const float h = x * 1.44269504f;
+    const float l = fmaf(x, 1.44269504f, -h) + x * 1.92596299e-8f;
+    const float r = __builtin_amdgcn_exp2f(h);
+    return x < -104.f ? 0.f : fmaf(r, l * 0.693147181f, r);
+}
+
+// ---------------------------------------------------------------------------
+// Gathering the rows that count
+// ---------------------------------------------------------------------------
+struct PackArgs {
+    XentArgs x;
+    int64_t n, v, d, kp, np;
+    uint16_t* h;     // planes [parts][np][kp]
+    int* map;        // gathered row -> token
+    int* tgt;        // its target, -1 where that is no row of W
+    float2* lg;      // (lse, grad) of the gathered row (gradient)
+    int* cnt;        // how many rows were gathered
+};
+
+__device__ __forceinline__ int64_t load_target(const XentArgs& a, int64_t i) {
+    return a.t64 ? ((const int64_t*)a.targets)[i] : (int64_t)((const int32_t*)a.targets)[i];
+}
+
+// eight elements of a row of length d from column c, zeros past its end; V8: rows 16-byte aligned
+template <bool BF16, bool V8>
+__device__ __forceinline__ void load8(const void* p, int64_t row, int64_t c, int64_t d, float (&v)[8]) {
+    if constexpr (V8) {
+        if (c >= d) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        } else if constexpr (BF16) {
+            const u32x4 w = *(const u32x4*)((const uint16_t*)p + row + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { v[2 * e] = up16(w[e]); v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u); }
+        } else {
+            const f32x4 w0 = *(const f32x4*)((const float*)p + row + c), w1 = *(const f32x4*)((const float*)p + row + c + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { v[e] = w0[e]; v[4 + e] = w1[e]; }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool in = c + e < d;
+            const int64_t i = row + (in ? c + e : 0);
+            const float f = BF16 ? up16(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+            v[e] = in ? f : 0.f;
+        }
+    }
+}
+
+template <int PARTS>
+__device__ __forceinline__ void store8(uint16_t* out, int64_t plane, int64_t i, const float (&v)[8]) {
+    uint32_t part[8][3];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split3(v[e], part[e]);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = part[2 * e][q] | (part[2 * e + 1][q] << 16);
+        *(u32x4*)(out + q * plane + i) = w;
+    }
+}
+
+constexpr int kPackRows = 16;
+
+// Sixteen tokens per workgroup, which counts the gathered rows before them itself (a read of the
+// targets from L2: fewer bytes than one row of H for all lengths up to the limit's thousands).
+template <bool BF16, bool V8, bool GRAD>
+__global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
+    __shared__ int before[4], slot[kPackRows];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int64_t t0 = (int64_t)blockIdx.x * kPackRows;
+    int c = 0;
+    for (int64_t i = tid; i < t0; i += 256) c += load_target(a.x, i) != a.x.ignore;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) c += __shfl_xor(c, o);
+    if (lane == 0) before[w] = c;
+    __syncthreads();
+    if (w == 0) {
+        const int64_t t = t0 + lane;
+        const bool row = lane < kPackRows && t < a.n;
+        const int64_t y = row ? load_target(a.x, t) : 0;
+        const bool keep = row && y != a.x.ignore;
+        const uint64_t kept = __ballot(keep);
+        const int base = before[0] + before[1] + before[2] + before[3];
+        const int j = base + __popcll(kept & ((1ull << lane) - 1));
+        if (lane < kPackRows) slot[lane] = keep ? j : -1;
+        if (keep) {
+            const bool in = y >= 0 && y < a.v;
+            a.map[j] = (int)t;
+            a.tgt[j] = in ? (int)y : -1;
+            if (GRAD) {
+                const float g = a.x.grad[a.x.grad_n == 1 ? 0 : t];
+                a.lg[j] = float2{a.x.lse[t], in ? g : __uint_as_float(0x7fc00000u)};
+            }
+        } else if (row && !GRAD) {
+            a.x.loss[t] = 0.f;
+            a.x.lse_out[t] = 0.f;
+        }
+        if (lane == 0 && blockIdx.x == gridDim.x - 1) a.cnt[0] = base + __popcll(kept);
+    }
+    __syncthreads();
+    const int nc = (int)(a.kp / 8);
+    for (int i = tid; i < kPackRows * nc; i += 256) {
+        const int r = i / nc, col = (i - r * nc) * 8;
+        const int64_t t = t0 + r;
+        if (t >= a.n) break;
+        if (slot[r] >= 0) {
+            float v[8];
+            load8<BF16, V8>(a.x.H, t * a.d, col, a.d, v);
+            store8<BF16 ? 1 : 3>(a.h, a.np * a.kp, (int64_t)slot[r] * a.kp + col, v);
+        } else if (GRAD && a.x.dH) {
+            for (int e = 0; e < 8; ++e)
+                if (col + e < a.d) {
+                    if (BF16) ((uint16_t*)a.x.dH)[t * a.d + col + e] = 0;
+                    else ((float*)a.x.dH)[t * a.d + col + e] = 0.f;
+                }
+        }
+    }
+}
+
+// Planes of `rows` rows of W (from row0) with zero columns up to kp.
+template <bool BF16, bool V8>
+__global__ __launch_bounds__(256) void plane_kernel(const void* W, uint16_t* out, int64_t row0, int64_t rows, int64_t d,
+                                                    int64_t kp, int64_t plane) {
+    const int64_t nc = kp / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= rows * nc) return;
+    const int64_t r = i / nc, col = (i - r * nc) * 8;
+    float v[8];
+    load8<BF16, V8>(W, (row0 + r) * d, col, d, v);
+    store8<BF16 ? 1 : 3>(out, plane, r * kp + col, v);
+}
+
+// ---------------------------------------------------------------------------
+// Products
+// ---------------------------------------------------------------------------
+// Tile of this workgroup: workgroups go to the eight XCDs in turn; each XCD takes a contiguous
+// range of the tiles, in bands of eight tile rows, so that its L2 serves the operands' re-reads.
+__device__ __forceinline__ bool tile_of(int tm, int tn, int& mt, int& nt) {
+    const int total = tm * tn, id = blockIdx.x;
+    if (id >= total) return false;
+    const int q = total / 8, r = total % 8, x = id % 8;
+    const int at = x * q + (x < r ? x : r) + id / 8;
+    constexpr int G = 8;
+    const int band = at / (G * tn), m0 = band * G, g = tm - m0 < G ? tm - m0 : G, in = at - band * G * tn;
+    mt = m0 + in % g;
+    nt = in / g;
+    return true;
+}
+
+struct LogitArgs {
+    mm::Operand w, h;      // w.rows: rows of this piece; h.rows is read from cnt
+    mm::Segments seg;
+    int kp;
+    const int* cnt;
+    const int* tgt;
+    int v0;                // first vocabulary row of the piece
+    // loss
+    float2* part;          // [np][nvt] maximum and sum of exponentials of a tile of logits
+    float* zt;             // the target's logit
+    int nvt;
+    // gradient
+    const float2* lg;
+    uint16_t* dl;          // planes [dparts][np][piece]
+    int64_t np, piece;
+};
+
+enum { EPI_LOSS, EPI_D1, EPI_D3 };
+
+template <class C, int EPI>
+__global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
+    const int count = a.cnt[0], rows = a.w.rows;
+    int mt, nt;
+    if (!tile_of((rows + C::BM - 1) / C::BM, (count + C::BN - 1) / C::BN, mt, nt)) return;
+    const int m0 = mt * C::BM, n0 = nt * C::BN;
+    a.h.rows = count;
+    typename C::Acc acc = {};
+    mm::Product<C>::run(a.w, a.h, m0, n0, 0, a.kp, a.seg, lds, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+    const int mw = m0 + wm * (C::BM / C::WM) + 4 * (lane / 16);   // this lane's first row, + 16 i + v
+    const int cw = wn * (C::BN / C::WN) + lane % 16;              // its first column in the tile, + 16 j
+    if constexpr (EPI == EPI_LOSS) {
+        __syncthreads();   // the last slab was read
+        float2* red = (float2*)lds;   // [WM][BN]
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) {
+            const int n = n0 + cw + 16 * j, y = n < count ? a.tgt[n] - a.v0 : -1;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int m = mw + 16 * i + v;
+                    if (m >= rows) acc[i][j][v] = -INFINITY;
+                    else if (m == y) a.zt[n] = acc[i][j][v];
+                    mx = fmaxf(mx, acc[i][j][v]);
+                }
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float ref = mx == -INFINITY ? 0.f : mx;   // an empty or all-minus-infinity column sums to 0, NaN to NaN
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) s += exp_exact(acc[i][j][v] - ref);
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (lane < 16) red[wm * C::BN + cw + 16 * j] = float2{mx, s};
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < C::BN && n0 + c < count; c += C::THREADS) {
+            float2 t = red[c];
+#pragma unroll
+            for (int i = 1; i < C::WM; ++i) {
+                const float2 u = red[i * C::BN + c];
+                const float m = fmaxf(t.x, u.x), ref = m == -INFINITY ? 0.f : m;
+                t.y = t.y * exp_exact(t.x - ref) + u.y * exp_exact(u.x - ref);
+                t.x = m;
+            }
+            a.part[(int64_t)(n0 + c) * a.nvt + (a.v0 + m0) / C::BM] = t;
+        }
+    } else {
+        constexpr int PD = EPI == EPI_D3 ? 3 : 1;
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) {
+            const int n = n0 + cw + 16 * j;
+            const bool in = n < count;
+            const int y = in ? a.tgt[n] - a.v0 : -1;
+            const float2 lg = in ? a.lg[n] : float2{0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i) {
+                uint32_t part[4][3];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int m = mw + 16 * i + v;
+                    const float p = exp_exact(acc[i][j][v] - lg.x) - (m == y ? 1.f : 0.f);
+                    split3(in && m < rows ? p * lg.y : 0.f, part[v]);
+                }
+#pragma unroll
+                for (int q = 0; q < PD; ++q) {
+                    uint16_t* to = a.dl + (q * a.np + n) * a.piece + mw + 16 * i;
+                    *(u32x2*)to = u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
+                    // zeros up to the end of a 64-token slab, which the last tile may not reach by itself
+                    if (C::BN < mm::kBK && n0 + C::BN >= count && n0 % mm::kBK == 0)
+                        *(u32x2*)(to + C::BN * a.piece) = u32x2{0, 0};
+                }
+            }
+        }
+    }
+}
+
+// loss and lse of the gathered tokens from their tiles' pairs, one wave per token
+__global__ __launch_bounds__(256) void loss_kernel(const float2* part, const float* zt, const int* tgt, const int* map,
+                                                   const int* cnt, int nvt, float* loss, float* lse) {
+    const int j = (int)(blockIdx.x * 4 + (threadIdx.x >> 6)), lane = threadIdx.x & 63;
+    if (j >= cnt[0]) return;
+    float m = -INFINITY, s = 0.f;
+    for (int i = lane; i < nvt; i += 64) {
+        const float2 u = part[(int64_t)j * nvt + i];
+        const float top = fmaxf(m, u.x), ref = top == -INFINITY ? 0.f : top;
+        s = s * exp_exact(m - ref) + u.y * exp_exact(u.x - ref);
+        m = top;
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        const float um = __shfl_xor(m, o), us = __shfl_xor(s, o);
+        const float top = fmaxf(m, um), ref = top == -INFINITY ? 0.f : top;
+        s = s * exp_exact(m - ref) + us * exp_exact(um - ref);
+        m = top;
+    }
+    if (lane == 0) {
+        const float ls = logf(s);
+        lse[map[j]] = m + ls;
+        loss[map[j]] = tgt[j] < 0 ? __uint_as_float(0x7fc00000u) : (m - zt[j]) + ls;
+    }
+}
+
+struct OutArgs {
+    mm::Operand a, b;
+    mm::Segments seg;
+    const int* cnt;
+    int d;                 // output columns (the matrix core's rows)
+    int rows;              // output rows, or -1: the gathered tokens
+    int k;                 // reduction length, or -1: the gathered tokens
+    int split, k_per;      // slices of the reduction (blockIdx.y) and their length
+    float* acc;            // fp32 [split][acc_rows][d], or null: straight to out
+    int64_t acc_rows;
+    int add;               // add to acc
+    void* out;
+    const int* map;        // output row of a gathered token, or null
+    int out_bf16, accumulate;
+};
+
+__device__ __forceinline__ void store_out(const OutArgs& a, int64_t at, int n, const float (&v)[4]) {
+    // n elements from `at`: four where the row's columns are a multiple of four, fewer at a ragged end
+    if (a.d % 4 == 0) {
+        float o[4];
+        if (a.out_bf16) {
+            u32x2* p = (u32x2*)((uint16_t*)a.out + at);
+            u32x2 w{0, 0};
+            if (a.accumulate) w = *p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = v[e] + (a.accumulate ? up16((w[e / 2] >> (16 * (e % 2))) & 0xffffu) : 0.f);
+            *p = u32x2{down16(o[0]) | (down16(o[1]) << 16), down16(o[2]) | (down16(o[3]) << 16)};
+        } else {
+            f32x4* p = (f32x4*)((float*)a.out + at);
+            f32x4 w{0.f, 0.f, 0.f, 0.f};
+            if (a.accumulate) w = *p;
+            *p = f32x4{w[0] + v[0], w[1] + v[1], w[2] + v[2], w[3] + v[3]};
+        }
+    } else {
+        for (int e = 0; e < n; ++e) {
+            if (a.out_bf16) {
+                uint16_t* p = (uint16_t*)a.out + at + e;
+                *p = (uint16_t)down16(v[e] + (a.accumulate ? up16(*p) : 0.f));
+            } else {
+                float* p = (float*)a.out + at + e;
+                *p = v[e] + (a.accumulate ? *p : 0.f);
+            }
+        }
+    }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
+    const int count = a.cnt[0], rows = a.rows < 0 ? count : a.rows, k = a.k < 0 ? (count + 63) / 64 * 64 : a.k;
+    int mt, nt;
+    if (!tile_of((a.d + C::BM - 1) / C::BM, (rows + C::BN - 1) / C::BN, mt, nt)) return;
+    const int m0 = mt * C::BM, n0 = nt * C::BN;
+    // dW reduces over the tokens: H's rows end at count (re-read behind it), D's go on with zeros to a whole slab
+    if (a.k < 0) { a.a.rows = count; a.b.rows = k; }
+    else a.b.rows = count;
+    const int k0 = (int)blockIdx.y * a.k_per, k1 = k0 + a.k_per < k ? k0 + a.k_per : k;
+    typename C::Acc acc = {};
+    if (k0 < k1) mm::Product<C>::run(a.a, a.b, m0, n0, k0, k1, a.seg, lds, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+#pragma unroll
+    for (int j = 0; j < C::NI; ++j) {
+        const int n = n0 + wn * (C::BN / C::WN) + 16 * j + lane % 16;
+        if (n >= rows) continue;
+        const int64_t row = a.acc ? blockIdx.y * a.acc_rows + n : a.map ? a.map[n] : n;
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i) {
+            const int m = m0 + wm * (C::BM / C::WM) + 16 * i + 4 * (lane / 16);
+            if (m >= a.d) continue;
+            const int64_t at = row * a.d + m;
+            float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            if (!a.acc) {
+                store_out(a, at, a.d - m < 4 ? a.d - m : 4, v);
+            } else if (a.d % 4 == 0) {
+                f32x4* p = (f32x4*)(a.acc + at);
+                *p = a.add ? *p + acc[i][j] : acc[i][j];
+            } else {
+                for (int e = 0; e < 4 && m + e < a.d; ++e) a.acc[at + e] = (a.add ? a.acc[at + e] : 0.f) + v[e];
+            }
+        }
+    }
+}
+
+// The slices' sums, rounded to the output.
+__global__ __launch_bounds__(256) void join_kernel(OutArgs a) {
+    const int rows = a.rows < 0 ? a.cnt[0] : a.rows, nc = (a.d + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)rows * nc) return;
+    const int64_t r = i / nc, c = (i - r * nc) * 4;
+    const int n = a.d - (int)c < 4 ? a.d - (int)c : 4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.split; ++s) {
+        const float* p = a.acc + (s * a.acc_rows + r) * a.d + c;
+        if (a.d % 4 == 0) {
+            const f32x4 w = *(const f32x4*)p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += w[e];
+        } else {
+            for (int e = 0; e < n; ++e) v[e] += p[e];
+        }
+    }
+    store_out(a, (a.map ? a.map[r] : r) * a.d + c, n, v);
+}
+
+// plane pairs (A's part, B's part), smallest products first
+mm::Segments segments(int pa, int pb) {
+    auto list = [](std::initializer_list<int> e) {
+        mm::Segments s{0, 0};
+        for (int x : e) s.list |= (uint32_t)x << (4 * s.n++);
+        return s;
+    };
+    if (pa == 3 && pb == 3) return list({1 | 1 << 2, 0 | 2 << 2, 2 | 0 << 2, 0 | 1 << 2, 1 | 0 << 2, 0});
+    if (pb == 3) return list({2 << 2, 1 << 2, 0});
+    if (pa == 3) return list({2, 1, 0});
+    return list({0});
+}
+
+using Z256 = mm::Config<256, 256, 2, 4, 2, false, false>;
+using Z128 = mm::Config<128, 128, 2, 2, 2, false, false>;
+using Z32 = mm::Config<128, 32, 4, 1, 4, false, false>;
+using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
+using H128 = mm::Config<128, 128, 2, 2, 2, true, false>;
+using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
+using W256 = mm::Config<256, 256, 2, 4, 2, true, true>;
+using W128 = mm::Config<128, 128, 2, 2, 2, true, true>;
+
+template <int EPI>
+void launch_logits(const LogitArgs& a, int tile, int64_t n, hipStream_t s) {
+    const dim3 grid((unsigned)(ceil_div64(a.w.rows, tile_m(tile)) * ceil_div64(n, tile_n(tile))));
+    if (tile == TILE_256) hipLaunchKernelGGL((logit_kernel<Z256, EPI>), grid, dim3(Z256::THREADS), 0, s, a);
+    else if (tile == TILE_128) hipLaunchKernelGGL((logit_kernel<Z128, EPI>), grid, dim3(Z128::THREADS), 0, s, a);
+    else hipLaunchKernelGGL((logit_kernel<Z32, EPI>), grid, dim3(Z32::THREADS), 0, s, a);
+}
+
+template <bool GRAD>
+void launch_pack(const PackArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div64(a.n, kPackRows));
+    if (a.x.bf16) {
+        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<true, true, GRAD>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((pack_kernel<true, false, GRAD>), grid, dim3(256), 0, s, a);
+    } else {
+        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<false, true, GRAD>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((pack_kernel<false, false, GRAD>), grid, dim3(256), 0, s, a);
+    }
+}
+
+// W's rows [v0, v0 + rows) as an operand: in place, or as planes in the workspace
+mm::Operand w_operand(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int64_t rows, hipStream_t s) {
+    if (!p.wpack) return mm::Operand{(const uint16_t*)x.W + v0 * p.d, 0, p.d, (int)rows};
+    uint16_t* out = (uint16_t*)(ws + p.w);
+    const int64_t plane = p.piece * p.kp;
+    const dim3 grid((unsigned)ceil_div64(rows * (p.kp / 8), 256));
+    if (x.bf16) {
+        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<true, true>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
+        else hipLaunchKernelGGL((plane_kernel<true, false>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
+    } else {
+        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<false, true>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
+        else hipLaunchKernelGGL((plane_kernel<false, false>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
+    }
+    return mm::Operand{out, plane, p.kp, (int)rows};
+}
+
+PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws) {
+    return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, (uint16_t*)(ws + p.h), (int*)(ws + p.map), (int*)(ws + p.tgt),
+                    (float2*)(ws + p.lg), (int*)(ws + p.cnt)};
+}
+
+void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div64(rows * ((a.d + 3) / 4), 256)), dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+int run_xent(const XentArgs& x, const XentPlan& p, char* ws, void* stream) {
+    const hipStream_t s = (hipStream_t)stream;
+    const PackArgs pk = pack_args(x, p, ws);
+    launch_pack<false>(pk, s);
+    LogitArgs a{};
+    a.h = mm::Operand{pk.h, p.np * p.kp, p.kp, 0};
+    a.seg = segments(p.parts, p.parts);
+    a.kp = (int)p.kp; a.cnt = pk.cnt; a.tgt = pk.tgt;
+    a.part = (float2*)(ws + p.part); a.zt = (float*)(ws + p.zt); a.nvt = (int)p.nvt;
+    for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
+        a.w = w_operand(x, p, ws, v0, p.v - v0 < p.piece ? p.v - v0 : p.piece, s);
+        a.v0 = (int)v0;
+        launch_logits<EPI_LOSS>(a, p.tile_z, p.n, s);
+    }
+    hipLaunchKernelGGL(loss_kernel, dim3((unsigned)ceil_div64(p.n, 4)), dim3(256), 0, s, a.part, a.zt, a.tgt, pk.map, pk.cnt,
+                       a.nvt, x.loss, x.lse_out);
+    return (int)hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(uint16_t* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) {
+    const hipStream_t s = (hipStream_t)stream;
+    if (p.n == 0) {   // no tokens: dW is zero
+        const int64_t n = p.v * p.d * (x.dw_bf16 ? 1 : 2), blocks = ceil_div64(n, 256 * 8);
+        hipLaunchKernelGGL(clear_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, (uint16_t*)x.dW, n);
+        return (int)hipGetLastError();
+    }
+    const PackArgs pk = pack_args(x, p, ws);
+    launch_pack<true>(pk, s);
+    LogitArgs z{};
+    z.h = mm::Operand{pk.h, p.np * p.kp, p.kp, 0};
+    z.seg = segments(p.parts, p.parts);
+    z.kp = (int)p.kp; z.cnt = pk.cnt; z.tgt = pk.tgt; z.lg = pk.lg;
+    z.dl = (uint16_t*)(ws + p.dl); z.np = p.np; z.piece = p.piece;
+    const mm::Operand dl{z.dl, p.np * p.piece, p.piece, 0};
+    OutArgs h{};
+    h.cnt = pk.cnt; h.d = (int)p.d; h.rows = -1; h.split = (int)p.split_h; h.map = pk.map; h.out = x.dH; h.out_bf16 = x.bf16;
+    h.acc = p.pieces > 1 || p.split_h > 1 ? (float*)(ws + p.acc_h) : nullptr;
+    h.acc_rows = p.np;
+    OutArgs w{};
+    w.cnt = pk.cnt; w.d = (int)p.d; w.k = -1; w.split = (int)p.split_w; w.out_bf16 = x.dw_bf16; w.accumulate = x.accumulate;
+    w.acc = p.split_w > 1 ? (float*)(ws + p.acc_w) : nullptr;
+    w.acc_rows = p.piece;
+    for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
+        const int64_t rows = p.v - v0 < p.piece ? p.v - v0 : p.piece;
+        z.w = w_operand(x, p, ws, v0, rows, s);
+        z.v0 = (int)v0;
+        if (p.dparts == 1) launch_logits<EPI_D1>(z, p.tile_z, p.n, s);
+        else launch_logits<EPI_D3>(z, p.tile_z, p.n, s);
+        if (x.dH) {
+            h.a = z.w; h.b = dl;
+            h.seg = segments(p.parts, x.bf16 ? 1 : 3);
+            h.k = (int)(ceil_div64(rows, 64) * 64);
+            h.k_per = (int)(ceil_div64(ceil_div64(h.k, p.split_h), 64) * 64);
+            h.add = v0 > 0;
+            const dim3 grid((unsigned)(ceil_div64(p.d, tile_m(p.tile_h)) * ceil_div64(p.n, tile_n(p.tile_h))), (unsigned)p.split_h);
+            if (p.tile_h == TILE_256) hipLaunchKernelGGL((out_kernel<H256>), grid, dim3(H256::THREADS), 0, s, h);
+            else if (p.tile_h == TILE_128) hipLaunchKernelGGL((out_kernel<H128>), grid, dim3(H128::THREADS), 0, s, h);
+            else hipLaunchKernelGGL((out_kernel<H32>), grid, dim3(H32::THREADS), 0, s, h);
+        }
+        if (x.dW) {
+            w.a = z.h; w.b = dl;
+            w.seg = segments(p.parts, p.dparts);
+            w.rows = (int)rows;
+            w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);
+            w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
+            const dim3 grid((unsigned)(ceil_div64(p.d, tile_m(p.tile_w)) * ceil_div64(rows, tile_n(p.tile_w))), (unsigned)p.split_w);
+            if (p.tile_w == TILE_256) hipLaunchKernelGGL((out_kernel<W256>), grid, dim3(W256::THREADS), 0, s, w);
+            else hipLaunchKernelGGL((out_kernel<W128>), grid, dim3(W128::THREADS), 0, s, w);
+            if (w.acc) launch_join(w, rows, s);
+        }
+    }
+    if (x.dH && h.acc) launch_join(h, p.n, s);
+    return (int)hipGetLastError();
+}
+
+}  // namespace dion

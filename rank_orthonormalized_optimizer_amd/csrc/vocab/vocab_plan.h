@@ -1,0 +1,158 @@
+// Host-side sizes and launch entry points of the vocabulary operators (arguments validated in
+// vocab_api.cpp).  Every run_* returns a hipError_t value.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+namespace dion {
+
+constexpr int64_t kVocabMax = (int64_t)1 << 24, kWidthMax = (int64_t)1 << 16;
+
+inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+struct EmbedArgs {
+    const void* ids;
+    const void* in;      // W or dY
+    void* out;           // Y or dW
+    int64_t tokens, vocab, width;
+    float scale;
+    int64_t padding_id;
+    int ids64, in_bf16, out_bf16, accumulate;
+};
+int run_embedding(const EmbedArgs& a, void* stream);
+
+// Layout of the table gradient's workspace: two (key, token) buffers, the radix counters, and the
+// fp32 partial rows of runs that cross chunk borders.
+struct EmbedGradPlan {
+    int64_t chunk;            // sorted tokens per chunk
+    int64_t nchunk;
+    int64_t sort_blocks;      // 0: the tokens are sorted by one workgroup
+    int digits;               // radix passes of eight bits
+    size_t keys[2], idx[2], counts, part, total;
+};
+
+constexpr int kSort1Items = 16, kSort1Max = 1024 * kSort1Items;   // one workgroup sorts up to 16384 tokens
+constexpr int kSortBlock = 4096;                                   // tokens per workgroup otherwise
+
+inline bool make_embed_grad_plan(int64_t tokens, int64_t vocab, int64_t width, EmbedGradPlan* p) {
+    EmbedGradPlan q{};
+    // about 512 chunks of at least 16 tokens: short enough to fill the chip, long enough that the
+    // partial rows at the chunk borders stay a fraction of the rows read
+    q.chunk = 16;
+    while (q.chunk * 512 < tokens) q.chunk *= 2;
+    q.nchunk = ceil_div64(tokens, q.chunk);
+    q.sort_blocks = tokens <= kSort1Max ? 0 : ceil_div64(tokens, kSortBlock);
+    q.digits = 1;
+    while (q.digits < 4 && (vocab >> (8 * q.digits)) != 0) ++q.digits;   // keys 0..vocab
+    size_t off = 0;
+    auto take = [&](size_t bytes) { const size_t at = off; off += align256(bytes); return at; };
+    for (int i = 0; i < 2; ++i) {
+        q.keys[i] = take((size_t)tokens * 4);
+        q.idx[i] = take((size_t)tokens * 4);
+    }
+    q.counts = take((size_t)q.sort_blocks * 256 * 4);
+    q.part = take((size_t)q.nchunk * 2 * (size_t)((width + 7) / 8 * 8) * 4);
+    q.total = off;
+    *p = q;
+    return true;
+}
+int run_embedding_grad(const EmbedArgs& a, const EmbedGradPlan& p, char* ws, void* stream);
+
+// Layout of a cross entropy call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32);
+// dparts: parts of D.  The vocabulary goes in `pieces` of `piece` rows (a multiple of 256).
+struct XentPlan {
+    int64_t n, v, d, kp;      // tokens, vocab, width, width rounded up to 64
+    int64_t np;               // tokens rounded up to 256
+    int parts, dparts;
+    bool wpack;               // W goes through packed planes (fp32, or a width that is no multiple of 64)
+    int64_t piece, pieces;
+    int64_t nvt;              // softmax partials per token (forward)
+    int tile_z, tile_h, tile_w;   // tile shapes of the logits, dH and dW (TILE_*)
+    int64_t split_h, split_w; // slices of the reductions of dH (over the piece) and dW (over the tokens)
+    size_t h, map, tgt, lg, cnt, part, zt, w, dl, acc_h, acc_w, total;
+};
+
+enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens)
+constexpr int64_t kPieceBytes = (int64_t)512 << 20;   // of D, and of W's planes, per piece of the vocabulary
+constexpr int kCUs = 256;
+
+// The largest tile that still gives half the CUs a workgroup: it reads each operand least often.
+inline int pick_tile(int64_t m, int64_t n) {
+    if (n <= 32) return TILE_32;
+    return ceil_div64(m, 256) * ceil_div64(n, 256) >= kCUs / 2 ? TILE_256 : TILE_128;
+}
+inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : 128; }
+inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : 32; }
+// Slices of a reduction of length k so that an output of m x n fills the chip, each at least 512 long.
+inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int tile) {
+    const int64_t tiles = ceil_div64(m, tile_m(tile)) * ceil_div64(n, tile_n(tile));
+    int64_t s = kCUs / (tiles < 1 ? 1 : tiles);
+    if (s > k / 512) s = k / 512;
+    return s < 1 ? 1 : s;
+}
+
+inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf16, int dw_bf16, int for_grad,
+                           XentPlan* p) {
+    XentPlan q{};
+    q.n = tokens; q.v = vocab; q.d = width;
+    q.kp = ceil_div64(width, 64) * 64;
+    q.np = ceil_div64(tokens < 1 ? 1 : tokens, 256) * 256;
+    q.parts = bf16 ? 1 : 3;
+    q.dparts = bf16 && dw_bf16 ? 1 : 3;
+    q.wpack = !bf16 || width % 64 != 0;
+    int64_t per_row = q.wpack ? q.parts * q.kp * 2 : 0;   // bytes of scratch per vocabulary row of a piece
+    if (for_grad && q.dparts * q.np * 2 > per_row) per_row = q.dparts * q.np * 2;
+    const int64_t all = ceil_div64(vocab, 256) * 256;
+    q.piece = all;
+    if (per_row > 0 && kPieceBytes / per_row < all) {
+        const int64_t most = kPieceBytes / per_row / 256 * 256;
+        q.pieces = ceil_div64(all, most < 256 ? 256 : most);
+        q.piece = ceil_div64(ceil_div64(all, q.pieces), 256) * 256;
+    }
+    q.pieces = ceil_div64(all, q.piece);
+    q.tile_z = pick_tile(q.piece, tokens);
+    q.nvt = ceil_div64(vocab, tile_m(q.tile_z));
+    size_t off = 0;
+    auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
+    q.cnt = take(256);
+    q.h = take(q.parts * q.np * q.kp * 2);
+    q.map = take(q.np * 4);
+    q.tgt = take(q.np * 4);
+    if (q.wpack) q.w = take(q.parts * q.piece * q.kp * 2);
+    if (!for_grad) {
+        q.part = take(q.np * q.nvt * 8);
+        q.zt = take(q.np * 4);
+    } else {
+        q.tile_h = pick_tile(width, tokens);
+        q.tile_w = pick_tile(width, q.piece);
+        q.split_h = pick_split(width, tokens, q.piece, q.tile_h);
+        q.split_w = pick_split(width, q.piece, tokens, q.tile_w);
+        q.lg = take(q.np * 8);
+        q.dl = take(q.dparts * q.np * q.piece * 2);
+        if (q.pieces > 1 || q.split_h > 1) q.acc_h = take(q.split_h * q.np * width * 4);
+        if (q.split_w > 1) q.acc_w = take(q.split_w * q.piece * width * 4);
+    }
+    q.total = off;
+    *p = q;
+    return off < ((size_t)1 << 46);
+}
+
+struct XentArgs {
+    const void* H;
+    const void* W;
+    const void* targets;
+    float* loss;         // forward
+    float* lse_out;      // forward
+    const float* lse;    // gradient
+    const float* grad;
+    int64_t grad_n;
+    void* dH;
+    void* dW;
+    int64_t ignore;
+    int t64, bf16, dw_bf16, accumulate;
+};
+int run_xent(const XentArgs& a, const XentPlan& p, char* ws, void* stream);
+int run_xent_grad(const XentArgs& a, const XentPlan& p, char* ws, void* stream);
+
+}  // namespace dion
