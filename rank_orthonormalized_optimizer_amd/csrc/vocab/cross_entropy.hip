@@ -284,16 +284,12 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
                 for (int v = 0; v < 4; ++v) {
                     const int m = mw + 16 * i + v;
                     const float p = exp_exact(acc[i][j][v] - lg.x) - (m == y ? 1.f : 0.f);
-                    split3(in && m < rows ? p * lg.y : 0.f, part[v]);
+                    split3(m < rows ? p * lg.y : 0.f, part[v]);
                 }
 #pragma unroll
-                for (int q = 0; q < PD; ++q) {
-                    uint16_t* to = a.dl + (q * a.np + n) * a.piece + mw + 16 * i;
-                    *(u32x2*)to = u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
-                    // zeros up to the end of a 64-token slab, which the last tile may not reach by itself
-                    if (C::BN < mm::kBK && n0 + C::BN >= count && n0 % mm::kBK == 0)
-                        *(u32x2*)(to + C::BN * a.piece) = u32x2{0, 0};
-                }
+                for (int q = 0; q < PD; ++q)
+                    if (in) *(u32x2*)(a.dl + (q * a.np + n) * a.piece + mw + 16 * i) =
+                        u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
             }
         }
     }
@@ -378,9 +374,8 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
     int mt, nt;
     if (!tile_of((a.d + C::BM - 1) / C::BM, (rows + C::BN - 1) / C::BN, mt, nt)) return;
     const int m0 = mt * C::BM, n0 = nt * C::BN;
-    // dW reduces over the tokens: H's rows end at count (re-read behind it), D's go on with zeros to a whole slab
-    if (a.k < 0) { a.a.rows = count; a.b.rows = k; }
-    else a.b.rows = count;
+    if (a.k < 0) a.a.rows = count;   // dW reduces over the tokens
+    a.b.rows = count;
     const int k0 = (int)blockIdx.y * a.k_per, k1 = k0 + a.k_per < k ? k0 + a.k_per : k;
     typename C::Acc acc = {};
     if (k0 < k1) mm::Product<C>::run(a.a, a.b, m0, n0, k0, k1, a.seg, lds, acc);

@@ -8,10 +8,10 @@
 // plane pairs to multiply, smallest first, and the k loop runs over all of them.
 //
 // A workgroup owns a BM x BN tile, its waves WM x WN parts of it.  Slabs of 64 k go from memory
-// straight to LDS (buffer loads with an LDS destination, 16 bytes per lane), STAGES - 1 slabs
-// ahead; one barrier per slab.  The LDS image is swizzled by permuting which 16 bytes a lane
-// fetches: chunk c of row x of an [x][64] tile sits at c ^ (x & 7), so that the 16 rows of a
-// fragment read fall on different banks; a [64][x] tile moves its 32-byte units by the row's
+// straight to LDS (buffer loads with an LDS destination, 16 bytes per lane) into a ring of STAGES
+// stages; one barrier per slab.  The LDS image is swizzled by permuting which 16 bytes a lane
+// fetches: chunk c of row x of an [x][64] tile sits at c ^ (x / 2 % 8), so that the 16 rows of a
+// fragment read (128 bytes apart) fall on different banks of 64; a [64][x] tile moves its 32-byte units by the row's
 // position in the fragment.
 //
 // Lane layout of v_mfma_f32_16x16x32_bf16: A[l % 16][8 (l / 16) + i], B likewise, D element v of
@@ -38,7 +38,7 @@ struct Operand {
     const uint16_t* p;
     int64_t plane;   // elements between part planes
     int64_t ld;      // elements between rows, a multiple of 8
-    int rows;        // rows: of x for a k-contiguous operand, of k for a transposed one; reads are clamped to them
+    int rows;        // of x for a k-contiguous operand (reads are clamped to them), of k for a transposed one (zeros behind them)
 };
 
 // Plane pairs of a product: entry s in bits 4s..: A's plane in two bits, B's in the next two.
@@ -46,6 +46,14 @@ struct Segments {
     uint32_t n;
     uint32_t list;
 };
+
+// 16 bytes per lane from the descriptor's range (zeros outside it) to 1 KB of LDS at byte address lds, which
+// must be the same for all lanes.  Written as assembly because the compiler waits for every load in flight before a
+// transposed LDS read that follows the builtin of this load, wherever it reads; it names no output register, and
+// wait_slab() is what waits for it.  (m0 is the compiler's only for instructions that do not occur here.)
+__device__ __forceinline__ void load_to_lds(u32x4 desc, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(desc), "s"(lds));
+}
 
 template <int X>   // rows of 16-byte chunks per [64][X] row
 __device__ __forceinline__ int tr_swz(int k) {
@@ -61,7 +69,6 @@ struct Tile {
     static constexpr int kLoads = X / 8 / WAVES;   // 1 KB wave loads per slab and wave
     static_assert(X / 8 % WAVES == 0, "whole wave loads");
     uint32_t off[kLoads];   // byte offset of this lane's chunk from the slab's base
-    int krow[TR ? kLoads : 1];
 
     // x0: first row of x of the tile (k-contiguous: the slab base is row x0; transposed: column x0)
     __device__ __forceinline__ void init(const Operand& o, int x0, int wave, int lane) {
@@ -69,41 +76,35 @@ struct Tile {
         for (int i = 0; i < kLoads; ++i) {
             const int q = wave * kLoads + i;
             if constexpr (!TR) {
-                const int x = q * 8 + lane / 8, c = (lane % 8) ^ (x & 7);
+                const int x = q * 8 + lane / 8, c = (lane % 8) ^ ((x >> 1) & 7);
                 const int row = x0 + x < o.rows ? x : o.rows - 1 - x0;
                 off[i] = (uint32_t)(row * o.ld + c * 8) * 2u;
             } else {
                 constexpr int NC = X / 8;   // chunks per row of k
                 const int k = q * (64 / NC) + lane / NC, c = (lane % NC) ^ tr_swz<X>(k);
-                krow[i] = k;
                 int64_t col = x0 + c * 8;
                 if (col > o.ld - 8) col = o.ld - 8;   // past the row: unused columns, any valid address
                 off[i] = (uint32_t)((k * o.ld + col) * 2);
             }
         }
     }
-    // Starts the loads of the slab at k0 of plane `part` into lds (this tile's image).
-    __device__ __forceinline__ void load(const Operand& o, int x0, int part, int k0, uint16_t* lds, int wave) const {
+    // The slab at k0 of plane `part`, as the descriptor its loads go through.
+    static __device__ __forceinline__ u32x4 slab(const Operand& o, int x0, int part, int k0) {
         const uint16_t* base = o.p + part * o.plane + (TR ? (int64_t)k0 * o.ld : (int64_t)x0 * o.ld + k0);
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7fffffff, 0x00027000);
-        if (TR && k0 + kBK > o.rows) {   // the last slab: rows of k past the end re-read the last row
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int over = k0 + krow[TR ? i : 0] - (o.rows - 1);
-                const uint32_t at = off[i] - (over > 0 ? (uint32_t)(over * o.ld * 2) : 0u);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave * kLoads + i) * 512), 16, at, 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave * kLoads + i) * 512), 16, off[i], 0, 0, 0);
-        }
+        // a transposed operand ends at its last row of k: the descriptor's range makes the rows behind it read as zeros
+        const int64_t left = TR ? (o.rows - k0) * o.ld * 2 : 0x7fffffff;
+        const uint64_t at = (uint64_t)base;
+        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)(left < 0x7fffffff ? left : 0x7fffffff), 0x00027000u};
+    }
+    // Starts the i-th of this wave's loads of a slab into lds (this tile's image).
+    __device__ __forceinline__ void load(u32x4 r, int i, uint32_t lds, int wave) const {
+        load_to_lds(r, off[i], lds + (wave * kLoads + i) * 1024);
     }
     // Fragment of the 16 rows from x (a multiple of 16, relative to the tile), k step ks (0 or 1).
     static __device__ __forceinline__ u32x4 frag(uint16_t* lds, int x, int ks, int lane) {
         if constexpr (!TR) {
             const int row = x + lane % 16;
-            return *(const u32x4*)&lds[row * kBK + (((ks * 4 + lane / 16) ^ (row & 7)) << 3)];
+            return *(const u32x4*)&lds[row * kBK + (((ks * 4 + lane / 16) ^ ((row >> 1) & 7)) << 3)];
         } else {
             const int j = lane % 16, k = ks * 32 + 8 * (lane / 16) + j / 4;
             uint16_t* at = lds + k * X + ((((x >> 3) + ((j >> 1) & 1)) ^ tr_swz<X>(k)) << 3) + 4 * (j & 1);
@@ -115,9 +116,12 @@ struct Tile {
     }
 };
 
+// All but the newest N loads of this wave landed, its LDS reads are done, and every wave is here.
 template <int N>
-__device__ __forceinline__ void wait_slab() {   // all but the newest N loads of this wave landed, and every wave is here
+__device__ __forceinline__ void wait_slab() {
+    __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_, bool TA_, bool TB_>
@@ -131,56 +135,127 @@ struct Config {
     typedef f32x4 Acc[MI][NI];
 };
 
-// acc += the product over k in [k0, k1) (multiples of 64) of every segment.  The caller's tile starts at
-// (m0, n0).  Every thread of the workgroup calls it.
+// run: acc += the product over k in [k0, k1) (multiples of 64, k0 < k1) of every segment.  The caller's
+// tile starts at (m0, n0).  Every thread of the workgroup calls it.
+//
+// A slab is two steps of 32 k.  While the matrix cores work on one step, the fragments of the next
+// one are read: a block row's A fragment as soon as that row's products are issued, so that one set
+// of A registers is enough.  The one barrier of a slab stands between its two steps: by then every
+// wave has read the whole slab, its stage is loaded again, and the next slab is there.
 template <class C>
 struct Product {
-static __device__ __forceinline__ void run(const Operand& a, const Operand& b, int m0, int n0, int k0, int k1,
-                                           Segments seg, uint16_t* lds, typename C::Acc& acc) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % C::WM, wn = wave / C::WM;
-    Tile<C::BM, C::TA, C::WAVES> ta;
-    Tile<C::BN, C::TB, C::WAVES> tb;
-    constexpr int kPer = Tile<C::BM, C::TA, C::WAVES>::kLoads + Tile<C::BN, C::TB, C::WAVES>::kLoads;
-    ta.init(a, m0, wave, lane);
-    tb.init(b, n0, wave, lane);
-    const int nk = (k1 - k0) / kBK, total = nk * (int)seg.n;
-    int ls = 0, lk = 0, lslot = 0;   // the next slab to load: segment, slab within it, LDS stage
-    auto load = [&]() {
-        const uint32_t e = seg.list >> (4 * ls);
-        uint16_t* t = lds + lslot * C::kStage;
-        ta.load(a, m0, e & 3, k0 + lk * kBK, t, wave);
-        tb.load(b, n0, (e >> 2) & 3, k0 + lk * kBK, t + C::BM * kBK, wave);
-        if (++lk == nk) { lk = 0; ++ls; }
-        if (++lslot == C::STAGES) lslot = 0;
-    };
-    const int ahead = C::STAGES - 1 < total ? C::STAGES - 1 : total;
-    for (int i = 0; i < ahead; ++i) load();
-    int slot = 0;
-    for (int it = 0; it < total; ++it) {
-        // slabs it + 1 .. it + STAGES - 2 may still be in flight, and near the end fewer are
-        if (it + C::STAGES - 2 < total) wait_slab<(C::STAGES - 2) * kPer>();
+    using TileA = Tile<C::BM, C::TA, C::WAVES>;
+    using TileB = Tile<C::BN, C::TB, C::WAVES>;
+
+    static __device__ __forceinline__ void run(const Operand& a, const Operand& b, int m0, int n0, int k0, int k1,
+                                               Segments seg, uint16_t* lds, typename C::Acc& acc) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int xa = (wave % C::WM) * (C::BM / C::WM), xb = (wave / C::WM) * (C::BN / C::WN);
+        TileA ta;
+        TileB tb;
+        constexpr int kPer = TileA::kLoads + TileB::kLoads;
+        ta.init(a, m0, wave, lane);
+        tb.init(b, n0, wave, lane);
+        const int nk = (k1 - k0) / kBK, total = nk * (int)seg.n;
+        Loads ld(k0, nk, seg.list);
+        auto load_all = [&]() {
+            ld.begin(a, b, m0, n0, lds);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) ld.one(ta, tb, i, wave);
+        };
+        const int ahead = C::STAGES < total ? C::STAGES : total;
+        for (int i = 0; i < ahead; ++i) load_all();
+        if (total >= C::STAGES) wait_slab<(C::STAGES - 1) * kPer>();
         else wait_slab<0>();
-        if (it + C::STAGES - 1 < total) load();
-        uint16_t* la = lds + slot * C::kStage;
-        uint16_t* lb = la + C::BM * kBK;
+        u32x4 fa[C::MI], fb[C::NI];
+        uint16_t* la = lds;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            u32x4 fa[C::MI], fb[C::NI];
+        for (int i = 0; i < C::MI; ++i) fa[i] = TileA::frag(la, xa + 16 * i, 0, lane);
 #pragma unroll
-            for (int i = 0; i < C::MI; ++i) fa[i] = ta.frag(la, wm * (C::BM / C::WM) + 16 * i, ks, lane);
-#pragma unroll
-            for (int j = 0; j < C::NI; ++j) fb[j] = tb.frag(lb, wn * (C::BN / C::WN) + 16 * j, ks, lane);
-#pragma unroll
-            for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-                for (int j = 0; j < C::NI; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa[i]),
-                                                                        __builtin_bit_cast(bf16x8, fb[j]), acc[i][j], 0, 0, 0);
+        for (int j = 0; j < C::NI; ++j) fb[j] = TileB::frag(la + C::BM * kBK, xb + 16 * j, 0, lane);
+        int slot = 0;
+        auto next = [&]() {
+            if (++slot == C::STAGES) slot = 0;
+            la = lds + slot * C::kStage;
+        };
+        int it = 0;
+        for (; it + C::STAGES < total; ++it) {
+            step<0>(la, 1, xa, xb, lane, fa, fb, acc, [](int) {});
+            ld.begin(a, b, m0, n0, lds);
+            next();
+            wait_slab<(C::STAGES - 2) * kPer>();
+            step<kPer>(la, 0, xa, xb, lane, fa, fb, acc, [&](int i) { ld.one(ta, tb, i, wave); });
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (++slot == C::STAGES) slot = 0;
+        for (; it < total; ++it) {   // nothing left to load
+            step<0>(la, 1, xa, xb, lane, fa, fb, acc, [](int) {});
+            wait_slab<0>();
+            next();
+            step<0>(la, 0, xa, xb, lane, fa, fb, acc, [](int) {});   // (behind the last slab it reads a stage whose values are not used)
+        }
     }
-}
+
+    // The loads of one slab, in the order of the segments: which is next, and its descriptors.
+    struct Loads {
+        int k0, nk;
+        int k = 0, slot = 0;
+        uint32_t list;
+        u32x4 ra, rb;
+        uint32_t to;
+        __device__ __forceinline__ Loads(int k0_, int nk_, uint32_t list_) : k0(k0_), nk(nk_), list(list_) {}
+        __device__ __forceinline__ void begin(const Operand& a, const Operand& b, int m0, int n0, uint16_t* lds) {
+            ra = TileA::slab(a, m0, list & 3, k0 + k * kBK);
+            rb = TileB::slab(b, n0, (list >> 2) & 3, k0 + k * kBK);
+            to = (uint32_t)(uintptr_t)(lds_void*)lds + slot * (C::kStage * 2);
+            if (++k == nk) { k = 0; list >>= 4; }
+            if (++slot == C::STAGES) slot = 0;
+        }
+        __device__ __forceinline__ void one(const TileA& ta, const TileB& tb, int i, int wave) const {
+            if (i < TileA::kLoads) ta.load(ra, i, to, wave);
+            else tb.load(rb, i - TileA::kLoads, to + C::BM * kBK * 2, wave);
+        }
+    };
+
+    // The products of the fragments at hand, and the fragments of step ks of the stage la in their place;
+    // load(0 .. LOADS - 1) starts the loads that go along.
+    template <int LOADS, class F>
+    static __device__ __forceinline__ void step(uint16_t* la, int ks, int xa, int xb, int lane, u32x4 (&fa)[C::MI],
+                                                u32x4 (&fb)[C::NI], typename C::Acc& acc, F load) {
+        constexpr int per_row = (LOADS + C::MI - 1) / C::MI;
+        constexpr int da = C::TA ? 2 : 1, db = C::TB ? 2 : 1;   // LDS reads per fragment
+        constexpr int gap = C::MI * C::NI * 3 / 4 / (C::MI * da + C::NI * db) > 1
+                                ? C::MI * C::NI * 3 / 4 / (C::MI * da + C::NI * db) : 1;   // products per LDS read
+        u32x4 nb[C::NI];
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) nb[j] = TileB::frag(la + C::BM * kBK, xb + 16 * j, ks, lane);
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i) {
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa[i]),
+                                                                    __builtin_bit_cast(bf16x8, fb[j]), acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < per_row; ++q)
+                if (i * per_row + q < LOADS) load(i * per_row + q);
+            fa[i] = TileA::frag(la, xa + 16 * i, ks, lane);
+        }
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) fb[j] = nb[j];
+        // keep the reads spread over the first three quarters of the products
+#pragma unroll
+        for (int r = 0; r < C::NI * db; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x008, gap, 0);   // matrix products
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
+        }
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i) {
+#pragma unroll
+            for (int r = 0; r < da; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x008, gap, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+        }
+    }
 };
 
 }  // namespace mm

@@ -77,19 +77,20 @@ enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2 };   // 256 x 256, 128 x 128, 128
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;   // of D, and of W's planes, per piece of the vocabulary
 constexpr int kCUs = 256;
 
-// The largest tile that still gives half the CUs a workgroup: it reads each operand least often.
-inline int pick_tile(int64_t m, int64_t n) {
-    if (n <= 32) return TILE_32;
-    return ceil_div64(m, 256) * ceil_div64(n, 256) >= kCUs / 2 ? TILE_256 : TILE_128;
-}
 inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : 128; }
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : 32; }
+inline int64_t tiles(int64_t m, int64_t n, int t) { return ceil_div64(m, tile_m(t)) * ceil_div64(n, tile_n(t)); }
 // Slices of a reduction of length k so that an output of m x n fills the chip, each at least 512 long.
 inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int tile) {
-    const int64_t tiles = ceil_div64(m, tile_m(tile)) * ceil_div64(n, tile_n(tile));
-    int64_t s = kCUs / (tiles < 1 ? 1 : tiles);
+    int64_t s = kCUs / tiles(m, n, tile);
     if (s > k / 512) s = k / 512;
     return s < 1 ? 1 : s;
+}
+// The largest tile, which reads each operand least often, that still gives half the CUs a workgroup, if the
+// reduction is long enough by slices of it (k = 0: the reduction is not sliced).
+inline int pick_tile(int64_t m, int64_t n, int64_t k) {
+    if (n <= 32) return TILE_32;
+    return tiles(m, n, TILE_256) * (k ? pick_split(m, n, k, TILE_256) : 1) >= kCUs / 2 ? TILE_256 : TILE_128;
 }
 
 inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf16, int dw_bf16, int for_grad,
@@ -111,7 +112,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.piece = ceil_div64(ceil_div64(all, q.pieces), 256) * 256;
     }
     q.pieces = ceil_div64(all, q.piece);
-    q.tile_z = pick_tile(q.piece, tokens);
+    q.tile_z = pick_tile(q.piece, tokens, 0);
     q.nvt = ceil_div64(vocab, tile_m(q.tile_z));
     size_t off = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
@@ -124,9 +125,9 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.part = take(q.np * q.nvt * 8);
         q.zt = take(q.np * 4);
     } else {
-        q.tile_h = pick_tile(width, tokens);
-        q.tile_w = pick_tile(width, q.piece);
-        q.split_h = pick_split(width, tokens, q.piece, q.tile_h);
+        q.tile_h = pick_tile(width, tokens, q.piece);
+        q.tile_w = pick_tile(width, q.piece, tokens);
+        q.split_h = pick_split(width, tokens < 1 ? 1 : tokens, q.piece, q.tile_h);
         q.split_w = pick_split(width, q.piece, tokens, q.tile_w);
         q.lg = take(q.np * 8);
         q.dl = take(q.dparts * q.np * q.piece * 2);
