@@ -44,12 +44,20 @@ __device__ __forceinline__ void split3(float a, uint32_t (&part)[3]) {
     part[2] = down16(r - up16(part[1]));
 }
 
-// exp(x) for x <= 0 to about an ulp: the rounding of x log2(e) is carried into the result.
-__device__ __forceinline__ float exp_exact(float x) {
-    const float h = x * 1.44269504f;
-    const float l = fmaf(x, 1.44269504f, -h) + x * 1.92596299e-8f;
+// The softmax runs in powers of two.  kLog2e is log2(e) rounded to fp32; 2^fma(z, kLog2e, -c) takes e to
+// z (1 + 1.3e-8), less than z's own rounding, and a sum's reference point c is kept in the same unit, so that its
+// rounding drops out.  kLn2 + kLn2Low is 1 / kLog2e.
+constexpr float kLog2e = 1.44269504f;
+constexpr float kLn2 = (float)(1.0 / (double)kLog2e);
+constexpr float kLn2Low = (float)(1.0 / (double)kLog2e - (double)kLn2);
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// exp(z - lse) to about two ulp of the difference: its rounding as a power of two is carried into the result.
+__device__ __forceinline__ float exp_exact(float z, float lse) {
+    const float x = z - lse, h = x * kLog2e;
+    const float l = fmaf(x, kLog2e, -h) + x * 1.92596299e-8f;   // log2(e) - kLog2e
     const float r = __builtin_amdgcn_exp2f(h);
-    return x < -104.f ? 0.f : fmaf(r, l * 0.693147181f, r);
+    return x < -87.f ? 0.f : fmaf(r, l * 0.693147181f, r);
 }
 
 // ---------------------------------------------------------------------------
@@ -183,19 +191,29 @@ __global__ __launch_bounds__(256) void plane_kernel(const void* W, uint16_t* out
 // ---------------------------------------------------------------------------
 // Products
 // ---------------------------------------------------------------------------
-// Tile of this workgroup: workgroups go to the eight XCDs in turn; each XCD takes a contiguous
-// range of the tiles, in bands of eight tile rows, so that its L2 serves the operands' re-reads.
-__device__ __forceinline__ bool tile_of(int tm, int tn, int& mt, int& nt) {
-    const int total = tm * tn, id = blockIdx.x;
-    if (id >= total) return false;
-    const int q = total / 8, r = total % 8, x = id % 8;
-    const int at = x * q + (x < r ? x : r) + id / 8;
-    constexpr int G = 8;
-    const int band = at / (G * tn), m0 = band * G, g = tm - m0 < G ? tm - m0 : G, in = at - band * G * tn;
-    mt = m0 + in % g;
-    nt = in / g;
-    return true;
-}
+// The tiles of this workgroup.  Workgroups go to the eight XCDs in turn; each XCD takes a contiguous
+// range of the tiles and its workgroups walk it side by side, in bands of eight tile rows, so that
+// its L2 serves the operands' re-reads.
+struct Walk {
+    int tm, tn, at, end, by;
+    __device__ __forceinline__ Walk(int tm_, int tn_, int slices) : tm(tm_), tn(tn_) {
+        const int total = tm * tn * slices, q = total / 8, r = total % 8, x = blockIdx.x % 8;
+        const int start = x * q + (x < r ? x : r);
+        by = ((int)gridDim.x - x + 7) / 8;   // workgroups on this XCD
+        at = start + blockIdx.x / 8;
+        end = start + q + (x < r ? 1 : 0);
+    }
+    __device__ __forceinline__ bool done() const { return at >= end; }
+    __device__ __forceinline__ void next() { at += by; }
+    __device__ __forceinline__ void tile(int& mt, int& nt, int& slice) const {
+        constexpr int G = 8;
+        slice = at / (tm * tn);
+        const int t = at - slice * tm * tn;
+        const int band = t / (G * tn), m0 = band * G, g = tm - m0 < G ? tm - m0 : G, in = t - band * G * tn;
+        mt = m0 + in % g;
+        nt = in / g;
+    }
+};
 
 struct LogitArgs {
     mm::Operand w, h;      // w.rows: rows of this piece; h.rows is read from cnt
@@ -205,12 +223,13 @@ struct LogitArgs {
     const int* tgt;
     int v0;                // first vocabulary row of the piece
     // loss
-    float2* part;          // [np][nvt] maximum and sum of exponentials of a tile of logits
+    float2* part;          // [np][nvt] maximum of a tile of logits and sum of exponentials, as powers of two
     float* zt;             // the target's logit
     int nvt;
     // gradient
     const float2* lg;
     uint16_t* dl;          // planes [dparts][np][piece]
+    float* rest;           // [np] what the first part of D leaves of the target's element
     int64_t np, piece;
 };
 
@@ -219,79 +238,123 @@ enum { EPI_LOSS, EPI_D1, EPI_D3 };
 template <class C, int EPI>
 __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
     __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
+    __shared__ float2 red[EPI == EPI_LOSS ? C::WM * C::BN : 1];
     const int count = a.cnt[0], rows = a.w.rows;
-    int mt, nt;
-    if (!tile_of((rows + C::BM - 1) / C::BM, (count + C::BN - 1) / C::BN, mt, nt)) return;
-    const int m0 = mt * C::BM, n0 = nt * C::BN;
+    Walk walk((rows + C::BM - 1) / C::BM, (count + C::BN - 1) / C::BN, 1);
+    if (walk.done()) return;
     a.h.rows = count;
-    typename C::Acc acc = {};
-    mm::Product<C>::run(a.w, a.h, m0, n0, 0, a.kp, a.seg, lds, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
-    const int mw = m0 + wm * (C::BM / C::WM) + 4 * (lane / 16);   // this lane's first row, + 16 i + v
-    const int cw = wn * (C::BN / C::WN) + lane % 16;              // its first column in the tile, + 16 j
-    if constexpr (EPI == EPI_LOSS) {
-        __syncthreads();   // the last slab was read
-        float2* red = (float2*)lds;   // [WM][BN]
+    mm::Product<C> mul(lds);
+    int mt, nt, slice;
+    walk.tile(mt, nt, slice);
+    mul.start(a.w, a.h, mt * C::BM, nt * C::BN, 0, a.kp, a.seg);
+    const int rl = mul.xa + 4 * (mul.lane / 16);   // this lane's first row in the tile, + 16 i + v
+    const int cl = mul.xb + mul.lane % 16;         // its first column, + 16 j
+    for (;;) {
+        const int m0 = mul.m0, n0 = mul.n0;
+        int y[C::NI];
+        float2 lg[C::NI];
 #pragma unroll
         for (int j = 0; j < C::NI; ++j) {
-            const int n = n0 + cw + 16 * j, y = n < count ? a.tgt[n] - a.v0 : -1;
-            float mx = -INFINITY;
+            const int n = n0 + cl + 16 * j, nn = n < count ? n : count - 1;
+            y[j] = a.tgt[nn] - a.v0;
+            if (EPI != EPI_LOSS) lg[j] = a.lg[nn];
+        }
+        typename C::Acc acc = {};
+        mul.finish(a.w, a.h, acc);
+        walk.next();
+        const bool more = !walk.done();
+        if (more) {
+            walk.tile(mt, nt, slice);
+            mul.start(a.w, a.h, mt * C::BM, nt * C::BN, 0, a.kp, a.seg);
+        }
+        if (m0 + C::BM > rows) {
 #pragma unroll
             for (int i = 0; i < C::MI; ++i)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int m = mw + 16 * i + v;
-                    if (m >= rows) acc[i][j][v] = -INFINITY;
-                    else if (m == y) a.zt[n] = acc[i][j][v];
-                    mx = fmaxf(mx, acc[i][j][v]);
-                }
-            mx = fmaxf(mx, __shfl_xor(mx, 16));
-            mx = fmaxf(mx, __shfl_xor(mx, 32));
-            const float ref = mx == -INFINITY ? 0.f : mx;   // an empty or all-minus-infinity column sums to 0, NaN to NaN
-            float s = 0.f;
+                for (int j = 0; j < C::NI; ++j)
 #pragma unroll
-            for (int i = 0; i < C::MI; ++i)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) s += exp_exact(acc[i][j][v] - ref);
-            s += __shfl_xor(s, 16);
-            s += __shfl_xor(s, 32);
-            if (lane < 16) red[wm * C::BN + cw + 16 * j] = float2{mx, s};
+                    for (int v = 0; v < 4; ++v)
+                        if (m0 + rl + 16 * i + v >= rows) acc[i][j][v] = -INFINITY;
         }
-        __syncthreads();
-        for (int c = threadIdx.x; c < C::BN && n0 + c < count; c += C::THREADS) {
-            float2 t = red[c];
-#pragma unroll
-            for (int i = 1; i < C::WM; ++i) {
-                const float2 u = red[i * C::BN + c];
-                const float m = fmaxf(t.x, u.x), ref = m == -INFINITY ? 0.f : m;
-                t.y = t.y * exp_exact(t.x - ref) + u.y * exp_exact(u.x - ref);
-                t.x = m;
-            }
-            a.part[(int64_t)(n0 + c) * a.nvt + (a.v0 + m0) / C::BM] = t;
-        }
-    } else {
-        constexpr int PD = EPI == EPI_D3 ? 3 : 1;
 #pragma unroll
         for (int j = 0; j < C::NI; ++j) {
-            const int n = n0 + cw + 16 * j;
-            const bool in = n < count;
-            const int y = in ? a.tgt[n] - a.v0 : -1;
-            const float2 lg = in ? a.lg[n] : float2{0.f, 0.f};
+            const int n = n0 + cl + 16 * j;
+            // the target's element is this lane's if it is 16 i + v rows behind its first; few tiles of a column have it
+            const int at = y[j] - m0 - rl;
+            const bool mine = n < count && at >= 0 && (at & 15) < 4 && at < 16 * C::MI && y[j] < rows;
+            if constexpr (EPI == EPI_LOSS) {
+                if (__any(mine)) {
 #pragma unroll
-            for (int i = 0; i < C::MI; ++i) {
-                uint32_t part[4][3];
+                    for (int i = 0; i < C::MI; ++i)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int m = mw + 16 * i + v;
-                    const float p = exp_exact(acc[i][j][v] - lg.x) - (m == y ? 1.f : 0.f);
-                    split3(m < rows ? p * lg.y : 0.f, part[v]);
+                        for (int v = 0; v < 4; ++v)
+                            if (mine && at == 16 * i + v) a.zt[n] = acc[i][j][v];
                 }
+                float mx = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < PD; ++q)
-                    if (in) *(u32x2*)(a.dl + (q * a.np + n) * a.piece + mw + 16 * i) =
-                        u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
+                for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) mx = fmaxf(mx, acc[i][j][v]);
+                mx = fmaxf(mx, __shfl_xor(mx, 16));
+                mx = fmaxf(mx, __shfl_xor(mx, 32)) * kLog2e;
+                const float ref = mx == -INFINITY ? 0.f : mx;   // an empty or all-minus-infinity column sums to 0, NaN to NaN
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) s += exp2_fast(fmaf(acc[i][j][v], kLog2e, -ref));
+                s += __shfl_xor(s, 16);
+                s += __shfl_xor(s, 32);
+                if (mul.lane < 16) red[mul.wave % C::WM * C::BN + cl + 16 * j] = float2{mx, s};
+            } else {
+                constexpr int PD = EPI == EPI_D3 ? 3 : 1;
+                const float c = lg[j].x * kLog2e;
+#pragma unroll
+                for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        acc[i][j][v] = PD == 3 ? exp_exact(acc[i][j][v], lg[j].x) : exp2_fast(fmaf(acc[i][j][v], kLog2e, -c));
+                if (__any(mine)) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (mine && at == 16 * i + v) {
+                                acc[i][j][v] -= 1.f;
+                                d = acc[i][j][v] * lg[j].y;
+                            }
+                    if (mine) a.rest[n] = d - up16(down16(d));
+                }
+                if (n < count) {
+#pragma unroll
+                    for (int i = 0; i < C::MI; ++i) {
+                        uint16_t* to = a.dl + n * a.piece + m0 + rl + 16 * i;
+                        uint32_t part[4][3];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) split3(acc[i][j][v] * lg[j].y, part[v]);
+#pragma unroll
+                        for (int q = 0; q < PD; ++q)
+                            *(u32x2*)(to + q * a.np * a.piece) = u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
+                    }
+                }
             }
         }
+        if constexpr (EPI == EPI_LOSS) {
+            __syncthreads();
+            for (int c = threadIdx.x; c < C::BN && n0 + c < count; c += C::THREADS) {
+                float2 t = red[c];
+#pragma unroll
+                for (int i = 1; i < C::WM; ++i) {
+                    const float2 u = red[i * C::BN + c];
+                    const float m = fmaxf(t.x, u.x), ref = m == -INFINITY ? 0.f : m;
+                    t.y = t.y * exp2_fast(t.x - ref) + u.y * exp2_fast(u.x - ref);
+                    t.x = m;
+                }
+                a.part[(int64_t)(n0 + c) * a.nvt + (a.v0 + m0) / C::BM] = t;
+            }
+        }
+        if (!more) return;   // (the barriers of the next tile's product come before red is written again)
     }
 }
 
@@ -304,20 +367,20 @@ __global__ __launch_bounds__(256) void loss_kernel(const float2* part, const flo
     for (int i = lane; i < nvt; i += 64) {
         const float2 u = part[(int64_t)j * nvt + i];
         const float top = fmaxf(m, u.x), ref = top == -INFINITY ? 0.f : top;
-        s = s * exp_exact(m - ref) + u.y * exp_exact(u.x - ref);
+        s = s * exp2_fast(m - ref) + u.y * exp2_fast(u.x - ref);
         m = top;
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
         const float um = __shfl_xor(m, o), us = __shfl_xor(s, o);
         const float top = fmaxf(m, um), ref = top == -INFINITY ? 0.f : top;
-        s = s * exp_exact(m - ref) + us * exp_exact(um - ref);
+        s = s * exp2_fast(m - ref) + us * exp2_fast(um - ref);
         m = top;
     }
     if (lane == 0) {
-        const float ls = logf(s);
-        lse[map[j]] = m + ls;
-        loss[map[j]] = tgt[j] < 0 ? __uint_as_float(0x7fc00000u) : (m - zt[j]) + ls;
+        const float ls = logf(s), low = m * kLn2Low;
+        lse[map[j]] = fmaf(m, kLn2, ls) + low;
+        loss[map[j]] = tgt[j] < 0 ? __uint_as_float(0x7fc00000u) : fmaf(m, kLn2, -zt[j]) + (ls + low);
     }
 }
 
@@ -328,17 +391,34 @@ struct OutArgs {
     int d;                 // output columns (the matrix core's rows)
     int rows;              // output rows, or -1: the gathered tokens
     int k;                 // reduction length, or -1: the gathered tokens
-    int split, k_per;      // slices of the reduction (blockIdx.y) and their length
+    int split, k_per;      // slices of the reduction and their length
     float* acc;            // fp32 [split][acc_rows][d], or null: straight to out
     int64_t acc_rows;
     int add;               // add to acc
     void* out;
     const int* map;        // output row of a gathered token, or null
     int out_bf16, accumulate;
+    // dH in bf16: what the rounding of D left of the target's element, times the target's row of W
+    const float* rest;     // or null
+    const int* tgt;
+    const uint16_t* w;     // bf16 [vocab][d]
 };
 
-__device__ __forceinline__ void store_out(const OutArgs& a, int64_t at, int n, const float (&v)[4]) {
-    // n elements from `at`: four where the row's columns are a multiple of four, fewer at a ragged end
+// n elements of the output from column c of row r of the reduction's result: four where the row's columns are a
+// multiple of four, fewer at a ragged end
+__device__ __forceinline__ void store_out(const OutArgs& a, int64_t r, int c, int n, float (&v)[4]) {
+    if (a.rest && a.tgt[r] >= 0) {
+        const float left = a.rest[r];
+        const uint16_t* w = a.w + (int64_t)a.tgt[r] * a.d + c;
+        if (a.d % 4 == 0) {
+            const u32x2 x = *(const u32x2*)w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(left, up16((x[e / 2] >> (16 * (e % 2))) & 0xffffu), v[e]);
+        } else {
+            for (int e = 0; e < n; ++e) v[e] = fmaf(left, up16(w[e]), v[e]);
+        }
+    }
+    const int64_t at = (a.map ? a.map[r] : r) * (int64_t)a.d + c;
     if (a.d % 4 == 0) {
         float o[4];
         if (a.out_bf16) {
@@ -371,35 +451,49 @@ template <class C>
 __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
     __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
     const int count = a.cnt[0], rows = a.rows < 0 ? count : a.rows, k = a.k < 0 ? (count + 63) / 64 * 64 : a.k;
-    int mt, nt;
-    if (!tile_of((a.d + C::BM - 1) / C::BM, (rows + C::BN - 1) / C::BN, mt, nt)) return;
-    const int m0 = mt * C::BM, n0 = nt * C::BN;
+    Walk walk((a.d + C::BM - 1) / C::BM, (rows + C::BN - 1) / C::BN, a.split);
+    if (walk.done()) return;
     if (a.k < 0) a.a.rows = count;   // dW reduces over the tokens
     a.b.rows = count;
-    const int k0 = (int)blockIdx.y * a.k_per, k1 = k0 + a.k_per < k ? k0 + a.k_per : k;
-    typename C::Acc acc = {};
-    if (k0 < k1) mm::Product<C>::run(a.a, a.b, m0, n0, k0, k1, a.seg, lds, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+    mm::Product<C> mul(lds);
+    int mt, nt, slice;
+    auto start = [&]() {   // false: a slice without any k
+        walk.tile(mt, nt, slice);
+        const int k0 = slice * a.k_per, k1 = k0 + a.k_per < k ? k0 + a.k_per : k;
+        mul.m0 = mt * C::BM;
+        mul.n0 = nt * C::BN;
+        if (k0 < k1) mul.start(a.a, a.b, mul.m0, mul.n0, k0, k1, a.seg);
+        return k0 < k1;
+    };
+    bool any = start();
+    for (;;) {
+        const int m0 = mul.m0, n0 = mul.n0, sl = slice;
+        typename C::Acc acc = {};
+        if (any) mul.finish(a.a, a.b, acc);
+        walk.next();
+        const bool more = !walk.done();
+        if (more) any = start();
 #pragma unroll
-    for (int j = 0; j < C::NI; ++j) {
-        const int n = n0 + wn * (C::BN / C::WN) + 16 * j + lane % 16;
-        if (n >= rows) continue;
-        const int64_t row = a.acc ? blockIdx.y * a.acc_rows + n : a.map ? a.map[n] : n;
+        for (int j = 0; j < C::NI; ++j) {
+            const int n = n0 + mul.xb + 16 * j + mul.lane % 16;
+            if (n >= rows) continue;
 #pragma unroll
-        for (int i = 0; i < C::MI; ++i) {
-            const int m = m0 + wm * (C::BM / C::WM) + 16 * i + 4 * (lane / 16);
-            if (m >= a.d) continue;
-            const int64_t at = row * a.d + m;
-            float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            if (!a.acc) {
-                store_out(a, at, a.d - m < 4 ? a.d - m : 4, v);
-            } else if (a.d % 4 == 0) {
-                f32x4* p = (f32x4*)(a.acc + at);
-                *p = a.add ? *p + acc[i][j] : acc[i][j];
-            } else {
-                for (int e = 0; e < 4 && m + e < a.d; ++e) a.acc[at + e] = (a.add ? a.acc[at + e] : 0.f) + v[e];
+            for (int i = 0; i < C::MI; ++i) {
+                const int m = m0 + mul.xa + 16 * i + 4 * (mul.lane / 16);
+                if (m >= a.d) continue;
+                float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                const int64_t at = (sl * a.acc_rows + n) * a.d + m;
+                if (!a.acc) {
+                    store_out(a, n, m, a.d - m < 4 ? a.d - m : 4, v);
+                } else if (a.d % 4 == 0) {
+                    f32x4* p = (f32x4*)(a.acc + at);
+                    *p = a.add ? *p + acc[i][j] : acc[i][j];
+                } else {
+                    for (int e = 0; e < 4 && m + e < a.d; ++e) a.acc[at + e] = (a.add ? a.acc[at + e] : 0.f) + v[e];
+                }
             }
         }
+        if (!more) return;
     }
 }
 
@@ -408,8 +502,8 @@ __global__ __launch_bounds__(256) void join_kernel(OutArgs a) {
     const int rows = a.rows < 0 ? a.cnt[0] : a.rows, nc = (a.d + 3) / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)rows * nc) return;
-    const int64_t r = i / nc, c = (i - r * nc) * 4;
-    const int n = a.d - (int)c < 4 ? a.d - (int)c : 4;
+    const int64_t r = i / nc;
+    const int c = (int)(i - r * nc) * 4, n = a.d - c < 4 ? a.d - c : 4;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < a.split; ++s) {
         const float* p = a.acc + (s * a.acc_rows + r) * a.d + c;
@@ -421,7 +515,7 @@ __global__ __launch_bounds__(256) void join_kernel(OutArgs a) {
             for (int e = 0; e < n; ++e) v[e] += p[e];
         }
     }
-    store_out(a, (a.map ? a.map[r] : r) * a.d + c, n, v);
+    store_out(a, r, c, n, v);
 }
 
 // plane pairs (A's part, B's part), smallest products first
@@ -446,12 +540,18 @@ using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
 using W256 = mm::Config<256, 256, 2, 4, 2, true, true>;
 using W128 = mm::Config<128, 128, 2, 2, 2, true, true>;
 
+// One workgroup per tile, or as many as the chip holds, which then walk the tiles.
+template <class C>
+dim3 walkers(int64_t tiles) {
+    return dim3((unsigned)(tiles < kCUs * C::kPerCU ? tiles : kCUs * C::kPerCU));
+}
+
 template <int EPI>
 void launch_logits(const LogitArgs& a, int tile, int64_t n, hipStream_t s) {
-    const dim3 grid((unsigned)(ceil_div64(a.w.rows, tile_m(tile)) * ceil_div64(n, tile_n(tile))));
-    if (tile == TILE_256) hipLaunchKernelGGL((logit_kernel<Z256, EPI>), grid, dim3(Z256::THREADS), 0, s, a);
-    else if (tile == TILE_128) hipLaunchKernelGGL((logit_kernel<Z128, EPI>), grid, dim3(Z128::THREADS), 0, s, a);
-    else hipLaunchKernelGGL((logit_kernel<Z32, EPI>), grid, dim3(Z32::THREADS), 0, s, a);
+    const int64_t t = tiles(a.w.rows, n, tile);
+    if (tile == TILE_256) hipLaunchKernelGGL((logit_kernel<Z256, EPI>), walkers<Z256>(t), dim3(Z256::THREADS), 0, s, a);
+    else if (tile == TILE_128) hipLaunchKernelGGL((logit_kernel<Z128, EPI>), walkers<Z128>(t), dim3(Z128::THREADS), 0, s, a);
+    else hipLaunchKernelGGL((logit_kernel<Z32, EPI>), walkers<Z32>(t), dim3(Z32::THREADS), 0, s, a);
 }
 
 template <bool GRAD>
@@ -529,12 +629,13 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
     z.h = mm::Operand{pk.h, p.np * p.kp, p.kp, 0};
     z.seg = segments(p.parts, p.parts);
     z.kp = (int)p.kp; z.cnt = pk.cnt; z.tgt = pk.tgt; z.lg = pk.lg;
-    z.dl = (uint16_t*)(ws + p.dl); z.np = p.np; z.piece = p.piece;
+    z.dl = (uint16_t*)(ws + p.dl); z.rest = (float*)(ws + p.rest); z.np = p.np; z.piece = p.piece;
     const mm::Operand dl{z.dl, p.np * p.piece, p.piece, 0};
     OutArgs h{};
     h.cnt = pk.cnt; h.d = (int)p.d; h.rows = -1; h.split = (int)p.split_h; h.map = pk.map; h.out = x.dH; h.out_bf16 = x.bf16;
     h.acc = p.pieces > 1 || p.split_h > 1 ? (float*)(ws + p.acc_h) : nullptr;
     h.acc_rows = p.np;
+    if (x.bf16) { h.rest = z.rest; h.tgt = pk.tgt; h.w = (const uint16_t*)x.W; }
     OutArgs w{};
     w.cnt = pk.cnt; w.d = (int)p.d; w.k = -1; w.split = (int)p.split_w; w.out_bf16 = x.dw_bf16; w.accumulate = x.accumulate;
     w.acc = p.split_w > 1 ? (float*)(ws + p.acc_w) : nullptr;
@@ -551,10 +652,10 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             h.k = (int)(ceil_div64(rows, 64) * 64);
             h.k_per = (int)(ceil_div64(ceil_div64(h.k, p.split_h), 64) * 64);
             h.add = v0 > 0;
-            const dim3 grid((unsigned)(ceil_div64(p.d, tile_m(p.tile_h)) * ceil_div64(p.n, tile_n(p.tile_h))), (unsigned)p.split_h);
-            if (p.tile_h == TILE_256) hipLaunchKernelGGL((out_kernel<H256>), grid, dim3(H256::THREADS), 0, s, h);
-            else if (p.tile_h == TILE_128) hipLaunchKernelGGL((out_kernel<H128>), grid, dim3(H128::THREADS), 0, s, h);
-            else hipLaunchKernelGGL((out_kernel<H32>), grid, dim3(H32::THREADS), 0, s, h);
+            const int64_t t = tiles(p.d, p.n, p.tile_h) * p.split_h;
+            if (p.tile_h == TILE_256) hipLaunchKernelGGL((out_kernel<H256>), walkers<H256>(t), dim3(H256::THREADS), 0, s, h);
+            else if (p.tile_h == TILE_128) hipLaunchKernelGGL((out_kernel<H128>), walkers<H128>(t), dim3(H128::THREADS), 0, s, h);
+            else hipLaunchKernelGGL((out_kernel<H32>), walkers<H32>(t), dim3(H32::THREADS), 0, s, h);
         }
         if (x.dW) {
             w.a = z.h; w.b = dl;
@@ -562,9 +663,9 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             w.rows = (int)rows;
             w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);
             w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
-            const dim3 grid((unsigned)(ceil_div64(p.d, tile_m(p.tile_w)) * ceil_div64(rows, tile_n(p.tile_w))), (unsigned)p.split_w);
-            if (p.tile_w == TILE_256) hipLaunchKernelGGL((out_kernel<W256>), grid, dim3(W256::THREADS), 0, s, w);
-            else hipLaunchKernelGGL((out_kernel<W128>), grid, dim3(W128::THREADS), 0, s, w);
+            const int64_t t = tiles(p.d, rows, p.tile_w) * p.split_w;
+            if (p.tile_w == TILE_256) hipLaunchKernelGGL((out_kernel<W256>), walkers<W256>(t), dim3(W256::THREADS), 0, s, w);
+            else hipLaunchKernelGGL((out_kernel<W128>), walkers<W128>(t), dim3(W128::THREADS), 0, s, w);
             if (w.acc) launch_join(w, rows, s);
         }
     }

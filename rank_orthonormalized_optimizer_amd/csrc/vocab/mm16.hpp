@@ -132,11 +132,14 @@ struct Config {
     static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;   // 16 x 16 blocks per wave
     static constexpr int kStage = (BM + BN) * kBK;               // elements of one slab's tiles
     static constexpr int kLds = STAGES * kStage;                 // elements
+    static constexpr int kPerCU = 163840 / (kLds * 2 + 4096) < 1 ? 1 : 163840 / (kLds * 2 + 4096);   // workgroups that LDS leaves room for
     typedef f32x4 Acc[MI][NI];
 };
 
-// run: acc += the product over k in [k0, k1) (multiples of 64, k0 < k1) of every segment.  The caller's
-// tile starts at (m0, n0).  Every thread of the workgroup calls it.
+// One tile product: start() sets out on the tile at (m0, n0) over k in [k0, k1) (multiples of 64, k0 < k1) of every
+// segment and starts its first loads, finish() adds the product to acc.  Every thread of the workgroup calls them.
+// Between finish() and the next start() no barrier is needed: the last barrier of finish() comes after the last LDS
+// read that counts, and start() only writes the stages.
 //
 // A slab is two steps of 32 k.  While the matrix cores work on one step, the fragments of the next
 // one are read: a block row's A fragment as soon as that row's products are issued, so that one set
@@ -146,27 +149,37 @@ template <class C>
 struct Product {
     using TileA = Tile<C::BM, C::TA, C::WAVES>;
     using TileB = Tile<C::BN, C::TB, C::WAVES>;
+    static constexpr int kPer = TileA::kLoads + TileB::kLoads;
 
-    static __device__ __forceinline__ void run(const Operand& a, const Operand& b, int m0, int n0, int k0, int k1,
-                                               Segments seg, uint16_t* lds, typename C::Acc& acc) {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int xa = (wave % C::WM) * (C::BM / C::WM), xb = (wave / C::WM) * (C::BN / C::WN);
-        TileA ta;
-        TileB tb;
-        constexpr int kPer = TileA::kLoads + TileB::kLoads;
+    int lane, wave, xa, xb, total, m0, n0;
+    uint16_t* lds;
+
+    __device__ __forceinline__ explicit Product(uint16_t* lds_) : lds(lds_) {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        xa = (wave % C::WM) * (C::BM / C::WM);
+        xb = (wave / C::WM) * (C::BN / C::WN);
+    }
+
+    __device__ __forceinline__ void start(const Operand& a, const Operand& b, int m0_, int n0_, int k0, int k1,
+                                          Segments seg) {
+        m0 = m0_;
+        n0 = n0_;
         ta.init(a, m0, wave, lane);
         tb.init(b, n0, wave, lane);
-        const int nk = (k1 - k0) / kBK, total = nk * (int)seg.n;
-        Loads ld(k0, nk, seg.list);
-        auto load_all = [&]() {
+        const int nk = (k1 - k0) / kBK;
+        total = nk * (int)seg.n;
+        ld = Loads(k0, nk, seg.list);
+        const int ahead = C::STAGES < total ? C::STAGES : total;
+        for (int i = 0; i < ahead; ++i) {
             ld.begin(a, b, m0, n0, lds);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) ld.one(ta, tb, i, wave);
-        };
-        const int ahead = C::STAGES < total ? C::STAGES : total;
-        for (int i = 0; i < ahead; ++i) load_all();
-        if (total >= C::STAGES) wait_slab<(C::STAGES - 1) * kPer>();
-        else wait_slab<0>();
+            for (int q = 0; q < kPer; ++q) ld.one(ta, tb, q, wave);
+        }
+    }
+
+    __device__ __forceinline__ void finish(const Operand& a, const Operand& b, typename C::Acc& acc) {
+        wait_slab<0>();   // whatever the caller stored since start() counts too, so no number tells the slabs apart
         u32x4 fa[C::MI], fb[C::NI];
         uint16_t* la = lds;
 #pragma unroll
@@ -180,28 +193,29 @@ struct Product {
         };
         int it = 0;
         for (; it + C::STAGES < total; ++it) {
-            step<0>(la, 1, xa, xb, lane, fa, fb, acc, [](int) {});
+            step<0>(la, 1, fa, fb, acc, [](int) {});
             ld.begin(a, b, m0, n0, lds);
             next();
             wait_slab<(C::STAGES - 2) * kPer>();
-            step<kPer>(la, 0, xa, xb, lane, fa, fb, acc, [&](int i) { ld.one(ta, tb, i, wave); });
+            step<kPer>(la, 0, fa, fb, acc, [&](int i) { ld.one(ta, tb, i, wave); });
             __builtin_amdgcn_sched_barrier(0);
         }
         for (; it < total; ++it) {   // nothing left to load
-            step<0>(la, 1, xa, xb, lane, fa, fb, acc, [](int) {});
+            step<0>(la, 1, fa, fb, acc, [](int) {});
             wait_slab<0>();
             next();
-            step<0>(la, 0, xa, xb, lane, fa, fb, acc, [](int) {});   // (behind the last slab it reads a stage whose values are not used)
+            step<0>(la, 0, fa, fb, acc, [](int) {});   // (behind the last slab it reads a stage whose values are not used)
         }
     }
 
+private:
     // The loads of one slab, in the order of the segments: which is next, and its descriptors.
     struct Loads {
-        int k0, nk;
-        int k = 0, slot = 0;
-        uint32_t list;
+        int k0 = 0, nk = 0, k = 0, slot = 0;
+        uint32_t list = 0;
         u32x4 ra, rb;
         uint32_t to;
+        Loads() = default;
         __device__ __forceinline__ Loads(int k0_, int nk_, uint32_t list_) : k0(k0_), nk(nk_), list(list_) {}
         __device__ __forceinline__ void begin(const Operand& a, const Operand& b, int m0, int n0, uint16_t* lds) {
             ra = TileA::slab(a, m0, list & 3, k0 + k * kBK);
@@ -216,11 +230,15 @@ struct Product {
         }
     };
 
+    TileA ta;
+    TileB tb;
+    Loads ld;
+
     // The products of the fragments at hand, and the fragments of step ks of the stage la in their place;
     // load(0 .. LOADS - 1) starts the loads that go along.
     template <int LOADS, class F>
-    static __device__ __forceinline__ void step(uint16_t* la, int ks, int xa, int xb, int lane, u32x4 (&fa)[C::MI],
-                                                u32x4 (&fb)[C::NI], typename C::Acc& acc, F load) {
+    __device__ __forceinline__ void step(uint16_t* la, int ks, u32x4 (&fa)[C::MI], u32x4 (&fb)[C::NI],
+                                         typename C::Acc& acc, F load) const {
         constexpr int per_row = (LOADS + C::MI - 1) / C::MI;
         constexpr int da = C::TA ? 2 : 1, db = C::TB ? 2 : 1;   // LDS reads per fragment
         constexpr int gap = C::MI * C::NI * 3 / 4 / (C::MI * da + C::NI * db) > 1

@@ -70,7 +70,7 @@ struct XentPlan {
     int64_t nvt;              // softmax partials per token (forward)
     int tile_z, tile_h, tile_w;   // tile shapes of the logits, dH and dW (TILE_*)
     int64_t split_h, split_w; // slices of the reductions of dH (over the piece) and dW (over the tokens)
-    size_t h, map, tgt, lg, cnt, part, zt, w, dl, acc_h, acc_w, total;
+    size_t h, map, tgt, lg, cnt, part, zt, w, dl, rest, acc_h, acc_w, total;
 };
 
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens)
@@ -130,6 +130,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.split_h = pick_split(width, tokens < 1 ? 1 : tokens, q.piece, q.tile_h);
         q.split_w = pick_split(width, q.piece, tokens, q.tile_w);
         q.lg = take(q.np * 8);
+        q.rest = take(q.np * 4);
         q.dl = take(q.dparts * q.np * q.piece * 2);
         if (q.pieces > 1 || q.split_h > 1) q.acc_h = take(q.split_h * q.np * width * 4);
         if (q.split_w > 1) q.acc_w = take(q.split_w * q.piece * width * 4);
