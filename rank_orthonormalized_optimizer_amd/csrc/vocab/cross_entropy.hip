@@ -326,16 +326,31 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
                             }
                     if (mine) a.rest[n] = d - up16(down16(d));
                 }
-                if (n < count) {
+                // Two blocks of 16 rows at a time: the lane quarters trade their four rows of one against the other's
+                // (v_permlane32_swap, v_permlane16_swap), so that a lane stores eight consecutive rows and four lanes 64 bytes.
+                const int quarter = mul.lane / 16;
+                uint16_t* to = a.dl + n * a.piece + m0 + mul.xa + 16 * (quarter / 2) + 8 * (quarter % 2);
 #pragma unroll
-                    for (int i = 0; i < C::MI; ++i) {
-                        uint16_t* to = a.dl + n * a.piece + m0 + rl + 16 * i;
-                        uint32_t part[4][3];
+                for (int i = 0; i < C::MI; i += 2) {
+                    uint32_t part[2][4][3];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) split3(acc[i][j][v] * lg[j].y, part[v]);
+                    for (int v = 0; v < 4; ++v) {
+                        split3(acc[i][j][v] * lg[j].y, part[0][v]);
+                        split3(acc[i + 1][j][v] * lg[j].y, part[1][v]);
+                    }
 #pragma unroll
-                        for (int q = 0; q < PD; ++q)
-                            *(u32x2*)(to + q * a.np * a.piece) = u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
+                    for (int q = 0; q < PD; ++q) {
+                        u32x4 w;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const auto x = __builtin_amdgcn_permlane32_swap(part[0][2 * h][q] | (part[0][2 * h + 1][q] << 16),
+                                                                            part[1][2 * h][q] | (part[1][2 * h + 1][q] << 16),
+                                                                            false, false);
+                            const auto z = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+                            w[h] = z[0];
+                            w[2 + h] = z[1];
+                        }
+                        if (n < count) *(u32x4*)(to + q * a.np * a.piece + 16 * i) = w;
                     }
                 }
             }
