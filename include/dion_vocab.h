@@ -21,7 +21,7 @@
  * one stream.  Sums, softmax statistics and products accumulate in fp32; each output is rounded
  * once to its type.
  *
- * Limits: tokens <= DION_VOCAB_MAX_TOKENS, 1 <= vocab <= 2^24, 1 <= width <= 2^16; beyond them DION_ERR_SHAPE.
+ * Limits: tokens <= DION_VOCAB_MAX_TOKENS, 1 <= vocab < 2^24, 1 <= width <= 2^16; beyond them DION_ERR_SHAPE.
  */
 #ifndef DION_VOCAB_MI355X_H
 #define DION_VOCAB_MI355X_H

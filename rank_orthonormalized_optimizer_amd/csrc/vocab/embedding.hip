@@ -3,8 +3,7 @@
 //   Y[t] = scale * W[ids[t]]                        one gather, bound by HBM (read and write d elements per token)
 //   dW[v] (+)= scale * sum over ids[t] = v of dY[t]
 //
-// The gradient sorts the tokens by id (stable radix sort of (id, token) pairs, eight bits a pass)
-// and cuts the sorted list into chunks of equal length, so that frequent ids load no workgroup
+// The gradient sorts the tokens by id, in their order where ids are equal, and cuts the sorted list into chunks of equal length, so that frequent ids load no workgroup
 // more than others.  A team of threads walks one chunk, adding rows of dY in fp32 registers; a run
 // of one id that lies inside the chunk is written to its row, the part of a run that crosses a
 // border goes to a partial row, and a second pass adds the partial rows of a run in chunk order.
@@ -124,12 +123,12 @@ __device__ __forceinline__ uint32_t token_key(const EmbedArgs& a, int64_t i) {
 }
 
 // Position of this lane's key among the keys of equal digit met so far by its wave, which are
-// counted in cnt[256]: all lanes of a digit read its count, then the first of them raises it.
+// counted in cnt[]: all lanes of a digit read its count, then the first of them raises it.
 // The wave's LDS accesses stay in order (volatile).
 __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, volatile uint32_t* cnt) {
     uint64_t same = ~0ull;
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < kDigitBits; ++b) {
         const bool bit = (digit >> b) & 1;
         const uint64_t bal = __ballot(bit);
         same &= bit ? bal : ~bal;
@@ -140,23 +139,6 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, volatile uint32_t*
     return seen + rank;
 }
 
-// Exclusive prefix over 256 values, one per thread of the first four waves; every thread of the
-// workgroup calls it.  tmp: four words of LDS.
-__device__ __forceinline__ uint32_t scan256(uint32_t v, uint32_t* tmp) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    uint32_t s = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t u = __shfl_up(s, o);
-        if (lane >= o) s += u;
-    }
-    if (w < 4 && lane == 63) tmp[w] = s;
-    __syncthreads();
-    uint32_t base = 0;
-    for (int i = 0; i < 4; ++i) base += i < w ? tmp[i] : 0;
-    return base + s - v;
-}
-
 // Zeros over the table by workgroups first..gridDim.x - 1 (base 16-byte aligned).
 __device__ void zero_fill(void* p, int64_t bytes, int first) {
     const int64_t n16 = bytes / 16, stride = (int64_t)(gridDim.x - first) * blockDim.x;
@@ -165,150 +147,166 @@ __device__ void zero_fill(void* p, int64_t bytes, int first) {
     for (int64_t i = 16 * n16 / 2 + i0; i < bytes / 2; i += stride) ((uint16_t*)p)[i] = 0;   // elements are 2 or 4 bytes
 }
 
-// Workgroup 0 sorts all tokens (at most 1024 * ITEMS), the others clear the table meanwhile.
-// Wave w ranks the positions [64 ITEMS w, 64 ITEMS (w + 1)) in order, which keeps the sort stable.
-template <int ITEMS>
-__global__ __launch_bounds__(1024) void sort1_kernel(EmbedArgs a, int digits, uint32_t* keys, uint32_t* idx,
-                                                     int64_t zero_bytes) {
-    if (blockIdx.x > 0) {
-        zero_fill(a.out, zero_bytes, 1);
+// Few tokens: a token's place is the number of tokens that sort before it, counted by comparing it with all of them.
+// Each workgroup places 64 tokens, its sixteen waves each going through a sixteenth of a piece of the keys in LDS; the
+// workgroups from `sorters` on clear the table meanwhile.  Keys are whole numbers below 2^24 and go as floats: a comparison
+// is a subtraction clamped to [0, 1] and an addition, exact, and nothing waits for a carry bit.
+__global__ __launch_bounds__(1024) void rank_kernel(EmbedArgs a, uint32_t* keys, uint32_t* idx, int sorters,
+                                                    int64_t zero_bytes) {
+    if ((int)blockIdx.x >= sorters) {
+        zero_fill(a.out, zero_bytes, sorters);
         return;
     }
-    __shared__ uint32_t sk[1024 * ITEMS], si[1024 * ITEMS], cnt[16 * 256], base[256], tmp[4];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = (int)a.tokens;
-    uint32_t key[ITEMS], tok[ITEMS], rk[ITEMS];
+    constexpr int PIECE = 8192;
+    __shared__ __attribute__((aligned(16))) float sk[PIECE];
+    __shared__ float sum[16][64];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n = (int)a.tokens;
+    const int t0 = blockIdx.x * 64, t = t0 + lane;
+    const uint32_t key = t < n ? token_key(a, t) : 0;
+    float before = 0.f;
+    const float below = (float)key, upto = below + 1.f;   // key < below, key < upto
+    float ahead[PIECE / 1024];   // the next piece's keys, fetched while this one is gone through
+    auto fetch = [&](int p0) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int pos = (w * ITEMS + i) * 64 + lane;
-        key[i] = pos < n ? token_key(a, pos) : 0xffffffffu;   // positions past the end stay last
-        tok[i] = (uint32_t)pos;
-    }
-    for (int d = 0; d < digits; ++d) {
-        for (int i = tid; i < 16 * 256; i += 1024) cnt[i] = 0;
+        for (int i = 0; i < PIECE / 1024; ++i) {
+            const int p = p0 + i * 1024 + tid;
+            ahead[i] = p < n ? (float)token_key(a, p) : 3e7f;   // behind every key
+        }
+    };
+    fetch(0);
+    for (int p0 = 0; p0 < n; p0 += PIECE) {
+        const int part = ((n - p0 < PIECE ? n - p0 : PIECE) + 63) / 64 * 4;   // keys per wave, a multiple of four
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) rk[i] = wave_rank((key[i] >> (8 * d)) & 255u, cnt + 256 * w);
+        for (int i = 0; i < PIECE / 1024; ++i) sk[i * 1024 + tid] = ahead[i];
         __syncthreads();
-        uint32_t run = 0;
-        if (tid < 256)
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t c = cnt[256 * i + tid];
-                cnt[256 * i + tid] = run;
-                run += c;
+        if (p0 + PIECE < n) fetch(p0 + PIECE);
+        const float* mine = sk + w * part;   // keys of the tokens q0 .. q0 + part - 1
+        const int q0 = p0 + w * part;
+        if (q0 + part <= t0) {              // all before this workgroup's tokens: equal ids come first
+#pragma unroll 4
+            for (int i = 0; i < part; i += 4) {
+                const f32x4_t k = *(const f32x4_t*)&mine[i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) before += __builtin_amdgcn_fmed3f(upto - k[e], 0.f, 1.f);
             }
-        const uint32_t b = scan256(run, tmp);
-        if (tid < 256) base[tid] = b;
-        __syncthreads();
+        } else if (q0 >= t0 + 64) {         // all behind them
+#pragma unroll 4
+            for (int i = 0; i < part; i += 4) {
+                const f32x4_t k = *(const f32x4_t*)&mine[i];
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const uint32_t g = (key[i] >> (8 * d)) & 255u, to = base[g] + cnt[256 * w + g] + rk[i];
-            sk[to] = key[i];
-            si[to] = tok[i];
-        }
-        __syncthreads();
+                for (int e = 0; e < 4; ++e) before += __builtin_amdgcn_fmed3f(below - k[e], 0.f, 1.f);
+            }
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < part; i += 4) {
+                const f32x4_t k = *(const f32x4_t*)&mine[i];
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int pos = (w * ITEMS + i) * 64 + lane;
-            key[i] = sk[pos];
-            tok[i] = si[pos];
+                for (int e = 0; e < 4; ++e) before += __builtin_amdgcn_fmed3f((q0 + i + e < t ? upto : below) - k[e], 0.f, 1.f);
+            }
         }
     }
+    sum[w][lane] = before;
+    __syncthreads();
+    if (w == 0 && t < n) {
+        float place = 0.f;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int pos = (w * ITEMS + i) * 64 + lane;
-        if (pos < n) {
-            keys[pos] = key[i];
-            idx[pos] = tok[i];
-        }
+        for (int i = 0; i < 16; ++i) place += sum[i][lane];
+        keys[(int)place] = key;
+        idx[(int)place] = (uint32_t)t;
     }
 }
 
-// One radix pass over many workgroups of kSortBlock tokens: digit counts per workgroup, their
-// prefix (digit-major), and the stable scatter.  The first pass reads the ids.
+// Many tokens: a stable radix sort, kDigitBits a pass, by workgroups of 256 ITEMS tokens: digit counts per
+// workgroup ([digit][workgroup]), then the scatter, which adds up the counts before its own by itself (reading all of
+// them from L2 took 3 us where a prefix kernel between the two took 21).  The first pass reads the ids.
+template <int ITEMS>
 __global__ __launch_bounds__(256) void radix_count_kernel(EmbedArgs a, int shift, const uint32_t* keys, uint32_t* counts,
                                                           int nblk, int64_t zero_bytes) {
     if ((int)blockIdx.x >= nblk) {
         zero_fill(a.out, zero_bytes, nblk);
         return;
     }
-    __shared__ uint32_t h[256];
-    h[threadIdx.x] = 0;
+    __shared__ uint32_t h[kDigits];
+    for (int i = threadIdx.x; i < kDigits; i += 256) h[i] = 0;
     __syncthreads();
-    for (int i = 0; i < kSortBlock / 256; ++i) {
-        const int64_t pos = (int64_t)blockIdx.x * kSortBlock + i * 256 + threadIdx.x;
-        if (pos < a.tokens) atomicAdd(&h[((keys ? keys[pos] : token_key(a, pos)) >> shift) & 255u], 1u);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int64_t pos = ((int64_t)blockIdx.x * ITEMS + i) * 256 + threadIdx.x;
+        if (pos < a.tokens) atomicAdd(&h[((keys ? keys[pos] : token_key(a, pos)) >> shift) & (kDigits - 1)], 1u);
     }
     __syncthreads();
-    counts[(int64_t)threadIdx.x * nblk + blockIdx.x] = h[threadIdx.x];
+    for (int i = threadIdx.x; i < kDigits; i += 256) counts[(int64_t)i * nblk + blockIdx.x] = h[i];
 }
 
-__global__ __launch_bounds__(1024) void radix_scan_kernel(uint32_t* counts, int64_t n) {
-    __shared__ uint32_t tmp[16], carry_s;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    uint32_t carry = 0;
-    for (int64_t i0 = 0; i0 < n; i0 += 4096) {
-        uint32_t v[4], sum = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t i = i0 + 4 * tid + e;
-            v[e] = i < n ? counts[i] : 0;
-            sum += v[e];
-        }
-        uint32_t s = sum;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t u = __shfl_up(s, o);
-            if (lane >= o) s += u;
-        }
-        if (lane == 63) tmp[w] = s;
-        __syncthreads();
-        uint32_t at = carry + s - sum;
-        for (int i = 0; i < w; ++i) at += tmp[i];
-        if (tid == 1023) carry_s = at + sum;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t i = i0 + 4 * tid + e;
-            if (i < n) counts[i] = at;
-            at += v[e];
-        }
-        __syncthreads();
-        carry = carry_s;
-    }
-}
-
+template <int ITEMS>
 __global__ __launch_bounds__(256) void radix_scatter_kernel(EmbedArgs a, int shift, const uint32_t* keys,
                                                             const uint32_t* idx, const uint32_t* counts, int nblk,
                                                             uint32_t* keys_out, uint32_t* idx_out) {
-    constexpr int ITEMS = kSortBlock / 256;
-    __shared__ uint32_t cnt[4 * 256];
+    static_assert(kDigits == 512, "two digits per thread");
+    __shared__ uint32_t cnt[4 * kDigits], tmp[4];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    for (int i = tid; i < 4 * 256; i += 256) cnt[i] = 0;
-    uint32_t key[ITEMS], rk[ITEMS];
-    const int64_t p0 = (int64_t)blockIdx.x * kSortBlock + w * 64 * ITEMS + lane;
+    for (int i = tid; i < 4 * kDigits; i += 256) cnt[i] = 0;
+    uint32_t key[ITEMS], rk[ITEMS], tok[ITEMS];
+    const int64_t p0 = (int64_t)blockIdx.x * 256 * ITEMS + w * 64 * ITEMS + lane;   // a wave's tokens in order: stable
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const int64_t pos = p0 + 64 * i;
         key[i] = pos < a.tokens ? (keys ? keys[pos] : token_key(a, pos)) : 0xffffffffu;
+        tok[i] = pos < a.tokens && keys ? idx[pos] : (uint32_t)pos;
     }
+    // this thread's digits 2 tid and 2 tid + 1: tokens of lower workgroups, and of all
+    uint32_t low[2] = {0, 0}, all[2] = {0, 0};
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        const uint32_t* c = counts + (int64_t)(2 * tid + d) * nblk;
+#pragma unroll 16
+        for (int b = 0; b < nblk; ++b) {
+            const uint32_t v = c[b];
+            all[d] += v;
+            low[d] += b < (int)blockIdx.x ? v : 0;
+        }
+    }
+    const uint32_t sum = all[0] + all[1];   // exclusive prefix over the digits
+    uint32_t s = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t u = __shfl_up(s, o);
+        if (lane >= o) s += u;
+    }
+    if (lane == 63) tmp[w] = s;
+    __syncthreads();
+    uint32_t first = s - sum;
+    for (int i = 0; i < w; ++i) first += tmp[i];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) rk[i] = wave_rank((key[i] >> shift) & (kDigits - 1), cnt + kDigits * w);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) rk[i] = wave_rank((key[i] >> shift) & 255u, cnt + 256 * w);
-    __syncthreads();
-    uint32_t run = counts[(int64_t)tid * nblk + blockIdx.x];
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t c = cnt[256 * i + tid];
-        cnt[256 * i + tid] = run;
-        run += c;
+    for (int d = 0; d < 2; ++d) {
+        uint32_t run = first + (d ? all[0] : 0) + low[d];
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = cnt[kDigits * i + 2 * tid + d];
+            cnt[kDigits * i + 2 * tid + d] = run;
+            run += c;
+        }
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const int64_t pos = p0 + 64 * i;
         if (pos >= a.tokens) continue;   // (past the end: the last positions of the last workgroup)
-        const uint32_t to = cnt[256 * w + ((key[i] >> shift) & 255u)] + rk[i];
+        const uint32_t to = cnt[kDigits * w + ((key[i] >> shift) & (kDigits - 1))] + rk[i];
         keys_out[to] = key[i];
-        idx_out[to] = keys ? idx[pos] : (uint32_t)pos;
+        idx_out[to] = tok[i];
     }
+}
+
+template <int ITEMS>
+void launch_radix(const EmbedArgs& a, int d, const uint32_t* kin, const uint32_t* iin, uint32_t* counts, int nblk,
+                  uint32_t* kout, uint32_t* iout, int64_t zero, unsigned fill, hipStream_t s) {
+    hipLaunchKernelGGL((radix_count_kernel<ITEMS>), dim3(nblk + fill), dim3(256), 0, s, a, kDigitBits * d, kin, counts, nblk, zero);
+    hipLaunchKernelGGL((radix_scatter_kernel<ITEMS>), dim3(nblk), dim3(256), 0, s, a, kDigitBits * d, kin, iin, counts, nblk,
+                       kout, iout);
 }
 
 // ---------------------------------------------------------------------------
@@ -366,25 +364,20 @@ struct Cols {
     }
 };
 
-template <bool O16, int VEC>
-__device__ __forceinline__ void write_row(const RunArgs& a, const Cols<VEC>& cols, uint32_t key, const float* acc) {
+template <bool O16, bool ADD, int VEC>
+__device__ __forceinline__ void write_row(const RunArgs& a, const Cols<VEC>& cols, uint32_t key, const float* acc, const float* old) {
     constexpr int W = Cols<VEC>::W;
     float v[W];
-    const int64_t row = (int64_t)key * a.e.width;
-    if (a.e.accumulate) {
-        cols.template load<O16>(a.e.out, row, v);
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] += a.e.scale * acc[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = a.e.scale * acc[e];
-    }
-    cols.template store<O16>(a.e.out, row, v);
+    for (int e = 0; e < W; ++e) v[e] = ADD ? old[e] + a.e.scale * acc[e] : a.e.scale * acc[e];
+    cols.template store<O16>(a.e.out, (int64_t)key * a.e.width, v);
 }
 
-template <bool Y16, bool O16, int VEC>
+// ADD: the rows to add to are fetched with the tokens' rows whose runs end there, not when they are written: most runs
+// are of one token, and each would wait for its own row.
+template <bool Y16, bool O16, bool ADD, int VEC>
 __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
-    constexpr int W = Cols<VEC>::W, U = 8;
+    constexpr int W = Cols<VEC>::W, U = ADD ? 4 : 8;
     const int tx = threadIdx.x & ((1 << a.tx_log2) - 1), ty = threadIdx.x >> a.tx_log2;
     const int64_t ch = (int64_t)blockIdx.x * (256 >> a.tx_log2) + ty;
     const Cols<VEC> cols(tx, a.tx_log2, blockIdx.y, a.e.width);
@@ -398,7 +391,7 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
     for (int e = 0; e < W; ++e) acc[e] = 0.f;
     for (int64_t p = p0; p < p1 && key != none; p += U) {
         uint32_t next[U], tok[U];
-        float v[U][W];
+        float v[U][W], old[ADD ? U : 1][W];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t q = p + u < p1 ? p + u : p1 - 1;
@@ -406,7 +399,13 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
             next[u] = q + 1 < n ? a.keys[q + 1] : none;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) cols.template load<Y16>(a.e.in, (int64_t)tok[u] * a.e.width, v[u]);
+        for (int u = 0; u < U; ++u) {
+            cols.template load<Y16>(a.e.in, (int64_t)tok[u] * a.e.width, v[u]);
+            if (ADD) {
+                const uint32_t here = u ? next[u - 1] : key;
+                if (here != none && next[u] != here) cols.template load<O16>(a.e.out, (int64_t)here * a.e.width, old[u]);
+            }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (p + u >= p1 || key == none) break;
@@ -414,7 +413,7 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
             for (int e = 0; e < W; ++e) acc[e] += v[u][e];
             if (next[u] != key) {
                 if (open) cols.template store<false>(a.part, ch * 2 * a.pitch, acc);
-                else write_row<O16, VEC>(a, cols, key, acc);
+                else write_row<O16, ADD, VEC>(a, cols, key, acc, old[ADD ? u : 0]);
                 open = false;
 #pragma unroll
                 for (int e = 0; e < W; ++e) acc[e] = 0.f;
@@ -427,37 +426,52 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
 }
 
 // Adds up the runs that begin in a chunk and go on behind it: its tail partial row, then the head
-// partial rows of the chunks that the run reaches.
-template <bool O16, int VEC>
+// partial rows of the chunks that the run reaches.  Eight teams of 32 threads share 32 accesses of the row's columns,
+// each adding every eighth chunk; their sums are added in order.
+template <bool O16, bool ADD, int VEC>
 __global__ __launch_bounds__(256) void run_join_kernel(RunArgs a) {
-    constexpr int W = Cols<VEC>::W, U = 8;
-    const int tx = threadIdx.x & ((1 << a.tx_log2) - 1), ty = threadIdx.x >> a.tx_log2;
-    const int64_t ch = (int64_t)blockIdx.x * (256 >> a.tx_log2) + ty;
-    const Cols<VEC> cols(tx, a.tx_log2, blockIdx.y, a.e.width);
-    if (ch + 1 >= a.nchunk || cols.n == 0) return;
-    const int64_t p0 = ch * a.chunk, p1 = p0 + a.chunk;
+    constexpr int W = Cols<VEC>::W, U = 4;
+    const int tx = threadIdx.x & 31, team = threadIdx.x >> 5;
+    const int64_t ch = blockIdx.x, p0 = ch * a.chunk, p1 = p0 + a.chunk;
     const uint32_t key = a.keys[p1];
     if (key == (uint32_t)a.e.vocab || a.keys[p1 - 1] != key || (p0 > 0 && a.keys[p0 - 1] == key)) return;
-    int64_t lo = ch + 1, hi = a.nchunk;   // the last chunk that starts with this id
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.keys[mid * a.chunk] == key) lo = mid;
-        else hi = mid;
-    }
-    float acc[W];
-    cols.template load<false>(a.part, (ch * 2 + 1) * a.pitch, acc);
-    for (int64_t c = ch + 1; c <= lo; c += U) {
-        float v[U][W];
+    const Cols<VEC> cols(tx, 5, blockIdx.y, a.e.width);
+    __shared__ float sums[8][32][W + 1];
+    float acc[W], old[W];
 #pragma unroll
-        for (int u = 0; u < U; ++u) cols.template load<false>(a.part, (c + u <= lo ? c + u : lo) * 2 * a.pitch, v[u]);
+    for (int e = 0; e < W; ++e) acc[e] = 0.f;
+    if (cols.n > 0) {
+        if (team == 0) {
+            cols.template load<false>(a.part, (ch * 2 + 1) * a.pitch, acc);
+            if (ADD) cols.template load<O16>(a.e.out, (int64_t)key * a.e.width, old);
+        }
+        for (int64_t c = ch + 1 + team;; c += 8 * U) {   // this team's chunks that start with the id
+            float v[U][W];
+            bool goes[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c + u <= lo) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) acc[e] += v[u][e];
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = c + 8 * u < a.nchunk ? c + 8 * u : a.nchunk - 1;
+                goes[u] = c + 8 * u < a.nchunk && a.keys[at * a.chunk] == key;
+                if (goes[u]) cols.template load<false>(a.part, at * 2 * a.pitch, v[u]);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (goes[u]) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) acc[e] += v[u][e];
+                }
+            if (!goes[U - 1]) break;
+        }
     }
-    write_row<O16, VEC>(a, cols, key, acc);
+#pragma unroll
+    for (int e = 0; e < W; ++e) sums[team][tx][e] = acc[e];
+    __syncthreads();
+    if (team > 0 || cols.n == 0) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < W; ++e) acc[e] += sums[i][tx][e];
+    write_row<O16, ADD, VEC>(a, cols, key, acc, old);
 }
 
 // Elements per access: eight where rows start at 16 bytes for bf16 and 32 for fp32, four, or single ones.
@@ -482,23 +496,31 @@ void launch_lookup(const EmbedArgs& a, hipStream_t s) {
     else hipLaunchKernelGGL((lookup_kernel<W16, O16, 1>), grid, dim3(256), 0, s, a, l);
 }
 
-template <bool Y16, bool O16, int VEC>
+template <bool Y16, bool O16, bool ADD, int VEC>
 void launch_runs(RunArgs r, hipStream_t s) {
     const int64_t chunks = ceil_div64(r.e.width, Cols<VEC>::W);
     r.tx_log2 = team_log2(chunks);
     const dim3 grid((unsigned)ceil_div64(r.nchunk, 256 >> r.tx_log2),
                     (unsigned)ceil_div64(chunks, (int64_t)1 << r.tx_log2));
-    hipLaunchKernelGGL((run_sum_kernel<Y16, O16, VEC>), grid, dim3(256), 0, s, r);
-    if (r.nchunk > 1) hipLaunchKernelGGL((run_join_kernel<O16, VEC>), grid, dim3(256), 0, s, r);
+    hipLaunchKernelGGL((run_sum_kernel<Y16, O16, ADD, VEC>), grid, dim3(256), 0, s, r);
+    if (r.nchunk > 1)
+        hipLaunchKernelGGL((run_join_kernel<O16, ADD, VEC>), dim3((unsigned)(r.nchunk - 1), (unsigned)ceil_div64(chunks, 32)),
+                           dim3(256), 0, s, r);
+}
+
+template <bool Y16, bool O16, bool ADD>
+void launch_runs(const RunArgs& r, hipStream_t s) {
+    switch (row_vec(r.e.width)) {
+        case 8: launch_runs<Y16, O16, ADD, 8>(r, s); break;
+        case 4: launch_runs<Y16, O16, ADD, 4>(r, s); break;
+        default: launch_runs<Y16, O16, ADD, 1>(r, s); break;
+    }
 }
 
 template <bool Y16, bool O16>
 void launch_runs(const RunArgs& r, hipStream_t s) {
-    switch (row_vec(r.e.width)) {
-        case 8: launch_runs<Y16, O16, 8>(r, s); break;
-        case 4: launch_runs<Y16, O16, 4>(r, s); break;
-        default: launch_runs<Y16, O16, 1>(r, s); break;
-    }
+    if (r.e.accumulate) launch_runs<Y16, O16, true>(r, s);
+    else launch_runs<Y16, O16, false>(r, s);
 }
 
 }  // namespace
@@ -519,10 +541,9 @@ int run_embedding_grad(const EmbedArgs& a, const EmbedGradPlan& p, char* ws, voi
     uint32_t* idx[2] = {(uint32_t*)(ws + p.idx[0]), (uint32_t*)(ws + p.idx[1])};
     int at = 0;
     if (p.sort_blocks == 0) {
-        const dim3 grid(1 + fill), block(1024);
-        if (a.tokens <= 1024) hipLaunchKernelGGL((sort1_kernel<1>), grid, block, 0, s, a, p.digits, keys[0], idx[0], zero);
-        else if (a.tokens <= 4096) hipLaunchKernelGGL((sort1_kernel<4>), grid, block, 0, s, a, p.digits, keys[0], idx[0], zero);
-        else hipLaunchKernelGGL((sort1_kernel<kSort1Items>), grid, block, 0, s, a, p.digits, keys[0], idx[0], zero);
+        const unsigned sorters = (unsigned)ceil_div64(a.tokens, 64);
+        if (sorters + fill > 0)
+            hipLaunchKernelGGL(rank_kernel, dim3(sorters + fill), dim3(1024), 0, s, a, keys[0], idx[0], (int)sorters, zero);
     } else {
         const int nblk = (int)p.sort_blocks;
         uint32_t* counts = (uint32_t*)(ws + p.counts);
@@ -530,11 +551,8 @@ int run_embedding_grad(const EmbedArgs& a, const EmbedGradPlan& p, char* ws, voi
             const uint32_t* kin = d ? keys[(d - 1) & 1] : nullptr;
             const uint32_t* iin = d ? idx[(d - 1) & 1] : nullptr;
             at = d & 1;
-            hipLaunchKernelGGL(radix_count_kernel, dim3(nblk + (d ? 0 : 4 * fill)), dim3(256), 0, s, a, 8 * d, kin, counts,
-                               nblk, d ? 0 : zero);
-            hipLaunchKernelGGL(radix_scan_kernel, dim3(1), dim3(1024), 0, s, counts, (int64_t)256 * nblk);
-            hipLaunchKernelGGL(radix_scatter_kernel, dim3(nblk), dim3(256), 0, s, a, 8 * d, kin, iin, counts, nblk,
-                               keys[at], idx[at]);
+            if (p.sort_items == 4) launch_radix<4>(a, d, kin, iin, counts, nblk, keys[at], idx[at], d ? 0 : zero, d ? 0 : 4 * fill, s);
+            else launch_radix<16>(a, d, kin, iin, counts, nblk, keys[at], idx[at], d ? 0 : zero, d ? 0 : 4 * fill, s);
         }
     }
     if (a.tokens > 0) {

@@ -6,7 +6,7 @@
 
 namespace dion {
 
-constexpr int64_t kVocabMax = (int64_t)1 << 24, kWidthMax = (int64_t)1 << 16;
+constexpr int64_t kVocabMax = ((int64_t)1 << 24) - 1, kWidthMax = (int64_t)1 << 16;
 
 inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
@@ -27,13 +27,14 @@ int run_embedding(const EmbedArgs& a, void* stream);
 struct EmbedGradPlan {
     int64_t chunk;            // sorted tokens per chunk
     int64_t nchunk;
-    int64_t sort_blocks;      // 0: the tokens are sorted by one workgroup
-    int digits;               // radix passes of eight bits
+    int64_t sort_blocks;      // 0: the tokens are sorted by counting
+    int sort_items;           // radix sort: tokens per thread (256 threads a workgroup)
+    int digits;               // radix passes
     size_t keys[2], idx[2], counts, part, total;
 };
 
-constexpr int kSort1Items = 16, kSort1Max = 1024 * kSort1Items;   // one workgroup sorts up to 16384 tokens
-constexpr int kSortBlock = 4096;                                   // tokens per workgroup otherwise
+constexpr int kRankMax = 16384;    // tokens sorted by counting, see rank_kernel
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;   // two passes up to a vocabulary of 2^18 - 1
 
 inline bool make_embed_grad_plan(int64_t tokens, int64_t vocab, int64_t width, EmbedGradPlan* p) {
     EmbedGradPlan q{};
@@ -42,16 +43,17 @@ inline bool make_embed_grad_plan(int64_t tokens, int64_t vocab, int64_t width, E
     q.chunk = 16;
     while (q.chunk * 512 < tokens) q.chunk *= 2;
     q.nchunk = ceil_div64(tokens, q.chunk);
-    q.sort_blocks = tokens <= kSort1Max ? 0 : ceil_div64(tokens, kSortBlock);
+    q.sort_items = tokens <= 1 << 17 ? 4 : 16;   // at most 256 workgroups, whose counts every one of them reads
+    q.sort_blocks = tokens <= kRankMax ? 0 : ceil_div64(tokens, 256 * q.sort_items);
     q.digits = 1;
-    while (q.digits < 4 && (vocab >> (8 * q.digits)) != 0) ++q.digits;   // keys 0..vocab
+    while (q.digits < 4 && (vocab >> (kDigitBits * q.digits)) != 0) ++q.digits;   // keys 0..vocab
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t at = off; off += align256(bytes); return at; };
     for (int i = 0; i < 2; ++i) {
         q.keys[i] = take((size_t)tokens * 4);
         q.idx[i] = take((size_t)tokens * 4);
     }
-    q.counts = take((size_t)q.sort_blocks * 256 * 4);
+    q.counts = take((size_t)q.sort_blocks * kDigits * 4);
     q.part = take((size_t)q.nchunk * 2 * (size_t)((width + 7) / 8 * 8) * 4);
     q.total = off;
     *p = q;
