@@ -128,6 +128,7 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int64_t t0 = (int64_t)blockIdx.x * kPackRows;
     int c = 0;
+#pragma unroll 8
     for (int64_t i = tid; i < t0; i += 256) c += load_target(a.x, i) != a.x.ignore;
 #pragma unroll
     for (int o = 32; o; o >>= 1) c += __shfl_xor(c, o);
@@ -547,13 +548,13 @@ mm::Segments segments(int pa, int pb) {
 }
 
 using Z256 = mm::Config<256, 256, 2, 4, 2, false, false>;
-using Z128 = mm::Config<128, 128, 2, 2, 2, false, false>;
+using Z128 = mm::Config<128, 128, 2, 2, 4, false, false>;
 using Z32 = mm::Config<128, 32, 4, 1, 4, false, false>;
 using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
-using H128 = mm::Config<128, 128, 2, 2, 2, true, false>;
+using H128 = mm::Config<128, 128, 2, 2, 4, true, false>;
 using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
 using W256 = mm::Config<256, 256, 2, 4, 2, true, true>;
-using W128 = mm::Config<128, 128, 2, 2, 2, true, true>;
+using W128 = mm::Config<128, 128, 2, 2, 4, true, true>;
 
 // One workgroup per tile, or as many as the chip holds, which then walk the tiles.
 template <class C>

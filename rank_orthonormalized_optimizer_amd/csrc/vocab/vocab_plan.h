@@ -82,17 +82,20 @@ constexpr int kCUs = 256;
 inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : 128; }
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : 32; }
 inline int64_t tiles(int64_t m, int64_t n, int t) { return ceil_div64(m, tile_m(t)) * ceil_div64(n, tile_n(t)); }
-// Slices of a reduction of length k so that an output of m x n fills the chip, each at least 512 long.
-inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int tile) {
+// Slices of a reduction of length k (`terms` part products of it) so that an output of m x n fills the chip, each of
+// eight slabs of 64 at least: a slice costs a pass over the output.
+inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int64_t terms, int tile) {
     int64_t s = kCUs / tiles(m, n, tile);
-    if (s > k / 512) s = k / 512;
+    const int64_t most = ceil_div64(k, 64) * terms / 8;
+    if (s > most) s = most;
+    if (s > ceil_div64(k, 64)) s = ceil_div64(k, 64);
     return s < 1 ? 1 : s;
 }
 // The largest tile, which reads each operand least often, that still gives half the CUs a workgroup, if the
 // reduction is long enough by slices of it (k = 0: the reduction is not sliced).
-inline int pick_tile(int64_t m, int64_t n, int64_t k) {
+inline int pick_tile(int64_t m, int64_t n, int64_t k, int64_t terms) {
     if (n <= 32) return TILE_32;
-    return tiles(m, n, TILE_256) * (k ? pick_split(m, n, k, TILE_256) : 1) >= kCUs / 2 ? TILE_256 : TILE_128;
+    return tiles(m, n, TILE_256) * (k ? pick_split(m, n, k, terms, TILE_256) : 1) >= kCUs / 2 ? TILE_256 : TILE_128;
 }
 
 inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf16, int dw_bf16, int for_grad,
@@ -114,7 +117,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.piece = ceil_div64(ceil_div64(all, q.pieces), 256) * 256;
     }
     q.pieces = ceil_div64(all, q.piece);
-    q.tile_z = pick_tile(q.piece, tokens, 0);
+    q.tile_z = pick_tile(q.piece, tokens, 0, 1);
     q.nvt = ceil_div64(vocab, tile_m(q.tile_z));
     size_t off = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
@@ -127,10 +130,12 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.part = take(q.np * q.nvt * 8);
         q.zt = take(q.np * 4);
     } else {
-        q.tile_h = pick_tile(width, tokens, q.piece);
-        q.tile_w = pick_tile(width, q.piece, tokens);
-        q.split_h = pick_split(width, tokens < 1 ? 1 : tokens, q.piece, q.tile_h);
-        q.split_w = pick_split(width, q.piece, tokens, q.tile_w);
+        const int64_t n = tokens < 1 ? 1 : tokens;
+        const int64_t terms_h = bf16 ? 1 : 6, terms_w = bf16 ? q.dparts : 6;
+        q.tile_h = pick_tile(width, n, q.piece, terms_h);
+        q.tile_w = pick_tile(width, q.piece, n, terms_w);
+        q.split_h = pick_split(width, n, q.piece, terms_h, q.tile_h);
+        q.split_w = pick_split(width, q.piece, n, terms_w, q.tile_w);
         q.lg = take(q.np * 8);
         q.rest = take(q.np * 4);
         q.dl = take(q.dparts * q.np * q.piece * 2);
