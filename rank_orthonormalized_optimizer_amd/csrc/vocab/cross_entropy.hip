@@ -44,6 +44,25 @@ __device__ __forceinline__ void split3(float a, uint32_t (&part)[3]) {
     part[2] = down16(r - up16(part[1]));
 }
 
+// a = (h + l) / scale to 2^-23 |a| and 2^-39 of the row's largest: fp16 parts of a scale, a power of two that puts the row's
+// largest value into [2^13, 2^14)
+__device__ __forceinline__ void split2(float a, float scale, uint32_t (&part)[2]) {
+    const _Float16 h = (_Float16)(a * scale);
+    const _Float16 l = (_Float16)(a * scale - (float)h);
+    part[0] = (uint32_t)__builtin_bit_cast(uint16_t, h);
+    part[1] = (uint32_t)__builtin_bit_cast(uint16_t, l);
+}
+
+// That scale for a row whose largest magnitude is `top`, and its inverse (1 where the row is zero or not finite;
+// clamped so that both stay normal numbers).
+__device__ __forceinline__ float row_scale(float top, float& inverse) {
+    int e = 140 - (int)(__float_as_uint(top) >> 23);   // 127 + 13 - biased exponent
+    if (top == 0.f || !(top < INFINITY)) e = 0;
+    e = e > 126 ? 126 : e;
+    inverse = __uint_as_float((uint32_t)(127 - e) << 23);
+    return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
 // The softmax runs in powers of two.  kLog2e is log2(e) rounded to fp32; 2^fma(z, kLog2e, -c) takes e to
 // z (1 + 1.3e-8), less than z's own rounding, and a sum's reference point c is kept in the same unit, so that its
 // rounding drops out.  kLn2 + kLn2Low is 1 / kLog2e.
@@ -66,7 +85,9 @@ __device__ __forceinline__ float exp_exact(float z, float lse) {
 struct PackArgs {
     XentArgs x;
     int64_t n, v, d, kp, np;
-    uint16_t* h;     // planes [parts][np][kp]
+    uint16_t* h;     // planes [parts][np][kp], null: not needed
+    uint16_t* h16;   // fp16 planes [2][np][kp] of fp32 rows and the inverse of their scales
+    float* inv;
     int* map;        // gathered row -> token
     int* tgt;        // its target, -1 where that is no row of W
     float2* lg;      // (lse, grad) of the gathered row (gradient)
@@ -118,6 +139,47 @@ __device__ __forceinline__ void store8(uint16_t* out, int64_t plane, int64_t i, 
     }
 }
 
+__device__ __forceinline__ void store8_f16(uint16_t* out, int64_t plane, int64_t i, const float (&v)[8], float scale) {
+    uint32_t part[8][2];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split2(v[e], scale, part[e]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = part[2 * e][q] | (part[2 * e + 1][q] << 16);
+        *(u32x4*)(out + q * plane + i) = w;
+    }
+}
+
+// One row of a matrix to its planes by one wave: fp32 rows become fp16 planes with the row's scale (p16, inv, if p16 is
+// given) and bf16 planes (p, if given); bf16 rows are copied to p.  Columns up to kp are zero.
+template <bool BF16, bool V8>
+__device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d, int64_t kp, uint16_t* p, int64_t plane,
+                                         uint16_t* p16, int64_t plane16, float* inv, int64_t to, int lane) {
+    float scale = 1.f;
+    if (!BF16 && p16) {
+        float top = 0.f;
+        for (int64_t c = lane * 8; c < kp; c += 512) {
+            float v[8];
+            load8<BF16, V8>(in, row * d, c, d, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+        }
+#pragma unroll
+        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        float inverse;
+        scale = row_scale(top, inverse);
+        if (lane == 0) inv[to] = inverse;
+    }
+    for (int64_t c = lane * 8; c < kp; c += 512) {
+        float v[8];
+        load8<BF16, V8>(in, row * d, c, d, v);
+        if (!BF16 && p16) store8_f16(p16, plane16, to * kp + c, v, scale);
+        if (p) store8<BF16 ? 1 : 3>(p, plane, to * kp + c, v);
+    }
+}
+
 constexpr int kPackRows = 16;
 
 // Sixteen tokens per workgroup, which counts the gathered rows before them itself (a read of the
@@ -158,35 +220,26 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
         if (lane == 0 && blockIdx.x == gridDim.x - 1) a.cnt[0] = base + __popcll(kept);
     }
     __syncthreads();
-    const int nc = (int)(a.kp / 8);
-    for (int i = tid; i < kPackRows * nc; i += 256) {
-        const int r = i / nc, col = (i - r * nc) * 8;
+    for (int r = w; r < kPackRows && t0 + r < a.n; r += 4) {
         const int64_t t = t0 + r;
-        if (t >= a.n) break;
         if (slot[r] >= 0) {
-            float v[8];
-            load8<BF16, V8>(a.x.H, t * a.d, col, a.d, v);
-            store8<BF16 ? 1 : 3>(a.h, a.np * a.kp, (int64_t)slot[r] * a.kp + col, v);
+            pack_row<BF16, V8>(a.x.H, t, a.d, a.kp, a.h, a.np * a.kp, a.h16, a.np * a.kp, a.inv, slot[r], lane);
         } else if (GRAD && a.x.dH) {
-            for (int e = 0; e < 8; ++e)
-                if (col + e < a.d) {
-                    if (BF16) ((uint16_t*)a.x.dH)[t * a.d + col + e] = 0;
-                    else ((float*)a.x.dH)[t * a.d + col + e] = 0.f;
-                }
+            for (int64_t c = lane; c < a.d; c += 64) {
+                if (BF16) ((uint16_t*)a.x.dH)[t * a.d + c] = 0;
+                else ((float*)a.x.dH)[t * a.d + c] = 0.f;
+            }
         }
     }
 }
 
-// Planes of `rows` rows of W (from row0) with zero columns up to kp.
+// Planes of `rows` rows of W (from row0), a wave per row.
 template <bool BF16, bool V8>
-__global__ __launch_bounds__(256) void plane_kernel(const void* W, uint16_t* out, int64_t row0, int64_t rows, int64_t d,
-                                                    int64_t kp, int64_t plane) {
-    const int64_t nc = kp / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * nc) return;
-    const int64_t r = i / nc, col = (i - r * nc) * 8;
-    float v[8];
-    load8<BF16, V8>(W, (row0 + r) * d, col, d, v);
-    store8<BF16 ? 1 : 3>(out, plane, r * kp + col, v);
+__global__ __launch_bounds__(256) void plane_kernel(const void* W, int64_t row0, int64_t rows, int64_t d, int64_t kp,
+                                                    uint16_t* p, uint16_t* p16, int64_t plane, float* inv) {
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (r < rows)
+        pack_row<BF16, V8>((const char*)W + row0 * d * (BF16 ? 2 : 4), r, d, kp, p, plane, p16, plane, inv, r, threadIdx.x & 63);
 }
 
 // ---------------------------------------------------------------------------
@@ -222,6 +275,8 @@ struct LogitArgs {
     int kp;
     const int* cnt;
     const int* tgt;
+    const float* hinv;     // F16: inverse scales of the rows of H's and W's fp16 planes
+    const float* winv;
     int v0;                // first vocabulary row of the piece
     // loss
     float2* part;          // [np][nvt] maximum of a tile of logits and sum of exponentials, as powers of two
@@ -254,10 +309,12 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
         const int m0 = mul.m0, n0 = mul.n0;
         int y[C::NI];
         float2 lg[C::NI];
+        float hinv[C::F16 ? C::NI : 1];
 #pragma unroll
         for (int j = 0; j < C::NI; ++j) {
             const int n = n0 + cl + 16 * j, nn = n < count ? n : count - 1;
             y[j] = a.tgt[nn] - a.v0;
+            if (C::F16) hinv[j] = a.hinv[nn];
             if (EPI != EPI_LOSS) lg[j] = a.lg[nn];
         }
         typename C::Acc acc = {};
@@ -267,6 +324,17 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
         if (more) {
             walk.tile(mt, nt, slice);
             mul.start(a.w, a.h, mt * C::BM, nt * C::BN, 0, a.kp, a.seg);
+        }
+        if constexpr (C::F16) {
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i) {
+                const int m = m0 + rl + 16 * i;   // (winv is allocated for whole tiles)
+                const f32x4 s = *(const f32x4*)(a.winv + m);
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[i][j][v] = acc[i][j][v] * hinv[j] * s[v];
+            }
         }
         if (m0 + C::BM > rows) {
 #pragma unroll
@@ -542,14 +610,17 @@ mm::Segments segments(int pa, int pb) {
         return s;
     };
     if (pa == 3 && pb == 3) return list({1 | 1 << 2, 0 | 2 << 2, 2 | 0 << 2, 0 | 1 << 2, 1 | 0 << 2, 0});
+    if (pa == 2) return list({1, 1 << 2, 0});   // fp16 parts h, l: l h, h l, h h
     if (pb == 3) return list({2 << 2, 1 << 2, 0});
-    if (pa == 3) return list({2, 1, 0});
     return list({0});
 }
 
 using Z256 = mm::Config<256, 256, 2, 4, 2, false, false>;
 using Z128 = mm::Config<128, 128, 2, 2, 4, false, false>;
 using Z32 = mm::Config<128, 32, 4, 1, 4, false, false>;
+using F256 = mm::Config<256, 256, 2, 4, 2, false, false, true>;
+using F128 = mm::Config<128, 128, 2, 2, 4, false, false, true>;
+using F32 = mm::Config<128, 32, 4, 1, 4, false, false, true>;
 using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
 using H128 = mm::Config<128, 128, 2, 2, 4, true, false>;
 using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
@@ -562,12 +633,18 @@ dim3 walkers(int64_t tiles) {
     return dim3((unsigned)(tiles < kCUs * C::kPerCU ? tiles : kCUs * C::kPerCU));
 }
 
-template <int EPI>
+template <class C256, class C128, class C32, int EPI>
 void launch_logits(const LogitArgs& a, int tile, int64_t n, hipStream_t s) {
     const int64_t t = tiles(a.w.rows, n, tile);
-    if (tile == TILE_256) hipLaunchKernelGGL((logit_kernel<Z256, EPI>), walkers<Z256>(t), dim3(Z256::THREADS), 0, s, a);
-    else if (tile == TILE_128) hipLaunchKernelGGL((logit_kernel<Z128, EPI>), walkers<Z128>(t), dim3(Z128::THREADS), 0, s, a);
-    else hipLaunchKernelGGL((logit_kernel<Z32, EPI>), walkers<Z32>(t), dim3(Z32::THREADS), 0, s, a);
+    if (tile == TILE_256) hipLaunchKernelGGL((logit_kernel<C256, EPI>), walkers<C256>(t), dim3(C256::THREADS), 0, s, a);
+    else if (tile == TILE_128) hipLaunchKernelGGL((logit_kernel<C128, EPI>), walkers<C128>(t), dim3(C128::THREADS), 0, s, a);
+    else hipLaunchKernelGGL((logit_kernel<C32, EPI>), walkers<C32>(t), dim3(C32::THREADS), 0, s, a);
+}
+
+template <int EPI>
+void launch_logits(const LogitArgs& a, const XentPlan& p, hipStream_t s) {
+    if (p.parts == 1) launch_logits<Z256, Z128, Z32, EPI>(a, p.tile_z, p.n, s);
+    else if constexpr (EPI != EPI_D1) launch_logits<F256, F128, F32, EPI>(a, p.tile_z, p.n, s);   // fp32: D in three parts
 }
 
 template <bool GRAD>
@@ -582,25 +659,44 @@ void launch_pack(const PackArgs& a, hipStream_t s) {
     }
 }
 
-// W's rows [v0, v0 + rows) as an operand: in place, or as planes in the workspace
-mm::Operand w_operand(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int64_t rows, hipStream_t s) {
-    if (!p.wpack) return mm::Operand{(const uint16_t*)x.W + v0 * p.d, 0, p.d, (int)rows};
-    uint16_t* out = (uint16_t*)(ws + p.w);
-    const int64_t plane = p.piece * p.kp;
-    const dim3 grid((unsigned)ceil_div64(rows * (p.kp / 8), 256));
-    if (x.bf16) {
-        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<true, true>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
-        else hipLaunchKernelGGL((plane_kernel<true, false>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
-    } else {
-        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<false, true>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
-        else hipLaunchKernelGGL((plane_kernel<false, false>), grid, dim3(256), 0, s, x.W, out, v0, rows, p.d, p.kp, plane);
+// W's rows [v0, v0 + rows) in place (bf16), or as planes in the workspace: bf16 ones (`exact`, for dH) and for fp32 fp16 ones.
+struct Weights {
+    mm::Operand z, h;   // for the logits and for dH
+};
+Weights weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int64_t rows, bool exact, hipStream_t s) {
+    if (!p.wpack) {
+        const mm::Operand o{(const uint16_t*)x.W + v0 * p.d, 0, p.d, (int)rows};
+        return Weights{o, o};
     }
-    return mm::Operand{out, plane, p.kp, (int)rows};
+    uint16_t* w = exact || x.bf16 ? (uint16_t*)(ws + p.w) : nullptr;
+    uint16_t* w16 = x.bf16 ? nullptr : (uint16_t*)(ws + p.w16);
+    float* inv = (float*)(ws + p.winv);
+    const int64_t plane = p.piece * p.kp;
+    const dim3 grid((unsigned)ceil_div64(rows, 4));
+    if (x.bf16) {
+        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<true, true>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
+        else hipLaunchKernelGGL((plane_kernel<true, false>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
+    } else {
+        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<false, true>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
+        else hipLaunchKernelGGL((plane_kernel<false, false>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
+    }
+    const mm::Operand h{w, plane, p.kp, (int)rows};
+    return Weights{x.bf16 ? h : mm::Operand{w16, plane, p.kp, (int)rows}, h};
 }
 
-PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws) {
-    return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, (uint16_t*)(ws + p.h), (int*)(ws + p.map), (int*)(ws + p.tgt),
-                    (float2*)(ws + p.lg), (int*)(ws + p.cnt)};
+PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws, bool exact) {
+    return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, exact || x.bf16 ? (uint16_t*)(ws + p.h) : nullptr,
+                    x.bf16 ? nullptr : (uint16_t*)(ws + p.h16), (float*)(ws + p.hinv), (int*)(ws + p.map),
+                    (int*)(ws + p.tgt), (float2*)(ws + p.lg), (int*)(ws + p.cnt)};
+}
+
+LogitArgs logit_args(const XentPlan& p, const PackArgs& pk, char* ws) {
+    LogitArgs a{};
+    a.h = mm::Operand{p.parts == 1 ? pk.h : pk.h16, p.np * p.kp, p.kp, 0};
+    a.seg = p.parts == 1 ? segments(1, 1) : segments(2, 2);
+    a.kp = (int)p.kp; a.cnt = pk.cnt; a.tgt = pk.tgt;
+    a.hinv = pk.inv; a.winv = (float*)(ws + p.winv);
+    return a;
 }
 
 void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
@@ -611,17 +707,14 @@ void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
 
 int run_xent(const XentArgs& x, const XentPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
-    const PackArgs pk = pack_args(x, p, ws);
+    const PackArgs pk = pack_args(x, p, ws, false);
     launch_pack<false>(pk, s);
-    LogitArgs a{};
-    a.h = mm::Operand{pk.h, p.np * p.kp, p.kp, 0};
-    a.seg = segments(p.parts, p.parts);
-    a.kp = (int)p.kp; a.cnt = pk.cnt; a.tgt = pk.tgt;
+    LogitArgs a = logit_args(p, pk, ws);
     a.part = (float2*)(ws + p.part); a.zt = (float*)(ws + p.zt); a.nvt = (int)p.nvt;
     for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
-        a.w = w_operand(x, p, ws, v0, p.v - v0 < p.piece ? p.v - v0 : p.piece, s);
+        a.w = weights(x, p, ws, v0, p.v - v0 < p.piece ? p.v - v0 : p.piece, false, s).z;
         a.v0 = (int)v0;
-        launch_logits<EPI_LOSS>(a, p.tile_z, p.n, s);
+        launch_logits<EPI_LOSS>(a, p, s);
     }
     hipLaunchKernelGGL(loss_kernel, dim3((unsigned)ceil_div64(p.n, 4)), dim3(256), 0, s, a.part, a.zt, a.tgt, pk.map, pk.cnt,
                        a.nvt, x.loss, x.lse_out);
@@ -639,12 +732,10 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
         hipLaunchKernelGGL(clear_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, (uint16_t*)x.dW, n);
         return (int)hipGetLastError();
     }
-    const PackArgs pk = pack_args(x, p, ws);
+    const PackArgs pk = pack_args(x, p, ws, true);
     launch_pack<true>(pk, s);
-    LogitArgs z{};
-    z.h = mm::Operand{pk.h, p.np * p.kp, p.kp, 0};
-    z.seg = segments(p.parts, p.parts);
-    z.kp = (int)p.kp; z.cnt = pk.cnt; z.tgt = pk.tgt; z.lg = pk.lg;
+    LogitArgs z = logit_args(p, pk, ws);
+    z.lg = pk.lg;
     z.dl = (uint16_t*)(ws + p.dl); z.rest = (float*)(ws + p.rest); z.np = p.np; z.piece = p.piece;
     const mm::Operand dl{z.dl, p.np * p.piece, p.piece, 0};
     OutArgs h{};
@@ -658,12 +749,13 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
     w.acc_rows = p.piece;
     for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
         const int64_t rows = p.v - v0 < p.piece ? p.v - v0 : p.piece;
-        z.w = w_operand(x, p, ws, v0, rows, s);
+        const Weights wt = weights(x, p, ws, v0, rows, x.dH != nullptr, s);
+        z.w = wt.z;
         z.v0 = (int)v0;
-        if (p.dparts == 1) launch_logits<EPI_D1>(z, p.tile_z, p.n, s);
-        else launch_logits<EPI_D3>(z, p.tile_z, p.n, s);
+        if (p.dparts == 1) launch_logits<EPI_D1>(z, p, s);
+        else launch_logits<EPI_D3>(z, p, s);
         if (x.dH) {
-            h.a = z.w; h.b = dl;
+            h.a = wt.h; h.b = dl;
             h.seg = segments(p.parts, x.bf16 ? 1 : 3);
             h.k = (int)(ceil_div64(rows, 64) * 64);
             h.k_per = (int)(ceil_div64(ceil_div64(h.k, p.split_h), 64) * 64);
@@ -674,7 +766,7 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             else hipLaunchKernelGGL((out_kernel<H32>), walkers<H32>(t), dim3(H32::THREADS), 0, s, h);
         }
         if (x.dW) {
-            w.a = z.h; w.b = dl;
+            w.a = mm::Operand{pk.h, p.np * p.kp, p.kp, 0}; w.b = dl;
             w.seg = segments(p.parts, p.dparts);
             w.rows = (int)rows;
             w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);

@@ -1,11 +1,12 @@
-// Tile products on the bf16 matrix cores of gfx950 (v_mfma_f32_16x16x32_bf16) for the vocabulary
+// Tile products on the 16-bit matrix cores of gfx950 (v_mfma_f32_16x16x32_bf16 and _f16) for the vocabulary
 // operators: C[m][n] = sum over segments and k of A[m][k] B[n][k], fp32 accumulation.
 //
-// Operands are bf16 planes in memory.  An operand is read either along its rows ([x][k], k
+// Operands are planes of 16-bit values in memory.  An operand is read either along its rows ([x][k], k
 // contiguous) or transposed ([k][x], x contiguous); a transposed one is turned around by the LDS
 // read itself (ds_read_b64_tr_b16), so that D, H and W serve several products in one layout.
 // fp32 operands come as three planes h + m + l (an exact split); a segment list then names the
-// plane pairs to multiply, smallest first, and the k loop runs over all of them.
+// plane pairs to multiply, smallest first, and every 64 k run over all of them.  Where the caller knows a
+// scale per row, two fp16 planes (11 + 11 bits) and three pairs do (F16).
 //
 // A workgroup owns a BM x BN tile, its waves WM x WN parts of it.  Slabs of 64 k go from memory
 // straight to LDS (buffer loads with an LDS destination, 16 bytes per lane) into a ring of STAGES
@@ -25,6 +26,7 @@ namespace dion {
 namespace mm {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -124,8 +126,9 @@ __device__ __forceinline__ void wait_slab() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_, bool TA_, bool TB_>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, bool TA_, bool TB_, bool F16_ = false>
 struct Config {
+    static constexpr bool F16 = F16_;   // fp16 planes
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
     static constexpr bool TA = TA_, TB = TB_;
     static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
@@ -167,9 +170,8 @@ struct Product {
         n0 = n0_;
         ta.init(a, m0, wave, lane);
         tb.init(b, n0, wave, lane);
-        const int nk = (k1 - k0) / kBK;
-        total = nk * (int)seg.n;
-        ld = Loads(k0, nk, seg.list);
+        total = (k1 - k0) / kBK * (int)seg.n;
+        ld = Loads(k0, seg);
         const int ahead = C::STAGES < total ? C::STAGES : total;
         for (int i = 0; i < ahead; ++i) {
             ld.begin(a, b, m0, n0, lds);
@@ -209,19 +211,22 @@ struct Product {
     }
 
 private:
-    // The loads of one slab, in the order of the segments: which is next, and its descriptors.
+    // The loads of one slab: which is next, and its descriptors.  All segments of 64 k come before the next 64, so that
+    // the planes they share are still in L2.
     struct Loads {
-        int k0 = 0, nk = 0, k = 0, slot = 0;
+        int k = 0, slot = 0, left = 0;
+        Segments all{0, 0};
         uint32_t list = 0;
         u32x4 ra, rb;
         uint32_t to;
         Loads() = default;
-        __device__ __forceinline__ Loads(int k0_, int nk_, uint32_t list_) : k0(k0_), nk(nk_), list(list_) {}
+        __device__ __forceinline__ Loads(int k0, Segments seg) : k(k0), left((int)seg.n), all(seg), list(seg.list) {}
         __device__ __forceinline__ void begin(const Operand& a, const Operand& b, int m0, int n0, uint16_t* lds) {
-            ra = TileA::slab(a, m0, list & 3, k0 + k * kBK);
-            rb = TileB::slab(b, n0, (list >> 2) & 3, k0 + k * kBK);
+            ra = TileA::slab(a, m0, list & 3, k);
+            rb = TileB::slab(b, n0, (list >> 2) & 3, k);
             to = (uint32_t)(uintptr_t)(lds_void*)lds + slot * (C::kStage * 2);
-            if (++k == nk) { k = 0; list >>= 4; }
+            list >>= 4;
+            if (--left == 0) { left = (int)all.n; list = all.list; k += kBK; }
             if (++slot == C::STAGES) slot = 0;
         }
         __device__ __forceinline__ void one(const TileA& ta, const TileB& tb, int i, int wave) const {
@@ -233,6 +238,13 @@ private:
     TileA ta;
     TileB tb;
     Loads ld;
+
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+        if constexpr (C::F16)
+            return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+        else
+            return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
 
     // The products of the fragments at hand, and the fragments of step ks of the stage la in their place;
     // load(0 .. LOADS - 1) starts the loads that go along.
@@ -250,8 +262,7 @@ private:
         for (int i = 0; i < C::MI; ++i) {
 #pragma unroll
             for (int j = 0; j < C::NI; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa[i]),
-                                                                    __builtin_bit_cast(bf16x8, fb[j]), acc[i][j], 0, 0, 0);
+                acc[i][j] = mma(fa[i], fb[j], acc[i][j]);
 #pragma unroll
             for (int q = 0; q < per_row; ++q)
                 if (i * per_row + q < LOADS) load(i * per_row + q);

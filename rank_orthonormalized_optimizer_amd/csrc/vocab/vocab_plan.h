@@ -61,7 +61,7 @@ inline bool make_embed_grad_plan(int64_t tokens, int64_t vocab, int64_t width, E
 }
 int run_embedding_grad(const EmbedArgs& a, const EmbedGradPlan& p, char* ws, void* stream);
 
-// Layout of a cross entropy call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32);
+// Layout of a cross entropy call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32, whose logits take two fp16 parts);
 // dparts: parts of D.  The vocabulary goes in `pieces` of `piece` rows (a multiple of 256).
 struct XentPlan {
     int64_t n, v, d, kp;      // tokens, vocab, width, width rounded up to 64
@@ -72,7 +72,7 @@ struct XentPlan {
     int64_t nvt;              // softmax partials per token (forward)
     int tile_z, tile_h, tile_w;   // tile shapes of the logits, dH and dW (TILE_*)
     int64_t split_h, split_w; // slices of the reductions of dH (over the piece) and dW (over the tokens)
-    size_t h, map, tgt, lg, cnt, part, zt, w, dl, rest, acc_h, acc_w, total;
+    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, w, w16, winv, dl, rest, acc_h, acc_w, total;
 };
 
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens)
@@ -107,7 +107,8 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.parts = bf16 ? 1 : 3;
     q.dparts = bf16 && dw_bf16 ? 1 : 3;
     q.wpack = !bf16 || width % 64 != 0;
-    int64_t per_row = q.wpack ? q.parts * q.kp * 2 : 0;   // bytes of scratch per vocabulary row of a piece
+    // bytes of scratch per vocabulary row of a piece: fp32 rows as two fp16 planes, and for the gradient three bf16 planes
+    int64_t per_row = !q.wpack ? 0 : bf16 ? q.kp * 2 : q.kp * (for_grad ? 10 : 4);
     if (for_grad && q.dparts * q.np * 2 > per_row) per_row = q.dparts * q.np * 2;
     const int64_t all = ceil_div64(vocab, 256) * 256;
     q.piece = all;
@@ -122,10 +123,16 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     size_t off = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
     q.cnt = take(256);
-    q.h = take(q.parts * q.np * q.kp * 2);
+    if (bf16 || for_grad) q.h = take(q.parts * q.np * q.kp * 2);
+    if (!bf16) {
+        q.h16 = take(2 * q.np * q.kp * 2);
+        q.hinv = take(q.np * 4);
+        q.w16 = take(2 * q.piece * q.kp * 2);
+        q.winv = take(q.piece * 4);
+    }
     q.map = take(q.np * 4);
     q.tgt = take(q.np * 4);
-    if (q.wpack) q.w = take(q.parts * q.piece * q.kp * 2);
+    if (q.wpack && (bf16 || for_grad)) q.w = take(q.parts * q.piece * q.kp * 2);
     if (!for_grad) {
         q.part = take(q.np * q.nvt * 8);
         q.zt = take(q.np * 4);

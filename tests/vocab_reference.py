@@ -7,9 +7,12 @@ lookup   one fp32 multiplication and one rounding: equal bit for bit to the same
 table    a row of c tokens: c - 1 additions, the scale and an addition to what was there, each one
          rounding of a partial result that is at most |scale| sum |dY| + |old|: (c + 4) u of that,
          then the output's rounding.
-logits   K products of bf16 parts added in fp32: at most nseg K additions, doubled for the matrix
-         core's own rounding (it need not be to nearest), of values at most sum_k |h||w|; fp32
-         operands drop part products below 2^-24 each, at most three: gamma_z = (2 nseg K + 8) u.
+logits   K products of 16-bit parts added in fp32: at most nseg K additions, doubled for the matrix
+         core's own rounding (it need not be to nearest), of values at most sum_k |h||w|: 2 nseg K u.
+         fp32 operands go as two fp16 parts of a row scaled to [2^13, 2^14): each part's rounding
+         leaves 2^-23 of the element or, where the low part is subnormal, 2^-39 of the row's largest;
+         the dropped l l product is below 2^-22: (2 + 2 + 4) u sum_k |h||w| and
+         2^-38 (max|h| sum|w| + max|w| sum|h|).  gamma_z = (2 nseg K + 12) u.
 lse      the largest logit error, plus sums of at most V exponentials (added in a tree of at most
          96 + V / 64 steps per path), four u for each exponential, and two roundings of |lse|.
 D        p (error of the logit and lse, and four u), then grad's multiplication and the rounding of
@@ -55,10 +58,13 @@ class Head:
         w = W.to(f64)
         parts = 1 if H.dtype == torch.bfloat16 else 3
         dparts = 1 if parts == 1 and dw_dtype in (None, torch.bfloat16) else 3
-        nz = {1: 1, 3: 6}[parts]
+        nz, nh = {1: (1, 1), 3: (3, 6)}[parts]             # part products of the logits and of dH
         z = h @ w.t()
-        gz = (2 * nz * d + 8) * U
+        gz = (2 * nz * d + 12) * U
         size = (h.abs() @ w.abs().t()).amax(1)             # an error bound of every logit of the row, over gz
+        if parts == 3:
+            wa = w.abs()
+            size = size + 2.0 ** -38 / gz * (h.abs().amax(1) * wa.sum(1).max() + wa.max() * h.abs().sum(1))
         self.lse = torch.where(keep, torch.logsumexp(z, 1), 0.0)
         inside = (y >= 0) & (y < V)
         rows = torch.arange(y.numel(), device=dev)
@@ -86,7 +92,7 @@ class Head:
         rh = half_step(torch.bfloat16) if H.dtype == torch.bfloat16 else U
         rw = half_step(torch.bfloat16) if dparts == 1 else U
         self.dH = D @ w
-        self.dH_bound = bound(rh, w, nz, V, True) + half_step(H.dtype) * self.dH.abs()
+        self.dH_bound = bound(rh, w, nh, V, True) + half_step(H.dtype) * self.dH.abs()
         old = 0.0 if dw_old is None else dw_old.to(f64)
         self.dW = D.t() @ h + old
         self.dW_bound = bound(rw, h, {(1, 1): 1, (1, 3): 3, (3, 3): 6}[parts, dparts], y.numel(), False) \
