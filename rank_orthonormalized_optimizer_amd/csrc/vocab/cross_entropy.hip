@@ -299,7 +299,7 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
     Walk walk((rows + C::BM - 1) / C::BM, (count + C::BN - 1) / C::BN, 1);
     if (walk.done()) return;
     a.h.rows = count;
-    mm::Product<C> mul(lds);
+    typename mm::ProductOf<C>::type mul(lds);
     int mt, nt, slice;
     walk.tile(mt, nt, slice);
     mul.start(a.w, a.h, mt * C::BM, nt * C::BN, 0, a.kp, a.seg);
@@ -395,12 +395,12 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
                             }
                     if (mine) a.rest[n] = d - up16(down16(d));
                 }
-                // Two blocks of 16 rows at a time: the lane quarters trade their four rows of one against the other's
+                // A lane has four consecutive rows of a block of 16.  Two blocks at a time, where there are two: the lane quarters trade their four rows of one against the other's
                 // (v_permlane32_swap, v_permlane16_swap), so that a lane stores eight consecutive rows and four lanes 64 bytes.
                 const int quarter = mul.lane / 16;
                 uint16_t* to = a.dl + n * a.piece + m0 + mul.xa + 16 * (quarter / 2) + 8 * (quarter % 2);
 #pragma unroll
-                for (int i = 0; i < C::MI; i += 2) {
+                for (int i = 0; i + 1 < C::MI; i += 2) {
                     uint32_t part[2][4][3];
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
@@ -421,6 +421,17 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
                         }
                         if (n < count) *(u32x4*)(to + q * a.np * a.piece + 16 * i) = w;
                     }
+                }
+                if constexpr (C::MI % 2 != 0) {
+                    constexpr int i = C::MI - 1;
+                    uint32_t part[4][3];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) split3(acc[i][j][v] * lg[j].y, part[v]);
+#pragma unroll
+                    for (int q = 0; q < PD; ++q)
+                        if (n < count)
+                            *(u32x2*)(a.dl + (q * a.np + n) * a.piece + m0 + rl + 16 * i) =
+                                u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
                 }
             }
         }
@@ -539,7 +550,7 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
     if (walk.done()) return;
     if (a.k < 0) a.a.rows = count;   // dW reduces over the tokens
     a.b.rows = count;
-    mm::Product<C> mul(lds);
+    typename mm::ProductOf<C>::type mul(lds);
     int mt, nt, slice;
     auto start = [&]() {   // false: a slice without any k
         walk.tile(mt, nt, slice);
@@ -621,6 +632,10 @@ using Z32 = mm::Config<128, 32, 4, 1, 4, false, false>;
 using F256 = mm::Config<256, 256, 2, 4, 2, false, false, true>;
 using F128 = mm::Config<128, 128, 2, 2, 4, false, false, true>;
 using F32 = mm::Config<128, 32, 4, 1, 4, false, false, true>;
+using P32 = mm::FewConfig<32, 3, false>;
+using P64 = mm::FewConfig<64, 2, false>;
+using Q32 = mm::FewConfig<32, 3, true>;
+using Q64 = mm::FewConfig<64, 2, true>;
 using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
 using H128 = mm::Config<128, 128, 2, 2, 4, true, false>;
 using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
@@ -633,18 +648,27 @@ dim3 walkers(int64_t tiles) {
     return dim3((unsigned)(tiles < kCUs * C::kPerCU ? tiles : kCUs * C::kPerCU));
 }
 
+template <class C, int EPI>
+void launch_logits(const LogitArgs& a, int64_t n, hipStream_t s) {
+    const int64_t t = ceil_div64(a.w.rows, C::BM) * ceil_div64(n, C::BN);
+    hipLaunchKernelGGL((logit_kernel<C, EPI>), walkers<C>(t), dim3(C::THREADS), 0, s, a);
+}
+
 template <class C256, class C128, class C32, int EPI>
 void launch_logits(const LogitArgs& a, int tile, int64_t n, hipStream_t s) {
-    const int64_t t = tiles(a.w.rows, n, tile);
-    if (tile == TILE_256) hipLaunchKernelGGL((logit_kernel<C256, EPI>), walkers<C256>(t), dim3(C256::THREADS), 0, s, a);
-    else if (tile == TILE_128) hipLaunchKernelGGL((logit_kernel<C128, EPI>), walkers<C128>(t), dim3(C128::THREADS), 0, s, a);
-    else hipLaunchKernelGGL((logit_kernel<C32, EPI>), walkers<C32>(t), dim3(C32::THREADS), 0, s, a);
+    if (tile == TILE_256) launch_logits<C256, EPI>(a, n, s);
+    else if (tile == TILE_128) launch_logits<C128, EPI>(a, n, s);
+    else launch_logits<C32, EPI>(a, n, s);
 }
 
 template <int EPI>
 void launch_logits(const LogitArgs& a, const XentPlan& p, hipStream_t s) {
     if (p.parts == 1) launch_logits<Z256, Z128, Z32, EPI>(a, p.tile_z, p.n, s);
-    else if constexpr (EPI != EPI_D1) launch_logits<F256, F128, F32, EPI>(a, p.tile_z, p.n, s);   // fp32: D in three parts
+    else if constexpr (EPI != EPI_D1) {   // fp32: D in three parts
+        if (p.few && p.n <= 32) launch_logits<P32, EPI>(a, p.n, s);
+        else if (p.few) launch_logits<P64, EPI>(a, p.n, s);
+        else launch_logits<F256, F128, F32, EPI>(a, p.tile_z, p.n, s);
+    }
 }
 
 template <bool GRAD>
@@ -659,13 +683,13 @@ void launch_pack(const PackArgs& a, hipStream_t s) {
     }
 }
 
-// W's rows [v0, v0 + rows) in place (bf16), or as planes in the workspace: bf16 ones (`exact`, for dH) and for fp32 fp16 ones.
+// W's rows [v0, v0 + rows) in place (bf16, or fp32 for few tokens), or as planes in the workspace: bf16 ones (`exact`, for dH) and for fp32 fp16 ones.
 struct Weights {
     mm::Operand z, h;   // for the logits and for dH
 };
 Weights weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int64_t rows, bool exact, hipStream_t s) {
     if (!p.wpack) {
-        const mm::Operand o{(const uint16_t*)x.W + v0 * p.d, 0, p.d, (int)rows};
+        const mm::Operand o{(const uint16_t*)((const char*)x.W + v0 * p.d * (x.bf16 ? 2 : 4)), 0, p.d, (int)rows};
         return Weights{o, o};
     }
     uint16_t* w = exact || x.bf16 ? (uint16_t*)(ws + p.w) : nullptr;
@@ -685,18 +709,24 @@ Weights weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int6
 }
 
 PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws, bool exact) {
-    return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, exact || x.bf16 ? (uint16_t*)(ws + p.h) : nullptr,
-                    x.bf16 ? nullptr : (uint16_t*)(ws + p.h16), (float*)(ws + p.hinv), (int*)(ws + p.map),
+    return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, exact || x.bf16 || p.few ? (uint16_t*)(ws + p.h) : nullptr,
+                    x.bf16 || p.few ? nullptr : (uint16_t*)(ws + p.h16), (float*)(ws + p.hinv), (int*)(ws + p.map),
                     (int*)(ws + p.tgt), (float2*)(ws + p.lg), (int*)(ws + p.cnt)};
 }
 
 LogitArgs logit_args(const XentPlan& p, const PackArgs& pk, char* ws) {
     LogitArgs a{};
-    a.h = mm::Operand{p.parts == 1 ? pk.h : pk.h16, p.np * p.kp, p.kp, 0};
+    a.h = mm::Operand{pk.h16 ? pk.h16 : pk.h, p.np * p.kp, p.kp, 0};
     a.seg = p.parts == 1 ? segments(1, 1) : segments(2, 2);
     a.kp = (int)p.kp; a.cnt = pk.cnt; a.tgt = pk.tgt;
     a.hinv = pk.inv; a.winv = (float*)(ws + p.winv);
     return a;
+}
+
+template <class C>
+void launch_out(const OutArgs& a, int64_t rows, hipStream_t s) {
+    const int64_t t = ceil_div64(a.d, C::BM) * ceil_div64(rows, C::BN) * a.split;
+    hipLaunchKernelGGL((out_kernel<C>), walkers<C>(t), dim3(C::THREADS), 0, s, a);
 }
 
 void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
@@ -760,10 +790,11 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             h.k = (int)(ceil_div64(rows, 64) * 64);
             h.k_per = (int)(ceil_div64(ceil_div64(h.k, p.split_h), 64) * 64);
             h.add = v0 > 0;
-            const int64_t t = tiles(p.d, p.n, p.tile_h) * p.split_h;
-            if (p.tile_h == TILE_256) hipLaunchKernelGGL((out_kernel<H256>), walkers<H256>(t), dim3(H256::THREADS), 0, s, h);
-            else if (p.tile_h == TILE_128) hipLaunchKernelGGL((out_kernel<H128>), walkers<H128>(t), dim3(H128::THREADS), 0, s, h);
-            else hipLaunchKernelGGL((out_kernel<H32>), walkers<H32>(t), dim3(H32::THREADS), 0, s, h);
+            if (p.few && p.n <= 32) launch_out<Q32>(h, p.n, s);
+            else if (p.few) launch_out<Q64>(h, p.n, s);
+            else if (p.tile_h == TILE_256) launch_out<H256>(h, p.n, s);
+            else if (p.tile_h == TILE_128) launch_out<H128>(h, p.n, s);
+            else launch_out<H32>(h, p.n, s);
         }
         if (x.dW) {
             w.a = mm::Operand{pk.h, p.np * p.kp, p.kp, 0}; w.b = dl;
@@ -771,9 +802,8 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             w.rows = (int)rows;
             w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);
             w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
-            const int64_t t = tiles(p.d, rows, p.tile_w) * p.split_w;
-            if (p.tile_w == TILE_256) hipLaunchKernelGGL((out_kernel<W256>), walkers<W256>(t), dim3(W256::THREADS), 0, s, w);
-            else hipLaunchKernelGGL((out_kernel<W128>), walkers<W128>(t), dim3(W128::THREADS), 0, s, w);
+            if (p.tile_w == TILE_256) launch_out<W256>(w, rows, s);
+            else launch_out<W128>(w, rows, s);
             if (w.acc) launch_join(w, rows, s);
         }
     }

@@ -49,12 +49,15 @@ struct Segments {
     uint32_t list;
 };
 
+constexpr uint32_t kOutside = 0x80000000u;   // an offset outside every descriptor's range
+
 // 16 bytes per lane from the descriptor's range (zeros outside it) to 1 KB of LDS at byte address lds, which
 // must be the same for all lanes.  Written as assembly because the compiler waits for every load in flight before a
 // transposed LDS read that follows the builtin of this load, wherever it reads; it names no output register, and
 // wait_slab() is what waits for it.  (m0 is the compiler's only for instructions that do not occur here.)
 __device__ __forceinline__ void load_to_lds(u32x4 desc, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(desc), "s"(lds));
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(desc),
+                 "s"(__builtin_amdgcn_readfirstlane(lds)));
 }
 
 template <int X>   // rows of 16-byte chunks per [64][X] row
@@ -128,7 +131,7 @@ __device__ __forceinline__ void wait_slab() {
 
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_, bool TA_, bool TB_, bool F16_ = false>
 struct Config {
-    static constexpr bool F16 = F16_;   // fp16 planes
+    static constexpr bool F16 = F16_, FEW = false;   // fp16 planes
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
     static constexpr bool TA = TA_, TB = TB_;
     static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
@@ -181,7 +184,9 @@ struct Product {
     }
 
     __device__ __forceinline__ void finish(const Operand& a, const Operand& b, typename C::Acc& acc) {
-        wait_slab<0>();   // whatever the caller stored since start() counts too, so no number tells the slabs apart
+        // loads end in order, so that what the caller stored since start() can only make this wait longer
+        if (total >= C::STAGES) wait_slab<(C::STAGES - 1) * kPer>();
+        else wait_slab<0>();
         u32x4 fa[C::MI], fb[C::NI];
         uint16_t* la = lds;
 #pragma unroll
@@ -286,6 +291,154 @@ private:
         }
     }
 };
+
+// ---------------------------------------------------------------------------
+// Products of few columns with an fp32 matrix read in place: A is fp32 ([x][k] or transposed [k][x], rows of a multiple of
+// four elements), B three bf16 planes.  Such a product is a stream of A: its tiles go to LDS as they are, and a wave splits
+// its fragments into the three parts in registers, all six part products of a slab at once.  (Planes of A in the workspace
+// would be written and read again: 4 + 6 bytes per element and more.)  A tile of 128 rows, eight waves of 16 rows each.
+//
+// LDS image of a [128][64] fp32 tile: 16-byte chunk c of row x at c ^ (x & 15); of a transposed [64][128] one: chunk c of
+// row k at c ^ 4 (k / 8 % 4), so that the four rows that a read takes together fall on different banks.
+template <int BN_, int STAGES_, bool TA_>
+struct FewConfig {
+    static constexpr int BM = 128, BN = BN_, WM = 8, WN = 1, STAGES = STAGES_;
+    static constexpr bool TA = TA_, TB = false, F16 = false, FEW = true;
+    static constexpr int WAVES = 8, THREADS = 512, MI = 1, NI = BN / 16;
+    static constexpr int kA = BM * kBK * 2, kStage = kA + 3 * BN * kBK;   // in 16-bit elements
+    static constexpr int kLds = STAGES * kStage;
+    static constexpr int kPerCU = 1;
+    typedef f32x4 Acc[MI][NI];
+};
+
+template <class C>
+struct FewProduct {
+    using TileB = Tile<C::BN, false, 4>;   // the planes are loaded by four waves each, two at a time
+    static constexpr int kLoadsA = C::BM * kBK * 4 / 1024 / 8, kLoadsB = 3 * C::BN * kBK * 2 / 1024;   // per wave; per workgroup
+    static constexpr int kRowsB = kBK * 2 * 8;   // bytes of eight rows of a plane: one wave load
+
+    int lane, wave, xa, xb, total, m0, n0;
+    uint16_t* lds;
+
+    __device__ __forceinline__ explicit FewProduct(uint16_t* lds_) : lds(lds_) {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        xa = wave * 16;
+        xb = 0;
+    }
+
+    __device__ __forceinline__ void start(const Operand& a, const Operand& b, int m0_, int n0_, int k0_, int k1, Segments) {
+        m0 = m0_;
+        n0 = n0_;
+        k = k0_;
+        total = (k1 - k0_) / kBK;
+        slot = 0;
+        const int ahead = C::STAGES < total ? C::STAGES : total;
+        for (int i = 0; i < ahead; ++i) load(a, b);
+    }
+
+    __device__ __forceinline__ void finish(const Operand& a, const Operand& b, typename C::Acc& acc) {
+        int at = 0;
+        for (int it = 0; it < total; ++it) {
+            // each later slab under way has at least this many loads in every wave
+            if (it + C::STAGES <= total) wait_slab<(C::STAGES - 1) * (kLoadsA + kLoadsB / 8)>();
+            else wait_slab<0>();
+            const uint16_t* la = lds + at * C::kStage;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4 fa[3];
+                split(la, ks, fa);
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j) {
+                    u32x4 fb[3];
+#pragma unroll
+                    for (int q = 0; q < 3; ++q)
+                        fb[q] = TileB::frag((uint16_t*)la + C::kA + q * C::BN * kBK, 16 * j, ks, lane);
+                    constexpr int ta[6] = {1, 0, 2, 0, 1, 0}, tb[6] = {1, 2, 0, 1, 0, 0};   // smallest first
+#pragma unroll
+                    for (int t = 0; t < 6; ++t)
+                        acc[0][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, fa[ta[t]]), __builtin_bit_cast(bf16x8, fb[tb[t]]), acc[0][j], 0, 0, 0);
+                }
+            }
+            if (++at == C::STAGES) at = 0;
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave has read the slab
+            if (it + C::STAGES < total) load(a, b);
+        }
+    }
+
+private:
+    int k, slot;
+
+    __device__ __forceinline__ void load(const Operand& a, const Operand& b) {
+        const uint32_t to = (uint32_t)(uintptr_t)(lds_void*)lds + slot * (C::kStage * 2);
+        const float* A = (const float*)a.p;
+        const int width = (int)a.ld;   // elements of a row, whose last slab or tile ends inside the row
+        // offsets outside the descriptor's range (columns behind the row, rows behind the matrix) read as zeros
+        const float* base = C::TA ? A + (int64_t)k * a.ld : A + (int64_t)m0 * a.ld + k;
+        const int64_t left = (C::TA ? (int64_t)(a.rows - k) * a.ld : (int64_t)(a.rows - m0) * a.ld - k) * 4;
+        const uint64_t p = (uint64_t)base;
+        const u32x4 ra{(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, (uint32_t)(left < 0x7fffffff ? left : 0x7fffffff), 0x00027000u};
+#pragma unroll
+        for (int i = 0; i < kLoadsA; ++i) {
+            const int q = wave * kLoadsA + i;
+            uint32_t off;
+            if constexpr (!C::TA) {
+                const int x = q * 4 + lane / 16, c = (lane % 16) ^ (x & 15);
+                off = k + 4 * c < width ? (uint32_t)(x * width + 4 * c) * 4u : kOutside;
+            } else {
+                const int r = q * 2 + lane / 32, c = (lane % 32) ^ (((r >> 3) & 3) << 2), col = m0 + 4 * c;
+                off = col < width ? (uint32_t)(r * width + col) * 4u : kOutside;
+            }
+            load_to_lds(ra, off, to + q * 1024);
+        }
+        for (int q = wave; q < kLoadsB; q += 8) {   // eight rows of a plane each
+            const int plane = q / (C::BN / 8), x = q % (C::BN / 8) * 8 + lane / 8, c = (lane % 8) ^ ((x >> 1) & 7);
+            const uint64_t pb = (uint64_t)(b.p + plane * b.plane + (int64_t)n0 * b.ld + k);
+            const u32x4 rb{(uint32_t)__builtin_amdgcn_readfirstlane((int)pb),
+                           (uint32_t)__builtin_amdgcn_readfirstlane((int)(pb >> 32)) & 0xffffu, 0x7fffffffu, 0x00027000u};
+            const int row = n0 + x < b.rows ? x : b.rows - 1 - n0;
+            load_to_lds(rb, (uint32_t)(row * b.ld + c * 8) * 2u, to + C::kA * 2 + q * 1024);
+        }
+        k += kBK;
+        if (++slot == C::STAGES) slot = 0;
+    }
+
+    // this wave's fragment of the slab's step ks in three parts
+    __device__ __forceinline__ void split(const uint16_t* la, int ks, u32x4 (&f)[3]) const {
+        const float* t = (const float*)la;
+        float v[8];
+        const int g = lane / 16, x = xa + lane % 16;
+        if constexpr (!C::TA) {
+            const f32x4 lo = *(const f32x4*)&t[x * kBK + (((ks * 8 + 2 * g) ^ (x & 15)) << 2)];
+            const f32x4 hi = *(const f32x4*)&t[x * kBK + (((ks * 8 + 2 * g + 1) ^ (x & 15)) << 2)];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { v[e] = lo[e]; v[4 + e] = hi[e]; }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = t[(ks * 32 + 8 * g + e) * C::BM + (((x >> 2) ^ (g << 2)) << 2) + (x & 3)];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t w[2][3];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float a = v[2 * e + h];
+                w[h][0] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a);
+                const float r = a - __uint_as_float(w[h][0] << 16);
+                w[h][1] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)r);
+                w[h][2] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(r - __uint_as_float(w[h][1] << 16)));
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q) f[q][e] = w[0][q] | (w[1][q] << 16);
+        }
+    }
+};
+
+template <class C, bool FEW = C::FEW>
+struct ProductOf { using type = Product<C>; };
+template <class C>
+struct ProductOf<C, true> { using type = FewProduct<C>; };
 
 }  // namespace mm
 }  // namespace dion

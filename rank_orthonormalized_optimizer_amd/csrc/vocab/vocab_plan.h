@@ -67,6 +67,7 @@ struct XentPlan {
     int64_t n, v, d, kp;      // tokens, vocab, width, width rounded up to 64
     int64_t np;               // tokens rounded up to 256
     int parts, dparts;
+    bool few;                 // fp32 and few tokens: the products over W read it in place
     bool wpack;               // W goes through packed planes (fp32, or a width that is no multiple of 64)
     int64_t piece, pieces;
     int64_t nvt;              // softmax partials per token (forward)
@@ -78,6 +79,7 @@ struct XentPlan {
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens)
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;   // of D, and of W's planes, per piece of the vocabulary
 constexpr int kCUs = 256;
+constexpr int64_t kFewTokens = 64;   // fp32: up to here a product over W is a stream of W (see FewProduct)
 
 inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : 128; }
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : 32; }
@@ -106,7 +108,8 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.np = ceil_div64(tokens < 1 ? 1 : tokens, 256) * 256;
     q.parts = bf16 ? 1 : 3;
     q.dparts = bf16 && dw_bf16 ? 1 : 3;
-    q.wpack = !bf16 || width % 64 != 0;
+    q.few = !bf16 && width % 4 == 0 && tokens <= kFewTokens;
+    q.wpack = !q.few && (!bf16 || width % 64 != 0);
     // bytes of scratch per vocabulary row of a piece: fp32 rows as two fp16 planes, and for the gradient three bf16 planes
     int64_t per_row = !q.wpack ? 0 : bf16 ? q.kp * 2 : q.kp * (for_grad ? 10 : 4);
     if (for_grad && q.dparts * q.np * 2 > per_row) per_row = q.dparts * q.np * 2;
@@ -118,13 +121,13 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.piece = ceil_div64(ceil_div64(all, q.pieces), 256) * 256;
     }
     q.pieces = ceil_div64(all, q.piece);
-    q.tile_z = pick_tile(q.piece, tokens, 0, 1);
+    q.tile_z = q.few ? TILE_32 : pick_tile(q.piece, tokens, 0, 1);
     q.nvt = ceil_div64(vocab, tile_m(q.tile_z));
     size_t off = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
     q.cnt = take(256);
-    if (bf16 || for_grad) q.h = take(q.parts * q.np * q.kp * 2);
-    if (!bf16) {
+    if (bf16 || for_grad || q.few) q.h = take(q.parts * q.np * q.kp * 2);
+    if (!bf16 && !q.few) {
         q.h16 = take(2 * q.np * q.kp * 2);
         q.hinv = take(q.np * 4);
         q.w16 = take(2 * q.piece * q.kp * 2);
@@ -139,7 +142,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     } else {
         const int64_t n = tokens < 1 ? 1 : tokens;
         const int64_t terms_h = bf16 ? 1 : 6, terms_w = bf16 ? q.dparts : 6;
-        q.tile_h = pick_tile(width, n, q.piece, terms_h);
+        q.tile_h = q.few ? TILE_32 : pick_tile(width, n, q.piece, terms_h);
         q.tile_w = pick_tile(width, q.piece, n, terms_w);
         q.split_h = pick_split(width, n, q.piece, terms_h, q.tile_h);
         q.split_w = pick_split(width, q.piece, n, terms_w, q.tile_w);
