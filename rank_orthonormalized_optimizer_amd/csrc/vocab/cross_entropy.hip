@@ -160,6 +160,7 @@ __device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d,
     float scale = 1.f;
     if (!BF16 && p16) {
         float top = 0.f;
+#pragma unroll 4
         for (int64_t c = lane * 8; c < kp; c += 512) {
             float v[8];
             load8<BF16, V8>(in, row * d, c, d, v);
@@ -172,6 +173,7 @@ __device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d,
         scale = row_scale(top, inverse);
         if (lane == 0) inv[to] = inverse;
     }
+#pragma unroll 4
     for (int64_t c = lane * 8; c < kp; c += 512) {
         float v[8];
         load8<BF16, V8>(in, row * d, c, d, v);
@@ -180,18 +182,18 @@ __device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d,
     }
 }
 
-constexpr int kPackRows = 16;
+constexpr int kPackRows = 8;
 
-// Sixteen tokens per workgroup, which counts the gathered rows before them itself (a read of the
-// targets from L2: fewer bytes than one row of H for all lengths up to the limit's thousands).
+// Eight tokens per workgroup, one per wave; it counts the gathered rows before them itself (a read of the
+// targets from L2: fewer bytes than its rows of H up to some thousand tokens).
 template <bool BF16, bool V8, bool GRAD>
-__global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
-    __shared__ int before[4], slot[kPackRows];
+__global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
+    __shared__ int before[8], slot[kPackRows];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int64_t t0 = (int64_t)blockIdx.x * kPackRows;
     int c = 0;
 #pragma unroll 8
-    for (int64_t i = tid; i < t0; i += 256) c += load_target(a.x, i) != a.x.ignore;
+    for (int64_t i = tid; i < t0; i += 512) c += load_target(a.x, i) != a.x.ignore;
 #pragma unroll
     for (int o = 32; o; o >>= 1) c += __shfl_xor(c, o);
     if (lane == 0) before[w] = c;
@@ -202,7 +204,9 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
         const int64_t y = row ? load_target(a.x, t) : 0;
         const bool keep = row && y != a.x.ignore;
         const uint64_t kept = __ballot(keep);
-        const int base = before[0] + before[1] + before[2] + before[3];
+        int base = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) base += before[i];
         const int j = base + __popcll(kept & ((1ull << lane) - 1));
         if (lane < kPackRows) slot[lane] = keep ? j : -1;
         if (keep) {
@@ -220,15 +224,14 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
         if (lane == 0 && blockIdx.x == gridDim.x - 1) a.cnt[0] = base + __popcll(kept);
     }
     __syncthreads();
-    for (int r = w; r < kPackRows && t0 + r < a.n; r += 4) {
-        const int64_t t = t0 + r;
-        if (slot[r] >= 0) {
-            pack_row<BF16, V8>(a.x.H, t, a.d, a.kp, a.h, a.np * a.kp, a.h16, a.np * a.kp, a.inv, slot[r], lane);
-        } else if (GRAD && a.x.dH) {
-            for (int64_t c = lane; c < a.d; c += 64) {
-                if (BF16) ((uint16_t*)a.x.dH)[t * a.d + c] = 0;
-                else ((float*)a.x.dH)[t * a.d + c] = 0.f;
-            }
+    const int64_t t = t0 + w;
+    if (t >= a.n) return;
+    if (slot[w] >= 0) {
+        pack_row<BF16, V8>(a.x.H, t, a.d, a.kp, a.h, a.np * a.kp, a.h16, a.np * a.kp, a.inv, slot[w], lane);
+    } else if (GRAD && a.x.dH) {
+        for (int64_t col = lane; col < a.d; col += 64) {
+            if (BF16) ((uint16_t*)a.x.dH)[t * a.d + col] = 0;
+            else ((float*)a.x.dH)[t * a.d + col] = 0.f;
         }
     }
 }
@@ -640,6 +643,7 @@ using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
 using H128 = mm::Config<128, 128, 2, 2, 4, true, false>;
 using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
 using W256 = mm::Config<256, 256, 2, 4, 2, true, true>;
+using W128s = mm::Config<128, 128, 2, 2, 2, true, true>;
 using W128 = mm::Config<128, 128, 2, 2, 4, true, true>;
 
 // One workgroup per tile, or as many as the chip holds, which then walk the tiles.
@@ -675,11 +679,11 @@ template <bool GRAD>
 void launch_pack(const PackArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div64(a.n, kPackRows));
     if (a.x.bf16) {
-        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<true, true, GRAD>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((pack_kernel<true, false, GRAD>), grid, dim3(256), 0, s, a);
+        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<true, true, GRAD>), grid, dim3(512), 0, s, a);
+        else hipLaunchKernelGGL((pack_kernel<true, false, GRAD>), grid, dim3(512), 0, s, a);
     } else {
-        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<false, true, GRAD>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((pack_kernel<false, false, GRAD>), grid, dim3(256), 0, s, a);
+        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<false, true, GRAD>), grid, dim3(512), 0, s, a);
+        else hipLaunchKernelGGL((pack_kernel<false, false, GRAD>), grid, dim3(512), 0, s, a);
     }
 }
 
@@ -803,6 +807,7 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);
             w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
             if (p.tile_w == TILE_256) launch_out<W256>(w, rows, s);
+            else if (p.n <= kShortTokens) launch_out<W128s>(w, rows, s);
             else launch_out<W128>(w, rows, s);
             if (w.acc) launch_join(w, rows, s);
         }

@@ -79,7 +79,11 @@ struct XentPlan {
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens)
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;   // of D, and of W's planes, per piece of the vocabulary
 constexpr int kCUs = 256;
-constexpr int64_t kFewTokens = 64;   // fp32: up to here a product over W is a stream of W (see FewProduct)
+// dW of so few tokens is a stream of writes: two workgroups per CU with smaller tiles
+constexpr int64_t kShortTokens = 128;
+// fp32: up to here the products over W read it in place (see FewProduct).  32000 x 1024 with gradients: 65 tokens 255 us
+// against 455 through planes of W in the workspace, 200 tokens 550 and 555, 256 tokens 630 and 581
+constexpr int64_t kFewTokens = 192;
 
 inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : 128; }
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : 32; }
@@ -143,7 +147,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         const int64_t n = tokens < 1 ? 1 : tokens;
         const int64_t terms_h = bf16 ? 1 : 6, terms_w = bf16 ? q.dparts : 6;
         q.tile_h = q.few ? TILE_32 : pick_tile(width, n, q.piece, terms_h);
-        q.tile_w = pick_tile(width, q.piece, n, terms_w);
+        q.tile_w = n <= kShortTokens ? TILE_128 : pick_tile(width, q.piece, n, terms_w);
         q.split_h = pick_split(width, n, q.piece, terms_h, q.tile_h);
         q.split_w = pick_split(width, q.piece, n, terms_w, q.tile_w);
         q.lg = take(q.np * 8);
