@@ -5,7 +5,7 @@ from collections import OrderedDict
 
 import torch
 
-from . import _lib
+from . import _lib, vocab
 
 _DT = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 
@@ -294,6 +294,11 @@ class MixedDion:
     (each step copies the group's weights and gradients into [b, m, n] stacks and back, since
     torch parameters are separate tensors); every other tensor gets element-wise state.
     ``step(grads)`` takes the gradients in the same order.
+
+    The vocabulary matrices among the parameters (an embedding table, an output head, or one
+    [vocab, width] matrix that is both) can be used through the optimizer, which then gathers their
+    gradients itself: ``lookup`` and ``lookup_grad``, ``head_loss``.  All contributions since the last
+    step add up (tied weights, microbatches), and ``step`` takes them where ``grads`` holds None.
     """
 
     def __init__(self, params, *, lr: float = 0.01, mu: float = 0.95, rank_fraction: float = 0.25,
@@ -317,10 +322,56 @@ class MixedDion:
         self.state = {i: (torch.zeros(self.params[i].numel(), dtype=torch.float32, device=self.params[i].device),
                           torch.zeros(self.params[i].numel(), dtype=torch.float32, device=self.params[i].device)
                           if other == "adamw" else None) for i in self.rest}
+        self.gathered = {}      # parameter index -> its gradient buffer
+        self.pending = set()    # those whose buffer holds contributions since the last step
+
+    def _gather(self, i: int):
+        """The gradient buffer of parameter i, and whether a contribution adds to what it holds."""
+        if i not in self.gathered:
+            self.gathered[i] = torch.empty_like(self.params[i])
+        return self.gathered[i], i in self.pending
+
+    @torch.no_grad()
+    def lookup(self, i: int, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+        """Rows ``scale * params[i][ids]`` (embedding_)."""
+        return vocab.embedding_(ids, self.params[i], scale)
+
+    @torch.no_grad()
+    def lookup_grad(self, i: int, ids: torch.Tensor, dY: torch.Tensor, scale: float = 1.0, *, padding_id: int = -1) -> None:
+        """Add the table gradient of ``lookup(i, ids, scale)`` for the gradient ``dY`` of its rows (embedding_grad_)."""
+        dW, add = self._gather(i)
+        vocab.embedding_grad_(ids, dY, dW, scale, padding_id=padding_id, accumulate=add)
+        self.pending.add(i)
+
+    @torch.no_grad()
+    def head_loss(self, i: int, H: torch.Tensor, targets: torch.Tensor, grad: torch.Tensor | None = None, *,
+                  ignore_index: int = -100):
+        """Cross entropy of the logits ``H params[i]^T`` (linear_cross_entropy_) and its gradients.
+
+        ``grad``: float32, the loss's gradient per token or one element for all (default: the mean over
+        the tokens that are not ignored).  Returns (per-token loss, dH) and adds the head's gradient.
+        """
+        W = self.params[i]
+        loss, lse = vocab.linear_cross_entropy_(H, W, targets, ignore_index=ignore_index)
+        if grad is None:
+            grad = (targets != ignore_index).sum().clamp_(min=1).to(torch.float32).reciprocal_().reshape(1)
+        dH = torch.empty_like(H)
+        dW, add = self._gather(i)
+        vocab.linear_cross_entropy_grad_(H, W, targets, lse, grad, dH, dW, ignore_index=ignore_index, accumulate=add)
+        self.pending.add(i)
+        return loss, dH
 
     @torch.no_grad()
     def step(self, grads) -> None:
         grads = list(grads)
+        for i, g in enumerate(grads):
+            if g is None and i not in self.pending:
+                raise ValueError(f"no gradient for parameter {i}: none given and none gathered")
+            if g is not None and i in self.pending:
+                raise ValueError(f"parameter {i} has a gathered gradient; pass None for it")
+            if g is None:
+                grads[i] = self.gathered[i]
+        self.pending.clear()
         self.t += 1
         for idx, st in self.groups:
             X = torch.stack([self.params[i] for i in idx]).contiguous()

@@ -213,3 +213,340 @@ def test_loss_gradient(cuda, tokens, vocab, width, dt, wdt, accumulate):
     if wdt == dt or dt == "f32":
         assert torch.equal(dH2, dH.t)
     assert torch.equal(dW2, dW.t)
+
+
+# sizes that go through several pieces of the vocabulary: D's bytes (many tokens), W's planes (wide fp32), D of few tokens
+@pytest.mark.parametrize("tokens,vocab,width,dt", [(16384, 6000, 64, "f32"), (65536, 5000, 32, "bf16"), (200, 14000, 4096, "f32"),
+                                                   (3, 400000, 8, "f32"), (193, 9000, 68, "f32"), (192, 9000, 68, "f32")])
+def test_pieces_of_the_vocabulary(cuda, tokens, vocab, width, dt):
+    import rank_orthonormalized_optimizer_amd as dion
+    g = gen(cuda, tokens, vocab, width, 3)
+    H, W, y = head_inputs(g, tokens, vocab, width, DT[dt], cuda)
+    grad = torch.rand(tokens, generator=g, device=cuda)
+    loss, lse = dion.linear_cross_entropy_(H, W, y)
+    dH, dW = Guarded(H.shape, DT[dt], cuda), Guarded(W.shape, DT[dt], cuda)
+    ws = dirty(dion.linear_cross_entropy_workspace_for(tokens, vocab, width, cuda, DT[dt], for_grad=True))
+    dion.linear_cross_entropy_grad_(H, W, y, lse, grad, dH.t, dW.t, workspace=ws)
+    want = Head(H, W, y, grad=grad)
+    close(loss, want.loss, want.loss_bound, "loss")
+    close(dH.check(), want.dH, want.dH_bound, "dH")
+    close(dW.check(), want.dW, want.dW_bound, "dW")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [20, 300])
+def test_ignored_and_bad_targets(cuda, tokens, dt):
+    """All ignored: nothing; another ignore_index; targets out of range make NaN of their own loss and row, and of dW."""
+    import rank_orthonormalized_optimizer_amd as dion
+    g = gen(cuda, tokens, 4)
+    H, W, y = head_inputs(g, tokens, 50, 40, DT[dt], cuda, ignored=0)
+    one = torch.ones(1, device=cuda)
+    none = torch.full_like(y, -100)
+    loss, lse = dion.linear_cross_entropy_(H, W, none)
+    assert not loss.any() and not lse.any()
+    dH, dW = torch.full_like(H, 3), torch.full_like(W, 3)
+    dion.linear_cross_entropy_grad_(H, W, none, lse, one, dH, dW, accumulate=True)
+    assert not dH.any() and (dW == 3).all()
+    dion.linear_cross_entropy_grad_(H, W, none, lse, one, dH, dW)
+    assert not dW.any()
+    # the targets of id 0 ignored, as padding
+    y[::3] = 0
+    loss, lse = dion.linear_cross_entropy_(H, W, y, ignore_index=0)
+    dion.linear_cross_entropy_grad_(H, W, y, lse, one, dH, dW, ignore_index=0)
+    want = Head(H, W, y, ignore=0, grad=one)
+    close(loss, want.loss, want.loss_bound, "loss")
+    close(dH, want.dH, want.dH_bound, "dH")
+    close(dW, want.dW, want.dW_bound, "dW")
+    y[1], y[2] = 50, -7
+    y[4] = 1 << 40
+    loss, lse = dion.linear_cross_entropy_(H, W, y, ignore_index=0)
+    dion.linear_cross_entropy_grad_(H, W, y, lse, one, dH, dW, ignore_index=0)
+    want = Head(H, W, y, ignore=0, grad=one)
+    close(loss, want.loss, want.loss_bound, "loss")
+    close(lse, want.lse, want.lse_bound, "lse")
+    close(dH, want.dH, want.dH_bound, "dH")
+    assert torch.isnan(dW).all()
+
+
+@pytest.mark.parametrize("tokens", [30, 400])
+def test_fp32_rows_of_any_scale(cuda, tokens):
+    """Rows from 2^-60 up, zero rows among them: fp32 logits stay accurate relative to each row's own terms."""
+    import rank_orthonormalized_optimizer_amd as dion
+    g = gen(cuda, tokens, 5)
+    H, W, y = head_inputs(g, tokens, 700, 136, F32, cuda)
+    H *= torch.exp2(torch.randint(-60, 1, (tokens, 1), generator=g, device=cuda).float())
+    W *= torch.exp2(torch.randint(-40, 1, (700, 1), generator=g, device=cuda).float())
+    H[3], W[5] = 0, 0
+    grad = torch.ones(1, device=cuda)
+    loss, lse = dion.linear_cross_entropy_(H, W, y)
+    dH, dW = torch.empty_like(H), torch.empty_like(W)
+    dion.linear_cross_entropy_grad_(H, W, y, lse, grad, dH, dW)
+    want = Head(H, W, y, grad=grad)
+    close(loss, want.loss, want.loss_bound, "loss")
+    close(dH, want.dH, want.dH_bound, "dH")
+    close(dW, want.dW, want.dW_bound, "dW")
+
+
+@pytest.mark.parametrize("tokens", [24, 260])
+def test_loss_gradient_matches_differences(cuda, tokens):
+    """Central differences of the summed loss along a direction in H and W.  With a = the largest change of a logit per
+    unit step, the third derivative of a token's loss is at most (2 a)^3: the difference is off by eps^2 (2 a)^3 / 6,
+    plus the two losses' own errors over 2 eps."""
+    import rank_orthonormalized_optimizer_amd as dion
+    g = gen(cuda, tokens, 6)
+    H, W, y = head_inputs(g, tokens, 300, 64, F32, cuda)
+    for which in ("H", "W"):
+        E = torch.randn((H if which == "H" else W).shape, generator=g, device=cuda) * 0.05
+        eps = 0.0625
+        X = H if which == "H" else W
+
+        def f(sign):
+            Z = X + sign * eps * E
+            a, b = (Z, W) if which == "H" else (H, Z)
+            want = Head(a, b, y)
+            return dion.linear_cross_entropy_(a, b, y)[0].double().sum(), want.loss_bound.sum()
+
+        (up, e1), (down, e2) = f(1), f(-1)
+        loss, lse = dion.linear_cross_entropy_(H, W, y)
+        dH, dW = torch.empty_like(H), torch.empty_like(W)
+        dion.linear_cross_entropy_grad_(H, W, y, lse, torch.ones(1, device=cuda), dH, dW)
+        got = ((dH if which == "H" else dW).double() * E.double()).sum()
+        rate = (E.double() @ W.double().t() if which == "H" else H.double() @ E.double().t()).abs().amax(1)
+        bound = (eps ** 2 * (2 * rate) ** 3 / 6).sum() + (e1 + e2) / (2 * eps)
+        exact = Head(H, W, y, grad=torch.ones(1, device=cuda))
+        bound = bound + ((exact.dH_bound if which == "H" else exact.dW_bound) * E.double().abs()).sum()
+        # X + eps E is rounded to fp32 once: half a step of X times the gradient, over 2 eps
+        slope = (exact.dH if which == "H" else exact.dW).abs()
+        bound = bound + 2 * (2.0 ** -24 * (X.double().abs() + eps * E.double().abs()) * slope).sum() / (2 * eps)
+        assert abs(float((up - down) / (2 * eps) - got)) <= float(bound)
+
+
+def test_offsets_past_32_bits(cuda):
+    """A table of 2.46e9 elements: its last rows looked up, its gradient written, its logits formed."""
+    import rank_orthonormalized_optimizer_amd as dion
+    vocab, width = 600001, 4096
+    g = gen(cuda, 7)
+    W = torch.empty(vocab, width, dtype=BF16, device=cuda)
+    for a in range(0, vocab, 100000):
+        W[a:a + 100000] = torch.randn(W[a:a + 100000].shape, generator=g, device=cuda) / 64
+    ids = torch.tensor([vocab - 1, 0, vocab - 2, 524288, vocab - 1, 524287], device=cuda)
+    assert torch.equal(dion.embedding_(ids, W, 2.0), W[ids] * 2)
+    dY = torch.randn(6, width, generator=g, device=cuda).to(BF16)
+    dW = torch.full_like(W, 5)
+    dion.embedding_grad_(ids, dY, dW)
+    rows = torch.zeros(vocab, dtype=torch.bool, device=cuda)
+    rows[ids] = True
+    assert not dW[~rows].any()
+    want = dY.double()
+    want[0] += want[4]
+    for k in (0, 1, 2, 3, 5):
+        assert torch.equal(dW[ids[k]], want[k].to(BF16))
+    H = torch.randn(6, width, generator=g, device=cuda).to(BF16)
+    loss, lse = dion.linear_cross_entropy_(H, W, ids)
+    z = torch.cat([H.double() @ W[a:a + 50000].double().t() for a in range(0, vocab, 50000)], 1)
+    true = torch.logsumexp(z, 1)
+    size = torch.cat([H.double().abs() @ W[a:a + 50000].double().abs().t() for a in range(0, vocab, 50000)], 1).amax(1)
+    bound = 2 * (2 * width + 12) * 2.0 ** -24 * size + (96 + vocab / 64 + 8) * 2.0 ** -24 + 4 * 2.0 ** -24 * true
+    close(lse, true, bound, "lse")
+    close(loss, true - z[torch.arange(6, device=cuda), ids], bound, "loss")
+    dH = torch.empty_like(H)
+    dion.linear_cross_entropy_grad_(H, W, ids, lse, torch.ones(1, device=cuda), dH, dW)
+    D = torch.exp(z - true[:, None])
+    D[torch.arange(6, device=cuda), ids] -= 1
+    for a in (0, 524280, vocab - 8):
+        part = D[:, a:a + 8].t() @ H.double()
+        e = (2 * (2 * width + 12) * 2.0 ** -24 * size.max() + vocab / 64 * 2.0 ** -24 + 2.0 ** -8 + 2.0 ** -16)
+        close(dW[a:a + 8], part, e * (torch.exp(z - true[:, None])[:, a:a + 8].t() + D[:, a:a + 8].abs().t()) @ H.double().abs()
+              + 2.0 ** -8 * part.abs(), "dW")
+
+
+# ---------------------------------------------------------------------------- together
+def _everything(dion, s, out):
+    """Lookup, loss, its gradients, table gradient on top of the head's: one tied step."""
+    h = dion.embedding_(s["ids"], s["W"], 4.0, out["h"])
+    dion.linear_cross_entropy_(h, s["W"], s["y"], loss=out["loss"], lse=out["lse"], workspace=out["w1"])
+    dion.linear_cross_entropy_grad_(h, s["W"], s["y"], out["lse"], s["g"], out["dH"], out["dW"], workspace=out["w2"])
+    dion.embedding_grad_(s["ids"], out["dH"], out["dW"], 4.0, padding_id=0, accumulate=True, workspace=out["w3"])
+
+
+def _state(dion, cuda, key, tokens, vocab, width, dt):
+    g = gen(cuda, 8, key)
+    s = {"W": (torch.randn(vocab, width, generator=g, device=cuda) / 8).to(dt), "ids": skewed_ids(g, tokens, vocab, cuda),
+         "y": skewed_ids(g, tokens, vocab, cuda), "g": torch.full((1,), 1.0 / tokens, device=cuda)}
+    s["y"][::5] = -100
+    return s
+
+
+def _outputs(dion, cuda, tokens, vocab, width, dt):
+    e = lambda *shape, t=dt: torch.empty(shape, dtype=t, device=cuda)   # noqa: E731
+    return {"h": e(tokens, width), "loss": e(tokens, t=F32), "lse": e(tokens, t=F32), "dH": e(tokens, width), "dW": e(vocab, width),
+            "w1": dion.linear_cross_entropy_workspace_for(tokens, vocab, width, cuda, dt),
+            "w2": dion.linear_cross_entropy_workspace_for(tokens, vocab, width, cuda, dt, for_grad=True),
+            "w3": dion.embedding_grad_workspace_for(tokens, vocab, width, cuda)}
+
+
+RESULTS = ("h", "loss", "lse", "dH", "dW")
+
+
+@pytest.mark.parametrize("tokens,vocab,width,dt", [(40, 300, 64, BF16), (700, 1000, 128, F32), (20000, 500, 72, BF16)])
+def test_graph_replays_match_eager_calls(cuda, tokens, vocab, width, dt):
+    """One captured step, replayed on new inputs with eager work and synchronizations between the replays."""
+    import rank_orthonormalized_optimizer_amd as dion
+    states = [_state(dion, cuda, k, tokens, vocab, width, dt) for k in range(3)]
+    want = []
+    for s in states:
+        out = _outputs(dion, cuda, tokens, vocab, width, dt)
+        _everything(dion, s, out)
+        torch.cuda.synchronize()
+        want.append({k: out[k].clone() for k in RESULTS})
+    held = {k: v.clone() for k, v in states[0].items()}
+    out = _outputs(dion, cuda, tokens, vocab, width, dt)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _everything(dion, held, out)
+    for k in (1, 0, 2, 1):
+        for name in held:
+            held[name].copy_(states[k][name])
+        for name in ("w1", "w2", "w3"):
+            dirty(out[name])
+        graph.replay()
+        eager = _outputs(dion, cuda, tokens, vocab, width, dt)
+        _everything(dion, states[(k + 1) % 3], eager)
+        torch.cuda.synchronize()
+        for name in RESULTS:
+            assert torch.equal(out[name], want[k][name]), f"replay {k}: {name}"
+            assert torch.equal(eager[name], want[(k + 1) % 3][name]), f"beside replay {k}: {name}"
+
+
+def test_calls_on_two_streams_at_once(cuda):
+    """Calls on side streams with scratch allocated inside them, beside each other and beside work on the current stream."""
+    import rank_orthonormalized_optimizer_amd as dion
+    tokens, vocab, width = 600, 4000, 256
+    states = [_state(dion, cuda, k, tokens, vocab, width, BF16) for k in range(2)]
+
+    def run(s, stream=None):
+        loss, lse = dion.linear_cross_entropy_(s["H"], s["W"], s["y"], stream=stream)
+        dH, dW = torch.empty_like(s["H"]), torch.empty_like(s["W"])
+        dion.linear_cross_entropy_grad_(s["H"], s["W"], s["y"], lse, s["g"], dH, dW, stream=stream)
+        dion.embedding_grad_(s["ids"], dH, dW, accumulate=True, stream=stream)
+        return loss, lse, dH, dW, dion.embedding_(s["ids"], dW, stream=stream)
+
+    for s in states:
+        s["H"] = dion.embedding_(s["ids"], s["W"])
+    want = [run(s) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(4):
+        got = [run(s, st) for s, st in zip(states, streams)]
+        here = run(states[0])
+        torch.cuda.synchronize()
+        for a, b in zip(got + [here], want + [want[0]]):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_refusals_on_the_gpu(cuda):
+    import rank_orthonormalized_optimizer_amd as dion
+    W, H = torch.zeros(10, 16, device=cuda), torch.zeros(4, 16, device=cuda)
+    ids = torch.zeros(4, dtype=torch.int64, device=cuda)
+    one = torch.ones(1, device=cuda)
+    with pytest.raises(ValueError, match="contiguous"):
+        dion.embedding_(ids, W[:, ::2])
+    with pytest.raises(TypeError, match="dtype"):
+        dion.embedding_(ids.float(), W)
+    with pytest.raises(TypeError, match="dtype"):
+        dion.embedding_(ids, W.double())
+    with pytest.raises(ValueError, match="shape"):
+        dion.embedding_(ids, W, out=torch.empty(4, 17, device=cuda))
+    with pytest.raises(ValueError, match="matrix"):
+        dion.embedding_(ids, W[0])
+    with pytest.raises(dion.DionError) as e:
+        dion.embedding_(ids, W.view(-1)[4:148].view(9, 16))     # 16 bytes in: accepted alignment
+        dion.embedding_(ids, W.view(-1)[1:145].view(9, 16))
+    assert e.value.status == -5
+    with pytest.raises(ValueError, match="shape"):
+        dion.embedding_grad_(ids, H[:3], W)
+    with pytest.raises(TypeError, match="dtype"):
+        dion.linear_cross_entropy_(H.to(BF16), W, ids)
+    with pytest.raises(ValueError, match="shape"):
+        dion.linear_cross_entropy_(H, W, ids[:3])
+    with pytest.raises(ValueError, match="CPU|cpu|GPU"):
+        dion.linear_cross_entropy_(H, W, ids.cpu())
+    loss, lse = dion.linear_cross_entropy_(H, W, ids)
+    with pytest.raises(ValueError, match="one element"):
+        dion.linear_cross_entropy_grad_(H, W, ids, lse, torch.ones(2, device=cuda), torch.empty_like(H))
+    with pytest.raises(dion.DionError) as e:
+        dion.linear_cross_entropy_grad_(H, W, ids, lse, one)
+    assert e.value.status == -1
+    with pytest.raises(dion.DionError) as e:
+        dion.linear_cross_entropy_grad_(H, W, ids, lse, one, H)
+    assert e.value.status == -6
+    with pytest.raises(dion.DionError) as e:
+        dion.embedding_grad_(ids, H, W, workspace=torch.empty(256, dtype=torch.uint8, device=cuda))
+    assert e.value.status == -7
+
+
+def test_empty_batches(cuda):
+    import rank_orthonormalized_optimizer_amd as dion
+    W, ids = torch.ones(9, 24, device=cuda), torch.zeros(0, 3, dtype=torch.int32, device=cuda)
+    H = dion.embedding_(ids, W)
+    assert H.shape == (0, 3, 24)
+    loss, lse = dion.linear_cross_entropy_(H, W, ids)
+    assert loss.shape == lse.shape == (0, 3)
+    dW = torch.ones_like(W)
+    dion.linear_cross_entropy_grad_(H, W, ids, lse, torch.ones(1, device=cuda), torch.empty_like(H), dW, accumulate=True)
+    dion.embedding_grad_(ids, H, dW, accumulate=True)
+    assert (dW == 1).all()
+    dion.linear_cross_entropy_grad_(H, W, ids, lse, torch.ones(1, device=cuda), None, dW)
+    assert not dW.any()
+    dW.fill_(1)
+    dion.embedding_grad_(ids, H, dW)
+    assert not dW.any()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("other", ["adamw", "lion"])
+def test_mixed_dion_trains_a_tied_model(cuda, dt, other):
+    """One tied matrix and one hidden layer through MixedDion, two microbatches a step: the gathered gradient is the one of
+    the formula, and step() with it equals step() with the same gradient given."""
+    import rank_orthonormalized_optimizer_amd as dion
+    g = gen(cuda, 9)
+    vocab, width, scale = 300, 64, 8.0
+    table_ = (torch.randn(vocab, width, generator=g, device=cuda) / 8).to(dt)
+    layer = (torch.randn(width, width, generator=g, device=cuda) / 8).to(dt)
+    bias = torch.zeros(width, dtype=dt, device=cuda)
+    a = dion.MixedDion([table_.clone(), layer.clone(), bias.clone()], other=other)
+    b = dion.MixedDion([table_.clone(), layer.clone(), bias.clone()], other=other)
+    batches = [(skewed_ids(g, 48, vocab, cuda).view(4, 12), skewed_ids(g, 48, vocab, cuda).view(4, 12)) for _ in range(4)]
+    for step in range(2):
+        W, L, c = (p.detach().double() for p in a.params)
+        dL, dc = torch.zeros_like(a.params[1]), torch.zeros_like(a.params[2])
+        Wd = W.clone().requires_grad_()
+        for ids, y in batches[2 * step:2 * step + 2]:
+            y = torch.where(y % 7 == 0, -100, y)
+            h = a.lookup(0, ids, scale)
+            H = torch.addmm(a.params[2], h.view(-1, width), a.params[1]).view(h.shape)
+            loss, dH = a.head_loss(0, H, y)
+            dh = (dH.view(-1, width) @ a.params[1].t().contiguous()).view(h.shape)
+            dL += h.view(-1, width).t().contiguous() @ dH.view(-1, width)
+            dc += dH.sum((0, 1))
+            a.lookup_grad(0, ids, dh, scale)
+            z = ((Wd[ids] * scale) @ L + c) @ Wd.t()
+            ref = torch.nn.functional.cross_entropy(z.view(-1, vocab), y.reshape(-1), ignore_index=-100)
+            ref.backward()
+            # the hidden states are rounded to dt between the operators: a few roundings of the loss's size
+            counted = loss[y != -100].double().mean()
+            assert abs(float(counted - ref)) <= 16 * torch.finfo(dt).eps * float(ref)
+        got = a.gathered[0].double()
+        # each of the at most 64 roundings between table and loss gives a relative 2^-24 or 2^-8 of the gradient's own scale
+        assert float((got - Wd.grad).norm()) <= 64 * torch.finfo(dt).eps / 2 * float(Wd.grad.norm())
+        given = [a.gathered[0].clone(), dL, dc]
+        a.step([None, dL, dc])
+        b.step(given)
+        torch.cuda.synchronize()
+        for p, q in zip(a.params, b.params):
+            assert torch.equal(p, q)
+    with pytest.raises(ValueError, match="no gradient"):
+        a.step([None, dL, dc])
+    a.head_loss(0, H, y)
+    with pytest.raises(ValueError, match="gathered"):
+        a.step(given)
