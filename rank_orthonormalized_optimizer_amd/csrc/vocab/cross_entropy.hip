@@ -214,7 +214,8 @@ __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
             a.map[j] = (int)t;
             a.tgt[j] = in ? (int)y : -1;
             if (GRAD) {
-                const float g = a.x.grad[a.x.grad_n == 1 ? 0 : t];
+                // one factor for all tokens is applied to the outputs: in D it would be rounded the same way everywhere
+                const float g = a.x.grad_n == 1 ? 1.f : a.x.grad[t];
                 a.lg[j] = float2{a.x.lse[t], in ? g : __uint_as_float(0x7fc00000u)};
             }
         } else if (row && !GRAD) {
@@ -486,16 +487,17 @@ struct OutArgs {
     mm::Operand a, b;
     mm::Segments seg;
     const int* cnt;
-    int d;                 // output columns (the matrix core's rows)
+    int d, dp;             // output columns (the matrix core's rows), and rounded up to four
     int rows;              // output rows, or -1: the gathered tokens
     int k;                 // reduction length, or -1: the gathered tokens
     int split, k_per;      // slices of the reduction and their length
-    float* acc;            // fp32 [split][acc_rows][d], or null: straight to out
+    float* acc;            // fp32 [split][acc_rows][dp], or null: straight to out
     int64_t acc_rows;
     int add;               // add to acc
     void* out;
     const int* map;        // output row of a gathered token, or null
     int out_bf16, accumulate;
+    const float* factor;   // of the outputs, or null
     // dH in bf16: what the rounding of D left of the target's element, times the target's row of W
     const float* rest;     // or null
     const int* tgt;
@@ -515,6 +517,11 @@ __device__ __forceinline__ void store_out(const OutArgs& a, int64_t r, int c, in
         } else {
             for (int e = 0; e < n; ++e) v[e] = fmaf(left, up16(w[e]), v[e]);
         }
+    }
+    if (a.factor) {
+        const float f = *a.factor;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= f;
     }
     const int64_t at = (a.map ? a.map[r] : r) * (int64_t)a.d + c;
     if (a.d % 4 == 0) {
@@ -580,14 +587,11 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
                 const int m = m0 + mul.xa + 16 * i + 4 * (mul.lane / 16);
                 if (m >= a.d) continue;
                 float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                const int64_t at = (sl * a.acc_rows + n) * a.d + m;
                 if (!a.acc) {
                     store_out(a, n, m, a.d - m < 4 ? a.d - m : 4, v);
-                } else if (a.d % 4 == 0) {
-                    f32x4* p = (f32x4*)(a.acc + at);
-                    *p = a.add ? *p + acc[i][j] : acc[i][j];
                 } else {
-                    for (int e = 0; e < 4 && m + e < a.d; ++e) a.acc[at + e] = (a.add ? a.acc[at + e] : 0.f) + v[e];
+                    f32x4* p = (f32x4*)(a.acc + (sl * a.acc_rows + n) * a.dp + m);
+                    *p = a.add ? *p + acc[i][j] : acc[i][j];
                 }
             }
         }
@@ -595,25 +599,25 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
     }
 }
 
-// The slices' sums, rounded to the output.
+// The slices' sums, rounded to the output: four columns per group of G lanes, which share the slices (many slices come
+// with few outputs).
+template <int G>
 __global__ __launch_bounds__(256) void join_kernel(OutArgs a) {
-    const int rows = a.rows < 0 ? a.cnt[0] : a.rows, nc = (a.d + 3) / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int rows = a.rows < 0 ? a.cnt[0] : a.rows, nc = a.dp / 4;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;
+    const int lane = threadIdx.x % G;
     if (i >= (int64_t)rows * nc) return;
     const int64_t r = i / nc;
     const int c = (int)(i - r * nc) * 4, n = a.d - c < 4 ? a.d - c : 4;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.split; ++s) {
-        const float* p = a.acc + (s * a.acc_rows + r) * a.d + c;
-        if (a.d % 4 == 0) {
-            const f32x4 w = *(const f32x4*)p;
+    f32x4 sum{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = lane; s < a.split; s += G) sum += *(const f32x4*)(a.acc + (s * a.acc_rows + r) * a.dp + c);
+    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += w[e];
-        } else {
-            for (int e = 0; e < n; ++e) v[e] += p[e];
-        }
-    }
-    store_out(a, r, c, n, v);
+    for (int o = G / 2; o; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o);
+    if (lane == 0) store_out(a, r, c, n, v);
 }
 
 // plane pairs (A's part, B's part), smallest products first
@@ -632,6 +636,8 @@ mm::Segments segments(int pa, int pb) {
 using Z256 = mm::Config<256, 256, 2, 4, 2, false, false>;
 using Z128 = mm::Config<128, 128, 2, 2, 4, false, false>;
 using Z32 = mm::Config<128, 32, 4, 1, 4, false, false>;
+using Z64 = mm::Config<64, 64, 2, 2, 8, false, false>;
+using F64 = mm::Config<64, 64, 2, 2, 8, false, false, true>;
 using F256 = mm::Config<256, 256, 2, 4, 2, false, false, true>;
 using F128 = mm::Config<128, 128, 2, 2, 4, false, false, true>;
 using F32 = mm::Config<128, 32, 4, 1, 4, false, false, true>;
@@ -658,20 +664,21 @@ void launch_logits(const LogitArgs& a, int64_t n, hipStream_t s) {
     hipLaunchKernelGGL((logit_kernel<C, EPI>), walkers<C>(t), dim3(C::THREADS), 0, s, a);
 }
 
-template <class C256, class C128, class C32, int EPI>
+template <class C256, class C128, class C64, class C32, int EPI>
 void launch_logits(const LogitArgs& a, int tile, int64_t n, hipStream_t s) {
     if (tile == TILE_256) launch_logits<C256, EPI>(a, n, s);
     else if (tile == TILE_128) launch_logits<C128, EPI>(a, n, s);
+    else if (tile == TILE_64) launch_logits<C64, EPI>(a, n, s);
     else launch_logits<C32, EPI>(a, n, s);
 }
 
 template <int EPI>
 void launch_logits(const LogitArgs& a, const XentPlan& p, hipStream_t s) {
-    if (p.parts == 1) launch_logits<Z256, Z128, Z32, EPI>(a, p.tile_z, p.n, s);
+    if (p.parts == 1) launch_logits<Z256, Z128, Z64, Z32, EPI>(a, p.tile_z, p.n, s);
     else if constexpr (EPI != EPI_D1) {   // fp32: D in three parts
         if (p.few && p.n <= 32) launch_logits<P32, EPI>(a, p.n, s);
         else if (p.few) launch_logits<P64, EPI>(a, p.n, s);
-        else launch_logits<F256, F128, F32, EPI>(a, p.tile_z, p.n, s);
+        else launch_logits<F256, F128, F64, F32, EPI>(a, p.tile_z, p.n, s);
     }
 }
 
@@ -734,7 +741,9 @@ void launch_out(const OutArgs& a, int64_t rows, hipStream_t s) {
 }
 
 void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div64(rows * ((a.d + 3) / 4), 256)), dim3(256), 0, s, a);
+    const int64_t n = rows * (a.dp / 4);
+    if (a.split >= 8) hipLaunchKernelGGL((join_kernel<8>), dim3((unsigned)ceil_div64(n * 8, 256)), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((join_kernel<1>), dim3((unsigned)ceil_div64(n, 256)), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -773,12 +782,13 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
     z.dl = (uint16_t*)(ws + p.dl); z.rest = (float*)(ws + p.rest); z.np = p.np; z.piece = p.piece;
     const mm::Operand dl{z.dl, p.np * p.piece, p.piece, 0};
     OutArgs h{};
-    h.cnt = pk.cnt; h.d = (int)p.d; h.rows = -1; h.split = (int)p.split_h; h.map = pk.map; h.out = x.dH; h.out_bf16 = x.bf16;
+    const float* factor = x.grad_n == 1 ? x.grad : nullptr;
+    h.cnt = pk.cnt; h.d = (int)p.d; h.dp = (int)p.dp; h.factor = factor; h.rows = -1; h.split = (int)p.split_h; h.map = pk.map; h.out = x.dH; h.out_bf16 = x.bf16;
     h.acc = p.pieces > 1 || p.split_h > 1 ? (float*)(ws + p.acc_h) : nullptr;
     h.acc_rows = p.np;
     if (x.bf16) { h.rest = z.rest; h.tgt = pk.tgt; h.w = (const uint16_t*)x.W; }
     OutArgs w{};
-    w.cnt = pk.cnt; w.d = (int)p.d; w.k = -1; w.split = (int)p.split_w; w.out_bf16 = x.dw_bf16; w.accumulate = x.accumulate;
+    w.cnt = pk.cnt; w.d = (int)p.d; w.dp = (int)p.dp; w.factor = factor; w.k = -1; w.split = (int)p.split_w; w.out_bf16 = x.dw_bf16; w.accumulate = x.accumulate;
     w.acc = p.split_w > 1 ? (float*)(ws + p.acc_w) : nullptr;
     w.acc_rows = p.piece;
     for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {

@@ -64,7 +64,7 @@ int run_embedding_grad(const EmbedArgs& a, const EmbedGradPlan& p, char* ws, voi
 // Layout of a cross entropy call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32, whose logits take two fp16 parts);
 // dparts: parts of D.  The vocabulary goes in `pieces` of `piece` rows (a multiple of 256).
 struct XentPlan {
-    int64_t n, v, d, kp;      // tokens, vocab, width, width rounded up to 64
+    int64_t n, v, d, kp, dp;  // tokens, vocab, width, width rounded up to 64 and to 4
     int64_t np;               // tokens rounded up to 256
     int parts, dparts;
     bool few;                 // fp32 and few tokens: the products over W read it in place
@@ -76,32 +76,39 @@ struct XentPlan {
     size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, w, w16, winv, dl, rest, acc_h, acc_w, total;
 };
 
-enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens)
+enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens), 64 x 64
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;   // of D, and of W's planes, per piece of the vocabulary
 constexpr int kCUs = 256;
 // dW of so few tokens is a stream of writes: two workgroups per CU with smaller tiles
 constexpr int64_t kShortTokens = 128;
-// fp32: up to here the products over W read it in place (see FewProduct).  32000 x 1024 with gradients: 65 tokens 255 us
-// against 455 through planes of W in the workspace, 200 tokens 550 and 555, 256 tokens 630 and 581
-constexpr int64_t kFewTokens = 192;
+// fp32: up to so many tokens the products over W read it in place (see FewProduct), if W has tiles for half the CUs.
+// 32000 x 1024 with gradients: 65 tokens 255 us against 455 through planes of W in the workspace, 128 tokens 367 and
+// 483, 200 tokens 550 and 555; 100544 x 2624: 164 tokens 3.4 ms against 2.4
+constexpr int64_t kFewTokens = 128, kFewVocab = 16384;
 
-inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : 128; }
-inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : 32; }
+inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : t == TILE_64 ? 64 : 128; }
+inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : t == TILE_64 ? 64 : 32; }
 inline int64_t tiles(int64_t m, int64_t n, int t) { return ceil_div64(m, tile_m(t)) * ceil_div64(n, tile_n(t)); }
 // Slices of a reduction of length k (`terms` part products of it) so that an output of m x n fills the chip, each of
-// eight slabs of 64 at least: a slice costs a pass over the output.
+// 24 slabs of 64 at least (8 for the narrow tiles, whose slabs are shorter): a slice costs a pass over the output.
 inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int64_t terms, int tile) {
     int64_t s = kCUs / tiles(m, n, tile);
-    const int64_t most = ceil_div64(k, 64) * terms / 8;
+    const int64_t most = ceil_div64(k, 64) * terms / (tile == TILE_32 ? 8 : 24);
     if (s > most) s = most;
     if (s > ceil_div64(k, 64)) s = ceil_div64(k, 64);
     return s < 1 ? 1 : s;
 }
 // The largest tile, which reads each operand least often, that still gives half the CUs a workgroup, if the
-// reduction is long enough by slices of it (k = 0: the reduction is not sliced).
+// reduction is long enough by slices of it.
 inline int pick_tile(int64_t m, int64_t n, int64_t k, int64_t terms) {
     if (n <= 32) return TILE_32;
-    return tiles(m, n, TILE_256) * (k ? pick_split(m, n, k, terms, TILE_256) : 1) >= kCUs / 2 ? TILE_256 : TILE_128;
+    return tiles(m, n, TILE_256) * pick_split(m, n, k, terms, TILE_256) >= kCUs / 2 ? TILE_256 : TILE_128;
+}
+// The logits' reduction is not sliced: where even 128 x 128 tiles leave half the CUs idle, 64 x 64 ones, whose ring of
+// eight slabs also hides more of the loads' latency.
+inline int pick_logit_tile(int64_t m, int64_t n) {
+    if (n <= 32) return TILE_32;
+    return tiles(m, n, TILE_256) >= kCUs / 2 ? TILE_256 : tiles(m, n, TILE_128) >= kCUs / 2 ? TILE_128 : TILE_64;
 }
 
 inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf16, int dw_bf16, int for_grad,
@@ -109,10 +116,11 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     XentPlan q{};
     q.n = tokens; q.v = vocab; q.d = width;
     q.kp = ceil_div64(width, 64) * 64;
+    q.dp = ceil_div64(width, 4) * 4;
     q.np = ceil_div64(tokens < 1 ? 1 : tokens, 256) * 256;
     q.parts = bf16 ? 1 : 3;
     q.dparts = bf16 && dw_bf16 ? 1 : 3;
-    q.few = !bf16 && width % 4 == 0 && tokens <= kFewTokens;
+    q.few = !bf16 && width % 4 == 0 && tokens <= kFewTokens && vocab >= kFewVocab;
     q.wpack = !q.few && (!bf16 || width % 64 != 0);
     // bytes of scratch per vocabulary row of a piece: fp32 rows as two fp16 planes, and for the gradient three bf16 planes
     int64_t per_row = !q.wpack ? 0 : bf16 ? q.kp * 2 : q.kp * (for_grad ? 10 : 4);
@@ -125,7 +133,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.piece = ceil_div64(ceil_div64(all, q.pieces), 256) * 256;
     }
     q.pieces = ceil_div64(all, q.piece);
-    q.tile_z = q.few ? TILE_32 : pick_tile(q.piece, tokens, 0, 1);
+    q.tile_z = q.few ? TILE_32 : pick_logit_tile(q.piece, tokens);
     q.nvt = ceil_div64(vocab, tile_m(q.tile_z));
     size_t off = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
@@ -153,8 +161,8 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.lg = take(q.np * 8);
         q.rest = take(q.np * 4);
         q.dl = take(q.dparts * q.np * q.piece * 2);
-        if (q.pieces > 1 || q.split_h > 1) q.acc_h = take(q.split_h * q.np * width * 4);
-        if (q.split_w > 1) q.acc_w = take(q.split_w * q.piece * width * 4);
+        if (q.pieces > 1 || q.split_h > 1) q.acc_h = take(q.split_h * q.np * q.dp * 4);
+        if (q.split_w > 1) q.acc_w = take(q.split_w * q.piece * q.dp * 4);
     }
     q.total = off;
     *p = q;
