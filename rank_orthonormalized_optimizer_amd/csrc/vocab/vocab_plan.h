@@ -77,7 +77,8 @@ struct XentPlan {
 };
 
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens), 64 x 64
-constexpr int64_t kPieceBytes = (int64_t)512 << 20;   // of D, and of W's planes, per piece of the vocabulary
+constexpr int64_t kPieceBytes = (int64_t)512 << 20;    // of D per piece of the vocabulary (2 GiB: -1 to +5% on 8192 tokens)
+constexpr int64_t kPlaneBytes = (int64_t)2048 << 20;   // of W's planes per piece: few pieces keep the products large
 constexpr int kCUs = 256;
 // dW of so few tokens is a stream of writes: two workgroups per CU with smaller tiles
 constexpr int64_t kShortTokens = 128;
@@ -123,15 +124,14 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.few = !bf16 && width % 4 == 0 && tokens <= kFewTokens && vocab >= kFewVocab;
     q.wpack = !q.few && (!bf16 || width % 64 != 0);
     // bytes of scratch per vocabulary row of a piece: fp32 rows as two fp16 planes, and for the gradient three bf16 planes
-    int64_t per_row = !q.wpack ? 0 : bf16 ? q.kp * 2 : q.kp * (for_grad ? 10 : 4);
-    if (for_grad && q.dparts * q.np * 2 > per_row) per_row = q.dparts * q.np * 2;
+    const int64_t plane_row = !q.wpack ? 0 : bf16 ? q.kp * 2 : q.kp * (for_grad ? 10 : 4);
+    const int64_t d_row = for_grad ? q.dparts * q.np * 2 : 0;
     const int64_t all = ceil_div64(vocab, 256) * 256;
-    q.piece = all;
-    if (per_row > 0 && kPieceBytes / per_row < all) {
-        const int64_t most = kPieceBytes / per_row / 256 * 256;
-        q.pieces = ceil_div64(all, most < 256 ? 256 : most);
-        q.piece = ceil_div64(ceil_div64(all, q.pieces), 256) * 256;
-    }
+    int64_t most = all;
+    if (plane_row > 0 && kPlaneBytes / plane_row < most) most = kPlaneBytes / plane_row;
+    if (d_row > 0 && kPieceBytes / d_row < most) most = kPieceBytes / d_row;
+    most = most < 256 ? 256 : most / 256 * 256;
+    q.piece = ceil_div64(ceil_div64(all, ceil_div64(all, most)), 256) * 256;   // equal pieces
     q.pieces = ceil_div64(all, q.piece);
     q.tile_z = q.few ? TILE_32 : pick_logit_tile(q.piece, tokens);
     q.nvt = ceil_div64(vocab, tile_m(q.tile_z));

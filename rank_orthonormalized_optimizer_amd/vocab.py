@@ -38,18 +38,19 @@ def _matrix(t, name: str, device=None):
 
 
 class _On:
-    """The stream a call runs on: torch's current device and stream are the tensors' device and that
-    stream inside the block, so that scratch allocated there is reused in the stream's order."""
-    __slots__ = ("stream", "handle", "guard")
+    """The stream a call runs on.  Inside the block torch's current device is the tensors', and its current
+    stream the one given, so that scratch allocated there is reused in that stream's order."""
+    __slots__ = ("handle", "guard")
 
     def __init__(self, device, stream):
-        current = torch.cuda.current_stream(device)
-        self.stream = current if stream is None else stream
-        self.handle = self.stream.cuda_stream
-        if self.stream.device != device:
-            raise ValueError(f"stream of {self.stream.device} for tensors on {device}")
-        same = device.index == torch.cuda.current_device() and self.handle == current.cuda_stream
-        self.guard = None if same else torch.cuda.stream(self.stream)
+        if stream is None:   # the raw handle: a stream object costs as much as a third of a small call
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            self.handle = stream.cuda_stream
+            self.guard = torch.cuda.stream(stream)
 
     def __enter__(self):
         if self.guard is not None:
