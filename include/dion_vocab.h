@@ -72,8 +72,10 @@ int dion_embedding_grad(const void* ids, const void* dY, void* dW, int64_t token
  *            target outside [0, vocab) gives that token a NaN loss
  *   loss     device fp32 [tokens], written
  *   lse      device fp32 [tokens], written: log sum_v exp z[t][v], for dion_linear_xent_grad
- * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores; fp32 operands are
- * split exactly into three bf16 parts, six part products kept (below 2^-24 relative per term dropped).
+ * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores.  fp32 operands give fp32-accurate
+ * logits from 16-bit parts, whichever is cheaper for the sizes: three bf16 parts (an exact split, six part products, terms
+ * below 2^-24 dropped), or two fp16 parts of each row scaled by a power of two (2^-23 of an element and 2^-39 of its row's
+ * largest left out, three part products, terms below 2^-22 dropped).
  * Workspace size for both calls: dion_linear_xent_workspace_size (for_grad 0 or 1; 0 for invalid sizes).
  */
 size_t dion_linear_xent_workspace_size(int64_t tokens, int64_t vocab, int64_t width, int dtype, int dw_dtype,
@@ -90,8 +92,9 @@ int dion_linear_xent(const void* H, const void* W, const void* targets, float* l
  *   dW       device, [vocab][width], dw_dtype (DION_F32 or DION_BF16), or NULL; accumulate 1 adds to
  *            what is there.  At least one of dH and dW is given
  * A token whose target is neither ignored nor in [0, vocab) makes its dH row and dW NaN.
- * Arithmetic: D is rounded to bf16 for the product with a bf16 operand that gives a bf16 output, and
- * split into three bf16 parts (fp32-accurate) where the output or the operands are fp32.
+ * Arithmetic: for bf16 outputs of bf16 operands D is rounded once to bf16 (without grad where grad_n is 1: that factor is
+ * applied to the fp32 sums), and what the rounding left of the target's element is added to dH in fp32.  Where the output or
+ * the operands are fp32, D and the operands are split into three bf16 parts, fp32-accurate.
  */
 int dion_linear_xent_grad(const void* H, const void* W, const void* targets, const float* lse, const float* grad,
                           int64_t grad_n, void* dH, void* dW, int64_t tokens, int64_t vocab, int64_t width,

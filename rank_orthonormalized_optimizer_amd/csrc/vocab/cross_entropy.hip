@@ -92,6 +92,7 @@ struct PackArgs {
     int* tgt;        // its target, -1 where that is no row of W
     float2* lg;      // (lse, grad) of the gathered row (gradient)
     int* cnt;        // how many rows were gathered
+    int* blocks;     // rows to gather in each kCountBlock tokens, or null: few tokens
 };
 
 __device__ __forceinline__ int64_t load_target(const XentArgs& a, int64_t i) {
@@ -184,16 +185,39 @@ __device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d,
 
 constexpr int kPackRows = 8;
 
-// Eight tokens per workgroup, one per wave; it counts the gathered rows before them itself (a read of the
-// targets from L2: fewer bytes than its rows of H up to some thousand tokens).
+// How many rows to gather in each kCountBlock tokens.
+__global__ __launch_bounds__(512) void count_kernel(PackArgs a) {
+    __shared__ int part[8];
+    const int64_t t0 = (int64_t)blockIdx.x * kCountBlock;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kCountBlock / 512; ++i) {
+        const int64_t t = t0 + i * 512 + threadIdx.x;
+        if (t < a.n) c += load_target(a.x, t) != a.x.ignore;
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) c += __shfl_xor(c, o);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = c;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 8; ++i) c += part[i];
+        a.blocks[blockIdx.x] = c;
+    }
+}
+
+// Eight tokens per workgroup, one per wave.  The workgroup counts the gathered rows before its own itself, a read of
+// the targets (or of the counts of whole blocks, and the targets since the last one) from L2.
 template <bool BF16, bool V8, bool GRAD>
 __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
     __shared__ int before[8], slot[kPackRows];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int64_t t0 = (int64_t)blockIdx.x * kPackRows;
     int c = 0;
+    const int64_t from = a.blocks ? t0 / kCountBlock * kCountBlock : 0;
+    if (a.blocks)
+        for (int64_t i = tid; i < t0 / kCountBlock; i += 512) c += a.blocks[i];
 #pragma unroll 8
-    for (int64_t i = tid; i < t0; i += 512) c += load_target(a.x, i) != a.x.ignore;
+    for (int64_t i = from + tid; i < t0; i += 512) c += load_target(a.x, i) != a.x.ignore;
 #pragma unroll
     for (int o = 32; o; o >>= 1) c += __shfl_xor(c, o);
     if (lane == 0) before[w] = c;
@@ -685,6 +709,7 @@ void launch_logits(const LogitArgs& a, const XentPlan& p, hipStream_t s) {
 template <bool GRAD>
 void launch_pack(const PackArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div64(a.n, kPackRows));
+    if (a.blocks) hipLaunchKernelGGL(count_kernel, dim3((unsigned)ceil_div64(a.n, kCountBlock)), dim3(512), 0, s, a);
     if (a.x.bf16) {
         if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<true, true, GRAD>), grid, dim3(512), 0, s, a);
         else hipLaunchKernelGGL((pack_kernel<true, false, GRAD>), grid, dim3(512), 0, s, a);
@@ -722,7 +747,8 @@ Weights weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int6
 PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws, bool exact) {
     return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, exact || x.bf16 || p.few ? (uint16_t*)(ws + p.h) : nullptr,
                     x.bf16 || p.few ? nullptr : (uint16_t*)(ws + p.h16), (float*)(ws + p.hinv), (int*)(ws + p.map),
-                    (int*)(ws + p.tgt), (float2*)(ws + p.lg), (int*)(ws + p.cnt)};
+                    (int*)(ws + p.tgt), (float2*)(ws + p.lg), (int*)(ws + p.cnt),
+                    p.n > kCountDirect ? (int*)(ws + p.cnt) + 64 : nullptr};
 }
 
 LogitArgs logit_args(const XentPlan& p, const PackArgs& pk, char* ws) {

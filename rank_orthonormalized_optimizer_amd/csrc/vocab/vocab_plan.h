@@ -80,6 +80,8 @@ enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 1
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;    // of D per piece of the vocabulary (2 GiB: -1 to +5% on 8192 tokens)
 constexpr int64_t kPlaneBytes = (int64_t)2048 << 20;   // of W's planes per piece: few pieces keep the products large
 constexpr int kCUs = 256;
+constexpr int kCountBlock = 4096;          // tokens per count of gathered rows,
+constexpr int64_t kCountDirect = 16384;    // which fewer tokens than this do without
 // dW of so few tokens is a stream of writes: two workgroups per CU with smaller tiles
 constexpr int64_t kShortTokens = 128;
 // fp32: up to so many tokens the products over W read it in place (see FewProduct), if W has tiles for half the CUs.
@@ -137,7 +139,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.nvt = ceil_div64(vocab, tile_m(q.tile_z));
     size_t off = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
-    q.cnt = take(256);
+    q.cnt = take(256 + ceil_div64(q.np, kCountBlock) * 4);
     if (bf16 || for_grad || q.few) q.h = take(q.parts * q.np * q.kp * 2);
     if (!bf16 && !q.few) {
         q.h16 = take(2 * q.np * q.kp * 2);
