@@ -672,6 +672,8 @@ using Q64 = mm::FewConfig<64, 2, true>;
 using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
 using H128 = mm::Config<128, 128, 2, 2, 4, true, false>;
 using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
+using H64 = mm::Config<64, 64, 2, 2, 8, true, false>;
+using W64 = mm::Config<64, 64, 2, 2, 8, true, true>;
 using W256 = mm::Config<256, 256, 2, 4, 2, true, true>;
 using W128s = mm::Config<128, 128, 2, 2, 2, true, true>;
 using W128 = mm::Config<128, 128, 2, 2, 4, true, true>;
@@ -834,6 +836,7 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             else if (p.few) launch_out<Q64>(h, p.n, s);
             else if (p.tile_h == TILE_256) launch_out<H256>(h, p.n, s);
             else if (p.tile_h == TILE_128) launch_out<H128>(h, p.n, s);
+            else if (p.tile_h == TILE_64) launch_out<H64>(h, p.n, s);
             else launch_out<H32>(h, p.n, s);
         }
         if (x.dW) {
@@ -843,6 +846,7 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);
             w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
             if (p.tile_w == TILE_256) launch_out<W256>(w, rows, s);
+            else if (p.tile_w == TILE_64) launch_out<W64>(w, rows, s);
             else if (p.n <= kShortTokens) launch_out<W128s>(w, rows, s);
             else launch_out<W128>(w, rows, s);
             if (w.acc) launch_join(w, rows, s);

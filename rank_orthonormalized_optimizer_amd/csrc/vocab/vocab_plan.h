@@ -93,10 +93,10 @@ inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : t == TILE_64 ? 64 : 
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : t == TILE_64 ? 64 : 32; }
 inline int64_t tiles(int64_t m, int64_t n, int t) { return ceil_div64(m, tile_m(t)) * ceil_div64(n, tile_n(t)); }
 // Slices of a reduction of length k (`terms` part products of it) so that an output of m x n fills the chip, each of
-// 24 slabs of 64 at least (8 for the narrow tiles, whose slabs are shorter): a slice costs a pass over the output.
+// 24 slabs of 64 at least (8 for the small tiles, whose slabs are shorter): a slice costs a pass over the output.
 inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int64_t terms, int tile) {
     int64_t s = kCUs / tiles(m, n, tile);
-    const int64_t most = ceil_div64(k, 64) * terms / (tile == TILE_32 ? 8 : 24);
+    const int64_t most = ceil_div64(k, 64) * terms / (tile == TILE_32 || tile == TILE_64 ? 8 : 24);
     if (s > most) s = most;
     if (s > ceil_div64(k, 64)) s = ceil_div64(k, 64);
     return s < 1 ? 1 : s;
@@ -105,10 +105,11 @@ inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int64_t terms, int ti
 // reduction is long enough by slices of it.
 inline int pick_tile(int64_t m, int64_t n, int64_t k, int64_t terms) {
     if (n <= 32) return TILE_32;
-    return tiles(m, n, TILE_256) * pick_split(m, n, k, terms, TILE_256) >= kCUs / 2 ? TILE_256 : TILE_128;
+    if (tiles(m, n, TILE_256) * pick_split(m, n, k, terms, TILE_256) >= kCUs / 2) return TILE_256;
+    return tiles(m, n, TILE_128) * pick_split(m, n, k, terms, TILE_128) >= kCUs / 2 ? TILE_128 : TILE_64;
 }
-// The logits' reduction is not sliced: where even 128 x 128 tiles leave half the CUs idle, 64 x 64 ones, whose ring of
-// eight slabs also hides more of the loads' latency.
+// The logits' reduction is not sliced.  Where even 128 x 128 tiles leave half the CUs idle, 64 x 64 ones serve, whose ring
+// of eight slabs also hides more of the loads' latency (fp32 257 x 1013 x 255: logits 31 -> 7 us).
 inline int pick_logit_tile(int64_t m, int64_t n) {
     if (n <= 32) return TILE_32;
     return tiles(m, n, TILE_256) >= kCUs / 2 ? TILE_256 : tiles(m, n, TILE_128) >= kCUs / 2 ? TILE_128 : TILE_64;
