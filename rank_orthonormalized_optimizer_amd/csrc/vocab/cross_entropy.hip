@@ -8,9 +8,18 @@
 // they hold reaches nothing.  The loss: one tile product over W, whose epilogue reduces each tile
 // of logits to a maximum and a sum of exponentials per token (online softmax across tiles), then
 // one pass over these pairs.  The gradient: per piece of the vocabulary the logits are formed
-// again, turned into D (bf16, one part or an exact split in three) and multiplied from both sides.
-// Matrix-core bound: 2 tokens vocab width flops for the loss, four times that for loss and
-// gradients together, the recomputed logits included.
+// again, turned into D (16-bit parts) and multiplied from both sides.
+//
+// What multiplies: bf16 operands as they are, D in one bf16 part; three parts for an fp32 dW.  fp32 operands: logits and dH
+// from two fp16 parts of W's and H's rows, each row scaled by a power of two (three products), dW from three bf16 parts of D
+// and H (six: D's columns for rare tokens are too small for fp16).  fp32 and few tokens: W in place, split in registers
+// (FewProduct).
+//
+// Bound by the matrix cores: 2 tokens vocab width flops for the loss, four times that for loss and gradients together, the
+// logits formed twice.  8192 tokens (5% ignored) x 32000 x 2048 in bf16: loss 0.78 to 0.81 ms (1.27 to 1.31 PFLOP/s, of the
+// 1.42 that the library's product of these sizes reaches), loss and gradients 3.2 to 3.3 ms; matrix cores busy 61 to 70% of
+// the cycles.  Without the matrix products the loss kernel takes 0.57 ms and the gradients' products 0.70 and 0.73, without
+// the loads 0.58 to 0.61: the two overlap but for the barrier of each slab.
 //
 // In every product the vocabulary (or width) runs along the matrix core's rows and the tokens (or
 // vocabulary) along its columns: a lane then holds four consecutive elements of the contiguous
@@ -53,12 +62,13 @@ __device__ __forceinline__ void split2(float a, float scale, uint32_t (&part)[2]
     part[1] = (uint32_t)__builtin_bit_cast(uint16_t, l);
 }
 
-// That scale for a row whose largest magnitude is `top`, and its inverse (1 where the row is zero or not finite;
-// clamped so that both stay normal numbers).
+// That scale for a row whose largest magnitude is `top`, at most 2^100 so that products of two inverses stay normal numbers,
+// and its inverse.  A row of zeros gets the largest scale: its inverse must not pass for the largest of a matrix.  (A row
+// that is not finite stays as it is.)
 __device__ __forceinline__ float row_scale(float top, float& inverse) {
     int e = 140 - (int)(__float_as_uint(top) >> 23);   // 127 + 13 - biased exponent
-    if (top == 0.f || !(top < INFINITY)) e = 0;
-    e = e > 126 ? 126 : e;
+    if (!(top < INFINITY)) e = 0;
+    e = e > 100 ? 100 : e;   // zero and subnormal numbers among them
     inverse = __uint_as_float((uint32_t)(127 - e) << 23);
     return __uint_as_float((uint32_t)(127 + e) << 23);
 }
@@ -91,6 +101,7 @@ struct PackArgs {
     int* map;        // gathered row -> token
     int* tgt;        // its target, -1 where that is no row of W
     float2* lg;      // (lse, grad) of the gathered row (gradient)
+    float* gscale;   // the power of two in grad (gradient of fp32 operands)
     int* cnt;        // how many rows were gathered
     int* blocks;     // rows to gather in each kCountBlock tokens, or null: few tokens
 };
@@ -241,6 +252,8 @@ __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
                 // one factor for all tokens is applied to the outputs: in D it would be rounded the same way everywhere
                 const float g = a.x.grad_n == 1 ? 1.f : a.x.grad[t];
                 a.lg[j] = float2{a.x.lse[t], in ? g : __uint_as_float(0x7fc00000u)};
+                const int e = (int)(__float_as_uint(g) >> 23 & 255u);
+                if (a.gscale) a.gscale[j] = e > 0 && e < 255 ? __uint_as_float((uint32_t)e << 23) : 1.f;   // g / gscale in [1, 2)
             }
         } else if (row && !GRAD) {
             a.x.loss[t] = 0.f;
@@ -261,7 +274,23 @@ __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
     }
 }
 
-// Planes of `rows` rows of W (from row0), a wave per row.
+// The largest of n inverse scales, to out.
+__global__ __launch_bounds__(1024) void top_kernel(const float* inv, int n, float* out) {
+    __shared__ float part[16];
+    float top = 0.f;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n; i += 1024) top = fmaxf(top, inv[i]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, part[i]);
+        *out = top;
+    }
+}
+
+// Planes of `rows` rows of W (from row0), a wave per row: fp16 ones of fp32 rows, a copy of bf16 ones.
 template <bool BF16, bool V8>
 __global__ __launch_bounds__(256) void plane_kernel(const void* W, int64_t row0, int64_t rows, int64_t d, int64_t kp,
                                                     uint16_t* p, uint16_t* p16, int64_t plane, float* inv) {
@@ -313,11 +342,29 @@ struct LogitArgs {
     // gradient
     const float2* lg;
     uint16_t* dl;          // planes [dparts][np][piece]
+    uint16_t* dl16;        // F16: fp16 planes [2][np][piece] of D times W's inverse row scales, for dH
+    const float* gscale;
+    const float* wtop;     // F16: the largest of the piece's inverse row scales
     float* rest;           // [np] what the first part of D leaves of the target's element
     int64_t np, piece;
 };
 
 enum { EPI_LOSS, EPI_D1, EPI_D3 };
+
+// Stores a lane's 4-row pieces of two neighbouring blocks of 16 rows: the lane quarters trade their four rows of one
+// against the other's (v_permlane32_swap, v_permlane16_swap), so that a lane stores eight consecutive rows and four lanes
+// 64 bytes.  a, b: the four values of each block, packed in two words; to: the address for this lane's quarter.
+__device__ __forceinline__ void store_pair(uint16_t* to, const uint32_t (&a)[2], const uint32_t (&b)[2], bool in) {
+    u32x4 w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const auto x = __builtin_amdgcn_permlane32_swap(a[h], b[h], false, false);
+        const auto z = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+        w[h] = z[0];
+        w[2 + h] = z[1];
+    }
+    if (in) *(u32x4*)to = w;
+}
 
 template <class C, int EPI>
 __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
@@ -337,13 +384,14 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
         const int m0 = mul.m0, n0 = mul.n0;
         int y[C::NI];
         float2 lg[C::NI];
-        float hinv[C::F16 ? C::NI : 1];
+        float hinv[C::F16 ? C::NI : 1], gs[C::F16 ? C::NI : 1];
 #pragma unroll
         for (int j = 0; j < C::NI; ++j) {
             const int n = n0 + cl + 16 * j, nn = n < count ? n : count - 1;
             y[j] = a.tgt[nn] - a.v0;
             if (C::F16) hinv[j] = a.hinv[nn];
             if (EPI != EPI_LOSS) lg[j] = a.lg[nn];
+            if (EPI != EPI_LOSS && C::F16) gs[j] = a.gscale[nn];
         }
         typename C::Acc acc = {};
         mul.finish(a.w, a.h, acc);
@@ -423,43 +471,59 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
                             }
                     if (mine) a.rest[n] = d - up16(down16(d));
                 }
-                // A lane has four consecutive rows of a block of 16.  Two blocks at a time, where there are two: the lane quarters trade their four rows of one against the other's
-                // (v_permlane32_swap, v_permlane16_swap), so that a lane stores eight consecutive rows and four lanes 64 bytes.
+                // A lane has four consecutive rows of a block of 16, and stores two blocks at a time, where there are two.
                 const int quarter = mul.lane / 16;
-                uint16_t* to = a.dl + n * a.piece + m0 + mul.xa + 16 * (quarter / 2) + 8 * (quarter % 2);
+                const int64_t at8 = n * a.piece + m0 + mul.xa + 16 * (quarter / 2) + 8 * (quarter % 2);
 #pragma unroll
-                for (int i = 0; i + 1 < C::MI; i += 2) {
+                for (int i = 0; i < C::MI; i += 2) {
+                    constexpr bool kPairs = C::MI % 2 == 0;
                     uint32_t part[2][4][3];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        split3(acc[i][j][v] * lg[j].y, part[0][v]);
-                        split3(acc[i + 1][j][v] * lg[j].y, part[1][v]);
-                    }
+                    for (int h = 0; h < (kPairs ? 2 : 1); ++h)
 #pragma unroll
-                    for (int q = 0; q < PD; ++q) {
-                        u32x4 w;
+                        for (int v = 0; v < 4; ++v) split3(acc[i + h][j][v] * lg[j].y, part[h][v]);
+                    if (a.dl) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const auto x = __builtin_amdgcn_permlane32_swap(part[0][2 * h][q] | (part[0][2 * h + 1][q] << 16),
-                                                                            part[1][2 * h][q] | (part[1][2 * h + 1][q] << 16),
-                                                                            false, false);
-                            const auto z = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
-                            w[h] = z[0];
-                            w[2 + h] = z[1];
+                        for (int q = 0; q < PD; ++q) {
+                            const uint32_t w0[2] = {part[0][0][q] | (part[0][1][q] << 16), part[0][2][q] | (part[0][3][q] << 16)};
+                            if constexpr (kPairs) {
+                                const uint32_t w1[2] = {part[1][0][q] | (part[1][1][q] << 16), part[1][2][q] | (part[1][3][q] << 16)};
+                                store_pair(a.dl + q * a.np * a.piece + at8 + 16 * i, w0, w1, n < count);
+                            } else if (n < count) {
+                                *(u32x2*)(a.dl + (q * a.np + n) * a.piece + m0 + rl + 16 * i) = u32x2{w0[0], w0[1]};
+                            }
                         }
-                        if (n < count) *(u32x4*)(to + q * a.np * a.piece + 16 * i) = w;
                     }
                 }
-                if constexpr (C::MI % 2 != 0) {
-                    constexpr int i = C::MI - 1;
-                    uint32_t part[4][3];
+                if constexpr (C::F16) {
+                    if (a.dl16) {
+                        // |D / gscale| < 2 and an inverse scale is at most wtop: the product goes to below 2^15
+                        const float unit = lg[j].y / gs[j] * (16384.f / a.wtop[0]);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) split3(acc[i][j][v] * lg[j].y, part[v]);
+                        for (int i = 0; i < C::MI; i += 2) {
+                            uint32_t w[2][2][2];   // [block][part][word]
 #pragma unroll
-                    for (int q = 0; q < PD; ++q)
-                        if (n < count)
-                            *(u32x2*)(a.dl + (q * a.np + n) * a.piece + m0 + rl + 16 * i) =
-                                u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
+                            for (int h = 0; h < 2; ++h) {
+                                f32x4 s = *(const f32x4*)(a.winv + m0 + rl + 16 * (i + h));
+                                if (m0 + C::BM > rows) {   // no scales behind the piece's rows, whose D is 0
+#pragma unroll
+                                    for (int v = 0; v < 4; ++v)
+                                        if (m0 + rl + 16 * (i + h) + v >= rows) s[v] = 0.f;
+                                }
+                                uint32_t part[4][2];
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) split2(acc[i + h][j][v], unit * s[v], part[v]);
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    w[h][q][0] = part[0][q] | (part[1][q] << 16);
+                                    w[h][q][1] = part[2][q] | (part[3][q] << 16);
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                store_pair(a.dl16 + q * a.np * a.piece + at8 + 16 * i, w[0][q], w[1][q], n < count);
+                        }
+                    }
                 }
             }
         }
@@ -522,6 +586,8 @@ struct OutArgs {
     const int* map;        // output row of a gathered token, or null
     int out_bf16, accumulate;
     const float* factor;   // of the outputs, or null
+    const float* wtop;     // D and W were scaled: multiply by *wtop 2^-14 (each piece's own) and by the row's scale; or null
+    const float* row_scale;
     // dH in bf16: what the rounding of D left of the target's element, times the target's row of W
     const float* rest;     // or null
     const int* tgt;
@@ -541,6 +607,11 @@ __device__ __forceinline__ void store_out(const OutArgs& a, int64_t r, int c, in
         } else {
             for (int e = 0; e < n; ++e) v[e] = fmaf(left, up16(w[e]), v[e]);
         }
+    }
+    if (a.row_scale) {
+        const float f = a.row_scale[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= f;
     }
     if (a.factor) {
         const float f = *a.factor;
@@ -602,6 +673,13 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
         walk.next();
         const bool more = !walk.done();
         if (more) any = start();
+        if (a.wtop) {
+            const float f = a.wtop[0] * (1.f / 16384.f);
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j) acc[i][j] *= f;
+        }
 #pragma unroll
         for (int j = 0; j < C::NI; ++j) {
             const int n = n0 + mul.xb + 16 * j + mul.lane % 16;
@@ -669,6 +747,10 @@ using P32 = mm::FewConfig<32, 3, false>;
 using P64 = mm::FewConfig<64, 2, false>;
 using Q32 = mm::FewConfig<32, 3, true>;
 using Q64 = mm::FewConfig<64, 2, true>;
+using E256 = mm::Config<256, 256, 2, 4, 2, true, false, true>;
+using E128 = mm::Config<128, 128, 2, 2, 4, true, false, true>;
+using E64 = mm::Config<64, 64, 2, 2, 8, true, false, true>;
+using E32 = mm::Config<128, 32, 4, 1, 4, true, false, true>;
 using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
 using H128 = mm::Config<128, 128, 2, 2, 4, true, false>;
 using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
@@ -721,17 +803,14 @@ void launch_pack(const PackArgs& a, hipStream_t s) {
     }
 }
 
-// W's rows [v0, v0 + rows) in place (bf16, or fp32 for few tokens), or as planes in the workspace: bf16 ones (`exact`, for dH) and for fp32 fp16 ones.
-struct Weights {
-    mm::Operand z, h;   // for the logits and for dH
-};
-Weights weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int64_t rows, bool exact, hipStream_t s) {
-    if (!p.wpack) {
-        const mm::Operand o{(const uint16_t*)((const char*)x.W + v0 * p.d * (x.bf16 ? 2 : 4)), 0, p.d, (int)rows};
-        return Weights{o, o};
-    }
-    uint16_t* w = exact || x.bf16 ? (uint16_t*)(ws + p.w) : nullptr;
-    uint16_t* w16 = x.bf16 ? nullptr : (uint16_t*)(ws + p.w16);
+// W's rows [v0, v0 + rows) as an operand of both products over W: in place (bf16, or fp32 for few tokens), or as planes in
+// the workspace, fp16 ones of fp32 rows, with the largest inverse scale if `top`.
+mm::Operand weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int64_t rows, bool top, hipStream_t s) {
+    if (!p.wpack)
+        return mm::Operand{(const uint16_t*)((const char*)x.W + v0 * p.d * (x.bf16 ? 2 : 4)), 0, p.d, (int)rows};
+    uint16_t* w = (uint16_t*)(ws + p.w);
+    uint16_t* w16 = x.bf16 ? nullptr : w;
+    if (!x.bf16) w = nullptr;
     float* inv = (float*)(ws + p.winv);
     const int64_t plane = p.piece * p.kp;
     const dim3 grid((unsigned)ceil_div64(rows, 4));
@@ -741,15 +820,16 @@ Weights weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, int6
     } else {
         if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<false, true>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
         else hipLaunchKernelGGL((plane_kernel<false, false>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
+        if (top) hipLaunchKernelGGL(top_kernel, dim3(1), dim3(1024), 0, s, inv, (int)rows, (float*)(ws + p.wtop));
     }
-    const mm::Operand h{w, plane, p.kp, (int)rows};
-    return Weights{x.bf16 ? h : mm::Operand{w16, plane, p.kp, (int)rows}, h};
+    return mm::Operand{(uint16_t*)(ws + p.w), plane, p.kp, (int)rows};
 }
 
 PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws, bool exact) {
     return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, exact || x.bf16 || p.few ? (uint16_t*)(ws + p.h) : nullptr,
                     x.bf16 || p.few ? nullptr : (uint16_t*)(ws + p.h16), (float*)(ws + p.hinv), (int*)(ws + p.map),
-                    (int*)(ws + p.tgt), (float2*)(ws + p.lg), (int*)(ws + p.cnt),
+                    (int*)(ws + p.tgt), (float2*)(ws + p.lg),
+                    x.bf16 || p.few ? nullptr : (float*)(ws + p.gscale), (int*)(ws + p.cnt),
                     p.n > kCountDirect ? (int*)(ws + p.cnt) + 64 : nullptr};
 }
 
@@ -758,7 +838,7 @@ LogitArgs logit_args(const XentPlan& p, const PackArgs& pk, char* ws) {
     a.h = mm::Operand{pk.h16 ? pk.h16 : pk.h, p.np * p.kp, p.kp, 0};
     a.seg = p.parts == 1 ? segments(1, 1) : segments(2, 2);
     a.kp = (int)p.kp; a.cnt = pk.cnt; a.tgt = pk.tgt;
-    a.hinv = pk.inv; a.winv = (float*)(ws + p.winv);
+    a.hinv = pk.inv; a.winv = (float*)(ws + p.winv); a.wtop = (float*)(ws + p.wtop); a.gscale = pk.gscale;
     return a;
 }
 
@@ -783,7 +863,7 @@ int run_xent(const XentArgs& x, const XentPlan& p, char* ws, void* stream) {
     LogitArgs a = logit_args(p, pk, ws);
     a.part = (float2*)(ws + p.part); a.zt = (float*)(ws + p.zt); a.nvt = (int)p.nvt;
     for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
-        a.w = weights(x, p, ws, v0, p.v - v0 < p.piece ? p.v - v0 : p.piece, false, s).z;
+        a.w = weights(x, p, ws, v0, p.v - v0 < p.piece ? p.v - v0 : p.piece, false, s);
         a.v0 = (int)v0;
         launch_logits<EPI_LOSS>(a, p, s);
     }
@@ -807,13 +887,17 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
     launch_pack<true>(pk, s);
     LogitArgs z = logit_args(p, pk, ws);
     z.lg = pk.lg;
-    z.dl = (uint16_t*)(ws + p.dl); z.rest = (float*)(ws + p.rest); z.np = p.np; z.piece = p.piece;
+    const bool scaled = !x.bf16 && !p.few;   // dH from fp16 parts of scaled D and W
+    z.dl = x.dW || !scaled ? (uint16_t*)(ws + p.dl) : nullptr;
+    z.dl16 = scaled && x.dH ? (uint16_t*)(ws + p.dl16) : nullptr;
+    z.rest = (float*)(ws + p.rest); z.np = p.np; z.piece = p.piece;
     const mm::Operand dl{z.dl, p.np * p.piece, p.piece, 0};
     OutArgs h{};
     const float* factor = x.grad_n == 1 ? x.grad : nullptr;
     h.cnt = pk.cnt; h.d = (int)p.d; h.dp = (int)p.dp; h.factor = factor; h.rows = -1; h.split = (int)p.split_h; h.map = pk.map; h.out = x.dH; h.out_bf16 = x.bf16;
     h.acc = p.pieces > 1 || p.split_h > 1 ? (float*)(ws + p.acc_h) : nullptr;
     h.acc_rows = p.np;
+    if (scaled) { h.wtop = z.wtop; h.row_scale = pk.gscale; }
     if (x.bf16) { h.rest = z.rest; h.tgt = pk.tgt; h.w = (const uint16_t*)x.W; }
     OutArgs w{};
     w.cnt = pk.cnt; w.d = (int)p.d; w.dp = (int)p.dp; w.factor = factor; w.k = -1; w.split = (int)p.split_w; w.out_bf16 = x.dw_bf16; w.accumulate = x.accumulate;
@@ -821,19 +905,23 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
     w.acc_rows = p.piece;
     for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
         const int64_t rows = p.v - v0 < p.piece ? p.v - v0 : p.piece;
-        const Weights wt = weights(x, p, ws, v0, rows, x.dH != nullptr, s);
-        z.w = wt.z;
+        z.w = weights(x, p, ws, v0, rows, x.dH != nullptr, s);
         z.v0 = (int)v0;
         if (p.dparts == 1) launch_logits<EPI_D1>(z, p, s);
         else launch_logits<EPI_D3>(z, p, s);
         if (x.dH) {
-            h.a = wt.h; h.b = dl;
-            h.seg = segments(p.parts, x.bf16 ? 1 : 3);
+            h.a = z.w;
+            h.b = scaled ? mm::Operand{z.dl16, p.np * p.piece, p.piece, 0} : dl;
+            h.seg = scaled ? segments(2, 2) : segments(p.parts, x.bf16 ? 1 : 3);
             h.k = (int)(ceil_div64(rows, 64) * 64);
             h.k_per = (int)(ceil_div64(ceil_div64(h.k, p.split_h), 64) * 64);
             h.add = v0 > 0;
             if (p.few && p.n <= 32) launch_out<Q32>(h, p.n, s);
             else if (p.few) launch_out<Q64>(h, p.n, s);
+            else if (scaled && p.tile_h == TILE_256) launch_out<E256>(h, p.n, s);
+            else if (scaled && p.tile_h == TILE_128) launch_out<E128>(h, p.n, s);
+            else if (scaled && p.tile_h == TILE_64) launch_out<E64>(h, p.n, s);
+            else if (scaled) launch_out<E32>(h, p.n, s);
             else if (p.tile_h == TILE_256) launch_out<H256>(h, p.n, s);
             else if (p.tile_h == TILE_128) launch_out<H128>(h, p.n, s);
             else if (p.tile_h == TILE_64) launch_out<H64>(h, p.n, s);

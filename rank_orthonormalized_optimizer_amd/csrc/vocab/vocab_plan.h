@@ -73,11 +73,13 @@ struct XentPlan {
     int64_t nvt;              // softmax partials per token (forward)
     int tile_z, tile_h, tile_w;   // tile shapes of the logits, dH and dW (TILE_*)
     int64_t split_h, split_w; // slices of the reductions of dH (over the piece) and dW (over the tokens)
-    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, w, w16, winv, dl, rest, acc_h, acc_w, total;
+    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, w, winv, wtop, gscale, dl, dl16, rest, acc_h, acc_w, total;
 };
 
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens), 64 x 64
-constexpr int64_t kPieceBytes = (int64_t)512 << 20;    // of D per piece of the vocabulary (2 GiB: -1 to +5% on 8192 tokens)
+// Elements of D per piece of the vocabulary: 512 MiB per bf16 part.  Four times as many gave -1 to +5% on 8192 tokens,
+// a fifth as many +14% (fp32, 4096 x 32000 x 1024: the products over a piece no longer fill the chip).
+constexpr int64_t kPieceElems = (int64_t)1 << 28;
 constexpr int64_t kPlaneBytes = (int64_t)2048 << 20;   // of W's planes per piece: few pieces keep the products large
 constexpr int kCUs = 256;
 constexpr int kCountBlock = 4096;          // tokens per count of gathered rows,
@@ -126,13 +128,12 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.dparts = bf16 && dw_bf16 ? 1 : 3;
     q.few = !bf16 && width % 4 == 0 && tokens <= kFewTokens && vocab >= kFewVocab;
     q.wpack = !q.few && (!bf16 || width % 64 != 0);
-    // bytes of scratch per vocabulary row of a piece: fp32 rows as two fp16 planes, and for the gradient three bf16 planes
-    const int64_t plane_row = !q.wpack ? 0 : bf16 ? q.kp * 2 : q.kp * (for_grad ? 10 : 4);
-    const int64_t d_row = for_grad ? q.dparts * q.np * 2 : 0;
+    const bool scaled = !bf16 && !q.few;   // products over W from two fp16 parts of scaled rows
+    const int64_t plane_row = !q.wpack ? 0 : q.kp * (bf16 ? 2 : 4);   // bytes of W's planes per row
     const int64_t all = ceil_div64(vocab, 256) * 256;
     int64_t most = all;
     if (plane_row > 0 && kPlaneBytes / plane_row < most) most = kPlaneBytes / plane_row;
-    if (d_row > 0 && kPieceBytes / d_row < most) most = kPieceBytes / d_row;
+    if (for_grad && kPieceElems / q.np < most) most = kPieceElems / q.np;
     most = most < 256 ? 256 : most / 256 * 256;
     q.piece = ceil_div64(ceil_div64(all, ceil_div64(all, most)), 256) * 256;   // equal pieces
     q.pieces = ceil_div64(all, q.piece);
@@ -142,21 +143,21 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
     q.cnt = take(256 + ceil_div64(q.np, kCountBlock) * 4);
     if (bf16 || for_grad || q.few) q.h = take(q.parts * q.np * q.kp * 2);
-    if (!bf16 && !q.few) {
+    if (scaled) {
         q.h16 = take(2 * q.np * q.kp * 2);
         q.hinv = take(q.np * 4);
-        q.w16 = take(2 * q.piece * q.kp * 2);
         q.winv = take(q.piece * 4);
+        q.wtop = take(4);
     }
     q.map = take(q.np * 4);
     q.tgt = take(q.np * 4);
-    if (q.wpack && (bf16 || for_grad)) q.w = take(q.parts * q.piece * q.kp * 2);
+    if (q.wpack) q.w = take(q.piece * plane_row);
     if (!for_grad) {
         q.part = take(q.np * q.nvt * 8);
         q.zt = take(q.np * 4);
     } else {
         const int64_t n = tokens < 1 ? 1 : tokens;
-        const int64_t terms_h = bf16 ? 1 : 6, terms_w = bf16 ? q.dparts : 6;
+        const int64_t terms_h = bf16 ? 1 : scaled ? 3 : 6, terms_w = bf16 ? q.dparts : 6;
         q.tile_h = q.few ? TILE_32 : pick_tile(width, n, q.piece, terms_h);
         q.tile_w = n <= kShortTokens ? TILE_128 : pick_tile(width, q.piece, n, terms_w);
         q.split_h = pick_split(width, n, q.piece, terms_h, q.tile_h);
@@ -164,6 +165,10 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         q.lg = take(q.np * 8);
         q.rest = take(q.np * 4);
         q.dl = take(q.dparts * q.np * q.piece * 2);
+        if (scaled) {
+            q.dl16 = take(2 * q.np * q.piece * 2);
+            q.gscale = take(q.np * 4);
+        }
         if (q.pieces > 1 || q.split_h > 1) q.acc_h = take(q.split_h * q.np * q.dp * 4);
         if (q.split_w > 1) q.acc_w = take(q.split_w * q.piece * q.dp * 4);
     }

@@ -216,9 +216,9 @@ def test_loss_gradient(cuda, tokens, vocab, width, dt, wdt, accumulate):
 
 
 # sizes that go through several pieces of the vocabulary: D's bytes (many tokens), W's planes (wide fp32), D of few tokens
-@pytest.mark.parametrize("tokens,vocab,width,dt", [(16384, 6000, 64, "f32"), (65536, 5000, 32, "bf16"), (100001, 300, 16, "bf16"),
-                                                   (200, 60000, 4096, "f32"),
-                                                   (3, 400000, 8, "f32"), (193, 9000, 68, "f32"), (192, 9000, 68, "f32")])
+@pytest.mark.parametrize("tokens,vocab,width,dt", [(32768, 9000, 24, "f32"), (65536, 5000, 32, "bf16"), (100001, 300, 16, "bf16"),
+                                                   (200, 140000, 4096, "f32"),
+                                                   (3, 1100000, 8, "f32"), (193, 9000, 68, "f32"), (192, 9000, 68, "f32")])
 def test_pieces_of_the_vocabulary(cuda, tokens, vocab, width, dt):
     import rank_orthonormalized_optimizer_amd as dion
     g = gen(cuda, tokens, vocab, width, 3)
@@ -279,6 +279,25 @@ def test_fp32_rows_of_any_scale(cuda, tokens):
     W *= torch.exp2(torch.randint(-40, 1, (700, 1), generator=g, device=cuda).float())
     H[3], W[5] = 0, 0
     grad = torch.ones(1, device=cuda)
+    loss, lse = dion.linear_cross_entropy_(H, W, y)
+    dH, dW = torch.empty_like(H), torch.empty_like(W)
+    dion.linear_cross_entropy_grad_(H, W, y, lse, grad, dH, dW)
+    want = Head(H, W, y, grad=grad)
+    close(loss, want.loss, want.loss_bound, "loss")
+    close(dH, want.dH, want.dH_bound, "dH")
+    close(dW, want.dW, want.dW_bound, "dW")
+
+
+@pytest.mark.parametrize("vocab,scale", [(300, 2.0 ** -30), (300, 1.0), (1000, 2.0 ** 20)])
+def test_fp32_padded_vocabulary(cuda, vocab, scale):
+    """Rows of zeros behind the true vocabulary take nothing from the others' precision, whatever their size."""
+    import rank_orthonormalized_optimizer_amd as dion
+    g = gen(cuda, vocab, 11)
+    H, W, y = head_inputs(g, 200, vocab, 72, F32, cuda)
+    H /= scale
+    W *= scale
+    W[vocab - 60:] = 0
+    grad = torch.rand(200, generator=g, device=cuda) * 2.0 ** -20
     loss, lse = dion.linear_cross_entropy_(H, W, y)
     dH, dW = torch.empty_like(H), torch.empty_like(W)
     dion.linear_cross_entropy_grad_(H, W, y, lse, grad, dH, dW)

@@ -18,6 +18,9 @@ lse      the largest logit error, plus sums of at most V exponentials (added in 
 D        p (error of the logit and lse, and four u), then grad's multiplication and the rounding of
          D to its parts: 2^-8 for one bf16 part, u for three.
 dH, dW   those errors through the products, and the products' own additions as for the logits.
+         dH of fp32 operands may come from two fp16 parts of D times W's inverse row scales (at most `top`) and of the
+         scaled rows of W: 2^-23 of each factor and 2^-22 for the dropped l l, 8 u in all, and where a low part of D is
+         subnormal 2^-39 top |W / inverse|, at most 2^-38 max |W| per row of W (a power of two of grad's size outside).
 """
 import math
 
@@ -93,6 +96,9 @@ class Head:
         rw = half_step(torch.bfloat16) if dparts == 1 else U
         self.dH = D @ w
         self.dH_bound = bound(rh, w, nh, V, True) + half_step(H.dtype) * self.dH.abs()
+        if parts == 3:
+            size_g = torch.where(keep, g, 0.0).abs()[:, None]
+            self.dH_bound = self.dH_bound + 8 * U * (D.abs() @ w.abs()) + 2.0 ** -38 * V * w.abs().max() * size_g
         old = 0.0 if dw_old is None else dw_old.to(f64)
         self.dW = D.t() @ h + old
         self.dW_bound = bound(rw, h, {(1, 1): 1, (1, 3): 3, (3, 3): 6}[parts, dparts], y.numel(), False) \
