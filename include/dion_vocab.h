@@ -95,7 +95,8 @@ int dion_linear_xent(const void* H, const void* W, const void* targets, float* l
  * Arithmetic: for bf16 outputs of bf16 operands D is rounded once to bf16 (without grad where grad_n is 1: that factor is
  * applied to the fp32 sums), and what the rounding left of the target's element is added to dH in fp32.  Where the output or
  * the operands are fp32, the products are fp32-accurate, from 16-bit parts as in dion_linear_xent: dW from three bf16 parts
- * of D and H, dH from three bf16 parts or from two scaled fp16 parts of D and W.
+ * of D and H, dH from three bf16 parts, or from two fp16 parts of D (per token) and of W (per row) scaled by powers of two,
+ * which leaves out 2^-39 of |grad[t]| times the largest |W| besides.
  */
 int dion_linear_xent_grad(const void* H, const void* W, const void* targets, const float* lse, const float* grad,
                           int64_t grad_n, void* dH, void* dW, int64_t tokens, int64_t vocab, int64_t width,

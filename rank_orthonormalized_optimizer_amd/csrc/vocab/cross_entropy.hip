@@ -743,10 +743,10 @@ using F64 = mm::Config<64, 64, 2, 2, 8, false, false, true>;
 using F256 = mm::Config<256, 256, 2, 4, 2, false, false, true>;
 using F128 = mm::Config<128, 128, 2, 2, 4, false, false, true>;
 using F32 = mm::Config<128, 32, 4, 1, 4, false, false, true>;
-using P32 = mm::FewConfig<32, 3, false>;
-using P64 = mm::FewConfig<64, 2, false>;
-using Q32 = mm::FewConfig<32, 3, true>;
-using Q64 = mm::FewConfig<64, 2, true>;
+template <bool V4> using P32 = mm::FewConfig<32, 3, false, V4>;
+template <bool V4> using P64 = mm::FewConfig<64, 2, false, V4>;
+template <bool V4> using Q32 = mm::FewConfig<32, 3, true, V4>;
+template <bool V4> using Q64 = mm::FewConfig<64, 2, true, V4>;
 using E256 = mm::Config<256, 256, 2, 4, 2, true, false, true>;
 using E128 = mm::Config<128, 128, 2, 2, 4, true, false, true>;
 using E64 = mm::Config<64, 64, 2, 2, 8, true, false, true>;
@@ -780,12 +780,18 @@ void launch_logits(const LogitArgs& a, int tile, int64_t n, hipStream_t s) {
     else launch_logits<C32, EPI>(a, n, s);
 }
 
+template <bool V4, int EPI>
+void launch_few_logits(const LogitArgs& a, int64_t n, hipStream_t s) {
+    if (n <= 32) launch_logits<P32<V4>, EPI>(a, n, s);
+    else launch_logits<P64<V4>, EPI>(a, n, s);
+}
+
 template <int EPI>
 void launch_logits(const LogitArgs& a, const XentPlan& p, hipStream_t s) {
     if (p.parts == 1) launch_logits<Z256, Z128, Z64, Z32, EPI>(a, p.tile_z, p.n, s);
     else if constexpr (EPI != EPI_D1) {   // fp32: D in three parts
-        if (p.few && p.n <= 32) launch_logits<P32, EPI>(a, p.n, s);
-        else if (p.few) launch_logits<P64, EPI>(a, p.n, s);
+        if (p.few && p.d % 4 == 0) launch_few_logits<true, EPI>(a, p.n, s);
+        else if (p.few) launch_few_logits<false, EPI>(a, p.n, s);
         else launch_logits<F256, F128, F64, F32, EPI>(a, p.tile_z, p.n, s);
     }
 }
@@ -846,6 +852,12 @@ template <class C>
 void launch_out(const OutArgs& a, int64_t rows, hipStream_t s) {
     const int64_t t = ceil_div64(a.d, C::BM) * ceil_div64(rows, C::BN) * a.split;
     hipLaunchKernelGGL((out_kernel<C>), walkers<C>(t), dim3(C::THREADS), 0, s, a);
+}
+
+template <bool V4>
+void launch_few_out(const OutArgs& a, int64_t n, hipStream_t s) {
+    if (n <= 32) launch_out<Q32<V4>>(a, n, s);
+    else launch_out<Q64<V4>>(a, n, s);
 }
 
 void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
@@ -916,8 +928,8 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             h.k = (int)(ceil_div64(rows, 64) * 64);
             h.k_per = (int)(ceil_div64(ceil_div64(h.k, p.split_h), 64) * 64);
             h.add = v0 > 0;
-            if (p.few && p.n <= 32) launch_out<Q32>(h, p.n, s);
-            else if (p.few) launch_out<Q64>(h, p.n, s);
+            if (p.few && p.d % 4 == 0) launch_few_out<true>(h, p.n, s);
+            else if (p.few) launch_few_out<false>(h, p.n, s);
             else if (scaled && p.tile_h == TILE_256) launch_out<E256>(h, p.n, s);
             else if (scaled && p.tile_h == TILE_128) launch_out<E128>(h, p.n, s);
             else if (scaled && p.tile_h == TILE_64) launch_out<E64>(h, p.n, s);

@@ -55,13 +55,18 @@ struct Segments {
 
 constexpr uint32_t kOutside = 0x80000000u;   // an offset outside every descriptor's range
 
-// 16 bytes per lane from the descriptor's range (zeros outside it) to 1 KB of LDS at byte address lds, which
-// must be the same for all lanes.  Written as assembly because the compiler waits for every load in flight before a
-// transposed LDS read that follows the builtin of this load, wherever it reads; it names no output register, and
+// WORDS (1 or 4) words per lane from the descriptor's range (zeros outside it) to 256 WORDS bytes of LDS at byte address
+// lds, which must be the same for all lanes.  Written as assembly because the compiler waits for every load in flight before
+// a transposed LDS read that follows the builtin of this load, wherever it reads; it names no output register, and
 // wait_slab() is what waits for it.  (m0 is the compiler's only for instructions that do not occur here.)
+template <int WORDS>
 __device__ __forceinline__ void load_to_lds(u32x4 desc, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(desc),
-                 "s"(__builtin_amdgcn_readfirstlane(lds)));
+    if constexpr (WORDS == 4)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(desc),
+                     "s"(__builtin_amdgcn_readfirstlane(lds)));
+    else
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(desc),
+                     "s"(__builtin_amdgcn_readfirstlane(lds)));
 }
 
 template <int X>   // rows of 16-byte chunks per [64][X] row
@@ -107,7 +112,7 @@ struct Tile {
     }
     // Starts the i-th of this wave's loads of a slab into lds (this tile's image).
     __device__ __forceinline__ void load(u32x4 r, int i, uint32_t lds, int wave) const {
-        load_to_lds(r, off[i], lds + (wave * kLoads + i) * 1024);
+        load_to_lds<4>(r, off[i], lds + (wave * kLoads + i) * 1024);
     }
     // Fragment of the 16 rows from x (a multiple of 16, relative to the tile), k step ks (0 or 1).
     static __device__ __forceinline__ u32x4 frag(uint16_t* lds, int x, int ks, int lane) {
@@ -297,17 +302,17 @@ private:
 };
 
 // ---------------------------------------------------------------------------
-// Products of few columns with an fp32 matrix read in place: A is fp32 ([x][k] or transposed [k][x], rows of a multiple of
-// four elements), B three bf16 planes.  Such a product is a stream of A: its tiles go to LDS as they are, and a wave splits
+// Products of few columns with an fp32 matrix read in place: A is fp32 ([x][k] or transposed [k][x]; V4: rows of a multiple
+// of four elements, loaded 16 bytes per lane, else four), B three bf16 planes.  Such a product is a stream of A: its tiles go to LDS as they are, and a wave splits
 // its fragments into the three parts in registers, all six part products of a slab at once.  (Planes of A in the workspace
 // would be written and read again: 4 + 6 bytes per element and more.)  A tile of 128 rows, eight waves of 16 rows each.
 //
 // LDS image of a [128][64] fp32 tile: 16-byte chunk c of row x at c ^ (x & 15); of a transposed [64][128] one: chunk c of
 // row k at c ^ 4 (k / 8 % 4), so that the four rows that a read takes together fall on different banks.
-template <int BN_, int STAGES_, bool TA_>
+template <int BN_, int STAGES_, bool TA_, bool V4_>
 struct FewConfig {
     static constexpr int BM = 128, BN = BN_, WM = 8, WN = 1, STAGES = STAGES_;
-    static constexpr bool TA = TA_, TB = false, F16 = false, FEW = true;
+    static constexpr bool TA = TA_, TB = false, F16 = false, FEW = true, V4 = V4_;
     static constexpr int WAVES = 8, THREADS = 512, MI = 1, NI = BN / 16;
     static constexpr int kA = BM * kBK * 2, kStage = kA + 3 * BN * kBK;   // in 16-bit elements
     static constexpr int kLds = STAGES * kStage;
@@ -318,7 +323,8 @@ struct FewConfig {
 template <class C>
 struct FewProduct {
     using TileB = Tile<C::BN, false, 4>;   // the planes are loaded by four waves each, two at a time
-    static constexpr int kLoadsA = C::BM * kBK * 4 / 1024 / 8, kLoadsB = 3 * C::BN * kBK * 2 / 1024;   // per wave; per workgroup
+    static constexpr int kVec = C::V4 ? 4 : 1;   // elements of A per lane and load
+    static constexpr int kLoadsA = C::BM * kBK / (64 * kVec) / 8, kLoadsB = 3 * C::BN * kBK * 2 / 1024;   // per wave; per workgroup
     static constexpr int kRowsB = kBK * 2 * 8;   // bytes of eight rows of a plane: one wave load
 
     int lane, wave, xa, xb, total, m0, n0;
@@ -386,15 +392,16 @@ private:
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i) {
             const int q = wave * kLoadsA + i;
+            const int at = (q * 64 + lane) * kVec, chunk = at / 4, e = at % 4;   // this lane's element of the image
             uint32_t off;
             if constexpr (!C::TA) {
-                const int x = q * 4 + lane / 16, c = (lane % 16) ^ (x & 15);
-                off = k + 4 * c < width ? (uint32_t)(x * width + 4 * c) * 4u : kOutside;
+                const int x = chunk / 16, c = ((chunk % 16) ^ (x & 15)) * 4 + e;
+                off = k + c < width ? (uint32_t)(x * width + c) * 4u : kOutside;
             } else {
-                const int r = q * 2 + lane / 32, c = (lane % 32) ^ (((r >> 3) & 3) << 2), col = m0 + 4 * c;
+                const int r = chunk / 32, col = m0 + ((chunk % 32) ^ (((r >> 3) & 3) << 2)) * 4 + e;
                 off = col < width ? (uint32_t)(r * width + col) * 4u : kOutside;
             }
-            load_to_lds(ra, off, to + q * 1024);
+            load_to_lds<kVec>(ra, off, to + q * 256 * kVec);
         }
         for (int q = wave; q < kLoadsB; q += 8) {   // eight rows of a plane each
             const int plane = q / (C::BN / 8), x = q % (C::BN / 8) * 8 + lane / 8, c = (lane % 8) ^ ((x >> 1) & 7);
@@ -402,7 +409,7 @@ private:
             const u32x4 rb{(uint32_t)__builtin_amdgcn_readfirstlane((int)pb),
                            (uint32_t)__builtin_amdgcn_readfirstlane((int)(pb >> 32)) & 0xffffu, 0x7fffffffu, 0x00027000u};
             const int row = n0 + x < b.rows ? x : b.rows - 1 - n0;
-            load_to_lds(rb, (uint32_t)(row * b.ld + c * 8) * 2u, to + C::kA * 2 + q * 1024);
+            load_to_lds<4>(rb, (uint32_t)(row * b.ld + c * 8) * 2u, to + C::kA * 2 + q * 1024);
         }
         k += kBK;
         if (++slot == C::STAGES) slot = 0;

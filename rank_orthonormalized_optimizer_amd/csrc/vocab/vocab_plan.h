@@ -80,6 +80,10 @@ enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 1
 // Elements of D per piece of the vocabulary: 512 MiB per bf16 part.  Four times as many gave -1 to +5% on 8192 tokens,
 // a fifth as many +14% (fp32, 4096 x 32000 x 1024: the products over a piece no longer fill the chip).
 constexpr int64_t kPieceElems = (int64_t)1 << 28;
+// but for many tokens as many as give the piece kPieceRows rows, up to kPieceMost: each piece adds to dH, a pass over
+// tokens x width in fp32 (131072 tokens x 32000 x 2048, bf16, with gradients: pieces of 2048 rows 60.9 ms, 4096 55.8, 8192
+// 53.0, 16384 53.7; fp32, 65536 tokens: 4096 rows 102.0 ms, 8192 95.9)
+constexpr int64_t kPieceRows = 8192, kPieceMost = (int64_t)1 << 30;
 constexpr int64_t kPlaneBytes = (int64_t)2048 << 20;   // of W's planes per piece: few pieces keep the products large
 constexpr int kCUs = 256;
 constexpr int kCountBlock = 4096;          // tokens per count of gathered rows,
@@ -126,14 +130,18 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.np = ceil_div64(tokens < 1 ? 1 : tokens, 256) * 256;
     q.parts = bf16 ? 1 : 3;
     q.dparts = bf16 && dw_bf16 ? 1 : 3;
-    q.few = !bf16 && width % 4 == 0 && tokens <= kFewTokens && vocab >= kFewVocab;
+    q.few = !bf16 && tokens <= kFewTokens && vocab >= kFewVocab;
     q.wpack = !q.few && (!bf16 || width % 64 != 0);
     const bool scaled = !bf16 && !q.few;   // products over W from two fp16 parts of scaled rows
     const int64_t plane_row = !q.wpack ? 0 : q.kp * (bf16 ? 2 : 4);   // bytes of W's planes per row
     const int64_t all = ceil_div64(vocab, 256) * 256;
     int64_t most = all;
     if (plane_row > 0 && kPlaneBytes / plane_row < most) most = kPlaneBytes / plane_row;
-    if (for_grad && kPieceElems / q.np < most) most = kPieceElems / q.np;
+    if (for_grad) {
+        const int64_t fit = kPieceMost / q.np, few = fit < kPieceRows ? fit : kPieceRows;
+        const int64_t rows = kPieceElems / q.np > few ? kPieceElems / q.np : few;
+        if (rows < most) most = rows;
+    }
     most = most < 256 ? 256 : most / 256 * 256;
     q.piece = ceil_div64(ceil_div64(all, ceil_div64(all, most)), 256) * 256;   // equal pieces
     q.pieces = ceil_div64(all, q.piece);

@@ -156,7 +156,8 @@ def test_table_gradient_matches_differences(cuda):
 
 # ---------------------------------------------------------------------------- linear cross entropy
 HEAD = [(1, 1, 1), (1, 7, 3), (1, 300, 64), (5, 257, 65), (32, 129, 8), (33, 1000, 72), (64, 256, 64), (100, 130, 200),
-        (257, 1013, 255), (700, 2048, 128), (1024, 8192, 128), (2048, 300, 4096), (70, 2048, 4160), (3, 40000, 96)]
+        (257, 1013, 255), (700, 2048, 128), (1024, 8192, 128), (2048, 300, 4096), (70, 2048, 4160), (3, 40000, 96),
+        (1, 16384, 3), (5, 20011, 70), (33, 16500, 133), (128, 16385, 65)]   # fp32: W read in place, rows of any length
 
 
 def head_inputs(g, tokens, vocab, width, dt, device, ignored=0.2):
@@ -217,6 +218,7 @@ def test_loss_gradient(cuda, tokens, vocab, width, dt, wdt, accumulate):
 
 # sizes that go through several pieces of the vocabulary: D's bytes (many tokens), W's planes (wide fp32), D of few tokens
 @pytest.mark.parametrize("tokens,vocab,width,dt", [(32768, 9000, 24, "f32"), (65536, 5000, 32, "bf16"), (100001, 300, 16, "bf16"),
+                                                   (65536, 9000, 32, "bf16"), (200001, 8000, 16, "bf16"),
                                                    (200, 140000, 4096, "f32"),
                                                    (3, 1100000, 8, "f32"), (193, 9000, 68, "f32"), (192, 9000, 68, "f32")])
 def test_pieces_of_the_vocabulary(cuda, tokens, vocab, width, dt):
