@@ -110,29 +110,30 @@ __device__ __forceinline__ int64_t load_target(const XentArgs& a, int64_t i) {
     return a.t64 ? ((const int64_t*)a.targets)[i] : (int64_t)((const int32_t*)a.targets)[i];
 }
 
-// eight elements of a row of length d from column c, zeros past its end; V8: rows 16-byte aligned
-template <bool BF16, bool V8>
+// Vectors at any element's address: rows of any length start there, and the memory unit takes such accesses whole.
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+
+// eight elements of a row of length d from column c, zeros past its end
+template <bool BF16>
 __device__ __forceinline__ void load8(const void* p, int64_t row, int64_t c, int64_t d, float (&v)[8]) {
-    if constexpr (V8) {
-        if (c >= d) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        } else if constexpr (BF16) {
-            const u32x4 w = *(const u32x4*)((const uint16_t*)p + row + c);
+    if (c + 8 <= d) {
+        if constexpr (BF16) {
+            const u32x4 w = *(const u32x4_any*)((const uint16_t*)p + row + c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) { v[2 * e] = up16(w[e]); v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u); }
         } else {
-            const f32x4 w0 = *(const f32x4*)((const float*)p + row + c), w1 = *(const f32x4*)((const float*)p + row + c + 4);
+            const f32x4_any* q = (const f32x4_any*)((const float*)p + row + c);
+            const f32x4 w0 = q[0], w1 = q[1];
 #pragma unroll
             for (int e = 0; e < 4; ++e) { v[e] = w0[e]; v[4 + e] = w1[e]; }
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const bool in = c + e < d;
-            const int64_t i = row + (in ? c + e : 0);
-            const float f = BF16 ? up16(((const uint16_t*)p)[i]) : ((const float*)p)[i];
-            v[e] = in ? f : 0.f;
+            v[e] = 0.f;
+            if (c + e < d) v[e] = BF16 ? up16(((const uint16_t*)p)[row + c + e]) : ((const float*)p)[row + c + e];
         }
     }
 }
@@ -166,7 +167,7 @@ __device__ __forceinline__ void store8_f16(uint16_t* out, int64_t plane, int64_t
 
 // One row of a matrix to its planes by one wave: fp32 rows become fp16 planes with the row's scale (p16, inv, if p16 is
 // given) and bf16 planes (p, if given); bf16 rows are copied to p.  Columns up to kp are zero.
-template <bool BF16, bool V8>
+template <bool BF16>
 __device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d, int64_t kp, uint16_t* p, int64_t plane,
                                          uint16_t* p16, int64_t plane16, float* inv, int64_t to, int lane) {
     float scale = 1.f;
@@ -175,7 +176,7 @@ __device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d,
 #pragma unroll 4
         for (int64_t c = lane * 8; c < kp; c += 512) {
             float v[8];
-            load8<BF16, V8>(in, row * d, c, d, v);
+            load8<BF16>(in, row * d, c, d, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
         }
@@ -188,7 +189,7 @@ __device__ __forceinline__ void pack_row(const void* in, int64_t row, int64_t d,
 #pragma unroll 4
     for (int64_t c = lane * 8; c < kp; c += 512) {
         float v[8];
-        load8<BF16, V8>(in, row * d, c, d, v);
+        load8<BF16>(in, row * d, c, d, v);
         if (!BF16 && p16) store8_f16(p16, plane16, to * kp + c, v, scale);
         if (p) store8<BF16 ? 1 : 3>(p, plane, to * kp + c, v);
     }
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(512) void count_kernel(PackArgs a) {
 
 // Eight tokens per workgroup, one per wave.  The workgroup counts the gathered rows before its own itself, a read of
 // the targets (or of the counts of whole blocks, and the targets since the last one) from L2.
-template <bool BF16, bool V8, bool GRAD>
+template <bool BF16, bool GRAD>
 __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
     __shared__ int before[8], slot[kPackRows];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -265,7 +266,7 @@ __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
     const int64_t t = t0 + w;
     if (t >= a.n) return;
     if (slot[w] >= 0) {
-        pack_row<BF16, V8>(a.x.H, t, a.d, a.kp, a.h, a.np * a.kp, a.h16, a.np * a.kp, a.inv, slot[w], lane);
+        pack_row<BF16>(a.x.H, t, a.d, a.kp, a.h, a.np * a.kp, a.h16, a.np * a.kp, a.inv, slot[w], lane);
     } else if (GRAD && a.x.dH) {
         for (int64_t col = lane; col < a.d; col += 64) {
             if (BF16) ((uint16_t*)a.x.dH)[t * a.d + col] = 0;
@@ -291,12 +292,12 @@ __global__ __launch_bounds__(1024) void top_kernel(const float* inv, int n, floa
 }
 
 // Planes of `rows` rows of W (from row0), a wave per row: fp16 ones of fp32 rows, a copy of bf16 ones.
-template <bool BF16, bool V8>
+template <bool BF16>
 __global__ __launch_bounds__(256) void plane_kernel(const void* W, int64_t row0, int64_t rows, int64_t d, int64_t kp,
                                                     uint16_t* p, uint16_t* p16, int64_t plane, float* inv) {
     const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (r < rows)
-        pack_row<BF16, V8>((const char*)W + row0 * d * (BF16 ? 2 : 4), r, d, kp, p, plane, p16, plane, inv, r, threadIdx.x & 63);
+        pack_row<BF16>((const char*)W + row0 * d * (BF16 ? 2 : 4), r, d, kp, p, plane, p16, plane, inv, r, threadIdx.x & 63);
 }
 
 // ---------------------------------------------------------------------------
@@ -594,14 +595,13 @@ struct OutArgs {
     const uint16_t* w;     // bf16 [vocab][d]
 };
 
-// n elements of the output from column c of row r of the reduction's result: four where the row's columns are a
-// multiple of four, fewer at a ragged end
+// n elements of the output from column c of row r of the reduction's result: four, fewer at a ragged end
 __device__ __forceinline__ void store_out(const OutArgs& a, int64_t r, int c, int n, float (&v)[4]) {
     if (a.rest && a.tgt[r] >= 0) {
         const float left = a.rest[r];
         const uint16_t* w = a.w + (int64_t)a.tgt[r] * a.d + c;
-        if (a.d % 4 == 0) {
-            const u32x2 x = *(const u32x2*)w;
+        if (n == 4) {
+            const u32x2 x = *(const u32x2_any*)w;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = fmaf(left, up16((x[e / 2] >> (16 * (e % 2))) & 0xffffu), v[e]);
         } else {
@@ -619,17 +619,17 @@ __device__ __forceinline__ void store_out(const OutArgs& a, int64_t r, int c, in
         for (int e = 0; e < 4; ++e) v[e] *= f;
     }
     const int64_t at = (a.map ? a.map[r] : r) * (int64_t)a.d + c;
-    if (a.d % 4 == 0) {
+    if (n == 4) {
         float o[4];
         if (a.out_bf16) {
-            u32x2* p = (u32x2*)((uint16_t*)a.out + at);
+            u32x2_any* p = (u32x2_any*)((uint16_t*)a.out + at);
             u32x2 w{0, 0};
             if (a.accumulate) w = *p;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = v[e] + (a.accumulate ? up16((w[e / 2] >> (16 * (e % 2))) & 0xffffu) : 0.f);
             *p = u32x2{down16(o[0]) | (down16(o[1]) << 16), down16(o[2]) | (down16(o[3]) << 16)};
         } else {
-            f32x4* p = (f32x4*)((float*)a.out + at);
+            f32x4_any* p = (f32x4_any*)((float*)a.out + at);
             f32x4 w{0.f, 0.f, 0.f, 0.f};
             if (a.accumulate) w = *p;
             *p = f32x4{w[0] + v[0], w[1] + v[1], w[2] + v[2], w[3] + v[3]};
@@ -800,13 +800,8 @@ template <bool GRAD>
 void launch_pack(const PackArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div64(a.n, kPackRows));
     if (a.blocks) hipLaunchKernelGGL(count_kernel, dim3((unsigned)ceil_div64(a.n, kCountBlock)), dim3(512), 0, s, a);
-    if (a.x.bf16) {
-        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<true, true, GRAD>), grid, dim3(512), 0, s, a);
-        else hipLaunchKernelGGL((pack_kernel<true, false, GRAD>), grid, dim3(512), 0, s, a);
-    } else {
-        if (a.d % 8 == 0) hipLaunchKernelGGL((pack_kernel<false, true, GRAD>), grid, dim3(512), 0, s, a);
-        else hipLaunchKernelGGL((pack_kernel<false, false, GRAD>), grid, dim3(512), 0, s, a);
-    }
+    if (a.x.bf16) hipLaunchKernelGGL((pack_kernel<true, GRAD>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((pack_kernel<false, GRAD>), grid, dim3(512), 0, s, a);
 }
 
 // W's rows [v0, v0 + rows) as an operand of both products over W: in place (bf16, or fp32 for few tokens), or as planes in
@@ -821,11 +816,9 @@ mm::Operand weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, 
     const int64_t plane = p.piece * p.kp;
     const dim3 grid((unsigned)ceil_div64(rows, 4));
     if (x.bf16) {
-        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<true, true>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
-        else hipLaunchKernelGGL((plane_kernel<true, false>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
+        hipLaunchKernelGGL((plane_kernel<true>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
     } else {
-        if (p.d % 8 == 0) hipLaunchKernelGGL((plane_kernel<false, true>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
-        else hipLaunchKernelGGL((plane_kernel<false, false>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
+        hipLaunchKernelGGL((plane_kernel<false>), grid, dim3(256), 0, s, x.W, v0, rows, p.d, p.kp, w, w16, plane, inv);
         if (top) hipLaunchKernelGGL(top_kernel, dim3(1), dim3(1024), 0, s, inv, (int)rows, (float*)(ws + p.wtop));
     }
     return mm::Operand{(uint16_t*)(ws + p.w), plane, p.kp, (int)rows};

@@ -168,7 +168,8 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         const int64_t terms_h = bf16 ? 1 : scaled ? 3 : 6, terms_w = bf16 ? q.dparts : 6;
         q.tile_h = q.few ? TILE_32 : pick_tile(width, n, q.piece, terms_h);
         q.tile_w = n <= kShortTokens ? TILE_128 : pick_tile(width, q.piece, n, terms_w);
-        q.split_h = pick_split(width, n, q.piece, terms_h, q.tile_h);
+        // (the products of few columns take 64 at a time where there are more than 32)
+        q.split_h = pick_split(width, q.few && n > 32 ? ceil_div64(n, 2) : n, q.piece, terms_h, q.tile_h);
         q.split_w = pick_split(width, q.piece, n, terms_w, q.tile_w);
         q.lg = take(q.np * 8);
         q.rest = take(q.np * 4);
