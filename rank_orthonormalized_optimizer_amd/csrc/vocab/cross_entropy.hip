@@ -552,10 +552,17 @@ __global__ __launch_bounds__(256) void loss_kernel(const float2* part, const flo
     const int j = (int)(blockIdx.x * 4 + (threadIdx.x >> 6)), lane = threadIdx.x & 63;
     if (j >= cnt[0]) return;
     float m = -INFINITY, s = 0.f;
-    for (int i = lane; i < nvt; i += 64) {
-        const float2 u = part[(int64_t)j * nvt + i];
-        const float top = fmaxf(m, u.x), ref = top == -INFINITY ? 0.f : top;
-        s = s * exp2_fast(m - ref) + u.y * exp2_fast(u.x - ref);
+    for (int i = lane; i < nvt; i += 64 * 8) {
+        float2 u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = i + 64 * e < nvt ? part[(int64_t)j * nvt + i + 64 * e] : float2{-INFINITY, 0.f};
+        float top = m;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, u[e].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        s *= exp2_fast(m - ref);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(u[e].y, exp2_fast(u[e].x - ref), s);
         m = top;
     }
 #pragma unroll
@@ -757,7 +764,7 @@ using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
 using H64 = mm::Config<64, 64, 2, 2, 8, true, false>;
 using W64 = mm::Config<64, 64, 2, 2, 8, true, true>;
 using W256 = mm::Config<256, 256, 2, 4, 2, true, true>;
-using W128s = mm::Config<128, 128, 2, 2, 2, true, true>;
+using Ws = mm::Config<128, 64, 2, 2, 2, true, true>;
 using W128 = mm::Config<128, 128, 2, 2, 4, true, true>;
 
 // One workgroup per tile, or as many as the chip holds, which then walk the tiles.
@@ -940,7 +947,7 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
             if (p.tile_w == TILE_256) launch_out<W256>(w, rows, s);
             else if (p.tile_w == TILE_64) launch_out<W64>(w, rows, s);
-            else if (p.n <= kShortTokens) launch_out<W128s>(w, rows, s);
+            else if (p.n <= kShortTokens) launch_out<Ws>(w, rows, s);
             else launch_out<W128>(w, rows, s);
             if (w.acc) launch_join(w, rows, s);
         }
