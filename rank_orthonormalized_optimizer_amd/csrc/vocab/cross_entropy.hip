@@ -729,6 +729,126 @@ __global__ __launch_bounds__(256) void join_kernel(OutArgs a) {
     if (lane == 0) store_out(a, r, c, n, v);
 }
 
+// Logits whose reduction was sliced: partial sums [split][n][piece], and the scales of fp16 parts (or null).
+struct SliceArgs {
+    const float* z;
+    int64_t n, piece;
+    int split, v;
+    const int* cnt;
+    const float* hinv;
+    const float* winv;
+    // D
+    const int* tgt;
+    const float2* lg;
+    const float* gscale;
+    const float* wtop;
+    uint16_t* dl;
+    uint16_t* dl16;
+    float* rest;
+    int64_t np;
+};
+
+// logits v .. v + 3 of gathered token j, -inf behind the vocabulary
+__device__ __forceinline__ f32x4 sum_slices(const SliceArgs& a, int64_t j, int v) {
+    f32x4 z{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < a.split; ++s) z += *(const f32x4*)(a.z + (s * a.n + j) * a.piece + v);
+    if (a.winv) {
+        const f32x4 w = *(const f32x4*)(a.winv + v);
+        const float h = a.hinv[j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = z[e] * h * w[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (v + e >= a.v) z[e] = -INFINITY;
+    return z;
+}
+
+// loss and lse from sliced logits, T threads (64 or 256) per gathered token
+template <int T>
+__global__ __launch_bounds__(256) void slice_loss_kernel(SliceArgs a, const int* map, float* loss, float* lse) {
+    __shared__ float2 red[4];
+    __shared__ float target[4];
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, team = threadIdx.x / T, at = threadIdx.x % T;
+    const int64_t j = (int64_t)blockIdx.x * (256 / T) + team;
+    const bool row = j < a.cnt[0];
+    float m = -INFINITY, s = 0.f;
+    if (row) {
+        const int y = a.tgt[j];
+        for (int v = at * 4; v < a.v; v += T * 4) {
+            const f32x4 z = sum_slices(a, j, v);
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, z[e] * kLog2e);
+            const float ref = top == -INFINITY ? 0.f : top;
+            s *= exp2_fast(m - ref);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s += exp2_fast(fmaf(z[e], kLog2e, -ref));
+                if (v + e == y) target[team] = z[e];
+            }
+            m = top;
+        }
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        const float um = __shfl_xor(m, o), us = __shfl_xor(s, o);
+        const float top = fmaxf(m, um), ref = top == -INFINITY ? 0.f : top;
+        s = s * exp2_fast(m - ref) + us * exp2_fast(um - ref);
+        m = top;
+    }
+    if (lane == 0) red[w] = float2{m, s};
+    __syncthreads();
+    if (at != 0 || !row) return;
+    if (T == 256) {
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            const float top = fmaxf(m, red[i].x), ref = top == -INFINITY ? 0.f : top;
+            s = s * exp2_fast(m - ref) + red[i].y * exp2_fast(red[i].x - ref);
+            m = top;
+        }
+    }
+    const float ls = logf(s), low = m * kLn2Low;
+    lse[map[j]] = fmaf(m, kLn2, ls) + low;
+    loss[map[j]] = a.tgt[j] < 0 ? __uint_as_float(0x7fc00000u) : fmaf(m, kLn2, -target[team]) + (ls + low);
+}
+
+// D from sliced logits as logit_kernel forms it, eight of a token's per thread, zeros up to a multiple of 64.
+template <int EPI>
+__global__ __launch_bounds__(256) void slice_grad_kernel(SliceArgs a) {
+    constexpr int PD = EPI == EPI_D3 ? 3 : 1;
+    const int64_t j = blockIdx.y;
+    const int v = (int)(blockIdx.x * 256 + threadIdx.x) * 8;
+    if (j >= a.cnt[0] || v >= (a.v + 63) / 64 * 64) return;
+    const int y = a.tgt[j];
+    const float2 lg = a.lg[j];
+    const f32x4 z0 = sum_slices(a, j, v), z1 = sum_slices(a, j, v + 4);
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float z = e < 4 ? z0[e & 3] : z1[e & 3];
+        p[e] = PD == 3 ? exp_exact(z, lg.x) : exp2_fast(fmaf(z, kLog2e, -(lg.x * kLog2e)));
+        if (v + e == y) {
+            p[e] -= 1.f;
+            const float d = p[e] * lg.y;
+            a.rest[j] = d - up16(down16(d));
+        }
+    }
+    if (a.dl) {
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = p[e] * lg.y;
+        store8<PD>(a.dl, a.np * a.piece, j * a.piece + v, d);
+    }
+    if (a.dl16) {
+        const float unit = lg.y / a.gscale[j] * (16384.f / a.wtop[0]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = v + e < a.v ? p[e] * (unit * a.winv[v + e]) : 0.f;
+        store8_f16(a.dl16, a.np * a.piece, j * a.piece + v, p, 1.f);
+    }
+}
+
 // plane pairs (A's part, B's part), smallest products first
 mm::Segments segments(int pa, int pb) {
     auto list = [](std::initializer_list<int> e) {
@@ -866,6 +986,33 @@ void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
     else hipLaunchKernelGGL((join_kernel<1>), dim3((unsigned)ceil_div64(n, 256)), dim3(256), 0, s, a);
 }
 
+// The logits with their reduction in slices, as partial sums of an output of p.n rows of p.piece columns.
+template <bool V4>
+void launch_few_slices(const OutArgs& a, int64_t n, hipStream_t s) {
+    if (n <= 32) launch_out<P32<V4>>(a, n, s);
+    else launch_out<P64<V4>>(a, n, s);
+}
+
+SliceArgs launch_slices(const LogitArgs& z, const XentPlan& p, char* ws, hipStream_t s) {
+    OutArgs o{};
+    o.a = z.w; o.b = z.h; o.seg = z.seg; o.cnt = z.cnt; o.d = z.w.rows; o.dp = (int)p.piece; o.rows = -1; o.k = z.kp;
+    o.split = (int)p.split_z; o.k_per = (int)(ceil_div64(p.kp / 64, p.split_z) * 64);
+    o.acc = (float*)(ws + p.z); o.acc_rows = p.n;
+    if (p.few && p.d % 4 == 0) launch_few_slices<true>(o, p.n, s);
+    else if (p.few) launch_few_slices<false>(o, p.n, s);
+    else if (p.parts == 1 && p.tile_z == TILE_256) launch_out<Z256>(o, p.n, s);
+    else if (p.parts == 1 && p.tile_z == TILE_128) launch_out<Z128>(o, p.n, s);
+    else if (p.parts == 1 && p.tile_z == TILE_64) launch_out<Z64>(o, p.n, s);
+    else if (p.parts == 1) launch_out<Z32>(o, p.n, s);
+    else if (p.tile_z == TILE_256) launch_out<F256>(o, p.n, s);
+    else if (p.tile_z == TILE_128) launch_out<F128>(o, p.n, s);
+    else if (p.tile_z == TILE_64) launch_out<F64>(o, p.n, s);
+    else launch_out<F32>(o, p.n, s);
+    const bool scaled = p.parts > 1 && !p.few;
+    return SliceArgs{o.acc, p.n, p.piece, o.split, (int)p.v, z.cnt, scaled ? z.hinv : nullptr, scaled ? z.winv : nullptr,
+                     z.tgt, z.lg, z.gscale, z.wtop, z.dl, z.dl16, z.rest, p.np};
+}
+
 }  // namespace
 
 int run_xent(const XentArgs& x, const XentPlan& p, char* ws, void* stream) {
@@ -873,6 +1020,13 @@ int run_xent(const XentArgs& x, const XentPlan& p, char* ws, void* stream) {
     const PackArgs pk = pack_args(x, p, ws, false);
     launch_pack<false>(pk, s);
     LogitArgs a = logit_args(p, pk, ws);
+    if (p.split_z > 1) {
+        a.w = weights(x, p, ws, 0, p.v, false, s);
+        const SliceArgs z = launch_slices(a, p, ws, s);
+        if (p.v <= 1024) hipLaunchKernelGGL((slice_loss_kernel<64>), dim3((unsigned)ceil_div64(p.n, 4)), dim3(256), 0, s, z, pk.map, x.loss, x.lse_out);
+        else hipLaunchKernelGGL((slice_loss_kernel<256>), dim3((unsigned)p.n), dim3(256), 0, s, z, pk.map, x.loss, x.lse_out);
+        return (int)hipGetLastError();
+    }
     a.part = (float2*)(ws + p.part); a.zt = (float*)(ws + p.zt); a.nvt = (int)p.nvt;
     for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
         a.w = weights(x, p, ws, v0, p.v - v0 < p.piece ? p.v - v0 : p.piece, false, s);
@@ -919,7 +1073,12 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
         const int64_t rows = p.v - v0 < p.piece ? p.v - v0 : p.piece;
         z.w = weights(x, p, ws, v0, rows, x.dH != nullptr, s);
         z.v0 = (int)v0;
-        if (p.dparts == 1) launch_logits<EPI_D1>(z, p, s);
+        if (p.split_z > 1) {
+            const SliceArgs a = launch_slices(z, p, ws, s);
+            const dim3 grid((unsigned)ceil_div64(p.v, 256 * 8), (unsigned)p.n);
+            if (p.dparts == 1) hipLaunchKernelGGL((slice_grad_kernel<EPI_D1>), grid, dim3(256), 0, s, a);
+            else hipLaunchKernelGGL((slice_grad_kernel<EPI_D3>), grid, dim3(256), 0, s, a);
+        } else if (p.dparts == 1) launch_logits<EPI_D1>(z, p, s);
         else launch_logits<EPI_D3>(z, p, s);
         if (x.dH) {
             h.a = z.w;

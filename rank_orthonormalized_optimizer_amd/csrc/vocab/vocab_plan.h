@@ -72,8 +72,8 @@ struct XentPlan {
     int64_t piece, pieces;
     int64_t nvt;              // softmax partials per token (forward)
     int tile_z, tile_h, tile_w;   // tile shapes of the logits, dH and dW (TILE_*)
-    int64_t split_h, split_w; // slices of the reductions of dH (over the piece) and dW (over the tokens)
-    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, w, winv, wtop, gscale, dl, dl16, rest, acc_h, acc_w, total;
+    int64_t split_z, split_h, split_w;   // slices of the reductions of the logits (over the width), dH (the piece), dW (the tokens)
+    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, z, w, winv, wtop, gscale, dl, dl16, rest, acc_h, acc_w, total;
 };
 
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens), 64 x 64
@@ -94,7 +94,7 @@ constexpr int64_t kShortTokens = 128;
 // fp32: up to so many tokens the products over W read it in place (see FewProduct), if W has tiles for half the CUs.
 // 32000 x 1024 with gradients: 65 tokens 255 us against 455 through planes of W in the workspace, 128 tokens 367 and
 // 483, 200 tokens 550 and 555; 100544 x 2624: 164 tokens 3.4 ms against 2.4
-constexpr int64_t kFewTokens = 128, kFewVocab = 16384;
+constexpr int64_t kFewTokens = 128, kFewVocab = 1024;
 
 inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : t == TILE_64 ? 64 : 128; }
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : t == TILE_64 ? 64 : 32; }
@@ -147,6 +147,17 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.piece = ceil_div64(ceil_div64(all, ceil_div64(all, most)), 256) * 256;   // equal pieces
     q.pieces = ceil_div64(all, q.piece);
     q.tile_z = q.few ? TILE_32 : pick_logit_tile(q.piece, tokens);
+    q.split_z = 1;
+    const int64_t zn = q.few && tokens > 32 ? ceil_div64(tokens, 2) : tokens;   // few: 64 columns a tile
+    if (q.pieces == 1 && tokens > 0 && tiles(q.piece, zn, q.few ? TILE_32 : TILE_128) < kCUs) {
+        const int64_t terms = bf16 ? 1 : q.few ? 6 : 3;
+        const int t = q.few ? TILE_32 : pick_tile(q.piece, zn, width, terms);
+        const int64_t slabs = ceil_div64(width, 64), s = pick_split(q.piece, zn, width, terms, t);
+        if (s > 1) {
+            q.tile_z = t;
+            q.split_z = ceil_div64(slabs, ceil_div64(slabs, s));   // none without any k
+        }
+    }
     q.nvt = ceil_div64(vocab, tile_m(q.tile_z));
     size_t off = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
@@ -161,9 +172,12 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.map = take(q.np * 4);
     q.tgt = take(q.np * 4);
     if (q.wpack) q.w = take(q.piece * plane_row);
+    if (q.split_z > 1) q.z = take(q.split_z * tokens * q.piece * 4);
     if (!for_grad) {
-        q.part = take(q.np * q.nvt * 8);
-        q.zt = take(q.np * 4);
+        if (q.split_z == 1) {
+            q.part = take(q.np * q.nvt * 8);
+            q.zt = take(q.np * 4);
+        }
     } else {
         const int64_t n = tokens < 1 ? 1 : tokens;
         const int64_t terms_h = bf16 ? 1 : scaled ? 3 : 6, terms_w = bf16 ? q.dparts : 6;

@@ -158,6 +158,7 @@ def test_table_gradient_matches_differences(cuda):
 HEAD = [(1, 1, 1), (1, 7, 3), (1, 300, 64), (5, 257, 65), (32, 129, 8), (33, 1000, 72), (64, 256, 64), (100, 130, 200),
         (257, 1013, 255), (700, 2048, 128), (1024, 8192, 128), (2048, 300, 4096), (70, 2048, 4160), (3, 40000, 96),
         (1, 16384, 3), (5, 20011, 70), (33, 16500, 133), (128, 16385, 65)]   # fp32: W read in place, rows of any length
+HEAD += [(1, 1030, 700), (20, 2000, 1290), (129, 1500, 1000), (300, 257, 2100), (33, 12347, 1100), (1198, 1640, 770)]   # sliced logits
 
 
 def head_inputs(g, tokens, vocab, width, dt, device, ignored=0.2):
