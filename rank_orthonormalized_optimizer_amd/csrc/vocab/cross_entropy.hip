@@ -708,6 +708,50 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
     }
 }
 
+// dW of up to N tokens, a stream of writes: four columns of H's rows per thread in registers, D's columns in LDS, fp32 sums.
+// D and H come from the parts that the other products use (their sum is exact).
+template <int N>
+__global__ __launch_bounds__(256) void rank_out_kernel(OutArgs a, int hparts, int dparts) {
+    constexpr int R = 64;
+    __shared__ __attribute__((aligned(16))) float d[R][N];
+    const int count = a.cnt[0], c = (int)(blockIdx.y * 256 + threadIdx.x) * 4, n = a.d - c < 4 ? a.d - c : 4;
+    f32x4 h[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        h[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (j < count && n > 0)   // (H's planes have columns up to a multiple of 64)
+            for (int q = hparts - 1; q >= 0; --q) {
+                const u32x2 w = *(const u32x2*)(a.a.p + q * a.a.plane + j * a.a.ld + c);
+                h[j] += f32x4{up16(w[0] & 0xffffu), up16(w[0] >> 16), up16(w[1] & 0xffffu), up16(w[1] >> 16)};
+            }
+    }
+    for (int r0 = blockIdx.x * R; r0 < a.rows; r0 += gridDim.x * R) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < R * N; i += 256) {
+            const int r = i % R, j = i / R;
+            float x = 0.f;
+            if (j < count && r0 + r < a.rows)
+                for (int q = dparts - 1; q >= 0; --q) x += up16(a.b.p[q * a.b.plane + j * a.b.ld + r0 + r]);
+            d[r][j] = x;
+        }
+        __syncthreads();
+        if (n <= 0) continue;
+        const int rows = a.rows - r0 < R ? a.rows - r0 : R;
+#pragma unroll 2
+        for (int r = 0; r < rows; ++r) {
+            f32x4 sum{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float x = d[r][j];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = fmaf(x, h[j][e], sum[e]);
+            }
+            float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+            store_out(a, r0 + r, c, n, v);
+        }
+    }
+}
+
 // The slices' sums, rounded to the output: four columns per group of G lanes, which share the slices (many slices come
 // with few outputs).
 template <int G>
@@ -986,6 +1030,13 @@ void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
     else hipLaunchKernelGGL((join_kernel<1>), dim3((unsigned)ceil_div64(n, 256)), dim3(256), 0, s, a);
 }
 
+template <int N>
+void launch_rank(const OutArgs& a, const XentPlan& p, hipStream_t s) {
+    const int64_t across = ceil_div64(a.d, 1024), down = ceil_div64(a.rows, 64), most = ceil_div64(kCUs * 8, across);
+    hipLaunchKernelGGL((rank_out_kernel<N>), dim3((unsigned)(down < most ? down : most), (unsigned)across), dim3(256), 0, s, a,
+                       p.parts, p.dparts);
+}
+
 // The logits with their reduction in slices, as partial sums of an output of p.n rows of p.piece columns.
 template <bool V4>
 void launch_few_slices(const OutArgs& a, int64_t n, hipStream_t s) {
@@ -1104,7 +1155,9 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             w.rows = (int)rows;
             w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);
             w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
-            if (p.tile_w == TILE_256) launch_out<W256>(w, rows, s);
+            if (p.n <= 8) launch_rank<8>(w, p, s);
+            else if (p.n <= kRankTokens) launch_rank<16>(w, p, s);
+            else if (p.tile_w == TILE_256) launch_out<W256>(w, rows, s);
             else if (p.tile_w == TILE_64) launch_out<W64>(w, rows, s);
             else if (p.n <= kShortTokens) launch_out<Ws>(w, rows, s);
             else launch_out<W128>(w, rows, s);

@@ -91,6 +91,9 @@ constexpr int64_t kCountDirect = 16384;    // which fewer tokens than this do wi
 // dW of so few tokens is a stream of writes: three workgroups per CU with tiles of 128 x 64 (128 x 128 and two: 22 tokens x
 // 111040 x 1024 bf16 with gradients 297 us instead of 275, 64 x 64 and four 272, but fp32 4 x 115186 x 636 441 us, not 414)
 constexpr int64_t kShortTokens = 128;
+// and of so few, with fp32 sums in the vector units (with gradients, matrix cores against that: fp32 2 x 82297 x 2232 949 and
+// 780 us, 8 x 32000 x 2048 316 and 267; bf16 9 x 40448 x 1024 113 and 107; 17 and more tokens 5 to 24% slower that way)
+constexpr int64_t kRankTokens = 16;
 // fp32: up to so many tokens the products over W read it in place (see FewProduct), if W has tiles for half the CUs.
 // 32000 x 1024 with gradients: 65 tokens 255 us against 455 through planes of W in the workspace, 128 tokens 367 and
 // 483, 200 tokens 550 and 555; 100544 x 2624: 164 tokens 3.4 ms against 2.4
