@@ -21,6 +21,9 @@
 // the cycles.  Without the matrix products the loss kernel takes 0.57 ms and the gradients' products 0.70 and 0.73, without
 // the loads 0.58 to 0.61: the two overlap but for the barrier of each slab.
 //
+// Where the tiles are too few for the chip, the logits' reduction over the width is sliced and the partial logits, few then,
+// are stored: one pass over them makes the loss or D.
+//
 // In every product the vocabulary (or width) runs along the matrix core's rows and the tokens (or
 // vocabulary) along its columns: a lane then holds four consecutive elements of the contiguous
 // dimension of what it writes, and the softmax's reduction runs mostly inside a lane.
@@ -913,7 +916,6 @@ using Z64 = mm::Config<64, 64, 2, 2, 8, false, false>;
 using F64 = mm::Config<64, 64, 2, 2, 8, false, false, true>;
 using F256 = mm::Config<256, 256, 2, 4, 2, false, false, true>;
 using F128 = mm::Config<128, 128, 2, 2, 4, false, false, true>;
-using F32 = mm::Config<128, 32, 4, 1, 4, false, false, true>;
 template <bool V4> using P32 = mm::FewConfig<32, 3, false, V4>;
 template <bool V4> using P64 = mm::FewConfig<64, 2, false, V4>;
 template <bool V4> using Q32 = mm::FewConfig<32, 3, true, V4>;
@@ -921,7 +923,6 @@ template <bool V4> using Q64 = mm::FewConfig<64, 2, true, V4>;
 using E256 = mm::Config<256, 256, 2, 4, 2, true, false, true>;
 using E128 = mm::Config<128, 128, 2, 2, 4, true, false, true>;
 using E64 = mm::Config<64, 64, 2, 2, 8, true, false, true>;
-using E32 = mm::Config<128, 32, 4, 1, 4, true, false, true>;
 using H256 = mm::Config<256, 256, 2, 4, 2, true, false>;
 using H128 = mm::Config<128, 128, 2, 2, 4, true, false>;
 using H32 = mm::Config<128, 32, 4, 1, 4, true, false>;
@@ -943,14 +944,6 @@ void launch_logits(const LogitArgs& a, int64_t n, hipStream_t s) {
     hipLaunchKernelGGL((logit_kernel<C, EPI>), walkers<C>(t), dim3(C::THREADS), 0, s, a);
 }
 
-template <class C256, class C128, class C64, class C32, int EPI>
-void launch_logits(const LogitArgs& a, int tile, int64_t n, hipStream_t s) {
-    if (tile == TILE_256) launch_logits<C256, EPI>(a, n, s);
-    else if (tile == TILE_128) launch_logits<C128, EPI>(a, n, s);
-    else if (tile == TILE_64) launch_logits<C64, EPI>(a, n, s);
-    else launch_logits<C32, EPI>(a, n, s);
-}
-
 template <bool V4, int EPI>
 void launch_few_logits(const LogitArgs& a, int64_t n, hipStream_t s) {
     if (n <= 32) launch_logits<P32<V4>, EPI>(a, n, s);
@@ -959,11 +952,17 @@ void launch_few_logits(const LogitArgs& a, int64_t n, hipStream_t s) {
 
 template <int EPI>
 void launch_logits(const LogitArgs& a, const XentPlan& p, hipStream_t s) {
-    if (p.parts == 1) launch_logits<Z256, Z128, Z64, Z32, EPI>(a, p.tile_z, p.n, s);
-    else if constexpr (EPI != EPI_D1) {   // fp32: D in three parts
+    if (p.parts == 1) {
+        if (p.tile_z == TILE_256) launch_logits<Z256, EPI>(a, p.n, s);
+        else if (p.tile_z == TILE_128) launch_logits<Z128, EPI>(a, p.n, s);
+        else if (p.tile_z == TILE_64) launch_logits<Z64, EPI>(a, p.n, s);
+        else launch_logits<Z32, EPI>(a, p.n, s);
+    } else if constexpr (EPI != EPI_D1) {   // fp32: D in three parts; more than kFewTokens tokens where W goes through planes
         if (p.few && p.d % 4 == 0) launch_few_logits<true, EPI>(a, p.n, s);
         else if (p.few) launch_few_logits<false, EPI>(a, p.n, s);
-        else launch_logits<F256, F128, F64, F32, EPI>(a, p.tile_z, p.n, s);
+        else if (p.tile_z == TILE_256) launch_logits<F256, EPI>(a, p.n, s);
+        else if (p.tile_z == TILE_128) launch_logits<F128, EPI>(a, p.n, s);
+        else launch_logits<F64, EPI>(a, p.n, s);
     }
 }
 
@@ -1057,8 +1056,7 @@ SliceArgs launch_slices(const LogitArgs& z, const XentPlan& p, char* ws, hipStre
     else if (p.parts == 1) launch_out<Z32>(o, p.n, s);
     else if (p.tile_z == TILE_256) launch_out<F256>(o, p.n, s);
     else if (p.tile_z == TILE_128) launch_out<F128>(o, p.n, s);
-    else if (p.tile_z == TILE_64) launch_out<F64>(o, p.n, s);
-    else launch_out<F32>(o, p.n, s);
+    else launch_out<F64>(o, p.n, s);
     const bool scaled = p.parts > 1 && !p.few;
     return SliceArgs{o.acc, p.n, p.piece, o.split, (int)p.v, z.cnt, scaled ? z.hinv : nullptr, scaled ? z.winv : nullptr,
                      z.tgt, z.lg, z.gscale, z.wtop, z.dl, z.dl16, z.rest, p.np};
@@ -1142,8 +1140,7 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             else if (p.few) launch_few_out<false>(h, p.n, s);
             else if (scaled && p.tile_h == TILE_256) launch_out<E256>(h, p.n, s);
             else if (scaled && p.tile_h == TILE_128) launch_out<E128>(h, p.n, s);
-            else if (scaled && p.tile_h == TILE_64) launch_out<E64>(h, p.n, s);
-            else if (scaled) launch_out<E32>(h, p.n, s);
+            else if (scaled) launch_out<E64>(h, p.n, s);
             else if (p.tile_h == TILE_256) launch_out<H256>(h, p.n, s);
             else if (p.tile_h == TILE_128) launch_out<H128>(h, p.n, s);
             else if (p.tile_h == TILE_64) launch_out<H64>(h, p.n, s);

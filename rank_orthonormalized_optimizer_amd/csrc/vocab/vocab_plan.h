@@ -94,10 +94,10 @@ constexpr int64_t kShortTokens = 128;
 // and of so few, with fp32 sums in the vector units (with gradients, matrix cores against that: fp32 2 x 82297 x 2232 949 and
 // 780 us, 8 x 32000 x 2048 316 and 267; bf16 9 x 40448 x 1024 113 and 107; 17 and more tokens 5 to 24% slower that way)
 constexpr int64_t kRankTokens = 16;
-// fp32: up to so many tokens the products over W read it in place (see FewProduct), if W has tiles for half the CUs.
-// 32000 x 1024 with gradients: 65 tokens 255 us against 455 through planes of W in the workspace, 128 tokens 367 and
-// 483, 200 tokens 550 and 555; 100544 x 2624: 164 tokens 3.4 ms against 2.4
-constexpr int64_t kFewTokens = 128, kFewVocab = 1024;
+// fp32: up to so many tokens the products over W read it in place (see FewProduct).  With gradients, against planes of W in
+// the workspace: 32000 x 1024, 65 tokens 232 us and 404, 128 tokens 330 and 446, 180 tokens 423 and 432; 100544 x 2624, 164
+// tokens 3.2 ms and 2.9.
+constexpr int64_t kFewTokens = 128;
 
 inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : t == TILE_64 ? 64 : 128; }
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : t == TILE_64 ? 64 : 32; }
@@ -118,8 +118,8 @@ inline int pick_tile(int64_t m, int64_t n, int64_t k, int64_t terms) {
     if (tiles(m, n, TILE_256) * pick_split(m, n, k, terms, TILE_256) >= kCUs / 2) return TILE_256;
     return tiles(m, n, TILE_128) * pick_split(m, n, k, terms, TILE_128) >= kCUs / 2 ? TILE_128 : TILE_64;
 }
-// The logits' reduction is not sliced.  Where even 128 x 128 tiles leave half the CUs idle, 64 x 64 ones serve, whose ring
-// of eight slabs also hides more of the loads' latency (fp32 257 x 1013 x 255: logits 31 -> 7 us).
+// The logits' tile where their reduction is not sliced.  Where even 128 x 128 tiles leave half the CUs idle, 64 x 64 ones
+// serve, whose ring of eight slabs also hides more of the loads' latency (fp32 257 x 1013 x 255: logits 31 -> 7 us).
 inline int pick_logit_tile(int64_t m, int64_t n) {
     if (n <= 32) return TILE_32;
     return tiles(m, n, TILE_256) >= kCUs / 2 ? TILE_256 : tiles(m, n, TILE_128) >= kCUs / 2 ? TILE_128 : TILE_64;
@@ -134,7 +134,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.np = ceil_div64(tokens < 1 ? 1 : tokens, 256) * 256;
     q.parts = bf16 ? 1 : 3;
     q.dparts = bf16 && dw_bf16 ? 1 : 3;
-    q.few = !bf16 && tokens <= kFewTokens && vocab >= kFewVocab;
+    q.few = !bf16 && tokens <= kFewTokens;
     q.wpack = !q.few && (!bf16 || width % 64 != 0);
     const bool scaled = !bf16 && !q.few;   // products over W from two fp16 parts of scaled rows
     const int64_t plane_row = !q.wpack ? 0 : q.kp * (bf16 ? 2 : 4);   // bytes of W's planes per row
@@ -150,6 +150,9 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.piece = ceil_div64(ceil_div64(all, ceil_div64(all, most)), 256) * 256;   // equal pieces
     q.pieces = ceil_div64(all, q.piece);
     q.tile_z = q.few ? TILE_32 : pick_logit_tile(q.piece, tokens);
+    // Too few tiles for the chip and a long reduction: it is sliced, and a pass over the partial logits, which are few, takes
+    // the epilogue's place (fp32 loss, one slice and more: 1 x 12347 x 3582 105 and 73 us, 15 x 2304 x 4032 98 and 32,
+    // 1198 x 1640 x 3923 189 and 96).
     q.split_z = 1;
     const int64_t zn = q.few && tokens > 32 ? ceil_div64(tokens, 2) : tokens;   // few: 64 columns a tile
     if (q.pieces == 1 && tokens > 0 && tiles(q.piece, zn, q.few ? TILE_32 : TILE_128) < kCUs) {

@@ -91,7 +91,10 @@ int main() {
                     const bool ok = x.piece % 256 == 0 && x.piece * x.pieces >= v && x.piece * (x.pieces - 1) < v &&
                                     x.kp % 64 == 0 && x.kp >= d && x.np % 256 == 0 && x.np >= t && x.nvt * bm >= v &&
                                     (!(k >> 2) || (x.split_h >= 1 && x.split_w >= 1 && x.split_h <= 256 && x.split_w <= 256)) &&
-                                    (!x.few || (d % 4 == 0 && !(k & 1)));
+                                    (!x.few || (t <= dion::kFewTokens && !(k & 1))) &&
+                                    // slices of the logits: of one piece, none empty, tokens within a grid's second dimension
+                                    (x.split_z == 1 || (x.split_z > 1 && x.pieces == 1 && t < 65536 &&
+                                                        dion::ceil_div64(x.kp / 64, x.split_z) * (x.split_z - 1) < x.kp / 64));
                     if (!ok) fprintf(stderr, "plan of %ld x %ld x %ld, kind %d\n", (long)t, (long)v, (long)d, k);
                     expect("cross entropy plan", ok, 1);
                 }
