@@ -17,9 +17,9 @@
  * default stream) with no host synchronization, safe to capture in a HIP graph; results bitwise
  * reproducible (no floating-point atomics); status codes of dion.h, checked on the host before
  * anything is enqueued.  Matrices must be 16-byte aligned, workspaces 256-byte, ids, targets and
- * the fp32 per-token arrays as their elements; any width is taken.  Written arrays must not overlap anything else.  Calls that share a workspace must be ordered on
- * one stream.  Sums, softmax statistics and products accumulate in fp32; each output is rounded
- * once to its type.
+ * the fp32 per-token arrays as their elements; any width is taken.  Written arrays must not
+ * overlap anything else.  Calls that share a workspace must be ordered on one stream.  Sums,
+ * softmax statistics and products accumulate in fp32; each output is rounded once to its type.
  *
  * Limits: tokens <= DION_VOCAB_MAX_TOKENS, 1 <= vocab < 2^24, 1 <= width <= 2^16; beyond them DION_ERR_SHAPE.
  */
