@@ -3,8 +3,8 @@
 //   Y[t] = scale * W[ids[t]]                        one gather, bound by HBM (read and write d elements per token)
 //   dW[v] (+)= scale * sum over ids[t] = v of dY[t]
 //
-// The gradient sorts the tokens by id, in their order where ids are equal, and cuts the sorted list into chunks of equal length, so that frequent ids load no workgroup
-// more than others.  A team of threads walks one chunk, adding rows of dY in fp32 registers; a run
+// The gradient sorts the tokens by id, in their order where ids are equal, and cuts the sorted list into chunks of equal
+// length, so that frequent ids load no workgroup more than others.  A team of threads walks one chunk, adding rows of dY in fp32 registers; a run
 // of one id that lies inside the chunk is written to its row, the part of a run that crosses a
 // border goes to a partial row, and a second pass adds the partial rows of a run in chunk order.
 // No floating-point atomics: the order of additions depends on the tokens alone.
@@ -31,19 +31,23 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ float up16(uint32_t b) { return __uint_as_float(b << 16); }
 __device__ __forceinline__ uint32_t down16(float f) { return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f); }
 
-// VEC consecutive elements (8, 4 or 1) of an fp32 or bf16 array as floats; the address is
-// aligned to VEC elements (16 bytes at most)
+// Vectors at any element's address: the memory unit takes such accesses whole.
+typedef f32x4_t __attribute__((aligned(4))) f32x4_any;
+typedef u32x4_t __attribute__((aligned(2))) u32x4_any;
+typedef u32x2_t __attribute__((aligned(2))) u32x2_any;
+
+// VEC consecutive elements (8, 4 or 1) of an fp32 or bf16 array as floats
 template <bool BF16, int VEC>
 struct Row {
     static __device__ __forceinline__ void load(const void* p, int64_t i, float* v) {
         if constexpr (BF16) {
             const uint16_t* s = (const uint16_t*)p + i;
             if constexpr (VEC == 8) {
-                const u32x4_t w = *(const u32x4_t*)s;
+                const u32x4_t w = *(const u32x4_any*)s;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) { v[2 * e] = up16(w[e]); v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u); }
             } else if constexpr (VEC == 4) {
-                const u32x2_t w = *(const u32x2_t*)s;
+                const u32x2_t w = *(const u32x2_any*)s;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) { v[2 * e] = up16(w[e]); v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u); }
             } else {
@@ -56,7 +60,7 @@ struct Row {
             } else {
 #pragma unroll
                 for (int q = 0; q < VEC / 4; ++q) {
-                    const f32x4_t w = *(const f32x4_t*)(s + 4 * q);
+                    const f32x4_t w = *(const f32x4_any*)(s + 4 * q);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[4 * q + e] = w[e];
                 }
@@ -70,12 +74,12 @@ struct Row {
                 u32x4_t w;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = down16(v[2 * e]) | (down16(v[2 * e + 1]) << 16);
-                *(u32x4_t*)s = w;
+                *(u32x4_any*)s = w;
             } else if constexpr (VEC == 4) {
                 u32x2_t w;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) w[e] = down16(v[2 * e]) | (down16(v[2 * e + 1]) << 16);
-                *(u32x2_t*)s = w;
+                *(u32x2_any*)s = w;
             } else {
                 *s = (uint16_t)down16(v[0]);
             }
@@ -86,7 +90,7 @@ struct Row {
             } else {
 #pragma unroll
                 for (int q = 0; q < VEC / 4; ++q)
-                    *(f32x4_t*)(s + 4 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                    *(f32x4_any*)(s + 4 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
             }
         }
     }
@@ -98,7 +102,8 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int64_t i, int ids64
 
 // ---------------------------------------------------------------------------
 // Lookup.  A team of tx threads (a power of two) covers the columns of a row in steps of
-// tx * VEC; 256 / tx rows per workgroup and pass.
+// tx * VEC; 256 / tx rows per workgroup and pass.  Rows may start at any element and end inside a vector, whose elements
+// then go one by one (20000 fp32 rows of 1250: 50 us all one by one, 25 this way; 50000 bf16 rows of 333: 41 and 19).
 // ---------------------------------------------------------------------------
 template <bool W16, bool O16, int VEC>
 __global__ __launch_bounds__(256) void lookup_kernel(EmbedArgs a, int tx_log2) {
@@ -111,10 +116,18 @@ __global__ __launch_bounds__(256) void lookup_kernel(EmbedArgs a, int tx_log2) {
     const int64_t step = (int64_t)VEC << tx_log2;
     for (int64_t c = (int64_t)tx * VEC + (int64_t)blockIdx.y * step; c < a.width; c += step * gridDim.y) {
         float v[VEC];
-        Row<W16, VEC>::load(a.in, src + c, v);
+        if (c + VEC <= a.width) {
+            Row<W16, VEC>::load(a.in, src + c, v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = ok ? v[e] * a.scale : __uint_as_float(0x7fc00000u);
-        Row<O16, VEC>::store(a.out, dst + c, v);
+            for (int e = 0; e < VEC; ++e) v[e] = ok ? v[e] * a.scale : __uint_as_float(0x7fc00000u);
+            Row<O16, VEC>::store(a.out, dst + c, v);
+        } else {
+            for (int e = 0; e < (int)(a.width - c); ++e) {
+                Row<W16, 1>::load(a.in, src + c + e, v);
+                v[0] = ok ? v[0] * a.scale : __uint_as_float(0x7fc00000u);
+                Row<O16, 1>::store(a.out, dst + c + e, v);
+            }
+        }
     }
 }
 
@@ -479,7 +492,7 @@ __global__ __launch_bounds__(256) void run_join_kernel(RunArgs a) {
     write_row<O16, ADD, VEC>(a, cols, key, acc, old);
 }
 
-// Elements per access: eight where rows start at 16 bytes for bf16 and 32 for fp32, four, or single ones.
+// Elements per access of the gradient: eight where rows start at 16 bytes for bf16 and 32 for fp32, four, or single ones.
 int row_vec(int64_t width) { return width % 8 == 0 ? 8 : width % 4 == 0 ? 4 : 1; }
 
 // log2 of the threads that share a row of `chunks` accesses: enough for the row, at most 256
@@ -489,16 +502,21 @@ int team_log2(int64_t chunks) {
     return l;
 }
 
-template <bool W16, bool O16>
+template <bool W16, bool O16, int VEC>
 void launch_lookup(const EmbedArgs& a, hipStream_t s) {
-    const int vec = row_vec(a.width);
-    const int64_t chunks = ceil_div64(a.width, vec);
+    const int64_t chunks = ceil_div64(a.width, VEC);
     const int l = team_log2(chunks);
     const int64_t steps = ceil_div64(chunks, (int64_t)1 << l);
     const dim3 grid((unsigned)ceil_div64(a.tokens, 256 >> l), (unsigned)steps);
-    if (vec == 8) hipLaunchKernelGGL((lookup_kernel<W16, O16, 8>), grid, dim3(256), 0, s, a, l);
-    else if (vec == 4) hipLaunchKernelGGL((lookup_kernel<W16, O16, 4>), grid, dim3(256), 0, s, a, l);
-    else hipLaunchKernelGGL((lookup_kernel<W16, O16, 1>), grid, dim3(256), 0, s, a, l);
+    hipLaunchKernelGGL((lookup_kernel<W16, O16, VEC>), grid, dim3(256), 0, s, a, l);
+}
+
+// Eight elements per access; four where an fp32 row fits a workgroup that way (fp32, 20000 rows of 1024: 21 us by eights, 20
+// by fours; of 1250: 25 and 28).
+template <bool W16, bool O16>
+void launch_lookup(const EmbedArgs& a, hipStream_t s) {
+    if (!(W16 && O16) && a.width <= 1024) launch_lookup<W16, O16, W16 && O16 ? 8 : 4>(a, s);
+    else launch_lookup<W16, O16, 8>(a, s);
 }
 
 template <bool Y16, bool O16, bool ADD, int VEC>

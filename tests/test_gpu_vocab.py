@@ -60,7 +60,7 @@ def close(got, want, bound, what):
 # ---------------------------------------------------------------------------- lookup
 @pytest.mark.parametrize("wdt,odt", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
 @pytest.mark.parametrize("tokens,vocab,width", [(0, 5, 8), (1, 1, 1), (3, 7, 5), (65, 33, 12), (1, 1000, 2048), (513, 129, 64),
-                                                (70, 31, 4104), (1030, 50, 255)])
+                                                (70, 31, 4104), (1030, 50, 255), (130, 33, 1301), (129, 40, 1023)])
 def test_lookup(cuda, tokens, vocab, width, wdt, odt):
     import rank_orthonormalized_optimizer_amd as dion
     g = gen(cuda, tokens, vocab, width)
