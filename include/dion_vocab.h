@@ -93,7 +93,8 @@ int dion_linear_xent(const void* H, const void* W, const void* targets, float* l
  *            what is there.  At least one of dH and dW is given
  * A token whose target is neither ignored nor in [0, vocab) makes its dH row and dW NaN.
  * Arithmetic: for bf16 outputs of bf16 operands D is rounded once to bf16 (without grad where grad_n is 1: that factor is
- * applied to the fp32 sums), and what the rounding left of the target's element is added to dH in fp32.  Where the output or
+ * applied to the fp32 sums), and what the rounding left of the target's element is added to dH and dW in fp32; small dW come
+ * from two bf16 parts of D.  Where the output or
  * the operands are fp32, the products are fp32-accurate, from 16-bit parts as in dion_linear_xent: dW from three bf16 parts
  * of D and H, dH from three bf16 parts, or from two fp16 parts of D (per token) and of W (per row) scaled by powers of two,
  * which leaves out 2^-39 of |grad[t]| times the largest |W| besides.

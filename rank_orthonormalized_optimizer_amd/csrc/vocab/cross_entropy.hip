@@ -10,7 +10,12 @@
 // one pass over these pairs.  The gradient: per piece of the vocabulary the logits are formed
 // again, turned into D (16-bit parts) and multiplied from both sides.
 //
-// What multiplies: bf16 operands as they are, D in one bf16 part; three parts for an fp32 dW.  fp32 operands: logits and dH
+// What multiplies: bf16 operands as they are, D in one bf16 part, or two for dW of small products; three parts for an fp32 dW.
+// Rounding D to one part would leave the same of every target's element where the factor is the same and the probability
+// small, rows of frequent targets then off by up to 2^-8 in one direction.  What it leaves of them goes to dH and dW in fp32:
+// rest[t] W[target] as dH is stored, and for dW the sums of rest[t] H[t] over the tokens of each target (sum_weighted_rows),
+// which its product adds.  dW of 8192 x 32000 x 2048 against 64 bits, relative: 1.80e-3 without them, 1.65e-3 with them and for
+// a correctly rounded dW.  fp32 operands: logits and dH
 // from two fp16 parts of W's and H's rows, each row scaled by a power of two (three products), dW from three bf16 parts of D
 // and H (six: D's columns for rare tokens are too small for fp16).  fp32 and few tokens: W in place, split in registers
 // (FewProduct).
@@ -103,6 +108,7 @@ struct PackArgs {
     float* inv;
     int* map;        // gathered row -> token
     int* tgt;        // its target, -1 where that is no row of W
+    int* pos;        // token -> gathered row, 0 for the ignored ones, or null
     float2* lg;      // (lse, grad) of the gathered row (gradient)
     float* gscale;   // the power of two in grad (gradient of fp32 operands)
     int* cnt;        // how many rows were gathered
@@ -248,6 +254,7 @@ __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
         for (int i = 0; i < 8; ++i) base += before[i];
         const int j = base + __popcll(kept & ((1ull << lane) - 1));
         if (lane < kPackRows) slot[lane] = keep ? j : -1;
+        if (GRAD && row && a.pos) a.pos[t] = keep ? j : 0;
         if (keep) {
             const bool in = y >= 0 && y < a.v;
             a.map[j] = (int)t;
@@ -349,11 +356,11 @@ struct LogitArgs {
     uint16_t* dl16;        // F16: fp16 planes [2][np][piece] of D times W's inverse row scales, for dH
     const float* gscale;
     const float* wtop;     // F16: the largest of the piece's inverse row scales
-    float* rest;           // [np] what the first part of D leaves of the target's element
+    float* rest;           // [np] what the first part of D leaves of the target's element, for dH and (one part) dW
     int64_t np, piece;
 };
 
-enum { EPI_LOSS, EPI_D1, EPI_D3 };
+enum { EPI_LOSS, EPI_D1, EPI_D2, EPI_D3 };
 
 // Stores a lane's 4-row pieces of two neighbouring blocks of 16 rows: the lane quarters trade their four rows of one
 // against the other's (v_permlane32_swap, v_permlane16_swap), so that a lane stores eight consecutive rows and four lanes
@@ -456,7 +463,7 @@ __global__ __launch_bounds__(C::THREADS) void logit_kernel(LogitArgs a) {
                 s += __shfl_xor(s, 32);
                 if (mul.lane < 16) red[mul.wave % C::WM * C::BN + cl + 16 * j] = float2{mx, s};
             } else {
-                constexpr int PD = EPI == EPI_D3 ? 3 : 1;
+                constexpr int PD = EPI == EPI_D3 ? 3 : EPI == EPI_D2 ? 2 : 1;
                 const float c = lg[j].x * kLog2e;
 #pragma unroll
                 for (int i = 0; i < C::MI; ++i)
@@ -603,7 +610,16 @@ struct OutArgs {
     const float* rest;     // or null
     const int* tgt;
     const uint16_t* w;     // bf16 [vocab][d]
+    // dW in bf16: the same for its rows, summed over the tokens by sum_weighted_rows
+    const int* slot;       // [rows], or null
+    const float* extra;
 };
+
+// the row of extra for output row r, or null
+__device__ __forceinline__ const float* extra_row(const OutArgs& a, int64_t r) {
+    const int s = a.slot ? a.slot[r] : 0;
+    return s > 0 ? a.extra + (s - 1) * (int64_t)a.dp : nullptr;
+}
 
 // n elements of the output from column c of row r of the reduction's result: four, fewer at a ragged end
 __device__ __forceinline__ void store_out(const OutArgs& a, int64_t r, int c, int n, float (&v)[4]) {
@@ -694,6 +710,15 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
         for (int j = 0; j < C::NI; ++j) {
             const int n = n0 + mul.xb + 16 * j + mul.lane % 16;
             if (n >= rows) continue;
+            if constexpr (C::TA && C::TB) {   // dW
+                if (const float* extra = a.acc ? nullptr : extra_row(a, n)) {   // all of a row before its stores, which they cannot pass
+#pragma unroll
+                    for (int i = 0; i < C::MI; ++i) {
+                        const int m = m0 + mul.xa + 16 * i + 4 * (mul.lane / 16);
+                        if (m < a.d) acc[i][j] += *(const f32x4*)(extra + m);   // (rows of a multiple of four)
+                    }
+                }
+            }
 #pragma unroll
             for (int i = 0; i < C::MI; ++i) {
                 const int m = m0 + mul.xa + 16 * i + 4 * (mul.lane / 16);
@@ -712,7 +737,7 @@ __global__ __launch_bounds__(C::THREADS) void out_kernel(OutArgs a) {
 }
 
 // dW of up to N tokens, a stream of writes: four columns of H's rows per thread in registers, D's columns in LDS, fp32 sums.
-// D and H come from the parts that the other products use (their sum is exact).
+// D and H come from the parts that the other products use.
 template <int N>
 __global__ __launch_bounds__(256) void rank_out_kernel(OutArgs a, int hparts, int dparts) {
     constexpr int R = 64;
@@ -773,7 +798,13 @@ __global__ __launch_bounds__(256) void join_kernel(OutArgs a) {
     for (int o = G / 2; o; o >>= 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o);
-    if (lane == 0) store_out(a, r, c, n, v);
+    if (lane > 0) return;
+    if (const float* extra = extra_row(a, r)) {
+        const f32x4 x = *(const f32x4*)(extra + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += x[e];
+    }
+    store_out(a, r, c, n, v);
 }
 
 // Logits whose reduction was sliced: partial sums [split][n][piece], and the scales of fp16 parts (or null).
@@ -864,7 +895,7 @@ __global__ __launch_bounds__(256) void slice_loss_kernel(SliceArgs a, const int*
 // D from sliced logits as logit_kernel forms it, eight of a token's per thread, zeros up to a multiple of 64.
 template <int EPI>
 __global__ __launch_bounds__(256) void slice_grad_kernel(SliceArgs a) {
-    constexpr int PD = EPI == EPI_D3 ? 3 : 1;
+    constexpr int PD = EPI == EPI_D3 ? 3 : EPI == EPI_D2 ? 2 : 1;
     const int64_t j = blockIdx.y;
     const int v = (int)(blockIdx.x * 256 + threadIdx.x) * 8;
     if (j >= a.cnt[0] || v >= (a.v + 63) / 64 * 64) return;
@@ -906,6 +937,7 @@ mm::Segments segments(int pa, int pb) {
     if (pa == 3 && pb == 3) return list({1 | 1 << 2, 0 | 2 << 2, 2 | 0 << 2, 0 | 1 << 2, 1 | 0 << 2, 0});
     if (pa == 2) return list({1, 1 << 2, 0});   // fp16 parts h, l: l h, h l, h h
     if (pb == 3) return list({2 << 2, 1 << 2, 0});
+    if (pb == 2) return list({1 << 2, 0});
     return list({0});
 }
 
@@ -957,7 +989,7 @@ void launch_logits(const LogitArgs& a, const XentPlan& p, hipStream_t s) {
         else if (p.tile_z == TILE_128) launch_logits<Z128, EPI>(a, p.n, s);
         else if (p.tile_z == TILE_64) launch_logits<Z64, EPI>(a, p.n, s);
         else launch_logits<Z32, EPI>(a, p.n, s);
-    } else if constexpr (EPI != EPI_D1) {   // fp32: D in three parts; more than kFewTokens tokens where W goes through planes
+    } else if constexpr (EPI == EPI_LOSS || EPI == EPI_D3) {   // fp32: D in three parts; more than kFewTokens tokens where W goes through planes
         if (p.few && p.d % 4 == 0) launch_few_logits<true, EPI>(a, p.n, s);
         else if (p.few) launch_few_logits<false, EPI>(a, p.n, s);
         else if (p.tile_z == TILE_256) launch_logits<F256, EPI>(a, p.n, s);
@@ -997,7 +1029,7 @@ mm::Operand weights(const XentArgs& x, const XentPlan& p, char* ws, int64_t v0, 
 PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws, bool exact) {
     return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, exact || x.bf16 || p.few ? (uint16_t*)(ws + p.h) : nullptr,
                     x.bf16 || p.few ? nullptr : (uint16_t*)(ws + p.h16), (float*)(ws + p.hinv), (int*)(ws + p.map),
-                    (int*)(ws + p.tgt), (float2*)(ws + p.lg),
+                    (int*)(ws + p.tgt), exact && p.exact_targets && x.dW ? (int*)(ws + p.pos) : nullptr, (float2*)(ws + p.lg),
                     x.bf16 || p.few ? nullptr : (float*)(ws + p.gscale), (int*)(ws + p.cnt),
                     p.n > kCountDirect ? (int*)(ws + p.cnt) + 64 : nullptr};
 }
@@ -1118,6 +1150,13 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
     w.cnt = pk.cnt; w.d = (int)p.d; w.dp = (int)p.dp; w.factor = factor; w.k = -1; w.split = (int)p.split_w; w.out_bf16 = x.dw_bf16; w.accumulate = x.accumulate;
     w.acc = p.split_w > 1 ? (float*)(ws + p.acc_w) : nullptr;
     w.acc_rows = p.piece;
+    const bool exact_targets = x.dW && p.exact_targets;
+    const EmbedArgs rows_of{x.targets, x.H, nullptr, p.n, p.v, p.d, 1.f, x.ignore, x.t64, 1, 0, 0};
+    if (exact_targets) {
+        const int e = sort_weighted_rows(rows_of, p.sorted, (int*)(ws + p.slot), ws + p.sort, stream);
+        if (e) return e;
+        w.extra = (const float*)(ws + p.extra);
+    }
     for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
         const int64_t rows = p.v - v0 < p.piece ? p.v - v0 : p.piece;
         z.w = weights(x, p, ws, v0, rows, x.dH != nullptr, s);
@@ -1126,8 +1165,10 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             const SliceArgs a = launch_slices(z, p, ws, s);
             const dim3 grid((unsigned)ceil_div64(p.v, 256 * 8), (unsigned)p.n);
             if (p.dparts == 1) hipLaunchKernelGGL((slice_grad_kernel<EPI_D1>), grid, dim3(256), 0, s, a);
+            else if (p.dparts == 2) hipLaunchKernelGGL((slice_grad_kernel<EPI_D2>), grid, dim3(256), 0, s, a);
             else hipLaunchKernelGGL((slice_grad_kernel<EPI_D3>), grid, dim3(256), 0, s, a);
         } else if (p.dparts == 1) launch_logits<EPI_D1>(z, p, s);
+        else if (p.dparts == 2) launch_logits<EPI_D2>(z, p, s);
         else launch_logits<EPI_D3>(z, p, s);
         if (x.dH) {
             h.a = z.w;
@@ -1152,6 +1193,13 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
             w.rows = (int)rows;
             w.k_per = (int)(ceil_div64(ceil_div64(p.np, p.split_w), 64) * 64);
             w.out = (char*)x.dW + v0 * p.d * (x.dw_bf16 ? 2 : 4);
+            if (exact_targets) {
+                const WeightedRows sums{z.rest, pk.pos, (int*)(ws + p.slot), (float*)(ws + p.extra), p.dp, v0, v0 + rows,
+                                        p.extra_by_row};
+                const int e = sum_weighted_rows(rows_of, p.sorted, sums, ws + p.sort, stream);
+                if (e) return e;
+                w.slot = (const int*)(ws + p.slot) + v0;
+            }
             if (p.n <= 8) launch_rank<8>(w, p, s);
             else if (p.n <= kRankTokens) launch_rank<16>(w, p, s);
             else if (p.tile_w == TILE_256) launch_out<W256>(w, rows, s);

@@ -337,6 +337,7 @@ struct RunArgs {
     float* part;            // [nchunk][2][pitch]: head and tail partial rows of each chunk
     int64_t chunk, nchunk, pitch;
     int tx_log2;
+    WeightedRows w;         // kernels with WEIGHTED
 };
 
 // A thread's columns: VEC > 1: one vector; VEC == 1: four columns tx apart.
@@ -391,9 +392,24 @@ __device__ __forceinline__ void write_row(const RunArgs& a, const Cols<VEC>& col
     cols.template store<O16>(a.e.out, (int64_t)key * a.e.width, v);
 }
 
+// WEIGHTED: the sum of a run, for the row of extra that sorted position `at` of the run, or its id, names
+template <int VEC>
+__device__ __forceinline__ void write_extra(const RunArgs& a, const Cols<VEC>& cols, uint32_t key, int64_t at, const float* acc) {
+    if (key < a.w.lo || key >= a.w.hi) return;
+    const int64_t row = a.w.by_row ? key - a.w.lo : at;
+    cols.template store<false>(a.w.extra, row * a.w.pitch, acc);
+    if (cols.c[0] == 0) a.w.slot[key] = (int)row + 1;
+}
+
+// Whether the run of `key` is one to sum: WEIGHTED kernels take the tokens a range of ids at a time.
+template <bool WEIGHTED>
+__device__ __forceinline__ bool outside(const RunArgs& a, uint32_t first, uint32_t last) {
+    return WEIGHTED && (last < a.w.lo || first >= a.w.hi);
+}
+
 // ADD: the rows to add to are fetched with the tokens' rows whose runs end there, not when they are written: most runs
 // are of one token, and each would wait for its own row.
-template <bool Y16, bool O16, bool ADD, int VEC>
+template <bool Y16, bool O16, bool ADD, int VEC, bool WEIGHTED>
 __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
     constexpr int W = Cols<VEC>::W, U = ADD ? 4 : 8;
     const int tx = threadIdx.x & ((1 << a.tx_log2) - 1), ty = threadIdx.x >> a.tx_log2;
@@ -403,13 +419,14 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
     const int64_t n = a.e.tokens, p0 = ch * a.chunk, p1 = p0 + a.chunk < n ? p0 + a.chunk : n;
     const uint32_t none = (uint32_t)a.e.vocab;
     uint32_t key = a.keys[p0];
+    if (outside<WEIGHTED>(a, key, a.keys[p1 - 1])) return;
     bool open = p0 > 0 && a.keys[p0 - 1] == key;   // the run began before this chunk
     float acc[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) acc[e] = 0.f;
     for (int64_t p = p0; p < p1 && key != none; p += U) {
         uint32_t next[U], tok[U];
-        float v[U][W], old[ADD ? U : 1][W];
+        float v[U][W], old[ADD ? U : 1][W], weight[WEIGHTED ? U : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t q = p + u < p1 ? p + u : p1 - 1;
@@ -419,6 +436,7 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             cols.template load<Y16>(a.e.in, (int64_t)tok[u] * a.e.width, v[u]);
+            if (WEIGHTED) weight[u] = a.w.weight[a.w.pos[tok[u]]];
             if (ADD) {
                 const uint32_t here = u ? next[u - 1] : key;
                 if (here != none && next[u] != here) cols.template load<O16>(a.e.out, (int64_t)here * a.e.width, old[u]);
@@ -428,9 +446,10 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
         for (int u = 0; u < U; ++u) {
             if (p + u >= p1 || key == none) break;
 #pragma unroll
-            for (int e = 0; e < W; ++e) acc[e] += v[u][e];
+            for (int e = 0; e < W; ++e) acc[e] = WEIGHTED ? fmaf(weight[WEIGHTED ? u : 0], v[u][e], acc[e]) : acc[e] + v[u][e];
             if (next[u] != key) {
                 if (open) cols.template store<false>(a.part, ch * 2 * a.pitch, acc);
+                else if constexpr (WEIGHTED) write_extra(a, cols, key, p + u, acc);
                 else write_row<O16, ADD, VEC>(a, cols, key, acc, old[ADD ? u : 0]);
                 open = false;
 #pragma unroll
@@ -446,13 +465,14 @@ __global__ __launch_bounds__(256) void run_sum_kernel(RunArgs a) {
 // Adds up the runs that begin in a chunk and go on behind it: its tail partial row, then the head
 // partial rows of the chunks that the run reaches.  Eight teams of 32 threads share 32 accesses of the row's columns,
 // each adding every eighth chunk; their sums are added in order.
-template <bool O16, bool ADD, int VEC>
+template <bool O16, bool ADD, int VEC, bool WEIGHTED>
 __global__ __launch_bounds__(256) void run_join_kernel(RunArgs a) {
     constexpr int W = Cols<VEC>::W, U = 4;
     const int tx = threadIdx.x & 31, team = threadIdx.x >> 5;
     const int64_t ch = blockIdx.x, p0 = ch * a.chunk, p1 = p0 + a.chunk;
     const uint32_t key = a.keys[p1];
     if (key == (uint32_t)a.e.vocab || a.keys[p1 - 1] != key || (p0 > 0 && a.keys[p0 - 1] == key)) return;
+    if (outside<WEIGHTED>(a, key, key)) return;
     const Cols<VEC> cols(tx, 5, blockIdx.y, a.e.width);
     __shared__ float sums[8][32][W + 1];
     float acc[W], old[W];
@@ -489,7 +509,8 @@ __global__ __launch_bounds__(256) void run_join_kernel(RunArgs a) {
     for (int i = 1; i < 8; ++i)
 #pragma unroll
         for (int e = 0; e < W; ++e) acc[e] += sums[i][tx][e];
-    write_row<O16, ADD, VEC>(a, cols, key, acc, old);
+    if constexpr (WEIGHTED) write_extra(a, cols, key, p1 - 1, acc);
+    else write_row<O16, ADD, VEC>(a, cols, key, acc, old);
 }
 
 // Elements per access of the gradient: eight where rows start at 16 bytes for bf16 and 32 for fp32, four, or single ones.
@@ -519,24 +540,24 @@ void launch_lookup(const EmbedArgs& a, hipStream_t s) {
     else launch_lookup<W16, O16, 8>(a, s);
 }
 
-template <bool Y16, bool O16, bool ADD, int VEC>
+template <bool Y16, bool O16, bool ADD, int VEC, bool WEIGHTED>
 void launch_runs(RunArgs r, hipStream_t s) {
     const int64_t chunks = ceil_div64(r.e.width, Cols<VEC>::W);
     r.tx_log2 = team_log2(chunks);
     const dim3 grid((unsigned)ceil_div64(r.nchunk, 256 >> r.tx_log2),
                     (unsigned)ceil_div64(chunks, (int64_t)1 << r.tx_log2));
-    hipLaunchKernelGGL((run_sum_kernel<Y16, O16, ADD, VEC>), grid, dim3(256), 0, s, r);
+    hipLaunchKernelGGL((run_sum_kernel<Y16, O16, ADD, VEC, WEIGHTED>), grid, dim3(256), 0, s, r);
     if (r.nchunk > 1)
-        hipLaunchKernelGGL((run_join_kernel<O16, ADD, VEC>), dim3((unsigned)(r.nchunk - 1), (unsigned)ceil_div64(chunks, 32)),
+        hipLaunchKernelGGL((run_join_kernel<O16, ADD, VEC, WEIGHTED>), dim3((unsigned)(r.nchunk - 1), (unsigned)ceil_div64(chunks, 32)),
                            dim3(256), 0, s, r);
 }
 
-template <bool Y16, bool O16, bool ADD>
+template <bool Y16, bool O16, bool ADD, bool WEIGHTED = false>
 void launch_runs(const RunArgs& r, hipStream_t s) {
     switch (row_vec(r.e.width)) {
-        case 8: launch_runs<Y16, O16, ADD, 8>(r, s); break;
-        case 4: launch_runs<Y16, O16, ADD, 4>(r, s); break;
-        default: launch_runs<Y16, O16, ADD, 1>(r, s); break;
+        case 8: launch_runs<Y16, O16, ADD, 8, WEIGHTED>(r, s); break;
+        case 4: launch_runs<Y16, O16, ADD, 4, WEIGHTED>(r, s); break;
+        default: launch_runs<Y16, O16, ADD, 1, WEIGHTED>(r, s); break;
     }
 }
 
@@ -544,6 +565,38 @@ template <bool Y16, bool O16>
 void launch_runs(const RunArgs& r, hipStream_t s) {
     if (r.e.accumulate) launch_runs<Y16, O16, true>(r, s);
     else launch_runs<Y16, O16, false>(r, s);
+}
+
+// Which of the two buffers the sorted tokens end in.
+int sorted_buffer(const EmbedGradPlan& p) { return p.sort_blocks == 0 ? 0 : (p.digits - 1) & 1; }
+
+// Sorts the tokens into the buffers sorted_buffer() names, and clears `zero` bytes at a.out meanwhile.
+void sort_tokens(const EmbedArgs& a, const EmbedGradPlan& p, int64_t zero, char* ws, hipStream_t s) {
+    const int64_t want = ceil_div64(zero, 1024 * 16 * 4);   // four 16-byte stores per thread
+    const unsigned fill = (unsigned)(want < 2048 ? want : 2048);
+    uint32_t* keys[2] = {(uint32_t*)(ws + p.keys[0]), (uint32_t*)(ws + p.keys[1])};
+    uint32_t* idx[2] = {(uint32_t*)(ws + p.idx[0]), (uint32_t*)(ws + p.idx[1])};
+    if (p.sort_blocks == 0) {
+        const unsigned sorters = (unsigned)ceil_div64(a.tokens, 64);
+        if (sorters + fill > 0)
+            hipLaunchKernelGGL(rank_kernel, dim3(sorters + fill), dim3(1024), 0, s, a, keys[0], idx[0], (int)sorters, zero);
+        return;
+    }
+    const int nblk = (int)p.sort_blocks;
+    uint32_t* counts = (uint32_t*)(ws + p.counts);
+    for (int d = 0; d < p.digits; ++d) {
+        const uint32_t* kin = d ? keys[(d - 1) & 1] : nullptr;
+        const uint32_t* iin = d ? idx[(d - 1) & 1] : nullptr;
+        const int at = d & 1;
+        if (p.sort_items == 4) launch_radix<4>(a, d, kin, iin, counts, nblk, keys[at], idx[at], d ? 0 : zero, d ? 0 : 4 * fill, s);
+        else launch_radix<16>(a, d, kin, iin, counts, nblk, keys[at], idx[at], d ? 0 : zero, d ? 0 : 4 * fill, s);
+    }
+}
+
+RunArgs run_args(const EmbedArgs& a, const EmbedGradPlan& p, char* ws) {
+    const int at = sorted_buffer(p);
+    return RunArgs{a, (uint32_t*)(ws + p.keys[at]), (uint32_t*)(ws + p.idx[at]), (float*)(ws + p.part), p.chunk, p.nchunk,
+                   (a.width + 7) / 8 * 8, 0, {}};
 }
 
 }  // namespace
@@ -557,32 +610,26 @@ int run_embedding(const EmbedArgs& a, void* stream) {
 
 int run_embedding_grad(const EmbedArgs& a, const EmbedGradPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t zero = a.accumulate ? 0 : a.vocab * a.width * (a.out_bf16 ? 2 : 4);
-    const int64_t want = ceil_div64(zero, 1024 * 16 * 4);   // four 16-byte stores per thread
-    const unsigned fill = (unsigned)(want < 2048 ? want : 2048);
-    uint32_t* keys[2] = {(uint32_t*)(ws + p.keys[0]), (uint32_t*)(ws + p.keys[1])};
-    uint32_t* idx[2] = {(uint32_t*)(ws + p.idx[0]), (uint32_t*)(ws + p.idx[1])};
-    int at = 0;
-    if (p.sort_blocks == 0) {
-        const unsigned sorters = (unsigned)ceil_div64(a.tokens, 64);
-        if (sorters + fill > 0)
-            hipLaunchKernelGGL(rank_kernel, dim3(sorters + fill), dim3(1024), 0, s, a, keys[0], idx[0], (int)sorters, zero);
-    } else {
-        const int nblk = (int)p.sort_blocks;
-        uint32_t* counts = (uint32_t*)(ws + p.counts);
-        for (int d = 0; d < p.digits; ++d) {
-            const uint32_t* kin = d ? keys[(d - 1) & 1] : nullptr;
-            const uint32_t* iin = d ? idx[(d - 1) & 1] : nullptr;
-            at = d & 1;
-            if (p.sort_items == 4) launch_radix<4>(a, d, kin, iin, counts, nblk, keys[at], idx[at], d ? 0 : zero, d ? 0 : 4 * fill, s);
-            else launch_radix<16>(a, d, kin, iin, counts, nblk, keys[at], idx[at], d ? 0 : zero, d ? 0 : 4 * fill, s);
-        }
-    }
+    sort_tokens(a, p, a.accumulate ? 0 : a.vocab * a.width * (a.out_bf16 ? 2 : 4), ws, s);
     if (a.tokens > 0) {
-        const RunArgs r{a, keys[at], idx[at], (float*)(ws + p.part), p.chunk, p.nchunk, (a.width + 7) / 8 * 8, 0};
+        const RunArgs r = run_args(a, p, ws);
         if (a.in_bf16) a.out_bf16 ? launch_runs<true, true>(r, s) : launch_runs<true, false>(r, s);
         else a.out_bf16 ? launch_runs<false, true>(r, s) : launch_runs<false, false>(r, s);
     }
+    return (int)hipGetLastError();
+}
+
+int sort_weighted_rows(const EmbedArgs& a, const EmbedGradPlan& p, int* slot, char* ws, void* stream) {
+    EmbedArgs clear = a;
+    clear.out = slot;
+    sort_tokens(clear, p, a.vocab * 4, ws, (hipStream_t)stream);
+    return (int)hipGetLastError();
+}
+
+int sum_weighted_rows(const EmbedArgs& a, const EmbedGradPlan& p, const WeightedRows& w, char* ws, void* stream) {
+    RunArgs r = run_args(a, p, ws);
+    r.w = w;
+    launch_runs<true, false, false, true>(r, (hipStream_t)stream);
     return (int)hipGetLastError();
 }
 

@@ -61,8 +61,24 @@ inline bool make_embed_grad_plan(int64_t tokens, int64_t vocab, int64_t width, E
 }
 int run_embedding_grad(const EmbedArgs& a, const EmbedGradPlan& p, char* ws, void* stream);
 
+// Sums of a few weighted rows per id, for the output of another kernel to add: extra[slot[v] - 1] = the sum over ids[t] = v of
+// weight[pos[t]] in[t], for the rows v in [lo, hi) that some token has; slot is 0 elsewhere.  A row of extra belongs to a row
+// of [lo, hi) (by_row), or to a sorted token.
+struct WeightedRows {
+    const float* weight;
+    const int* pos;
+    int* slot;           // [vocab]
+    float* extra;        // [rows][pitch]
+    int64_t pitch;
+    int64_t lo, hi;
+    int by_row;
+};
+// sorts the tokens by id (a.in unused) and clears slot; then any number of ranges
+int sort_weighted_rows(const EmbedArgs& a, const EmbedGradPlan& p, int* slot, char* ws, void* stream);
+int sum_weighted_rows(const EmbedArgs& a, const EmbedGradPlan& p, const WeightedRows& w, char* ws, void* stream);
+
 // Layout of a cross entropy call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32, whose logits take two fp16 parts);
-// dparts: parts of D.  The vocabulary goes in `pieces` of `piece` rows (a multiple of 256).
+// dparts: parts of D (1 or 2 for bf16 alone, see kTwoParts; 3).  The vocabulary goes in `pieces` of `piece` rows (a multiple of 256).
 struct XentPlan {
     int64_t n, v, d, kp, dp;  // tokens, vocab, width, width rounded up to 64 and to 4
     int64_t np;               // tokens rounded up to 256
@@ -72,8 +88,11 @@ struct XentPlan {
     int64_t piece, pieces;
     int64_t nvt;              // softmax partials per token (forward)
     int tile_z, tile_h, tile_w;   // tile shapes of the logits, dH and dW (TILE_*)
+    bool exact_targets;       // dW gets what the one part of D leaves of each target's element, by rows summed beside the product
+    bool extra_by_row;        // those sums: one row per row of the piece, or per token, whichever are fewer
+    EmbedGradPlan sorted;     // the tokens by target
     int64_t split_z, split_h, split_w;   // slices of the reductions of the logits (over the width), dH (the piece), dW (the tokens)
-    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, z, w, winv, wtop, gscale, dl, dl16, rest, acc_h, acc_w, total;
+    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, z, w, winv, wtop, gscale, dl, dl16, rest, pos, slot, extra, sort, acc_h, acc_w, total;
 };
 
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens), 64 x 64
@@ -94,6 +113,11 @@ constexpr int64_t kShortTokens = 128;
 // and of so few, with fp32 sums in the vector units (with gradients, matrix cores against that: fp32 2 x 82297 x 2232 949 and
 // 780 us, 8 x 32000 x 2048 316 and 267; bf16 9 x 40448 x 1024 113 and 107; 17 and more tokens 5 to 24% slower that way)
 constexpr int64_t kRankTokens = 16;
+// bf16 gradients: up to so many tokens x vocab x width dW is made of two parts of D, beyond of one and the exact sums for the
+// targets' elements, three launches beside a second product (two parts and sums: 257 x 1013 x 255 32 and 51 us, 22 x 111040 x
+// 1024 240 and 254, 300 x 32000 x 1024 167 and 176; 4096 x 8192 x 512 210 and 193, 1024 x 32000 x 768 280 and 239, 128 x 131072
+// x 4096 1410 and 1259)
+constexpr double kTwoParts = 1.25e10;
 // fp32: up to so many tokens the products over W read it in place (see FewProduct).  With gradients, against planes of W in
 // the workspace: 32000 x 1024, 65 tokens 232 us and 404, 128 tokens 330 and 446, 180 tokens 423 and 432; 100544 x 2624, 164
 // tokens 3.2 ms and 2.9.
@@ -133,7 +157,7 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.dp = ceil_div64(width, 4) * 4;
     q.np = ceil_div64(tokens < 1 ? 1 : tokens, 256) * 256;
     q.parts = bf16 ? 1 : 3;
-    q.dparts = bf16 && dw_bf16 ? 1 : 3;
+    q.dparts = !bf16 || !dw_bf16 ? 3 : tokens <= kRankTokens || (double)tokens * vocab * width <= kTwoParts ? 2 : 1;
     q.few = !bf16 && tokens <= kFewTokens;
     q.wpack = !q.few && (!bf16 || width % 64 != 0);
     const bool scaled = !bf16 && !q.few;   // products over W from two fp16 parts of scaled rows
@@ -198,6 +222,15 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
         if (scaled) {
             q.dl16 = take(2 * q.np * q.piece * 2);
             q.gscale = take(q.np * 4);
+        }
+        q.exact_targets = q.dparts == 1;
+        if (q.exact_targets) {
+            q.extra_by_row = q.piece <= q.np;
+            make_embed_grad_plan(tokens, vocab, width, &q.sorted);
+            q.pos = take(q.np * 4);
+            q.slot = take(vocab * 4);
+            q.extra = take((q.extra_by_row ? q.piece : q.np) * q.dp * 4);
+            q.sort = take((int64_t)q.sorted.total);
         }
         if (q.pieces > 1 || q.split_h > 1) q.acc_h = take(q.split_h * q.np * q.dp * 4);
         if (q.split_w > 1) q.acc_w = take(q.split_w * q.piece * q.dp * 4);
