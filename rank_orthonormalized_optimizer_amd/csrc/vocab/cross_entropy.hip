@@ -112,6 +112,7 @@ struct PackArgs {
     float2* lg;      // (lse, grad) of the gathered row (gradient)
     float* gscale;   // the power of two in grad (gradient of fp32 operands)
     int* cnt;        // how many rows were gathered
+    float* factor;   // the one factor of all of them, 1 where there are none: it may be 1 / 0 then, and dW stays what it is
     int* blocks;     // rows to gather in each kCountBlock tokens, or null: few tokens
 };
 
@@ -270,7 +271,11 @@ __global__ __launch_bounds__(512) void pack_kernel(PackArgs a) {
             a.x.loss[t] = 0.f;
             a.x.lse_out[t] = 0.f;
         }
-        if (lane == 0 && blockIdx.x == gridDim.x - 1) a.cnt[0] = base + __popcll(kept);
+        if (lane == 0 && blockIdx.x == gridDim.x - 1) {
+            const int all = base + __popcll(kept);
+            a.cnt[0] = all;
+            if (GRAD && a.x.grad_n == 1) *a.factor = all > 0 ? a.x.grad[0] : 1.f;
+        }
     }
     __syncthreads();
     const int64_t t = t0 + w;
@@ -1030,7 +1035,7 @@ PackArgs pack_args(const XentArgs& x, const XentPlan& p, char* ws, bool exact) {
     return PackArgs{x, p.n, p.v, p.d, p.kp, p.np, exact || x.bf16 || p.few ? (uint16_t*)(ws + p.h) : nullptr,
                     x.bf16 || p.few ? nullptr : (uint16_t*)(ws + p.h16), (float*)(ws + p.hinv), (int*)(ws + p.map),
                     (int*)(ws + p.tgt), exact && p.exact_targets && x.dW ? (int*)(ws + p.pos) : nullptr, (float2*)(ws + p.lg),
-                    x.bf16 || p.few ? nullptr : (float*)(ws + p.gscale), (int*)(ws + p.cnt),
+                    x.bf16 || p.few ? nullptr : (float*)(ws + p.gscale), (int*)(ws + p.cnt), (float*)(ws + p.cnt) + 1,
                     p.n > kCountDirect ? (int*)(ws + p.cnt) + 64 : nullptr};
 }
 
@@ -1140,7 +1145,7 @@ int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) 
     z.rest = (float*)(ws + p.rest); z.np = p.np; z.piece = p.piece;
     const mm::Operand dl{z.dl, p.np * p.piece, p.piece, 0};
     OutArgs h{};
-    const float* factor = x.grad_n == 1 ? x.grad : nullptr;
+    const float* factor = x.grad_n == 1 ? pk.factor : nullptr;
     h.cnt = pk.cnt; h.d = (int)p.d; h.dp = (int)p.dp; h.factor = factor; h.rows = -1; h.split = (int)p.split_h; h.map = pk.map; h.out = x.dH; h.out_bf16 = x.bf16;
     h.acc = p.pieces > 1 || p.split_h > 1 ? (float*)(ws + p.acc_h) : nullptr;
     h.acc_rows = p.np;
