@@ -298,7 +298,8 @@ class MixedDion:
     The vocabulary matrices among the parameters (an embedding table, an output head, or one
     [vocab, width] matrix that is both) can be used through the optimizer, which then gathers their
     gradients itself: ``lookup`` and ``lookup_grad``, ``head_loss``.  All contributions since the last
-    step add up (tied weights, microbatches), and ``step`` takes them where ``grads`` holds None.
+    step add up (tied weights, microbatches), in float32 whatever the parameter's type, and ``step``
+    takes them where ``grads`` holds None.
     """
 
     def __init__(self, params, *, lr: float = 0.01, mu: float = 0.95, rank_fraction: float = 0.25,
@@ -322,13 +323,13 @@ class MixedDion:
         self.state = {i: (torch.zeros(self.params[i].numel(), dtype=torch.float32, device=self.params[i].device),
                           torch.zeros(self.params[i].numel(), dtype=torch.float32, device=self.params[i].device)
                           if other == "adamw" else None) for i in self.rest}
-        self.gathered = {}      # parameter index -> its gradient buffer
+        self.gathered = {}      # parameter index -> its gradient buffer, float32: bf16 would drop small contributions
         self.pending = set()    # those whose buffer holds contributions since the last step
 
     def _gather(self, i: int):
         """The gradient buffer of parameter i, and whether a contribution adds to what it holds."""
         if i not in self.gathered:
-            self.gathered[i] = torch.empty_like(self.params[i])
+            self.gathered[i] = torch.empty(self.params[i].shape, dtype=torch.float32, device=self.params[i].device)
         return self.gathered[i], i in self.pending
 
     @torch.no_grad()
@@ -375,7 +376,7 @@ class MixedDion:
         self.t += 1
         for idx, st in self.groups:
             X = torch.stack([self.params[i] for i in idx]).contiguous()
-            G = torch.stack([grads[i] for i in idx]).contiguous()
+            G = torch.stack([grads[i] for i in idx]).contiguous()   # bf16 beside a gathered float32: float32
             st.step(X, G)
             for k, i in enumerate(idx):
                 self.params[i].copy_(X[k])
