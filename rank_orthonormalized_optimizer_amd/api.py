@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 from collections import OrderedDict
+from functools import reduce
 
 import torch
 
@@ -365,14 +366,25 @@ class MixedDion:
     @torch.no_grad()
     def step(self, grads) -> None:
         grads = list(grads)
-        for i, g in enumerate(grads):
-            if g is None and i not in self.pending:
+        if len(grads) < len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        for i, p in enumerate(self.params):   # everything is looked at before anything is updated
+            if grads[i] is None and i not in self.pending:
                 raise ValueError(f"no gradient for parameter {i}: none given and none gathered")
-            if g is not None and i in self.pending:
+            if grads[i] is not None and i in self.pending:
                 raise ValueError(f"parameter {i} has a gathered gradient; pass None for it")
-            if g is None:
+            if grads[i] is None:
                 grads[i] = self.gathered[i]
-        self.pending.clear()
+            if not isinstance(grads[i], torch.Tensor):
+                raise TypeError(f"gradient of parameter {i} must be a torch.Tensor")
+            if grads[i].numel() != p.numel() or (p.dim() == 2 and grads[i].shape != p.shape):
+                raise ValueError(f"gradient of parameter {i} has shape {tuple(grads[i].shape)}, expected {tuple(p.shape)}")
+            if grads[i].device != p.device:
+                raise ValueError(f"gradient of parameter {i} lives on {grads[i].device}, expected {p.device}")
+        for idx in [idx for idx, _ in self.groups] + [[i] for i in self.rest]:
+            dtype = reduce(torch.promote_types, [grads[i].dtype for i in idx])   # of a stack's gradients together
+            if dtype not in _DT:
+                raise TypeError(f"gradients of parameters {idx} have dtype {dtype}, expected one of {tuple(_DT)}")
         self.t += 1
         for idx, st in self.groups:
             X = torch.stack([self.params[i] for i in idx]).contiguous()
@@ -387,3 +399,4 @@ class MixedDion:
                 adamw_step_(p, g, m, v, self.t, self.other_lr, self.betas[0], self.betas[1], self.eps, self.wd)
             else:
                 lion_step_(p, g, m, self.other_lr, self.betas[0], self.betas[1], self.wd)
+        self.pending.clear()   # only now: a refused step leaves them for the next
