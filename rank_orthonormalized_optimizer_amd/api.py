@@ -1,6 +1,7 @@
 """torch-facing wrappers of dion_step_batched (marshalling only, no arithmetic)."""
 from __future__ import annotations
 
+import operator
 from collections import OrderedDict
 from functools import reduce
 
@@ -327,6 +328,13 @@ class MixedDion:
         self.gathered = {}      # parameter index -> its gradient buffer, float32: bf16 would drop small contributions
         self.pending = set()    # those whose buffer holds contributions since the last step
 
+    def _index(self, i: int) -> int:
+        """i counted from the front, as the buffers are kept (-1 is the last parameter)."""
+        n, k = len(self.params), operator.index(i)
+        if not -n <= k < n:
+            raise IndexError(f"parameter {k} of {n}")
+        return k % n
+
     def _gather(self, i: int):
         """The gradient buffer of parameter i, and whether a contribution adds to what it holds."""
         if i not in self.gathered:
@@ -336,11 +344,12 @@ class MixedDion:
     @torch.no_grad()
     def lookup(self, i: int, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
         """Rows ``scale * params[i][ids]`` (embedding_)."""
-        return vocab.embedding_(ids, self.params[i], scale)
+        return vocab.embedding_(ids, self.params[self._index(i)], scale)
 
     @torch.no_grad()
     def lookup_grad(self, i: int, ids: torch.Tensor, dY: torch.Tensor, scale: float = 1.0, *, padding_id: int = -1) -> None:
         """Add the table gradient of ``lookup(i, ids, scale)`` for the gradient ``dY`` of its rows (embedding_grad_)."""
+        i = self._index(i)
         dW, add = self._gather(i)
         vocab.embedding_grad_(ids, dY, dW, scale, padding_id=padding_id, accumulate=add)
         self.pending.add(i)
@@ -353,6 +362,7 @@ class MixedDion:
         ``grad``: float32, the loss's gradient per token or one element for all (default: the mean over
         the tokens that are not ignored).  Returns (per-token loss, dH) and adds the head's gradient.
         """
+        i = self._index(i)
         W = self.params[i]
         loss, lse = vocab.linear_cross_entropy_(H, W, targets, ignore_index=ignore_index)
         if grad is None:
