@@ -4,6 +4,11 @@ matrices (marshalling only, no arithmetic).
 Tensors are contiguous and on one GPU; everything is enqueued on ``stream`` (default: torch's
 current stream of that GPU) with no host sync.  Scratch and outputs that are not given are
 allocated by torch on that stream.
+
+No call records a graph for autograd: gradients are calls of their own (``embedding_grad_``,
+``linear_cross_entropy_grad_``).  Where autograd would expect one, ``embedding_`` and
+``linear_cross_entropy_`` refuse tensors that require a gradient: call them under
+``torch.no_grad()`` or on detached tensors.
 """
 from __future__ import annotations
 
@@ -28,6 +33,14 @@ def _need(t, name: str, dtypes, device=None, shape=None) -> None:
         raise ValueError(f"{name} lives on {t.device}, expected {device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _no_graph(call: str, **tensors) -> None:
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{call} records no graph, but {name} requires a gradient: call it under torch.no_grad() "
+                                 f"or detach {name}, and {call[:-1]}_grad_ for the gradient")
 
 
 def _matrix(t, name: str, device=None):
@@ -79,6 +92,7 @@ def embedding_(ids: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: torc
     ids: int32 or int64 of any shape; W: [vocab, width] float32 or bfloat16; out: ids' shape + [width],
     float32 or bfloat16 (default: W's type).  An id outside [0, vocab) gives a row of NaN.
     """
+    _no_graph("embedding_", W=W, out=out)
     vocab, width = _matrix(W, "W")
     device = W.device
     _need(ids, "ids", _IT, device)
@@ -148,6 +162,7 @@ def linear_cross_entropy_(H: torch.Tensor, W: torch.Tensor, targets: torch.Tenso
     int64.  Returns (or fills) float32 ``loss`` and ``lse`` (log-sum-exp of the logits) of targets' shape: 0
     where the target is ``ignore_index``; NaN loss for any other target outside [0, vocab).
     """
+    _no_graph("linear_cross_entropy_", H=H, W=W, loss=loss, lse=lse)
     tokens, vocab, width = _head(H, W, targets)
     device = W.device
     with _On(device, stream) as handle:
