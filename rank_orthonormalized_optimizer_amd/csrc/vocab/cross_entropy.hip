@@ -790,26 +790,27 @@ __global__ __launch_bounds__(256) void rank_out_kernel(OutArgs a, int hparts, in
 template <int G>
 __global__ __launch_bounds__(256) void join_kernel(OutArgs a) {
     const int rows = a.rows < 0 ? a.cnt[0] : a.rows, nc = a.dp / 4;
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;
     const int lane = threadIdx.x % G;
-    if (i >= (int64_t)rows * nc) return;
-    const int64_t r = i / nc;
-    const int c = (int)(i - r * nc) * 4, n = a.d - c < 4 ? a.d - c : 4;
-    f32x4 sum{0.f, 0.f, 0.f, 0.f};
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G; i < (int64_t)rows * nc; i += (int64_t)gridDim.x * (256 / G)) {
+        const int64_t r = i / nc;
+        const int c = (int)(i - r * nc) * 4, n = a.d - c < 4 ? a.d - c : 4;
+        f32x4 sum{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int s = lane; s < a.split; s += G) sum += *(const f32x4*)(a.acc + (s * a.acc_rows + r) * a.dp + c);
-    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+        for (int s = lane; s < a.split; s += G) sum += *(const f32x4*)(a.acc + (s * a.acc_rows + r) * a.dp + c);
+        float v[4] = {sum[0], sum[1], sum[2], sum[3]};
 #pragma unroll
-    for (int o = G / 2; o; o >>= 1)
+        for (int o = G / 2; o; o >>= 1)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o);
-    if (lane > 0) return;
-    if (const float* extra = extra_row(a, r)) {
-        const f32x4 x = *(const f32x4*)(extra + c);
+            for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o);
+        if (lane == 0) {
+            if (const float* extra = extra_row(a, r)) {
+                const f32x4 x = *(const f32x4*)(extra + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += x[e];
+                for (int e = 0; e < 4; ++e) v[e] += x[e];
+            }
+            store_out(a, r, c, n, v);
+        }
     }
-    store_out(a, r, c, n, v);
 }
 
 // Logits whose reduction was sliced: partial sums [split][n][piece], and the scales of fp16 parts (or null).
@@ -1061,9 +1062,9 @@ void launch_few_out(const OutArgs& a, int64_t n, hipStream_t s) {
 }
 
 void launch_join(const OutArgs& a, int64_t rows, hipStream_t s) {
-    const int64_t n = rows * (a.dp / 4);
-    if (a.split >= 8) hipLaunchKernelGGL((join_kernel<8>), dim3((unsigned)ceil_div64(n * 8, 256)), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((join_kernel<1>), dim3((unsigned)ceil_div64(n, 256)), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)join_blocks(rows, a.dp, a.split));
+    if (join_lanes(a.split) == 8) hipLaunchKernelGGL((join_kernel<8>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((join_kernel<1>), grid, dim3(256), 0, s, a);
 }
 
 template <int N>
@@ -1131,8 +1132,8 @@ __global__ __launch_bounds__(256) void clear_kernel(uint16_t* p, int64_t n) {
 int run_xent_grad(const XentArgs& x, const XentPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
     if (p.n == 0) {   // no tokens: dW is zero
-        const int64_t n = p.v * p.d * (x.dw_bf16 ? 1 : 2), blocks = ceil_div64(n, 256 * 8);
-        hipLaunchKernelGGL(clear_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, (uint16_t*)x.dW, n);
+        const int64_t n = p.v * p.d * (x.dw_bf16 ? 1 : 2);
+        hipLaunchKernelGGL(clear_kernel, dim3((unsigned)stride_blocks(ceil_div64(n, 256 * 8))), dim3(256), 0, s, (uint16_t*)x.dW, n);
         return (int)hipGetLastError();
     }
     const PackArgs pk = pack_args(x, p, ws, true);

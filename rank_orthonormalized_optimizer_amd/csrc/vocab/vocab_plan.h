@@ -9,6 +9,9 @@ namespace dion {
 constexpr int64_t kVocabMax = ((int64_t)1 << 24) - 1, kWidthMax = (int64_t)1 << 16;
 
 inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Workgroups for a pass that strides over its items where `blocks` are more: HIP takes fewer than 2^32 threads per grid
+// dimension, which a pass over tokens x width of the largest sizes would reach.
+inline int64_t stride_blocks(int64_t blocks) { return blocks < 65536 ? blocks : 65536; }
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct EmbedArgs {
@@ -238,6 +241,12 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     q.total = off;
     *p = q;
     return off < ((size_t)1 << 46);
+}
+
+// Lanes that share the slices of four columns of the output, and the workgroups of 256 that join them.
+inline int join_lanes(int64_t split) { return split >= 8 ? 8 : 1; }
+inline int64_t join_blocks(int64_t rows, int64_t dp, int64_t split) {
+    return stride_blocks(ceil_div64(rows * (dp / 4) * join_lanes(split), 256));
 }
 
 struct XentArgs {
