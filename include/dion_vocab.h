@@ -9,8 +9,13 @@
  *   dion_linear_xent_grad  D[t][v] = grad[t] (exp(z[t][v] - lse[t]) - [v = target[t]]);
  *                          dH = D W;  dW (+)= D^T H
  *
- * The logits z (tokens x vocab) are never stored: the loss keeps a running maximum and sum per
- * tile of the vocabulary, the gradient forms them again in pieces of the vocabulary.
+ * The logits z (tokens x vocab) are not kept from the loss to the gradient.  The loss keeps a running maximum and sum per
+ * tile of the vocabulary (where the tiles do not fill the chip, it stores partial logits, few then, in its workspace).  The
+ * gradient forms them again, a piece of the vocabulary at a time, and holds D of that piece in its workspace: 16-bit parts
+ * of 2^28 elements each, or of as many as 8192 rows of the vocabulary need, at most 2^30.  Up to 2^28 elements that is D of
+ * the whole vocabulary, which is as large as logits.  Workspaces of 8192 tokens x 32000 x 2048: loss 40 MiB, gradient
+ * 604 MiB for bf16 outputs (one part) and 1532 MiB for an fp32 dW (three), where bf16 logits are 500; 8192 x 131072 x 4096:
+ * 96, 849 and 1728 MiB (2048); 4096 x 32000 x 1024 in fp32: 145 and 1479 MiB (fp32 logits 500).
  *
  * Memory, execution and errors are those of dion.h: caller-owned device memory, row-major and
  * contiguous, nothing allocated and nothing kept between calls; asynchronous on `stream` (NULL =
@@ -74,8 +79,9 @@ int dion_embedding_grad(const void* ids, const void* dY, void* dW, int64_t token
  *   lse      device fp32 [tokens], written: log sum_v exp z[t][v], for dion_linear_xent_grad
  * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores.  fp32 operands give fp32-accurate
  * logits from 16-bit parts, whichever is cheaper for the sizes: three bf16 parts (an exact split, six part products, terms
- * below 2^-24 dropped), or two fp16 parts of each row scaled by a power of two (2^-23 of an element and 2^-39 of its row's
- * largest left out, three part products, terms below 2^-22 dropped).
+ * below 2^-24 dropped), or two fp16 parts of each row scaled by a power of two (2^-23 of an element and 2^-38 of its row's
+ * largest left out, or 2^-125 where that is more, three part products, terms below 2^-22 dropped).
+ * Operands are taken to be finite and logits below 2^127; others make what they reach NaN or infinite.
  * Workspace size for both calls: dion_linear_xent_workspace_size (for_grad 0 or 1; 0 for invalid sizes).
  */
 size_t dion_linear_xent_workspace_size(int64_t tokens, int64_t vocab, int64_t width, int dtype, int dw_dtype,
@@ -94,10 +100,11 @@ int dion_linear_xent(const void* H, const void* W, const void* targets, float* l
  * A token whose target is neither ignored nor in [0, vocab) makes its dH row and dW NaN.
  * Arithmetic: for bf16 outputs of bf16 operands D is rounded once to bf16 (without grad where grad_n is 1: that factor is
  * applied to the fp32 sums), and what the rounding left of the target's element is added to dH and dW in fp32; small dW come
- * from two bf16 parts of D.  Where the output or
- * the operands are fp32, the products are fp32-accurate, from 16-bit parts as in dion_linear_xent: dW from three bf16 parts
- * of D and H, dH from three bf16 parts, or from two fp16 parts of D (per token) and of W (per row) scaled by powers of two,
- * which leaves out 2^-39 of |grad[t]| times the largest |W| besides.
+ * from two bf16 parts of D.  Where the output or the operands are fp32, the products are fp32-accurate, from 16-bit parts as
+ * in dion_linear_xent: dW from three bf16 parts of D and H, dH from three bf16 parts, or from two fp16 parts of D (per token)
+ * and of W (per row) scaled by powers of two, which leaves out vocab 2^-38 of |grad[t]| times the largest |W| besides.
+ * Products below fp32's normal numbers may count as zeros.
+ * Where no target counts, grad is not used (1 / count may be infinite then).
  */
 int dion_linear_xent_grad(const void* H, const void* W, const void* targets, const float* lse, const float* grad,
                           int64_t grad_n, void* dH, void* dW, int64_t tokens, int64_t vocab, int64_t width,

@@ -1,4 +1,4 @@
-// Softmax cross entropy of a linear head without stored logits, and its gradients.
+// Softmax cross entropy of a linear head, and its gradients, the logits formed where they are used.
 //
 //   z = H W^T (tokens x vocab);  lse = log sum_v exp z;  loss = lse - z[target]
 //   D = grad (exp(z - lse) - onehot(target));  dH = D W;  dW = D^T H
@@ -61,8 +61,8 @@ __device__ __forceinline__ void split3(float a, uint32_t (&part)[3]) {
     part[2] = down16(r - up16(part[1]));
 }
 
-// a = (h + l) / scale to 2^-23 |a| and 2^-39 of the row's largest: fp16 parts of a scale, a power of two that puts the row's
-// largest value into [2^13, 2^14)
+// a = (h + l) / scale to 2^-23 |a| and 2^-38 of the row's largest: fp16 parts of a scale, a power of two that puts the row's
+// largest value into [2^13, 2^14); a low part below the normal numbers is off by up to 2^-25
 __device__ __forceinline__ void split2(float a, float scale, uint32_t (&part)[2]) {
     const _Float16 h = (_Float16)(a * scale);
     const _Float16 l = (_Float16)(a * scale - (float)h);
@@ -70,9 +70,9 @@ __device__ __forceinline__ void split2(float a, float scale, uint32_t (&part)[2]
     part[1] = (uint32_t)__builtin_bit_cast(uint16_t, l);
 }
 
-// That scale for a row whose largest magnitude is `top`, at most 2^100 so that products of two inverses stay normal numbers,
-// and its inverse.  A row of zeros gets the largest scale: its inverse must not pass for the largest of a matrix.  (A row
-// that is not finite stays as it is.)
+// That scale for a row whose largest magnitude is `top`, at most 2^100: its inverse, and 2^14 over that as D is scaled, stay
+// normal numbers (a row whose largest is below 2^-87 is then good to 2^-125).  And its inverse.  A row of zeros gets the
+// largest scale: its inverse must not pass for the largest of a matrix.  (A row that is not finite stays as it is.)
 __device__ __forceinline__ float row_scale(float top, float& inverse) {
     int e = 140 - (int)(__float_as_uint(top) >> 23);   // 127 + 13 - biased exponent
     if (!(top < INFINITY)) e = 0;

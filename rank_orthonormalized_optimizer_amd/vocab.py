@@ -156,7 +156,7 @@ def _head(H, W, targets):
 def linear_cross_entropy_(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, *, ignore_index: int = -100,
                           loss: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None, stream=None):
-    """Softmax cross entropy of the logits ``H W^T`` per token, which are never stored (dion_linear_xent).
+    """Softmax cross entropy of the logits ``H W^T`` per token, which are not kept (dion_linear_xent).
 
     H: targets' shape + [width]; W: [vocab, width] of the same type, float32 or bfloat16; targets: int32 or
     int64.  Returns (or fills) float32 ``loss`` and ``lse`` (log-sum-exp of the logits) of targets' shape: 0
@@ -192,7 +192,8 @@ def linear_cross_entropy_grad_(H: torch.Tensor, W: torch.Tensor, targets: torch.
 
     lse: linear_cross_entropy_'s for the same H, W, targets; grad: float32, of targets' shape or one element for
     every token (1 / count for a mean).  dH (H's shape and type) and dW ([vocab, width], float32 or bfloat16) are
-    written; one of them may be None, which saves its product.  ``accumulate`` adds to dW instead.  Ignored tokens
+    written; one of them may be None, which saves its product.  An fp32 dW of bf16 operands is fp32-accurate and takes
+    three times the product of a bf16 one, and its workspace.  ``accumulate`` adds to dW instead.  Ignored tokens
     get zeros in dH and leave nothing in dW.
     """
     tokens, vocab, width = _head(H, W, targets)
