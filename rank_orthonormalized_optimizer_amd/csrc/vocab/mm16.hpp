@@ -325,7 +325,6 @@ struct FewProduct {
     using TileB = Tile<C::BN, false, 4>;   // the planes are loaded by four waves each, two at a time
     static constexpr int kVec = C::V4 ? 4 : 1;   // elements of A per lane and load
     static constexpr int kLoadsA = C::BM * kBK / (64 * kVec) / 8, kLoadsB = 3 * C::BN * kBK * 2 / 1024;   // per wave; per workgroup
-    static constexpr int kRowsB = kBK * 2 * 8;   // bytes of eight rows of a plane: one wave load
 
     int lane, wave, xa, xb, total, m0, n0;
     uint16_t* lds;
