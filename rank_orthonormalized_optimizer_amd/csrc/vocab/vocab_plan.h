@@ -36,13 +36,19 @@ struct EmbedGradPlan {
     size_t keys[2], idx[2], counts, part, total;
 };
 
-constexpr int kRankMax = 16384;    // tokens sorted by counting, see rank_kernel
+// Up to so many tokens are sorted by counting (rank_kernel, every key against every other), more by radix (table gradient of
+// 32000 x 2048 bf16 by counting and by radix: 8192 tokens 35 and 52 us, 16384 52 and 58, 32768 99 and 80; 16384 tokens added
+// to 65536 x 256 41 and 39)
+constexpr int kRankMax = 16384;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;   // two passes up to a vocabulary of 2^18 - 1
 
 inline bool make_embed_grad_plan(int64_t tokens, int64_t vocab, int64_t width, EmbedGradPlan* p) {
     EmbedGradPlan q{};
-    // about 512 chunks of at least 16 tokens: short enough to fill the chip, long enough that the
-    // partial rows at the chunk borders stay a fraction of the rows read
+    // At most 512 chunks of at least 16 tokens: with wide rows short enough to fill the chip (a workgroup takes a chunk where
+    // a row has 2048 bf16 elements or more) and long enough that the partial rows at the chunk borders stay a fraction of the
+    // rows read.  Against 256, 1024 and 2048 chunks: 16384 tokens x 2048 bf16 52 us and 57, 54, 54; 65536 x 4096 added to
+    // fp32 286 and 357, 308, 291.  Narrow rows, many chunks to a workgroup, would gain from more: 65536 x 1024 82 and 119, 71, 73;
+    // 65536 x 255 fp32 88 and 138, 64, 59; 65536 x 64 bf16 71 and 111, 53, 47.
     q.chunk = 16;
     while (q.chunk * 512 < tokens) q.chunk *= 2;
     q.nchunk = ceil_div64(tokens, q.chunk);
@@ -81,7 +87,8 @@ int sort_weighted_rows(const EmbedArgs& a, const EmbedGradPlan& p, int* slot, ch
 int sum_weighted_rows(const EmbedArgs& a, const EmbedGradPlan& p, const WeightedRows& w, char* ws, void* stream);
 
 // Layout of a cross entropy call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32, whose logits take two fp16 parts);
-// dparts: parts of D (1 or 2 for bf16 alone, see kTwoParts; 3).  The vocabulary goes in `pieces` of `piece` rows (a multiple of 256).
+// dparts: parts of D (1 or 2 for bf16 alone, see kTwoParts; 3).  The vocabulary goes in `pieces` of `piece` rows (a multiple of
+// 256).
 struct XentPlan {
     int64_t n, v, d, kp, dp;  // tokens, vocab, width, width rounded up to 64 and to 4
     int64_t np;               // tokens rounded up to 256
@@ -95,7 +102,8 @@ struct XentPlan {
     bool extra_by_row;        // those sums: one row per row of the piece, or per token, whichever are fewer
     EmbedGradPlan sorted;     // the tokens by target
     int64_t split_z, split_h, split_w;   // slices of the reductions of the logits (over the width), dH (the piece), dW (the tokens)
-    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, z, w, winv, wtop, gscale, dl, dl16, rest, pos, slot, extra, sort, acc_h, acc_w, total;
+    size_t h, h16, hinv, map, tgt, lg, cnt, part, zt, z, w, winv, wtop, gscale, dl, dl16, rest, pos, slot, extra, sort, acc_h, acc_w;
+    size_t total;
 };
 
 enum { TILE_256 = 0, TILE_128 = 1, TILE_32 = 2, TILE_64 = 3 };   // 256 x 256, 128 x 128, 128 x 32 (few tokens), 64 x 64
@@ -106,10 +114,14 @@ constexpr int64_t kPieceElems = (int64_t)1 << 28;
 // tokens x width in fp32 (131072 tokens x 32000 x 2048, bf16, with gradients: pieces of 2048 rows 60.9 ms, 4096 55.8, 8192
 // 53.0, 16384 53.7; fp32, 65536 tokens: 4096 rows 102.0 ms, 8192 95.9)
 constexpr int64_t kPieceRows = 8192, kPieceMost = (int64_t)1 << 30;
-constexpr int64_t kPlaneBytes = (int64_t)2048 << 20;   // of W's planes per piece: few pieces keep the products large
+// of W's planes per piece, a bound of the workspace alone: 512 MiB, this and 8 GiB are within 1% (fp32 loss 1024 x 131072 x 4096
+// 3.33, 3.29 and 3.30 ms, with gradients 4096 x 65536 x 4096 25.7, 25.7 and 25.8; bf16 loss 2048 x 131072 x 1000 534, 535 and 531 us)
+constexpr int64_t kPlaneBytes = (int64_t)2048 << 20;
 constexpr int kCUs = 256;
 constexpr int kCountBlock = 4096;          // tokens per count of gathered rows,
-constexpr int64_t kCountDirect = 16384;    // which fewer tokens than this do without
+// which up to so many tokens do without, each workgroup of the gathering counting from the first token (with counts and without,
+// bf16 loss over 1000 x 128: 8192 tokens 26.6 and 24.6 us, 16384 32.8 and 35.4, 32768 54 and 73, 65536 94 and 185)
+constexpr int64_t kCountDirect = 16384;
 // dW of so few tokens is a stream of writes: three workgroups per CU with tiles of 128 x 64 (128 x 128 and two: 22 tokens x
 // 111040 x 1024 bf16 with gradients 297 us instead of 275, 64 x 64 and four 272, but fp32 4 x 115186 x 636 441 us, not 414)
 constexpr int64_t kShortTokens = 128;
@@ -130,7 +142,9 @@ inline int64_t tile_m(int t) { return t == TILE_256 ? 256 : t == TILE_64 ? 64 : 
 inline int64_t tile_n(int t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : t == TILE_64 ? 64 : 32; }
 inline int64_t tiles(int64_t m, int64_t n, int t) { return ceil_div64(m, tile_m(t)) * ceil_div64(n, tile_n(t)); }
 // Slices of a reduction of length k (`terms` part products of it) so that an output of m x n fills the chip, each of
-// 24 slabs of 64 at least (8 for the small tiles, whose slabs are shorter): a slice costs a pass over the output.
+// 24 slabs of 64 at least (8 for the small tiles, whose slabs are shorter): a slice costs a pass over the output.  Against
+// half and twice as many: fp32 with gradients 257 x 1013 x 255 66 us and 69, 71, 300 x 5000 x 1024 191 and 200, 197; bf16 1024 x
+// 8192 x 1024 170 and 176, 189; fp32 loss 1198 x 1640 x 3923 95 and 95, 145; bf16 loss 64 x 8192 x 2048 23 and 29, 23.
 inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int64_t terms, int tile) {
     int64_t s = kCUs / tiles(m, n, tile);
     const int64_t most = ceil_div64(k, 64) * terms / (tile == TILE_32 || tile == TILE_64 ? 8 : 24);
@@ -139,7 +153,9 @@ inline int64_t pick_split(int64_t m, int64_t n, int64_t k, int64_t terms, int ti
     return s < 1 ? 1 : s;
 }
 // The largest tile, which reads each operand least often, that still gives half the CUs a workgroup, if the
-// reduction is long enough by slices of it.
+// reduction is long enough by slices of it.  Against a quarter and all of the CUs: fp32 with gradients 300 x 5000 x 1024 191 us
+// and 234, 197; bf16 700 x 2048 x 2048 114 and 147, 114, 1024 x 8192 x 1024 170 and 184, 176; fp32 loss 1198 x 1640 x 3923 95 and
+// 94, 139.
 inline int pick_tile(int64_t m, int64_t n, int64_t k, int64_t terms) {
     if (n <= 32) return TILE_32;
     if (tiles(m, n, TILE_256) * pick_split(m, n, k, terms, TILE_256) >= kCUs / 2) return TILE_256;
@@ -243,7 +259,9 @@ inline bool make_xent_plan(int64_t tokens, int64_t vocab, int64_t width, int bf1
     return off < ((size_t)1 << 46);
 }
 
-// Lanes that share the slices of four columns of the output, and the workgroups of 256 that join them.
+// Lanes that share the slices of four columns of the output, and the workgroups of 256 that join them.  Eight lanes and one, with
+// gradients: fp32 1 x 100000 x 64 61 and 76 us, 64 x 131072 x 255 182 and 190; bf16 32 x 131072 x 256 87 and 96, 512 x 32000 x 2048
+// (eight slices) 317 and 310.
 inline int join_lanes(int64_t split) { return split >= 8 ? 8 : 1; }
 inline int64_t join_blocks(int64_t rows, int64_t dp, int64_t split) {
     return stride_blocks(ceil_div64(rows * (dp / 4) * join_lanes(split), 256));
