@@ -15,16 +15,17 @@
 // small, rows of frequent targets then off by up to 2^-8 in one direction.  What it leaves of them goes to dH and dW in fp32:
 // rest[t] W[target] as dH is stored, and for dW the sums of rest[t] H[t] over the tokens of each target (sum_weighted_rows),
 // which its product adds.  dW of 8192 x 32000 x 2048 against 64 bits, relative: 1.80e-3 without them, 1.65e-3 with them and for
-// a correctly rounded dW.  fp32 operands: logits and dH
-// from two fp16 parts of W's and H's rows, each row scaled by a power of two (three products), dW from three bf16 parts of D
-// and H (six: D's columns for rare tokens are too small for fp16).  fp32 and few tokens: W in place, split in registers
-// (FewProduct).
+// a correctly rounded dW.
+// fp32 operands: logits and dH from two fp16 parts of W's and H's rows, each row scaled by a power of two (three products), dW
+// from three bf16 parts of D and H (six: D's columns for rare tokens are too small for fp16).  fp32 and few tokens: W in place,
+// split in registers (FewProduct).
 //
 // Bound by the matrix cores: 2 tokens vocab width flops for the loss, four times that for loss and gradients together, the
-// logits formed twice.  8192 tokens (5% ignored) x 32000 x 2048 in bf16: loss 0.78 to 0.81 ms (1.27 to 1.31 PFLOP/s, of the
-// 1.42 that the library's product of these sizes reaches), loss and gradients 3.2 to 3.3 ms; matrix cores busy 61 to 70% of
-// the cycles.  Without the matrix products the loss kernel takes 0.57 ms and the gradients' products 0.70 and 0.73, without
-// the loads 0.58 to 0.61: the two overlap but for the barrier of each slab.
+// logits formed twice.  8192 tokens (5% ignored) x 32000 x 2048 in bf16: loss 0.80 to 0.82 ms (1.25 to 1.28 PFLOP/s, of the
+// 1.42 that the library's product of these sizes reaches), loss and gradients 3.40 to 3.45 ms, 0.08 of them the targets'
+// elements of dW (sorting 15 us, sums 24, their rows in the product's epilogue 40); matrix cores busy 59 to 65% of the cycles.
+// Without the matrix products the loss kernel takes 0.57 ms and the gradients' products 0.70 and 0.73, without the loads 0.58
+// to 0.61: the two overlap but for the barrier of each slab.
 //
 // Where the tiles are too few for the chip, the logits' reduction over the width is sliced and the partial logits, few then,
 // are stored: one pass over them makes the loss or D.
