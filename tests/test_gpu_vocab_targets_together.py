@@ -84,3 +84,29 @@ def test_two_streams_at_once(cuda):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(a[k], b[k]) for k in RESULTS)
+
+
+@pytest.mark.parametrize("tokens,vocab,width", SIZES)
+def test_int32_targets_and_an_ignored_id_of_the_vocabulary(cuda, tokens, vocab, width):
+    """int32 and int64 targets give the same bits; an ignored id that is a row of W leaves nothing in that row but the
+    probabilities of the others, and a target outside the vocabulary makes dW NaN."""
+    import rank_orthonormalized_optimizer_amd as dion
+    s = state(cuda, tokens, vocab, width, 5)
+    y = s["y"].clamp(min=0)          # the ignored ones become targets of id 0, the most frequent one
+    one = torch.full((1,), 1.0 / tokens, device=cuda)
+
+    def grads(targets, ignore):
+        _, lse = dion.linear_cross_entropy_(s["H"], s["W"], targets, ignore_index=ignore)
+        dH, dW = torch.empty_like(s["H"]), torch.empty_like(s["W"])
+        dion.linear_cross_entropy_grad_(s["H"], s["W"], targets, lse, one, dH, dW, ignore_index=ignore)
+        return dH, dW
+
+    dH, dW = grads(y, 0)
+    for a, b in zip((dH, dW), grads(y.to(torch.int32), 0)):
+        assert torch.equal(a, b)
+    for a, b in zip((dH, dW), grads(torch.where(y == 0, -100, y), -100)):
+        assert torch.equal(a, b)
+    assert not dH[y == 0].any() and torch.isfinite(dW.float()).all()
+    y[3] = vocab
+    dH, dW = grads(y, 0)
+    assert torch.isnan(dW).all() and torch.isnan(dH[3]).all() and torch.isfinite(dH[4:].float()).all()
