@@ -1,0 +1,129 @@
+/*
+ * dion_block.h — C ABI of the operators of a model's residual blocks: dropout whose mask is never stored, the
+ * root-mean-square norm with the residual's addition in front of it (and dropout, and an output in 8 bits), the gated
+ * feed-forward block, and their gradients.  They stand between the vocabulary operators of dion_vocab.h at the two ends of
+ * the model; the weight gradients go where the optimizer steps of dion.h read them.
+ *
+ *   dion_dropout         out = residual + keep x / (1 - p)
+ *   dion_rms_norm        h = residual + keep x / (1 - p);  rstd = (mean h^2 + eps)^(-1/2);  y = h rstd w
+ *                        in 8 bits: q = e4m3(y / scale), scale the least power of two with max |y| <= 448 scale
+ *   dion_rms_norm_grad   n = h rstd;  g = dY w;  dh = rstd (g - n mean(g n)) + dsum;  dx = keep dh / (1 - p);  dw (+)= sum dY n
+ *   dion_gated_ffn       a = X Wg^T;  b = X Wu^T;  u = act(a) b;  Y = u Wd^T
+ *   dion_gated_ffn_grad  du = dY Wd;  da = du b act'(a);  db = du act(a);  dX = da Wg + db Wu;
+ *                        dWg (+)= da^T X;  dWu (+)= db^T X;  dWd (+)= dY^T u
+ *
+ * The mask.  keep of element i of an array (row-major, of any shape) is: word i % 4 of Philox4x32-10 (Salmon, Moraes, Dror
+ * and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with the counter (i / 4, site), 64 bits each, and the key
+ * `seed` is at least p 2^32 (rounded, and at most 2^32 - 1).  It depends on the seed, the site and the element's number alone, so that the gradient
+ * forms it again: dion_dropout without residual of the output's gradient, or dx of dion_rms_norm_grad.  The seed is read
+ * from device memory when the kernel runs; a captured graph draws another mask on each replay if the program changes it.
+ * Sites keep the masks of different layers apart.
+ *
+ * Memory, execution and errors are those of dion.h: caller-owned device memory, row-major and contiguous, nothing allocated
+ * and nothing kept between calls; asynchronous on `stream` (NULL = default stream) with no host synchronization, safe to
+ * capture in a HIP graph; results bitwise reproducible (no floating-point atomics); status codes of dion.h, checked on the
+ * host before anything is enqueued.  Matrices and vectors must be 16-byte aligned, workspaces 256-byte, fp32 per-row arrays
+ * as their elements, the seed 8-byte; any width is taken.  Written arrays must not overlap anything else, but for what is
+ * said below.  Calls that share a workspace must be ordered on one stream.  Sums, norms and products accumulate in fp32
+ * or more; each output is rounded once to its type.
+ *
+ * Limits: rows <= DION_BLOCK_MAX_ROWS, 1 <= width <= 2^16, 1 <= hidden <= 2^17; beyond them DION_ERR_SHAPE.
+ */
+#ifndef DION_BLOCK_MI355X_H
+#define DION_BLOCK_MI355X_H
+
+#include "dion.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* a third element type where it is named: OCP e4m3 (no infinities, largest 448) with an fp32 scale per row */
+#define DION_E4M3 2
+
+typedef enum { DION_SILU = 0, DION_GELU = 1 } dion_activation;   /* a / (1 + exp(-a)); the tanh form of gelu */
+
+#define DION_BLOCK_MAX_ROWS ((int64_t)1 << 20)
+
+/*
+ * Dropout with an optional addition, formed in fp32 and rounded once.
+ *   x         device, [n], x_dtype (DION_F32 or DION_BF16), read only.  0 <= n <= 2^36
+ *   residual  device, [n], out_dtype, or NULL
+ *   out       device, [n], out_dtype, written; may be residual itself (added to in place)
+ *   p         probability of dropping an element, in [0, 1)
+ *   seed      device, one int64; may be NULL where p is 0
+ */
+int dion_dropout(const void* x, const void* residual, void* out, int64_t n, double p, const int64_t* seed, int64_t site,
+                 int x_dtype, int out_dtype, void* stream);
+
+/*
+ * Root-mean-square norm of each row.
+ *   x         device, [rows][width], x_dtype, read only
+ *   residual  device, [rows][width], s_dtype (of the residual stream), or NULL
+ *   w         device, [width], w_dtype
+ *   h         device, [rows][width], s_dtype, written; may be residual itself; or NULL: not written
+ *   y         device, [rows][width], y_dtype (DION_F32, DION_BF16 or DION_E4M3), written
+ *   scale     device fp32 [rows], written where y_dtype is DION_E4M3 (1 for a row of zeros), else NULL
+ *   rstd      device fp32 [rows], written, or NULL
+ *   eps       >= 0, finite.  p, seed, site as above, over rows x width elements
+ * Arithmetic: in fp32; y is formed from h before its rounding.  With DION_E4M3 in fp64, so that no rounding on the way moves
+ * a value across a border of its 8-bit numbers.  Elements that are not finite become NaN in 8 bits and do not count for scale.
+ */
+int dion_rms_norm(const void* x, const void* residual, const void* w, void* h, void* y, float* scale, float* rstd,
+                  int64_t rows, int64_t width, double eps, double p, const int64_t* seed, int64_t site, int x_dtype,
+                  int s_dtype, int w_dtype, int y_dtype, void* stream);
+
+/*
+ * Gradients of the norm, its dropout and its addition.
+ *   dY         device, [rows][width], y_dtype (DION_F32 or DION_BF16)
+ *   h, rstd    from dion_rms_norm (h is x itself where there was neither residual nor dropout); h has s_dtype
+ *   dsum       device, [rows][width], s_dtype: the gradient that reaches h by other ways (the stream behind it), or NULL
+ *   dh         device, [rows][width], s_dtype, written: h's gradient, which is the residual's; may be dsum itself
+ *   dx         device, [rows][width], y_dtype, written: the gradient of x; or NULL
+ *   dw         device, [width], dw_dtype, written, or added to with accumulate 1; or NULL
+ *   workspace  device, >= dion_rms_norm_grad_workspace_size(rows, width) bytes, 256-byte aligned; may be NULL where that is 0
+ */
+size_t dion_rms_norm_grad_workspace_size(int64_t rows, int64_t width);
+int dion_rms_norm_grad(const void* dY, const void* h, const void* w, const float* rstd, const void* dsum, void* dh, void* dx,
+                       void* dw, int64_t rows, int64_t width, double p, const int64_t* seed, int64_t site, int y_dtype,
+                       int s_dtype, int w_dtype, int dw_dtype, int accumulate, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Gated feed-forward block.
+ *   X         device, [rows][width], x_dtype: dtype, or DION_E4M3 with x_scale, fp32 [rows] (else NULL)
+ *   Wg, Wu    device, [hidden][width], dtype (DION_F32 or DION_BF16)
+ *   Wd        device, [width][hidden], dtype
+ *   gate, up  device, [rows][hidden], dtype: a and b, written for the gradient; both or neither NULL
+ *   Y         device, [rows][width], dtype, written
+ *   act       dion_activation
+ * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores; u is rounded to bf16 for the second
+ * product.  fp32 operands go as three bf16 parts (an exact split, six part products, terms below 2^-24 dropped).  8-bit
+ * rows go as bf16, which holds x scale exactly where scale is a power of two, as dion_rms_norm leaves it, and is rounded
+ * else.  Operands are taken to be finite; others make what they reach NaN or infinite.
+ * Workspace size: for_grad 0 for dion_gated_ffn, 1 for dion_gated_ffn_grad given gate and up, 2 without them; 0 for invalid
+ * sizes.
+ */
+size_t dion_gated_ffn_workspace_size(int64_t rows, int64_t width, int64_t hidden, int dtype, int x_dtype, int for_grad);
+int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const void* Wu, const void* Wd, void* gate, void* up,
+                   void* Y, int64_t rows, int64_t width, int64_t hidden, int act, int x_dtype, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients.
+ *   dY             device, [rows][width], dtype
+ *   gate, up       from dion_gated_ffn on the same X, Wg, Wu, read only; or both NULL: formed again
+ *   dX             device, [rows][width], dtype, written (of the values that X stands for), or NULL
+ *   dWg, dWu, dWd  device, shaped as the weights, dw_dtype, written, or added to with accumulate 1; dWg and dWu both or
+ *                  neither NULL, dWd or NULL.  One output at least is given
+ * Arithmetic: as above; da, db and u are rounded to bf16 where dtype is bf16, and so are gate and up as they are kept.
+ */
+int dion_gated_ffn_grad(const void* X, const float* x_scale, const void* Wg, const void* Wu, const void* Wd, const void* dY,
+                        const void* gate, const void* up, void* dX, void* dWg, void* dWu, void* dWd, int64_t rows,
+                        int64_t width, int64_t hidden, int act, int x_dtype, int dtype, int dw_dtype, int accumulate,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* DION_BLOCK_MI355X_H */

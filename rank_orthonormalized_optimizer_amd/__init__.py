@@ -14,6 +14,8 @@ element-wise AdamW or Lion, as the page describes.
 ``embedding_``, ``embedding_grad_``, ``linear_cross_entropy_`` and
 ``linear_cross_entropy_grad_`` are the operators at the two ends of the model over its
 vocabulary matrices; they leave those matrices' gradients where the steps above read them.
+``dropout_``, ``rms_norm_``, ``rms_norm_8bit_``, ``rms_norm_grad_``, ``gated_ffn_`` and ``gated_ffn_grad_`` are those of
+the residual blocks between them.
 """
 from __future__ import annotations
 
@@ -23,5 +25,7 @@ from ._lib import (BF16, EXPORTS, F32, FLAG_F64, FLAG_HOUSEHOLDER, FLAG_NONFINIT
                    step_batched_raw, strerror, version, workspace_size)
 from .api import (DionStack, GraphedStep, MixedDion, StickyF64Hint, adamw_step_, group_matrices,  # noqa: F401
                   lambda_max_, lion_step_, step_)
+from .block import (dropout_, gated_ffn_, gated_ffn_grad_, gated_ffn_workspace_for, rms_norm_,  # noqa: F401
+                    rms_norm_8bit_, rms_norm_grad_, rms_norm_grad_workspace_for)
 from .vocab import (embedding_, embedding_grad_, embedding_grad_workspace_for,  # noqa: F401
                     linear_cross_entropy_, linear_cross_entropy_grad_, linear_cross_entropy_workspace_for)

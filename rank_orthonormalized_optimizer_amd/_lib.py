@@ -50,6 +50,13 @@ VOCAB_MAX_TOKENS = 1 << 20
 VOCAB_EXPORTS = ("dion_embedding", "dion_embedding_grad_workspace_size", "dion_embedding_grad",
                  "dion_linear_xent_workspace_size", "dion_linear_xent", "dion_linear_xent_grad")
 
+# include/dion_block.h
+E4M3 = 2
+SILU, GELU = 0, 1
+BLOCK_MAX_ROWS = 1 << 20
+BLOCK_EXPORTS = ("dion_dropout", "dion_rms_norm", "dion_rms_norm_grad_workspace_size", "dion_rms_norm_grad",
+                 "dion_gated_ffn_workspace_size", "dion_gated_ffn", "dion_gated_ffn_grad")
+
 
 class StepOutputs(ctypes.Structure):
     """dion_step_outputs: optional phase events and the per-matrix momentum-change output."""
@@ -112,6 +119,21 @@ def load() -> ctypes.CDLL:
     lib.dion_linear_xent_grad.restype = ctypes.c_int
     lib.dion_linear_xent_grad.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, i32, i32, i32, i32, vp, sz,
                                           vp]
+    f64 = ctypes.c_double
+    lib.dion_dropout.restype = ctypes.c_int
+    lib.dion_dropout.argtypes = [vp, vp, vp, i64, f64, vp, i64, i32, i32, vp]
+    lib.dion_rms_norm.restype = ctypes.c_int
+    lib.dion_rms_norm.argtypes = [vp] * 7 + [i64, i64, f64, f64, vp, i64, i32, i32, i32, i32, vp]
+    lib.dion_rms_norm_grad_workspace_size.restype = sz
+    lib.dion_rms_norm_grad_workspace_size.argtypes = [i64, i64]
+    lib.dion_rms_norm_grad.restype = ctypes.c_int
+    lib.dion_rms_norm_grad.argtypes = [vp] * 8 + [i64, i64, f64, vp, i64, i32, i32, i32, i32, i32, vp, sz, vp]
+    lib.dion_gated_ffn_workspace_size.restype = sz
+    lib.dion_gated_ffn_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
+    lib.dion_gated_ffn.restype = ctypes.c_int
+    lib.dion_gated_ffn.argtypes = [vp] * 8 + [i64, i64, i64, i32, i32, i32, vp, sz, vp]
+    lib.dion_gated_ffn_grad.restype = ctypes.c_int
+    lib.dion_gated_ffn_grad.argtypes = [vp] * 12 + [i64, i64, i64, i32, i32, i32, i32, i32, vp, sz, vp]
     lib.dion_strerror.restype = ctypes.c_char_p
     lib.dion_strerror.argtypes = [ctypes.c_int]
     lib.dion_version.restype = ctypes.c_int

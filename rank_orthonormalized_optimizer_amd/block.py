@@ -1,0 +1,292 @@
+"""torch-facing wrappers of include/dion_block.h: dropout, the root-mean-square norm with the residual's
+addition, the gated feed-forward block, and their gradients (marshalling only, no arithmetic).
+
+Tensors are contiguous and on one GPU; everything is enqueued on ``stream`` (default: torch's
+current stream of that GPU) with no host sync.  Scratch and outputs that are not given are
+allocated by torch on that stream.
+
+No call records a graph for autograd: gradients are calls of their own.  Where autograd would expect
+one, the forward calls refuse tensors that require a gradient: call them under ``torch.no_grad()`` or
+on detached tensors.
+
+Dropout's mask is never stored: it is a function of ``seed`` (an int64 tensor of one element on the
+GPU, read when the kernel runs), ``site`` (a whole number that keeps the masks of different layers
+apart) and an element's number, so that the gradient forms it again from the same three.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from .vocab import _DT, _given_scratch, _need, _On, _scratch
+
+E4M3 = torch.float8_e4m3fn
+_ACT = {"silu": _lib.SILU, "gelu": _lib.GELU}
+
+
+def _no_graph(call: str, gradient: str, **tensors) -> None:
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{call} records no graph, but {name} requires a gradient: call it under torch.no_grad() "
+                                 f"or detach {name}, and {gradient} for the gradient")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _seed(seed, p: float, device):
+    if seed is None:
+        if p != 0:
+            raise ValueError("dropout needs a seed: an int64 GPU tensor of one element")
+        return None
+    _need(seed, "seed", (torch.int64,), device)
+    if seed.numel() != 1:
+        raise ValueError(f"seed has shape {tuple(seed.shape)}, expected one element")
+    return seed.data_ptr()
+
+
+def _rows(x, name: str):
+    """(rows, width) of a tensor [..., width]."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name} must have a width of at least 1, got shape {tuple(x.shape)}")
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def dropout_(x: torch.Tensor, p: float, seed: torch.Tensor | None = None, site: int = 0, *,
+             residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``out = residual + keep * x / (1 - p)`` with a mask that is never stored (dion_dropout).
+
+    x: float32 or bfloat16 of any shape; residual and out: x's shape, float32 or bfloat16 (default: the
+    residual's type, else x's); out may be residual.  The gradient of x is the same call, without residual,
+    on the output's gradient.
+    """
+    _no_graph("dropout_", "dropout_ of the output's gradient", x=x, residual=residual, out=out)
+    _need(x, "x", _DT)
+    device = x.device
+    with _On(device, stream) as handle:
+        if residual is not None:
+            _need(residual, "residual", _DT, device, x.shape)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype if residual is None else residual.dtype, device=device)
+        else:
+            _need(out, "out", _DT if residual is None else (residual.dtype,), device, x.shape)
+        st = _lib.load().dion_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), x.numel(), float(p),
+                                      _seed(seed, p, device), int(site), _DT[x.dtype], _DT[out.dtype], handle)
+    if st != _lib.OK:
+        raise _lib.DionError(st, "dion_dropout")
+    return out
+
+
+def _norm(call, x, w, eps, residual, p, seed, site, h, y, scale, rstd, eight, stream):
+    _no_graph(call, "rms_norm_grad_", x=x, w=w, residual=residual)
+    _need(x, "x", _DT)
+    device = x.device
+    rows, width = _rows(x, "x")
+    _need(w, "w", _DT, device, (width,))
+    with _On(device, stream) as handle:
+        if residual is not None:
+            _need(residual, "residual", _DT, device, x.shape)
+        s_dtype = x.dtype if residual is None else residual.dtype
+        if h is not None:
+            _need(h, "h", _DT if residual is None else (s_dtype,), device, x.shape)
+            s_dtype = h.dtype
+        elif residual is not None or p != 0:
+            h = torch.empty(x.shape, dtype=s_dtype, device=device)
+        if y is None:
+            y = torch.empty(x.shape, dtype=E4M3 if eight else x.dtype, device=device)
+        else:
+            _need(y, "out", (E4M3,) if eight else _DT, device, x.shape)
+        per_row = x.shape[:-1]
+        if eight and scale is None:
+            scale = torch.empty(per_row, dtype=torch.float32, device=device)
+        elif eight:
+            _need(scale, "scale", (torch.float32,), device, per_row)
+        if rstd is None:
+            rstd = torch.empty(per_row, dtype=torch.float32, device=device)
+        else:
+            _need(rstd, "rstd", (torch.float32,), device, per_row)
+        st = _lib.load().dion_rms_norm(x.data_ptr(), _ptr(residual), w.data_ptr(), _ptr(h), y.data_ptr(), _ptr(scale),
+                                       rstd.data_ptr(), rows, width, float(eps), float(p), _seed(seed, p, device), int(site),
+                                       _DT[x.dtype], _DT[s_dtype], _DT[w.dtype], _lib.E4M3 if eight else _DT[y.dtype], handle)
+    if st != _lib.OK:
+        raise _lib.DionError(st, "dion_rms_norm")
+    return y, scale, x if h is None else h, rstd
+
+
+def rms_norm_(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, *, residual: torch.Tensor | None = None, p: float = 0.0,
+              seed: torch.Tensor | None = None, site: int = 0, h: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, rstd: torch.Tensor | None = None, stream=None):
+    """``h = residual + dropout(x)`` and its root-mean-square norm ``y = h * rstd * w`` (dion_rms_norm).
+
+    x: [..., width], w: [width], residual: x's shape, each float32 or bfloat16.  Returns (or fills) ``(y, h,
+    rstd)``: y of x's shape and type (or out's), h of the residual's type (x itself where there is neither residual nor
+    dropout and no ``h`` is given; ``h`` may be ``residual``), rstd float32 of x's shape without the width.
+    """
+    y, _, h, rstd = _norm("rms_norm_", x, w, eps, residual, p, seed, site, h, out, None, rstd, False, stream)
+    return y, h, rstd
+
+
+def rms_norm_8bit_(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, *, residual: torch.Tensor | None = None,
+                   p: float = 0.0, seed: torch.Tensor | None = None, site: int = 0, h: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, scale: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+                   stream=None):
+    """rms_norm_ with y in 8 bits: returns (or fills) ``(q, scale, h, rstd)``, y standing as ``q * scale``.
+
+    q: float8_e4m3fn; scale: float32 per row, the least power of two with max |y| <= 448 scale.  gated_ffn_ and
+    gated_ffn_grad_ take the two; the gradient of the rounding is taken to be 1 (rms_norm_grad_ with y's gradient).
+    """
+    return _norm("rms_norm_8bit_", x, w, eps, residual, p, seed, site, h, out, scale, rstd, True, stream)
+
+
+def rms_norm_grad_workspace_for(rows: int, width: int, device) -> torch.Tensor:
+    """Scratch for one rms_norm_grad_ call of these sizes."""
+    return _scratch(int(_lib.load().dion_rms_norm_grad_workspace_size(rows, width)), device)
+
+
+def rms_norm_grad_(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, dw: torch.Tensor | None = None, *,
+                   dsum: torch.Tensor | None = None, p: float = 0.0, seed: torch.Tensor | None = None, site: int = 0,
+                   dh: torch.Tensor | None = None, dx: torch.Tensor | None = None, accumulate: bool = False,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of rms_norm_ and rms_norm_8bit_ (dion_rms_norm_grad); returns ``(dh, dx)`` and fills dw.
+
+    dY: y's gradient, [..., width]; h, rstd: the forward call's; dsum: the gradient that reaches h by other ways, of
+    h's type; dh: h's gradient, which is the residual's (may be dsum); dx: x's gradient, of dY's type, with the same p, seed and site.
+    Without dropout dx is dh, unless a ``dx`` is given (where x has another type than the stream).  dw: [width] float32
+    or bfloat16, written, or added to with ``accumulate``.
+    """
+    _need(dY, "dY", _DT)
+    device = dY.device
+    rows, width = _rows(dY, "dY")
+    _need(h, "h", _DT, device, dY.shape)
+    _need(w, "w", _DT, device, (width,))
+    _need(rstd, "rstd", (torch.float32,), device, dY.shape[:-1])
+    if dsum is not None:
+        _need(dsum, "dsum", (h.dtype,), device, h.shape)
+    if dw is not None:
+        _need(dw, "dw", _DT, device, (width,))
+    with _On(device, stream) as handle:
+        if dh is None:
+            dh = torch.empty(h.shape, dtype=h.dtype, device=device)
+        else:
+            _need(dh, "dh", (h.dtype,), device, h.shape)
+        if dx is not None:
+            _need(dx, "dx", (dY.dtype,), device, dY.shape)
+        elif p != 0:
+            dx = torch.empty(dY.shape, dtype=dY.dtype, device=device)
+        if dw is None:
+            ws = None
+        elif workspace is None:
+            ws = rms_norm_grad_workspace_for(rows, width, device)
+        else:
+            ws = _given_scratch(workspace, device)
+        st = _lib.load().dion_rms_norm_grad(dY.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _ptr(dsum),
+                                            dh.data_ptr(), _ptr(dx), _ptr(dw), rows, width, float(p), _seed(seed, p, device),
+                                            int(site), _DT[dY.dtype], _DT[h.dtype], _DT[w.dtype],
+                                            _DT[w.dtype if dw is None else dw.dtype], int(bool(accumulate)), _ptr(ws),
+                                            0 if ws is None else ws.numel(), handle)
+    if st != _lib.OK:
+        raise _lib.DionError(st, "dion_rms_norm_grad")
+    return dh, dh if dx is None else dx
+
+
+def gated_ffn_workspace_for(rows: int, width: int, hidden: int, device, dtype=torch.bfloat16, *, x_dtype=None,
+                            for_grad: bool = False, saved: bool = True) -> torch.Tensor:
+    """Scratch for one gated_ffn_ call, or with ``for_grad`` one gated_ffn_grad_ call (``saved``: given gate and up)."""
+    x = _lib.E4M3 if x_dtype == E4M3 else _DT[dtype]
+    return _scratch(int(_lib.load().dion_gated_ffn_workspace_size(rows, width, hidden, _DT[dtype], x,
+                                                                  (1 if saved else 2) if for_grad else 0)), device)
+
+
+def _block(X, Wg, Wu, Wd, act, scale):
+    _need(Wg, "Wg", _DT)
+    if Wg.dim() != 2:
+        raise ValueError(f"Wg must be a matrix [hidden, width], got shape {tuple(Wg.shape)}")
+    hidden, width = Wg.shape
+    device, dtype = Wg.device, Wg.dtype
+    _need(Wu, "Wu", (dtype,), device, Wg.shape)
+    _need(Wd, "Wd", (dtype,), device, (width, hidden))
+    _need(X, "X", (dtype,) if scale is None else (E4M3,), device)
+    if X.dim() < 1 or X.shape[-1] != width:
+        raise ValueError(f"X has shape {tuple(X.shape)}, expected [..., {width}]")
+    if scale is not None:
+        _need(scale, "scale", (torch.float32,), device, X.shape[:-1])
+    if act not in _ACT:
+        raise ValueError(f"act is {act!r}, expected one of {tuple(_ACT)}")
+    return X.numel() // width, width, hidden, _DT[dtype], _DT[dtype] if scale is None else _lib.E4M3
+
+
+def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor, *, act: str = "silu",
+               scale: torch.Tensor | None = None, gate: torch.Tensor | None = None, up: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gated feed-forward block ``(act(X Wg^T) * (X Wu^T)) Wd^T`` (dion_gated_ffn).
+
+    X: [..., width]; Wg, Wu: [hidden, width]; Wd: [width, hidden]; all float32 or all bfloat16.  With ``scale`` (float32 per
+    row) X is float8_e4m3fn and stands for ``X * scale``, as rms_norm_8bit_ leaves it.  act: "silu" or "gelu" (its tanh form).
+    gate, up: [..., hidden] of the weights' type, both or neither: filled with the two projections for gated_ffn_grad_.
+    Returns (or fills) out, [..., width] of the weights' type.
+    """
+    _no_graph("gated_ffn_", "gated_ffn_grad_", X=X, Wg=Wg, Wu=Wu, Wd=Wd, out=out)
+    rows, width, hidden, dt, xt = _block(X, Wg, Wu, Wd, act, scale)
+    device, dtype, inner = Wg.device, Wg.dtype, X.shape[:-1] + (hidden,)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are kept together: give both or neither")
+    if gate is not None:
+        _need(gate, "gate", (dtype,), device, inner)
+        _need(up, "up", (dtype,), device, inner)
+    with _On(device, stream) as handle:
+        if out is None:
+            out = torch.empty(X.shape, dtype=dtype, device=device)
+        else:
+            _need(out, "out", (dtype,), device, X.shape)
+        ws = gated_ffn_workspace_for(rows, width, hidden, device, dtype, x_dtype=X.dtype) if workspace is None \
+            else _given_scratch(workspace, device)
+        st = _lib.load().dion_gated_ffn(X.data_ptr(), _ptr(scale), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), _ptr(gate),
+                                        _ptr(up), out.data_ptr(), rows, width, hidden, _ACT[act], xt, dt, ws.data_ptr(),
+                                        ws.numel(), handle)
+    if st != _lib.OK:
+        raise _lib.DionError(st, "dion_gated_ffn")
+    return out
+
+
+def gated_ffn_grad_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor, dY: torch.Tensor,
+                    gate: torch.Tensor | None = None, up: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                    dWg: torch.Tensor | None = None, dWu: torch.Tensor | None = None, dWd: torch.Tensor | None = None, *,
+                    act: str = "silu", scale: torch.Tensor | None = None, accumulate: bool = False,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of gated_ffn_ (dion_gated_ffn_grad), into those of dX, dWg, dWu and dWd that are given; returns the four.
+
+    dY: the output's gradient, [..., width] of the weights' type; gate, up: gated_ffn_'s for the same X, Wg, Wu, or both
+    None, which forms them again.  dX: [..., width] of the weights' type; dWg and dWu (both or neither) and dWd: shaped as
+    the weights, float32 or bfloat16, written, or added to with ``accumulate``.  What is not asked for costs no product.
+    """
+    rows, width, hidden, dt, xt = _block(X, Wg, Wu, Wd, act, scale)
+    device, dtype, inner = Wg.device, Wg.dtype, X.shape[:-1] + (hidden,)
+    _need(dY, "dY", (dtype,), device, X.shape)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are kept together: give both or neither")
+    if gate is not None:
+        _need(gate, "gate", (dtype,), device, inner)
+        _need(up, "up", (dtype,), device, inner)
+    if dX is not None:
+        _need(dX, "dX", (dtype,), device, X.shape)
+    if (dWg is None) != (dWu is None):
+        raise ValueError("dWg and dWu come from one product: give both or neither")
+    dw = dtype
+    for name, t, like in (("dWg", dWg, Wg), ("dWu", dWu, Wu), ("dWd", dWd, Wd)):
+        if t is not None:
+            _need(t, name, _DT, device, like.shape)
+            dw = t.dtype
+    if any(t is not None and t.dtype != dw for t in (dWg, dWu, dWd)):
+        raise TypeError("dWg, dWu and dWd must have one dtype")
+    with _On(device, stream) as handle:
+        ws = gated_ffn_workspace_for(rows, width, hidden, device, dtype, x_dtype=X.dtype, for_grad=True, saved=gate is not None) \
+            if workspace is None else _given_scratch(workspace, device)
+        st = _lib.load().dion_gated_ffn_grad(X.data_ptr(), _ptr(scale), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
+                                             dY.data_ptr(), _ptr(gate), _ptr(up), _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(dWd),
+                                             rows, width, hidden, _ACT[act], xt, dt, _DT[dw], int(bool(accumulate)),
+                                             ws.data_ptr(), ws.numel(), handle)
+    if st != _lib.OK:
+        raise _lib.DionError(st, "dion_gated_ffn_grad")
+    return dX, dWg, dWu, dWd

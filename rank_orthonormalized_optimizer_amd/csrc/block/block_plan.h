@@ -1,0 +1,183 @@
+// Host-side sizes and launch entry points of the residual blocks' operators (arguments validated in
+// block_api.cpp).  Every run_* returns a hipError_t value.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include "vocab/vocab_plan.h"
+
+namespace dion {
+
+constexpr int64_t kHiddenMax = (int64_t)1 << 17;
+
+// The mask of dropout: an element is kept where its word is at least `threshold`, and multiplied by `scale`.
+struct Mask {
+    const int64_t* seed;
+    int64_t site;
+    uint32_t threshold;
+    double scale;
+    int on;
+};
+
+struct DropoutArgs {
+    const void* x;
+    const void* residual;
+    void* out;
+    int64_t n;
+    Mask mask;
+    int x_bf16, out_bf16;
+};
+int run_dropout(const DropoutArgs& a, void* stream);
+
+struct NormArgs {
+    const void* x;
+    const void* residual;
+    const void* w;
+    void* h;
+    void* y;
+    float* scale;
+    float* rstd;
+    int64_t rows;
+    int d;
+    double eps;
+    Mask mask;
+    int x_bf16, s_bf16, w_bf16, y_bf16;   // (scale is given: y in 8 bits)
+};
+int run_rms_norm(const NormArgs& a, void* stream);
+
+struct NormGradArgs {
+    const void* dy;
+    const void* h;
+    const void* w;
+    const float* rstd;
+    const void* dsum;
+    void* dh;
+    void* dx;
+    void* dw;
+    float* part;        // [blocks][d] sums of dw, where there are several blocks
+    int64_t rows;
+    int d;
+    Mask mask;
+    int y_bf16, s_bf16, w_bf16, dw_bf16, accumulate;
+};
+
+// A row is a team's: the threads that hold it in registers, `vecs` vectors of eight elements each.  The narrowest team
+// whose threads hold few elements: a wave needs no barrier for its sums.
+struct NormPlan {
+    int team, vecs;
+    int64_t per_block;   // rows of a workgroup at a time
+    int64_t blocks;      // gradient: workgroups, which stride over the rows and leave one partial dw each
+    size_t total;        // bytes of the partial sums
+};
+
+inline NormPlan make_norm_plan(int64_t rows, int64_t width) {
+    NormPlan p{};
+    const int64_t v = ceil_div64(width, 8);   // vectors of a row
+    p.team = v <= 128 ? 64 : v <= 1024 ? 256 : 1024;
+    p.vecs = 1;
+    while ((int64_t)p.team * p.vecs < v) p.vecs *= 2;
+    p.per_block = p.team == 64 ? 4 : 1;
+    const int64_t most = p.team == 1024 ? kCUs : kCUs * 4, all = ceil_div64(rows, p.per_block);
+    p.blocks = all < most ? all : most;
+    p.total = p.blocks > 1 ? align256((size_t)(p.blocks * width * 4)) : 0;
+    return p;
+}
+int run_rms_norm_grad(const NormGradArgs& a, const NormPlan& p, void* stream);
+
+// Layout of a feed-forward call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32).  The packed planes have rows of
+// a multiple of 64 elements, zeros behind the matrix; Wg's and Wu's are one matrix of 2 fk rows, da and db one of 2 fk columns.
+struct Product {
+    int tile;            // TILE_*
+    int64_t split;       // slices of the reduction
+    int64_t k, k_per;    // its length, and a slice's, multiples of 64
+};
+struct FfnPlan {
+    int64_t t, d, f, dk, fk;
+    int parts;
+    bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
+    Product gu, y, du, dx, dgu, dd;
+    size_t x, w, wd, u, dab, dy, gate, up, acc;
+    size_t total;
+};
+
+inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms) {
+    Product p{};
+    p.tile = pick_tile(m, n, k, terms);
+    const int64_t slabs = ceil_div64(k, 64), per = ceil_div64(slabs, pick_split(m, n, k, terms, p.tile));
+    p.k = slabs * 64;
+    p.k_per = per * 64;
+    p.split = ceil_div64(slabs, per);   // none without any k
+    return p;
+}
+
+// for_grad: the gradient; saved: gate and up are given to it
+inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16, int x8, int for_grad, int saved, FfnPlan* p) {
+    FfnPlan q{};
+    q.t = rows; q.d = width; q.f = hidden;
+    q.dk = ceil_div64(width, 64) * 64;
+    q.fk = ceil_div64(hidden, 64) * 64;
+    q.parts = bf16 ? 1 : 3;
+    q.xpack = !bf16 || x8 || width != q.dk;
+    q.wpack = !bf16 || width != q.dk;
+    q.dpack = !bf16 || hidden != q.fk;
+    q.ypack = !bf16 || width != q.dk;
+    const int64_t n = rows < 1 ? 1 : rows, terms = bf16 ? 1 : 6;
+    size_t off = 0, acc = 0;
+    auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
+    auto partial = [&](const Product& r, int64_t elems) {
+        const size_t b = r.split > 1 ? (size_t)(r.split * elems * 4) : 0;
+        if (b > acc) acc = b;
+    };
+    if (q.xpack) q.x = take(q.parts * n * q.dk * 2);
+    if (q.wpack) q.w = take(q.parts * 2 * q.fk * q.dk * 2);
+    if (q.dpack) q.wd = take(q.parts * width * q.fk * 2);
+    q.u = take(q.parts * n * q.fk * 2);
+    q.gu = pick_product(2 * q.fk, n, width, terms);
+    partial(q.gu, n * 2 * q.fk);
+    if (!for_grad) {
+        q.y = pick_product(width, n, hidden, terms);
+        partial(q.y, n * q.dk);
+    } else {
+        if (!saved) {
+            q.gate = take(n * hidden * (bf16 ? 2 : 4));
+            q.up = take(n * hidden * (bf16 ? 2 : 4));
+        }
+        if (q.ypack) q.dy = take(q.parts * n * q.dk * 2);
+        q.dab = take(q.parts * n * 2 * q.fk * 2);
+        q.du = pick_product(q.fk, n, width, terms);
+        partial(q.du, n * q.fk);
+        q.dx = q.wpack ? pick_product(width, n, 2 * q.fk, terms) : pick_product(width, n, hidden, 2);   // (in place: two terms of fk)
+        partial(q.dx, n * q.dk);
+        q.dgu = pick_product(width, 2 * q.fk, n, terms);
+        partial(q.dgu, 2 * q.fk * q.dk);
+        q.dd = pick_product(q.fk, width, n, terms);
+        partial(q.dd, width * q.fk);
+    }
+    q.acc = take((int64_t)acc);
+    q.total = off;
+    *p = q;
+    return off < ((size_t)1 << 46);
+}
+
+struct FfnArgs {
+    const void* X;
+    const float* x_scale;   // X in 8 bits, or null
+    const void* Wg;
+    const void* Wu;
+    const void* Wd;
+    void* Y;                // forward
+    void* gate;             // forward: written, or null.  Gradient: read, or null: formed again
+    void* up;
+    const void* dY;         // gradient
+    void* dX;
+    void* dWg;
+    void* dWu;
+    void* dWd;
+    int act, bf16, dw_bf16, accumulate;
+};
+int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
+int run_ffn_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
+// nothing but zeros, in n 16-bit words
+int run_zeros(void* out, int64_t n, void* stream);
+
+}  // namespace dion

@@ -26,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace dion {
 namespace mm {
 
@@ -45,6 +47,7 @@ struct Operand {
     int64_t plane;   // elements between part planes
     int64_t ld;      // elements between rows, a multiple of 8
     int rows;        // of x for a k-contiguous operand (reads are clamped to them), of k for a transposed one (zeros behind them)
+    int64_t pair = 0;   // PairTile: elements from the first matrix to the second
 };
 
 // Plane pairs of a product: entry s in bits 4s..: A's plane in two bits, B's in the next two.
@@ -130,6 +133,30 @@ struct Tile {
     }
 };
 
+// A tile whose rows come from two k-contiguous matrices of the same shape, o.pair elements apart, 16 of each in turn: X / 2
+// rows of either, from row x0 / 2.  A wave then has the same rows of both products in the same lanes.
+template <int X, int WAVES>
+struct PairTile : Tile<X, false, WAVES> {
+    using Base = Tile<X, false, WAVES>;
+    static_assert(Base::kLoads % 2 == 0, "a wave load of eight rows belongs to one matrix, and so do two in a row");
+    // of the i-th load of a wave
+    static __device__ __forceinline__ int matrix(int i, int wave) {
+        return Base::kLoads % 4 == 0 ? (i >> 1) & 1 : ((wave * Base::kLoads + i) >> 1) & 1;
+    }
+    __device__ __forceinline__ void init(const Operand& o, int x0, int wave, int lane) {
+#pragma unroll
+        for (int i = 0; i < Base::kLoads; ++i) {
+            const int q = wave * Base::kLoads + i, x = q * 8 + lane / 8, c = (lane % 8) ^ ((x >> 1) & 7);
+            const int r = x / 32 * 16 + x % 16, row = x0 / 2 + r < o.rows ? r : o.rows - 1 - x0 / 2;
+            this->off[i] = (uint32_t)(row * o.ld + c * 8) * 2u;
+        }
+    }
+    static __device__ __forceinline__ u32x4 slab(const Operand& o, int x0, int part, int k0, int matrix) {
+        const uint64_t at = (uint64_t)(o.p + part * o.plane + matrix * o.pair + (int64_t)(x0 / 2) * o.ld + k0);
+        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
+    }
+};
+
 // All but the newest N loads of this wave landed, its LDS reads are done, and every wave is here.
 template <int N>
 __device__ __forceinline__ void wait_slab() {
@@ -138,9 +165,10 @@ __device__ __forceinline__ void wait_slab() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_, bool TA_, bool TB_, bool F16_ = false>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, bool TA_, bool TB_, bool F16_ = false, bool PAIR_ = false>
 struct Config {
     static constexpr bool F16 = F16_, FEW = false;   // fp16 planes
+    static constexpr bool PAIR = PAIR_;              // A is a PairTile
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
     static constexpr bool TA = TA_, TB = TB_;
     static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
@@ -162,7 +190,7 @@ struct Config {
 // wave has read the whole slab, its stage is loaded again, and the next slab is there.
 template <class C>
 struct Product {
-    using TileA = Tile<C::BM, C::TA, C::WAVES>;
+    using TileA = typename std::conditional<C::PAIR, PairTile<C::BM, C::WAVES>, Tile<C::BM, C::TA, C::WAVES>>::type;
     using TileB = Tile<C::BN, C::TB, C::WAVES>;
     static constexpr int kPer = TileA::kLoads + TileB::kLoads;
 
@@ -231,12 +259,17 @@ private:
         int k = 0, slot = 0, left = 0;
         Segments all{0, 0};
         uint32_t list = 0;
-        u32x4 ra, rb;
+        u32x4 ra, rb, ra2;
         uint32_t to;
         Loads() = default;
         __device__ __forceinline__ Loads(int k0, Segments seg) : k(k0), left((int)seg.n), all(seg), list(seg.list) {}
         __device__ __forceinline__ void begin(const Operand& a, const Operand& b, int m0, int n0, uint16_t* lds) {
-            ra = TileA::slab(a, m0, list & 3, k);
+            if constexpr (C::PAIR) {
+                ra = TileA::slab(a, m0, list & 3, k, 0);
+                ra2 = TileA::slab(a, m0, list & 3, k, 1);
+            } else {
+                ra = TileA::slab(a, m0, list & 3, k);
+            }
             rb = TileB::slab(b, n0, (list >> 2) & 3, k);
             to = (uint32_t)(uintptr_t)(lds_void*)lds + slot * (C::kStage * 2);
             list >>= 4;
@@ -244,6 +277,12 @@ private:
             if (++slot == C::STAGES) slot = 0;
         }
         __device__ __forceinline__ void one(const TileA& ta, const TileB& tb, int i, int wave) const {
+            if constexpr (C::PAIR) {
+                if (i < TileA::kLoads) {
+                    ta.load(TileA::matrix(i, wave) ? ra2 : ra, i, to, wave);
+                    return;
+                }
+            }
             if (i < TileA::kLoads) ta.load(ra, i, to, wave);
             else tb.load(rb, i - TileA::kLoads, to + C::BM * kBK * 2, wave);
         }

@@ -157,10 +157,10 @@ struct Walk {
     }
 };
 
-// Stores a lane's 4-row pieces of two neighbouring blocks of 16 rows: the lane quarters trade their four rows of one
-// against the other's (v_permlane32_swap, v_permlane16_swap), so that a lane stores eight consecutive rows and four lanes
-// 64 bytes.  a, b: the four values of each block, packed in two words; to: the address for this lane's quarter.
-__device__ __forceinline__ void store_pair(uint16_t* to, const uint32_t (&a)[2], const uint32_t (&b)[2], bool in) {
+// A lane's 4-row pieces of two neighbouring blocks of 16 rows: the lane quarters trade their four rows of one
+// against the other's (v_permlane32_swap, v_permlane16_swap), so that a lane has eight consecutive rows and four lanes
+// 64 bytes.  a, b: the four values of each block, packed in two words.
+__device__ __forceinline__ u32x4 trade(const uint32_t (&a)[2], const uint32_t (&b)[2]) {
     u32x4 w;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -169,6 +169,12 @@ __device__ __forceinline__ void store_pair(uint16_t* to, const uint32_t (&a)[2],
         w[h] = z[0];
         w[2 + h] = z[1];
     }
+    return w;
+}
+
+// Stores such pieces; to: the address for this lane's quarter.
+__device__ __forceinline__ void store_pair(uint16_t* to, const uint32_t (&a)[2], const uint32_t (&b)[2], bool in) {
+    const u32x4 w = trade(a, b);
     if (in) *(u32x4*)to = w;
 }
 
