@@ -94,7 +94,10 @@ int dion_rms_norm_grad(const void* dY, const void* h, const void* w, const float
  *   X         device, [rows][width], x_dtype: dtype, or DION_E4M3 with x_scale, fp32 [rows] (else NULL)
  *   Wg, Wu    device, [hidden][width], dtype (DION_F32 or DION_BF16)
  *   Wd        device, [width][hidden], dtype
- *   gate, up  device, [rows][hidden], dtype: a and b, written for the gradient; both or neither NULL
+ *   gate, up  device, [rows][hidden], elements of dtype's size: a and b, written for the gradient; both or neither NULL.  In
+ *             fp32 for fp32.  For bf16 in 16 bits of their own, more exact than bf16 where it counts: bit 15 the sign; bit 14
+ *             set for magnitudes in [2^-8, 2^8), with 4 bits of exponent (from 2^-8) and 10 of fraction below it; else clear,
+ *             with the upper 14 bits of the magnitude's fp32 form (8 of exponent, 6 of fraction).  Rounded to nearest, ties away from zero
  *   Y         device, [rows][width], dtype, written
  *   act       dion_activation
  * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores; u is rounded to bf16 for the second
@@ -116,7 +119,7 @@ int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const vo
  *   dX             device, [rows][width], dtype, written (of the values that X stands for), or NULL
  *   dWg, dWu, dWd  device, shaped as the weights, dw_dtype, written, or added to with accumulate 1; dWg and dWu both or
  *                  neither NULL, dWd or NULL.  One output at least is given
- * Arithmetic: as above; da, db and u are rounded to bf16 where dtype is bf16, and so are gate and up as they are kept.
+ * Arithmetic: as above; da, db and u are rounded to bf16 where dtype is bf16, a and b to the form in which they are kept.
  */
 int dion_gated_ffn_grad(const void* X, const float* x_scale, const void* Wg, const void* Wu, const void* Wd, const void* dY,
                         const void* gate, const void* up, void* dX, void* dWg, void* dWu, void* dWd, int64_t rows,

@@ -224,7 +224,8 @@ def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Te
 
     X: [..., width]; Wg, Wu: [hidden, width]; Wd: [width, hidden]; all float32 or all bfloat16.  With ``scale`` (float32 per
     row) X is float8_e4m3fn and stands for ``X * scale``, as rms_norm_8bit_ leaves it.  act: "silu" or "gelu" (its tanh form).
-    gate, up: [..., hidden] of the weights' type, both or neither: filled with the two projections for gated_ffn_grad_.
+    gate, up: [..., hidden] of the weights' type, both or neither: filled with what gated_ffn_grad_ needs of the two
+    projections (for bfloat16 their bits are a 16-bit form of its own, described in dion_block.h, not bfloat16 numbers).
     Returns (or fills) out, [..., width] of the weights' type.
     """
     _no_graph("gated_ffn_", "gated_ffn_grad_", X=X, Wg=Wg, Wu=Wu, Wd=Wd, out=out)

@@ -86,28 +86,60 @@ int run_rms_norm_grad(const NormGradArgs& a, const NormPlan& p, void* stream);
 
 // Layout of a feed-forward call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32).  The packed planes have rows of
 // a multiple of 64 elements, zeros behind the matrix; Wg's and Wu's are one matrix of 2 fk rows, da and db one of 2 fk columns.
+// How a product's tiles go over the chip: `full` of them whole, the `rem` others cut into slices of the reduction.
+struct Cut {
+    int full, rem, slices;
+    int k, k_per;   // the reduction's length, and a slice's, multiples of 64
+};
 struct Product {
-    int tile;            // TILE_*
-    int64_t split;       // slices of the reduction
-    int64_t k, k_per;    // its length, and a slice's, multiples of 64
+    int tile;       // TILE_*
+    Cut cut;
+    size_t acc;     // bytes of the slices' sums
 };
 struct FfnPlan {
     int64_t t, d, f, dk, fk;
     int parts;
     bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
-    Product gu, y, du, dx, dgu, dd;
+    Product gu, y, du, dx, dgu, dd, dw;   // (dw: dgu and dd at once)
     size_t x, w, wd, u, dab, dy, gate, up, acc;
     size_t total;
 };
 
-inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms) {
-    Product p{};
-    p.tile = pick_tile(m, n, k, terms);
-    const int64_t slabs = ceil_div64(k, 64), per = ceil_div64(slabs, pick_split(m, n, k, terms, p.tile));
-    p.k = slabs * 64;
-    p.k_per = per * 64;
-    p.split = ceil_div64(slabs, per);   // none without any k
-    return p;
+// Times in microseconds of a tile's slab of 64 k where the chip is full of them, of its start and its epilogue; and the
+// workgroups that a CU holds.
+struct TileCost {
+    int tile;
+    double slab, ends;
+    int64_t slots;
+};
+constexpr TileCost kTileCosts[] = {{TILE_256, 1.6, 9.0, kCUs}, {TILE_128, 1.2, 6.0, 2 * kCUs}, {TILE_64, 0.5, 4.0, kCUs}};
+
+// The tile and the cut of least estimated time for one product of m x n, or two (whose tiles are counted together).
+// narrow: few rows go in tiles of 128 x 32.
+inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms, bool narrow, int64_t m2 = 0, int64_t n2 = 0) {
+    Product best{};
+    double least = 1e300;
+    const int64_t slabs = ceil_div64(k, 64);
+    for (const TileCost& c : kTileCosts) {
+        TileCost t = c;
+        if (narrow && n <= 32) t = TileCost{TILE_32, 0.5, 4.0, kCUs};
+        const int64_t all = tiles(m, n, t.tile) + (m2 ? tiles(m2, n2, t.tile) : 0);
+        const int64_t rounds = all / t.slots, rest = all % t.slots;
+        const double bytes = 4.0 * tile_m(t.tile) * tile_n(t.tile);
+        for (int64_t s = 1; s <= 16 && (s == 1 || (s <= slabs && rest * s <= t.slots)); ++s) {
+            const int64_t per = ceil_div64(slabs, s);
+            if (s > 1 && ceil_div64(slabs, per) != s) continue;   // a slice without any k
+            double time = (double)rounds * ((double)(slabs * terms) * t.slab + t.ends);
+            if (rest) time += (double)(per * terms) * t.slab + t.ends;
+            if (rest && s > 1) time += 6.0 + (double)(rest * s) * bytes * 0.5e-6;   // sums written and read at 4 TB/s, a launch
+            if (time >= least) continue;
+            least = time;
+            best.tile = t.tile;
+            best.cut = Cut{(int)(s > 1 ? all - rest : all), (int)(s > 1 ? rest : 0), (int)(s > 1 ? s : 0), (int)(slabs * 64), (int)(per * 64)};
+            best.acc = s > 1 ? (size_t)(rest * s) * (size_t)bytes : 0;
+        }
+    }
+    return best;
 }
 
 // for_grad: the gradient; saved: gate and up are given to it
@@ -124,19 +156,17 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
     const int64_t n = rows < 1 ? 1 : rows, terms = bf16 ? 1 : 6;
     size_t off = 0, acc = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
-    auto partial = [&](const Product& r, int64_t elems) {
-        const size_t b = r.split > 1 ? (size_t)(r.split * elems * 4) : 0;
-        if (b > acc) acc = b;
+    auto plan = [&](Product& r, int64_t m, int64_t n, int64_t k, int64_t t, bool narrow, int64_t m2 = 0, int64_t n2 = 0) {
+        r = pick_product(m, n, k, t, narrow, m2, n2);
+        if (r.acc > acc) acc = r.acc;
     };
     if (q.xpack) q.x = take(q.parts * n * q.dk * 2);
     if (q.wpack) q.w = take(q.parts * 2 * q.fk * q.dk * 2);
     if (q.dpack) q.wd = take(q.parts * width * q.fk * 2);
     q.u = take(q.parts * n * q.fk * 2);
-    q.gu = pick_product(2 * q.fk, n, width, terms);
-    partial(q.gu, n * 2 * q.fk);
+    plan(q.gu, 2 * q.fk, n, width, terms, true);
     if (!for_grad) {
-        q.y = pick_product(width, n, hidden, terms);
-        partial(q.y, n * q.dk);
+        plan(q.y, width, n, hidden, terms, true);
     } else {
         if (!saved) {
             q.gate = take(n * hidden * (bf16 ? 2 : 4));
@@ -144,14 +174,11 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
         }
         if (q.ypack) q.dy = take(q.parts * n * q.dk * 2);
         q.dab = take(q.parts * n * 2 * q.fk * 2);
-        q.du = pick_product(q.fk, n, width, terms);
-        partial(q.du, n * q.fk);
-        q.dx = q.wpack ? pick_product(width, n, 2 * q.fk, terms) : pick_product(width, n, hidden, 2);   // (in place: two terms of fk)
-        partial(q.dx, n * q.dk);
-        q.dgu = pick_product(width, 2 * q.fk, n, terms);
-        partial(q.dgu, 2 * q.fk * q.dk);
-        q.dd = pick_product(q.fk, width, n, terms);
-        partial(q.dd, width * q.fk);
+        plan(q.du, q.fk, n, width, terms, true);
+        plan(q.dx, width, n, q.wpack ? 2 * q.fk : hidden, q.wpack ? terms : 2, true);   // (in place: two terms of hidden)
+        plan(q.dgu, width, 2 * q.fk, n, terms, false);
+        plan(q.dd, hidden, width, n, terms, false);
+        plan(q.dw, width, 2 * q.fk, n, terms, false, hidden, width);
     }
     q.acc = take((int64_t)acc);
     q.total = off;

@@ -28,54 +28,76 @@ namespace {
 // ---------------------------------------------------------------------------
 // Activations
 // ---------------------------------------------------------------------------
-// 1 / (1 + exp(-z)), zero below -87.  EXACT: to a few ulp (the rounding of -z log2(e) is carried into the result); else that
-// rounding's |z| 2^-24 stays, which is far below bf16's.
+// 1 / (1 + exp(-z)), zero below -87.  EXACT: to a few ulp (the rounding of -z log2(e) is carried into the result, and the
+// reciprocal is refined once); else that rounding's |z| 2^-24 stays, which is far below bf16's.
 template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float z) {
     const float h = z * -1.44269504f;
     float e = __builtin_amdgcn_exp2f(h);
     if constexpr (!EXACT) return __builtin_amdgcn_rcpf(1.f + e);
     const float l = fmaf(z, -1.44269504f, -h) - z * 1.92596299e-8f;   // log2(e) - 1.44269504f
-    e = fmaf(e, l * 0.693147181f, e);
-    return z < -87.f ? 0.f : 1.f / (1.f + e);
+    e = 1.f + fmaf(e, l * 0.693147181f, e);
+    const float r = __builtin_amdgcn_rcpf(e);
+    return z < -87.f ? 0.f : fmaf(r, fmaf(-e, r, 1.f), r);
 }
 
-// act(a) and its derivative
+// act(a) and its derivative: a r and r + x r (1 - r) z' with r = 1 / (1 + exp(-z)) and
+//   silu  z = a;  gelu  z = 2 sqrt(2 / pi) (x + 0.044715 x^3), as (1 + tanh(z / 2)) / 2 = r, and z is past every border at |a| = 30
 template <bool EXACT>
 __device__ __forceinline__ float activate(int act, float a, float& slope) {
-    if (act == DION_SILU) {
-        const float r = sigmoid<EXACT>(a);
-        slope = r * fmaf(a, 1.f - r, 1.f);
-        return a * r;
+    float x = a, z = a, dz = 1.f;
+    if (act != DION_SILU) {
+        x = fminf(fmaxf(a, -30.f), 30.f);
+        const float q = x * x;
+        z = 1.59576912f * x * fmaf(0.044715f, q, 1.f);
+        dz = 1.59576912f * fmaf(0.134145f, q, 1.f);
     }
-    // a / (1 + exp(-2 s)) = a (1 + tanh s) / 2 with s = sqrt(2 / pi) (a + 0.044715 a^3), which is past every border at 30
-    const float x = fminf(fmaxf(a, -30.f), 30.f), q = x * x;
-    const float r = sigmoid<EXACT>(1.59576912f * x * fmaf(0.044715f, q, 1.f));
-    slope = fmaf(x * r * (1.f - r), 1.59576912f * fmaf(0.134145f, q, 1.f), r);
+    const float r = sigmoid<EXACT>(z);
+    slope = fmaf(x * r * (1.f - r), dz, r);
     return a * r;
 }
 
 // ---------------------------------------------------------------------------
 // Planes
 // ---------------------------------------------------------------------------
-// Rows [rows][d] of a matrix to bf16 planes [PARTS][plane] with `all` rows of kp elements, a wave per row, zeros behind the
-// matrix; kind: 0 fp32, 1 bf16, 2 e4m3 with a scale per row.
+// Rows [rows][d] of a matrix to bf16 planes [PARTS][plane] with `all` rows of kp elements, zeros behind the matrix; kind: 0
+// fp32, 1 bf16, 2 e4m3 with a scale per row.
+struct PackJob {
+    const void* in;
+    const float* scale;
+    uint16_t* out;
+    int64_t rows, all, plane;
+    int kind, d, kp;
+    unsigned first;   // its first workgroup
+};
+constexpr int kPackJobs = 5;   // X, Wg, Wu, Wd, dY
+struct PackJobs {
+    PackJob job[kPackJobs];
+    int n;
+    unsigned blocks;
+};
+
+// A wave per row, four of a matrix to a workgroup.
 template <int PARTS>
-__global__ __launch_bounds__(256) void planes_kernel(const void* in, const float* scale, int kind, int64_t rows, int64_t all, int d,
-                                                     int kp, uint16_t* out, int64_t plane) {
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (r >= all) return;
-    const float s = scale && r < rows ? scale[r] : 1.f;
-    if (r >= rows) d = 0;
+__global__ __launch_bounds__(256) void planes_kernel(PackJobs jobs) {
+    int at = 0;
+    while (at + 1 < jobs.n && blockIdx.x >= jobs.job[at + 1].first) ++at;
+    const PackJob& job = jobs.job[at];
+    const int64_t r = (int64_t)(blockIdx.x - job.first) * 4 + (threadIdx.x >> 6);
+    if (r >= job.all) return;
+    const int d = r < job.rows ? job.d : 0, kp = job.kp, kind = job.kind;
+    const void* in = job.in;
+    const float s = job.scale && r < job.rows ? job.scale[r] : 1.f;
+    const int64_t row = r * job.d;
 #pragma unroll 4
     for (int c = (threadIdx.x & 63) * 8; c < kp; c += 512) {
         float v[8];
         if (kind == 0) {
-            load8<false>(in, r * d, c, d, v);
+            load8<false>(in, row, c, d, v);
         } else if (kind == 1) {
-            load8<true>(in, r * d, c, d, v);
+            load8<true>(in, row, c, d, v);
         } else {
-            const uint8_t* p = (const uint8_t*)in + r * d + c;
+            const uint8_t* p = (const uint8_t*)in + row + c;
             uint32_t w[2] = {0, 0};
             if (c + 8 <= d) {
                 const u32x2_bytes q = *(const u32x2_bytes*)p;
@@ -95,340 +117,513 @@ __global__ __launch_bounds__(256) void planes_kernel(const void* in, const float
                 v[4 * h + 3] = hi[1] * s;
             }
         }
-        store8<PARTS>(out, plane, r * kp + c, v);
+        store8<PARTS>(job.out, job.plane, r * kp + c, v);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Products
 // ---------------------------------------------------------------------------
-// The tiles of this workgroup: tm x tn of them times the slices of the reduction; the next tile's loads start before
-// epilogue(m0, n0, slice, acc) of this one.
-template <class C, class E>
-__device__ __forceinline__ void walk_tiles(mm::Product<C>& mul, const mm::Operand& a, const mm::Operand& b, mm::Segments seg, int tm,
-                                           int tn, int split, int k, int k_per, E epilogue) {
-    Walk walk(tm, tn, split);
-    if (walk.done()) return;
-    int mt, nt, slice;
+// A workgroup's share of `total` items.  Workgroups go to the eight XCDs in turn; each XCD takes a contiguous range, which its
+// workgroups walk side by side.
+struct Turn {
+    int at, end, by;
+    __device__ __forceinline__ explicit Turn(int total) {
+        const int q = total / 8, r = total % 8, x = blockIdx.x % 8;
+        by = ((int)gridDim.x - x + 7) / 8;
+        const int start = x * q + (x < r ? x : r);
+        at = start + blockIdx.x / 8;
+        end = start + q + (x < r ? 1 : 0);
+    }
+    __device__ __forceinline__ bool done() const { return at >= end; }
+};
+
+// Tile `t` of a grid of tm rows, in bands of eight tile rows, so that an XCD's L2 serves the operands' re-reads.
+__device__ __forceinline__ void place(int t, int tm, int tn, int& mt, int& nt) {
+    constexpr int G = 8;
+    const int band = t / (G * tn), m0 = band * G, g = tm - m0 < G ? tm - m0 : G, in = t - band * G * tn;
+    mt = m0 + in % g;
+    nt = in / g;
+}
+
+// One product, or two whose reductions have the same length: the second one's tiles come behind the first one's.
+struct Operands {
+    mm::Operand a, b;
+    int64_t m, n;   // rows of a and b that the tiles cover
+};
+
+// A lane's place in a tile: column block j's row, the first block's column.
+struct Lane {
+    int xa, row, quarter;
+};
+
+// The tiles of P, whole ones first, then those whose reduction is cut into slices, which leave their sums in `acc` as the lanes
+// hold them.  The next tile's loads start before the epilogue of this one.
+template <class C, class P>
+__global__ __launch_bounds__(C::THREADS) void product_kernel(P p, Cut cut, mm::Segments seg, float* acc) {
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
+    mm::Product<C> mul(lds);
+    Turn turn(cut.full);
+    bool sliced = false;
+    auto seek = [&]() {
+        if (turn.done() && !sliced) {
+            sliced = true;
+            turn = Turn(cut.rem * cut.slices);
+        }
+        return !turn.done();
+    };
+    if (!seek()) return;
+    Operands o;
+    int which, unit;
     auto start = [&]() {
-        walk.tile(mt, nt, slice);
-        const int k0 = slice * k_per, k1 = k0 + k_per < k ? k0 + k_per : k;
-        mul.start(a, b, mt * C::BM, nt * C::BN, k0, k1, seg);
+        const int slice = sliced ? turn.at / cut.rem : 0, in = sliced ? turn.at - slice * cut.rem : 0;
+        int tile = sliced ? cut.full + in : turn.at, mt, nt;
+        unit = sliced ? in * cut.slices + slice : -1;
+        which = P::kProducts == 2 && tile >= p.template tiles<C>(0);
+        if (which) tile -= p.template tiles<C>(0);
+        o = p.operands(which);
+        place(tile, ((int)o.m + C::BM - 1) / C::BM, ((int)o.n + C::BN - 1) / C::BN, mt, nt);
+        const int k0 = slice * cut.k_per, k1 = sliced && k0 + cut.k_per < cut.k ? k0 + cut.k_per : cut.k;
+        mul.start(o.a, o.b, mt * C::BM, nt * C::BN, k0, k1, seg);
     };
     start();
     for (;;) {
-        const int m0 = mul.m0, n0 = mul.n0, sl = slice;
-        typename C::Acc acc = {};
-        mul.finish(a, b, acc);
-        walk.next();
-        const bool more = !walk.done();
+        const int m0 = mul.m0, n0 = mul.n0, was = which, u = unit;
+        typename C::Acc sum = {};
+        mul.finish(o.a, o.b, sum);
+        turn.at += turn.by;
+        const bool more = seek();
         if (more) start();
-        epilogue(m0, n0, sl, acc);
+        if (u >= 0) {
+            f32x4* to = (f32x4*)acc + (int64_t)u * C::MI * C::NI * C::THREADS + threadIdx.x;
+#pragma unroll
+            for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j) to[(i * C::NI + j) * C::THREADS] = sum[i][j];
+        } else {
+            const auto store = [&](auto edge) {
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j) {
+                    f32x4 v[C::MI];
+#pragma unroll
+                    for (int i = 0; i < C::MI; ++i) v[i] = sum[i][j];
+                    p.template column<C, decltype(edge)::value>(
+                        was, m0, n0, Lane{mul.xa, mul.xb + 16 * j + mul.lane % 16, mul.lane / 16}, v);
+                    __builtin_amdgcn_sched_barrier(0);   // a column's values die before the next one's are formed
+                }
+            };
+            if (p.template inside<C>(was, m0)) store(std::false_type());
+            else store(std::true_type());
+        }
         if (!more) return;
     }
 }
 
-// Four packed bf16 from four values.
-__device__ __forceinline__ void pack4(const float (&v)[4], uint32_t (&w)[2]) {
-    w[0] = down16(v[0]) | (down16(v[1]) << 16);
-    w[1] = down16(v[2]) | (down16(v[3]) << 16);
+// The epilogue of the sliced tiles, a workgroup for each of a tile's NI columns of blocks.
+template <class C, class P>
+__global__ __launch_bounds__(C::THREADS) void join_kernel(P p, Cut cut, const float* acc) {
+    const int in = blockIdx.x / C::NI, j = blockIdx.x % C::NI;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int tile = cut.full + in, mt, nt;
+    const int which = P::kProducts == 2 && tile >= p.template tiles<C>(0);
+    if (which) tile -= p.template tiles<C>(0);
+    const Operands o = p.operands(which);
+    place(tile, ((int)o.m + C::BM - 1) / C::BM, ((int)o.n + C::BN - 1) / C::BN, mt, nt);
+    const f32x4* from = (const f32x4*)acc + ((int64_t)in * cut.slices * C::MI * C::NI + j) * C::THREADS + threadIdx.x;
+    f32x4 v[C::MI];
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) v[i] = from[i * C::NI * C::THREADS];
+#pragma unroll 2
+    for (int s = 1; s < cut.slices; ++s)
+#pragma unroll
+        for (int i = 0; i < C::MI; ++i) v[i] += from[((int64_t)s * C::MI + i) * C::NI * C::THREADS];
+    p.template column<C, true>(which, mt * C::BM, nt * C::BN,
+                               Lane{wave % C::WM * (C::BM / C::WM), wave / C::WM * (C::BN / C::WN) + 16 * j + lane % 16, lane / 16}, v);
 }
 
 struct GatedArgs {
-    mm::Operand w, x, g;   // Wg and Wu (x), X; du: Wd and dY (g unused)
-    mm::Segments seg;
+    Operands o;            // Wg and Wu (a PairTile) and X, or Wd and dY
     int64_t rows;
     int f, fk, act;
-    int k, k_per, split;
     void* gate;            // [rows][f], or null
     void* up;
     uint16_t* u;           // planes [PARTS][rows][fk], or null (du)
     uint16_t* dab;         // du: planes [PARTS][rows][2 fk], or null
-    float* acc;            // slices: [split][rows][2][fk], du: [split][rows][fk]; or null
 };
 
-// Columns c .. c + N - 1 (N 4 or 8) of a row of planes.
-template <int PARTS, int N>
-__device__ __forceinline__ void put_planes(uint16_t* out, int64_t plane, int64_t at, const float (&v)[N]) {
-    uint32_t part[N][3];
+// a and b as the gradient is handed them, for bf16 operands: 16 bits, a sign and either, for magnitudes in [2^-8, 2^8), a set
+// bit, four of exponent and ten of fraction, or a clear bit and the upper 14 of the magnitude's fp32 form (six of fraction),
+// both rounded to nearest, ties away from zero.  In bf16 (seven of fraction) da, db and u would carry its rounding twice more: dW of 8192 x 2048 x
+// 5632 against 64 bits 3.5e-3, with this form 2.4e-3, where the rounding of da and of dW to bf16 alone leaves 2.3e-3.
+__device__ __forceinline__ uint32_t keep32(float x0, float x1) {   // two of them
+    uint32_t c[2];
 #pragma unroll
-    for (int e = 0; e < N; ++e) split3(v[e], part[e]);
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t m = __float_as_uint(h ? x1 : x0) & 0x7fffffffu;
+        const uint32_t fine = m - ((119u << 23) - 0x1000u);
+        uint32_t far = m + 0x10000u;
+        far = far > 0x7fffffffu ? 0x7fffffffu : far;   // (a NaN stays one)
+        c[h] = fine < (16u << 23) ? (fine >> 13) | 0x4000u : far >> 17;
+    }
+    const uint32_t signs = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302u);
+    return ((c[0] | (c[1] << 16)) & 0x7fff7fffu) | (signs & 0x80008000u);
+}
+__device__ __forceinline__ float kept16(uint32_t c) {
+    const uint32_t v = c & 0x3fffu;
+    return __uint_as_float((c & 0x4000u ? (v + (119u << 10)) << 13 : v << 17) | ((c & 0x8000u) << 16));
+}
+
+// Rows of a matrix from one of them on, read and written through a descriptor: offsets are 32 bits, what lies behind the last
+// row reads as zero and is not written.
+struct Rows {
+    __amdgpu_buffer_rsrc_t to;
+    int ld;   // elements
+    template <int BYTES>
+    static __device__ __forceinline__ Rows of(const void* p, int64_t row, int64_t rows, int ld) {
+        const int64_t left = row < rows ? (rows - row) * ld * BYTES : 0;
+        return Rows{__builtin_amdgcn_make_buffer_rsrc((void*)((const char*)p + row * ld * BYTES), 0,
+                                                      (int)(left < 0x7fffffff ? left : 0x7fffffff), 0x00027000), ld};
+    }
+};
+
+// A tile's values as a lane has them: H (1 or 2) neighbouring blocks of 16 columns, of which its quarter has four each.  Two
+// blocks of 16-bit values are traded, so that the lane stores eight in a row.
+struct Spot {
+    int row;       // from the first of Rows
+    int c0;        // the first block's first column, the same for the wave
+    int quarter;
+    __device__ __forceinline__ int own(int h) const { return c0 + 16 * h + 4 * quarter; }                     // of four
+    __device__ __forceinline__ int traded() const { return c0 + 16 * (quarter / 2) + 8 * (quarter % 2); }     // of eight
+};
+
+// 16-bit words to columns below d.  EDGE: the tile may reach behind them (else nothing is checked).  ROUND: rows of a multiple
+// of eight elements, which end with a lane's.
+template <int H, bool EDGE, bool ROUND>
+__device__ __forceinline__ void put_words(const Rows& to, const Spot& s, int d, const uint32_t (&w)[H][2]) {
+    constexpr int N = 4 * H;
+    const int c = H == 2 ? s.traded() : s.own(0);
+    const uint32_t off = (uint32_t)(s.row * to.ld + c) * 2u;
+    u32x4 t;
+    if constexpr (H == 2) t = trade(w[0], w[1]);
+    else t = u32x4{w[0][0], w[0][1], 0, 0};
+    if (!EDGE || ROUND || s.c0 + 16 * H <= d) {
+        const uint32_t at = EDGE && ROUND && c >= d ? mm::kOutside : off;
+        if constexpr (H == 2) __builtin_amdgcn_raw_buffer_store_b128(t, to.to, at, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(u32x2{t[0], t[1]}, to.to, at, 0, 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(t[e / 2] >> (16 * (e % 2))), to.to,
+                                                  c + e < d ? off + 2u * e : mm::kOutside, 0, 0);
+    }
+}
+
+// Two blocks' words as this lane stores them, columns below d (the others may be anything).  A ragged end is read one by
+// one: a vector whose last word is half behind the last row reads as zero there.
+template <bool EDGE>
+__device__ __forceinline__ u32x4 load_words(const Rows& from, const Spot& s, int d) {
+    const int c = s.traded();
+    const uint32_t off = (uint32_t)(s.row * from.ld + c) * 2u;
+    if (!EDGE || s.c0 + 32 <= d) return __builtin_amdgcn_raw_buffer_load_b128(from.to, off, 0, 0);
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        h[e] = __builtin_amdgcn_raw_buffer_load_b16(from.to, c + e < d ? off + 2u * e : mm::kOutside, 0, 0);
+    u32x4 t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = h[2 * e] | (h[2 * e + 1] << 16);
+    return t;
+}
+
+template <bool EDGE>
+__device__ __forceinline__ void put_floats(const Rows& to, const Spot& s, int h, int d, const float (&v)[4]) {
+    const int c = s.own(h);
+    const uint32_t off = (uint32_t)(s.row * to.ld + c) * 4u;
+    if (!EDGE || s.c0 + 16 * h + 16 <= d) {
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                     __float_as_uint(v[3])}, to.to, off, 0, 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), to.to, c + e < d ? off + 4u * e : mm::kOutside, 0, 0);
+    }
+}
+
+__device__ __forceinline__ void get_floats(const Rows& from, const Spot& s, int h, float (&v)[4]) {
+    const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(from.to, (uint32_t)(s.row * from.ld + s.own(h)) * 4u, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(t[e]);
+}
+
+// Parts of the values to planes whose rows end at `kp` columns, a multiple of 64: each the rounding of what the ones before it
+// leave, an exact split.
+template <int PARTS, int H, bool EDGE>
+__device__ __forceinline__ void put_parts(const Rows (&to)[PARTS], const Spot& s, int kp, float (&v)[H][4]) {
 #pragma unroll
     for (int q = 0; q < PARTS; ++q) {
-        if constexpr (N == 8) {
-            u32x4 w;
+        uint32_t w[H][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = part[2 * e][q] | (part[2 * e + 1][q] << 16);
-            *(u32x4*)(out + q * plane + at) = w;
-        } else {
-            *(u32x2*)(out + q * plane + at) = u32x2{part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16)};
-        }
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const uint32_t a = down16(v[h][e]), b = down16(v[h][e + 1]);
+                w[h][e / 2] = a | (b << 16);
+                v[h][e] -= up16(a);
+                v[h][e + 1] -= up16(b);
+            }
+        put_words<H, EDGE, true>(to[q], s, kp, w);
     }
 }
 
-// The eight values of two blocks of four as their lane quarter holds them after the trade: trade() for fp32 values.
-__device__ __forceinline__ void trade8(const float (&lo)[4], const float (&hi)[4], float (&v)[8]) {
+// a or b to its buffer, rows of d elements
+template <int PARTS, int H, bool EDGE>
+__device__ __forceinline__ void put_kept(const Rows& to, const Spot& s, int d, const float (&v)[H][4]) {
+    if constexpr (PARTS == 1) {
+        uint32_t w[H][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo[e]), __float_as_uint(hi[e]), false, false);
-        const auto z = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
-        v[e] = __uint_as_float(z[0]);
-        v[4 + e] = __uint_as_float(z[1]);
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) w[h][e / 2] = keep32(v[h][e], v[h][e + 1]);
+        put_words<H, EDGE, false>(to, s, d, w);
+    } else {
+#pragma unroll
+        for (int h = 0; h < H; ++h) put_floats<EDGE>(to, s, h, d, v[h]);
     }
 }
 
-// u of eight columns from a and b; gate and up are kept where asked for.
+// Two blocks of a or b as they are in memory.
 template <int PARTS>
-__device__ __forceinline__ void gated8(const GatedArgs& g, int64_t n, int c, float (&a)[8], float (&b)[8]) {
-    if (g.gate) {
-        put8<PARTS == 1>(g.gate, n * g.f, c, g.f, a);
-        put8<PARTS == 1>(g.up, n * g.f, c, g.f, b);
-    }
-    if (!g.u) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float slope;
-        a[e] = c + e < g.f ? activate<PARTS != 1>(g.act, a[e], slope) * b[e] : 0.f;
-    }
-    put_planes<PARTS>(g.u, g.rows * g.fk, n * g.fk + c, a);
-}
-
-// da, db and u of eight columns from du.
-template <int PARTS>
-__device__ __forceinline__ void dgated8(const GatedArgs& g, int64_t n, int c, const float (&du)[8], const Raw8<PARTS == 1>& a,
-                                        const Raw8<PARTS == 1>& b) {
-    float da[8], db[8], u[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {   // (a and b are zero behind column f, and du may be anything there)
-        float slope;
-        const float be = b.get(e), v = activate<PARTS != 1>(g.act, a.get(e), slope), d = c + e < g.f ? du[e] : 0.f;
-        da[e] = d * be * slope;
-        db[e] = d * v;
-        u[e] = v * be;
-    }
-    if (g.dab) {
-        put_planes<PARTS>(g.dab, g.rows * 2 * g.fk, n * 2 * g.fk + c, da);
-        put_planes<PARTS>(g.dab, g.rows * 2 * g.fk, n * 2 * g.fk + g.fk + c, db);
-    }
-    if (g.u) put_planes<PARTS>(g.u, g.rows * g.fk, n * g.fk + c, u);
-}
-
-template <class C, int PARTS>
-__global__ __launch_bounds__(C::THREADS) void gated_kernel(GatedArgs g) {
-    __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
-    mm::Product<C> mul(lds);
-    const int rows = (int)g.rows, quarter = mul.lane / 16;
-    walk_tiles(mul, g.w, g.x, g.seg, (2 * g.fk + C::BM - 1) / C::BM, (rows + C::BN - 1) / C::BN, g.split, g.k, g.k_per,
-               [&](int m0, int n0, int slice, typename C::Acc& acc) {
-        const int c0 = (m0 + mul.xa) / 2;   // blocks 2 i and 2 i + 1: a and b of columns c0 + 16 i ..
-#pragma unroll
-        for (int j = 0; j < C::NI; ++j) {
-            const int n = n0 + mul.xb + 16 * j + mul.lane % 16;
-            if (g.acc) {
-#pragma unroll
-                for (int i = 0; i < C::MI; ++i) {
-                    const int c = c0 + 16 * (i / 2) + 4 * quarter;
-                    if (n < rows && c < g.fk) *(f32x4*)(g.acc + ((slice * g.rows + n) * 2 + i % 2) * g.fk + c) = acc[i][j];
-                }
-                continue;
-            }
-            if constexpr (C::MI % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < C::MI; i += 4) {
-                    float v[4][4], a[8], b[8];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[h][e] = acc[i + h][j][e];
-                    trade8(v[0], v[2], a);
-                    trade8(v[1], v[3], b);
-                    const int c = c0 + 8 * i + 16 * (quarter / 2) + 8 * (quarter % 2);
-                    if (n < rows && c < g.fk) gated8<PARTS>(g, n, c, a, b);
-                }
-            } else {   // one block of 16 columns: two quarters have eight of them
-                float v[2][4], zero[4] = {0.f, 0.f, 0.f, 0.f}, a[8], b[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[h][e] = acc[h][j][e];
-                trade8(v[0], zero, a);
-                trade8(v[1], zero, b);
-                const int c = c0 + 8 * (quarter % 2);
-                if (quarter < 2 && n < rows && c < g.fk) gated8<PARTS>(g, n, c, a, b);
-            }
-        }
-    });
-}
-
-template <class C, int PARTS>
-__global__ __launch_bounds__(C::THREADS) void dgated_kernel(GatedArgs g) {
-    __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
-    mm::Product<C> mul(lds);
-    const int rows = (int)g.rows, quarter = mul.lane / 16;
-    walk_tiles(mul, g.w, g.x, g.seg, (g.fk + C::BM - 1) / C::BM, (rows + C::BN - 1) / C::BN, g.split, g.k, g.k_per,
-               [&](int m0, int n0, int slice, typename C::Acc& acc) {
-        const int c0 = m0 + mul.xa;
-#pragma unroll
-        for (int j = 0; j < C::NI; ++j) {
-            const int n = n0 + mul.xb + 16 * j + mul.lane % 16;
-            if (g.acc) {
-#pragma unroll
-                for (int i = 0; i < C::MI; ++i) {
-                    const int c = c0 + 16 * i + 4 * quarter;
-                    if (n < rows && c < g.fk) *(f32x4*)(g.acc + (slice * g.rows + n) * g.fk + c) = acc[i][j];
-                }
-                continue;
-            }
-            Raw8<PARTS == 1> a[C::MI / 2], b[C::MI / 2];
-#pragma unroll
-            for (int i = 0; i < C::MI; i += 2) {
-                const int c = c0 + 16 * i + 16 * (quarter / 2) + 8 * (quarter % 2);
-                if (n < rows && c < g.fk) {
-                    a[i / 2].load(g.gate, (int64_t)n * g.f, c, g.f);
-                    b[i / 2].load(g.up, (int64_t)n * g.f, c, g.f);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < C::MI; i += 2) {
-                float v[2][4], du[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[h][e] = acc[i + h][j][e];
-                trade8(v[0], v[1], du);
-                const int c = c0 + 16 * i + 16 * (quarter / 2) + 8 * (quarter % 2);
-                if (n < rows && c < g.fk) dgated8<PARTS>(g, n, c, du, a[i / 2], b[i / 2]);
-            }
-        }
-    });
-}
-
-// Eight columns of the slices' sums.
-__device__ __forceinline__ void sum8(const float* acc, int64_t stride, int split, float (&v)[8]) {
-    f32x4 lo{0.f, 0.f, 0.f, 0.f}, hi = lo;
-#pragma unroll 4
-    for (int s = 0; s < split; ++s) {
-        lo += *(const f32x4*)(acc + s * stride);
-        hi += *(const f32x4*)(acc + s * stride + 4);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { v[e] = lo[e]; v[4 + e] = hi[e]; }
-}
-
-// The epilogues over sliced sums, eight columns a thread.
-template <int PARTS, bool GRAD>
-__global__ __launch_bounds__(256) void gated_join_kernel(GatedArgs g) {
-    const int64_t per = g.fk / 8, all = g.rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int64_t n = i / per;
-        const int c = (int)(i - n * per) * 8;
-        if constexpr (GRAD) {
-            Raw8<PARTS == 1> a, b;
-            a.load(g.gate, n * g.f, c, g.f);
-            b.load(g.up, n * g.f, c, g.f);
-            float du[8];
-            sum8(g.acc + n * g.fk + c, g.rows * g.fk, g.split, du);
-            dgated8<PARTS>(g, n, c, du, a, b);
+struct Raw {
+    u32x4 w[PARTS == 1 ? 1 : 2];
+    template <bool EDGE>
+    __device__ __forceinline__ void load(const Rows& from, const Spot& s, int d) {
+        if constexpr (PARTS == 1) {
+            w[0] = load_words<EDGE>(from, s, d);
         } else {
-            float a[8], b[8];
-            sum8(g.acc + n * 2 * g.fk + c, g.rows * 2 * g.fk, g.split, a);
-            sum8(g.acc + n * 2 * g.fk + g.fk + c, g.rows * 2 * g.fk, g.split, b);
-            gated8<PARTS>(g, n, c, a, b);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[h] = __builtin_amdgcn_raw_buffer_load_b128(from.to, (uint32_t)(s.row * from.ld + s.own(h)) * 4u, 0, 0);
         }
     }
-}
-
-struct OutArgs {
-    mm::Operand a, b;
-    mm::Segments seg;
-    int k, k_per, split;
-    int cols;               // of the output
-    int64_t rows;           // of the product: the output's, or those of two outputs, the second's from row `second`
-    int64_t second, valid;  // and how many rows each has (second: rows where there is one output)
-    void* out;
-    void* out2;
-    int out_bf16, accumulate;
-    float* acc;             // [split][rows][cols rounded up to 8], or null
-    int ldacc;
+    __device__ __forceinline__ void get(float (&v)[2][4]) const {
+        if constexpr (PARTS == 1) {
+            uint32_t t[2][2];
+            untrade(w[0], t[0], t[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[h][e] = kept16(t[h][e / 2] >> (16 * (e % 2)) & 0xffffu);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[h][e] = __uint_as_float(w[h][e]);
+        }
+    }
 };
 
-// where row n goes, or null
-__device__ __forceinline__ void* out_row(const OutArgs& a, int64_t n, int64_t& row) {
-    const bool two = n >= a.second;
-    row = two ? n - a.second : n;
-    return row < a.valid && n < a.rows ? (two ? a.out2 : a.out) : nullptr;
+// What the epilogues write and read, from row n on.
+template <int PARTS>
+struct GatedRows {
+    Rows gate, up, u[PARTS], da[PARTS], db[PARTS];
+    __device__ __forceinline__ GatedRows(const GatedArgs& g, int64_t n) {
+        constexpr int B = PARTS == 1 ? 2 : 4;
+        gate = Rows::of<B>(g.gate, n, g.gate ? g.rows : 0, g.f);
+        up = Rows::of<B>(g.up, n, g.up ? g.rows : 0, g.f);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            u[q] = Rows::of<2>(g.u + q * g.rows * g.fk, n, g.u ? g.rows : 0, g.fk);
+            da[q] = Rows::of<2>(g.dab + q * g.rows * 2 * g.fk, n, g.dab ? g.rows : 0, 2 * g.fk);
+            db[q] = da[q];
+            db[q].to = Rows::of<2>(g.dab + q * g.rows * 2 * g.fk + g.fk, n, g.dab ? g.rows : 0, 2 * g.fk).to;
+        }
+    }
+};
+
+// u of H blocks from a and b, which are kept where asked for.
+template <int PARTS, int H, bool EDGE>
+__device__ __forceinline__ void gated(const GatedArgs& g, const GatedRows<PARTS>& to, const Spot& s, const float (&a)[H][4],
+                                      const float (&b)[H][4]) {
+    if (g.gate) {
+        put_kept<PARTS, H, EDGE>(to.gate, s, g.f, a);
+        put_kept<PARTS, H, EDGE>(to.up, s, g.f, b);
+    }
+    if (!g.u) return;
+    float u[H][4];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float slope;
+            u[h][e] = activate<PARTS != 1>(g.act, a[h][e], slope) * b[h][e];
+            if (EDGE && s.own(h) + e >= g.f) u[h][e] = 0.f;
+        }
+    put_parts<PARTS, H, EDGE>(to.u, s, g.fk, u);
 }
 
-__device__ __forceinline__ void put_out8(const OutArgs& a, void* out, int64_t row, int c, float (&v)[8]) {
-    const int64_t at = row * a.cols;
-    if (a.out_bf16) {
-        if (a.accumulate) {
-            Raw8<true> r;
-            r.load(out, at, c, a.cols);
+// da, db and u of two blocks from du, a and b.
+template <int PARTS, bool EDGE>
+__device__ __forceinline__ void dgated(const GatedArgs& g, const GatedRows<PARTS>& to, const Spot& s, const float (&du)[2][4],
+                                       const float (&a)[2][4], const float (&b)[2][4]) {
+    float da[2][4], db[2][4], u[2][4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += r.get(e);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float slope;
+            const float v = activate<PARTS != 1>(g.act, a[h][e], slope);
+            da[h][e] = du[h][e] * b[h][e] * slope;
+            db[h][e] = du[h][e] * v;
+            u[h][e] = v * b[h][e];
+            if (EDGE && s.own(h) + e >= g.f) da[h][e] = db[h][e] = u[h][e] = 0.f;   // (made of anything there)
         }
-        put8<true>(out, at, c, a.cols, v);
+    if (g.dab) {
+        put_parts<PARTS, 2, EDGE>(to.da, s, g.fk, da);
+        put_parts<PARTS, 2, EDGE>(to.db, s, g.fk, db);
+    }
+    if (g.u) put_parts<PARTS, 2, EDGE>(to.u, s, g.fk, u);
+}
+
+struct Single {
+    static constexpr int kProducts = 1;
+    template <class C>
+    __device__ __forceinline__ int tiles(int) const { return 0; }
+};
+
+// a and b: blocks 2 i and 2 i + 1 of a tile are a and b of the same 16 columns
+template <int PARTS>
+struct Gated : Single {
+    GatedArgs g;
+    explicit Gated(const GatedArgs& a) : g(a) {}
+    __device__ __forceinline__ const Operands& operands(int) const { return g.o; }
+    template <class C>
+    __device__ __forceinline__ bool inside(int, int m0) const { return m0 + C::BM <= 2 * g.f; }
+    template <class C, bool EDGE>
+    __device__ __forceinline__ void column(int, int m0, int n0, const Lane& l, const f32x4 (&v)[C::MI]) const {
+        constexpr int H = C::MI % 4 == 0 ? 2 : 1;
+        const GatedRows<PARTS> to(g, n0);
+        const int c0 = (m0 + l.xa) / 2;
+#pragma unroll
+        for (int i = 0; i < C::MI; i += 2 * H) {
+            float a[H][4], b[H][4];
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { a[h][e] = v[i + 2 * h][e]; b[h][e] = v[i + 2 * h + 1][e]; }
+            gated<PARTS, H, EDGE>(g, to, Spot{l.row, c0 + 8 * i, l.quarter}, a, b);
+        }
+    }
+};
+
+// du.  A column's a and b are all on their way before the first is used.
+template <int PARTS>
+struct Dgated : Single {
+    GatedArgs g;
+    explicit Dgated(const GatedArgs& a) : g(a) {}
+    __device__ __forceinline__ const Operands& operands(int) const { return g.o; }
+    template <class C>
+    __device__ __forceinline__ bool inside(int, int m0) const { return m0 + C::BM <= g.f; }
+    template <class C, bool EDGE>
+    __device__ __forceinline__ void column(int, int m0, int n0, const Lane& l, const f32x4 (&v)[C::MI]) const {
+        const GatedRows<PARTS> to(g, n0);
+        Raw<PARTS> ra[C::MI / 2], rb[C::MI / 2];
+#pragma unroll
+        for (int i = 0; i < C::MI; i += 2) {
+            const Spot s{l.row, m0 + l.xa + 16 * i, l.quarter};
+            ra[i / 2].template load<EDGE>(to.gate, s, g.f);
+            rb[i / 2].template load<EDGE>(to.up, s, g.f);
+        }
+#pragma unroll
+        for (int i = 0; i < C::MI; i += 2) {
+            float du[2][4], a[2][4], b[2][4];
+            ra[i / 2].get(a);
+            rb[i / 2].get(b);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) du[h][e] = v[i + h][e];
+            dgated<PARTS, EDGE>(g, to, Spot{l.row, m0 + l.xa + 16 * i, l.quarter}, du, a, b);
+        }
+    }
+};
+
+struct OutArgs {
+    Operands o;
+    int cols;               // of the output
+    int64_t second, valid;  // rows of the product from which they are the second output's (all where there is one), rows of each
+    void* out;
+    void* out2;
+    int bf16, accumulate;
+};
+
+// Rows n .. n + 15 of the product (n a multiple of 16) in their output.
+__device__ __forceinline__ Rows out_rows(const OutArgs& a, int64_t n) {
+    const bool two = n >= a.second;   // (a multiple of 64 where there are two outputs)
+    void* out = two ? a.out2 : a.out;
+    const int64_t row = two ? n - a.second : n, rows = two && !a.out2 ? 0 : a.valid;
+    return a.bf16 ? Rows::of<2>(out, row, rows, a.cols) : Rows::of<4>(out, row, rows, a.cols);
+}
+
+template <bool EDGE>
+__device__ __forceinline__ void put_out(const OutArgs& a, const Rows& to, const Spot& s, float (&v)[2][4]) {
+    if (a.bf16) {
+        uint32_t w[2][2];
+        if (a.accumulate) {
+            untrade(load_words<EDGE>(to, s, a.cols), w[0], w[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[h][e] += up16(w[h][e / 2] >> (16 * (e % 2)) & 0xffffu);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) w[h][e / 2] = down16(v[h][e]) | (down16(v[h][e + 1]) << 16);
+        put_words<2, EDGE, false>(to, s, a.cols, w);
     } else {
-        if (a.accumulate) {
-            Raw8<false> r;
-            r.load(out, at, c, a.cols);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += r.get(e);
+        for (int h = 0; h < 2; ++h) {
+            if (a.accumulate) {
+                float old[4];
+                get_floats(to, s, h, old);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[h][e] += old[e];
+            }
+            put_floats<EDGE>(to, s, h, a.cols, v[h]);
         }
-        put8<false>(out, at, c, a.cols, v);
     }
 }
 
-template <class C>
-__global__ __launch_bounds__(C::THREADS) void ffn_out_kernel(OutArgs a) {
-    __shared__ __attribute__((aligned(1024))) uint16_t lds[C::kLds];
-    mm::Product<C> mul(lds);
-    const int rows = (int)a.rows, quarter = mul.lane / 16;
-    walk_tiles(mul, a.a, a.b, a.seg, (a.cols + C::BM - 1) / C::BM, (rows + C::BN - 1) / C::BN, a.split, a.k, a.k_per,
-               [&](int m0, int n0, int slice, typename C::Acc& acc) {
-        const int c0 = m0 + mul.xa;
-#pragma unroll
-        for (int j = 0; j < C::NI; ++j) {
-            const int n = n0 + mul.xb + 16 * j + mul.lane % 16;
-            if (a.acc) {
-#pragma unroll
-                for (int i = 0; i < C::MI; ++i) {
-                    const int c = c0 + 16 * i + 4 * quarter;
-                    if (n < rows && c < a.ldacc) *(f32x4*)(a.acc + (slice * a.rows + n) * a.ldacc + c) = acc[i][j];
-                }
-                continue;
-            }
-            int64_t row;
-            void* out = out_row(a, n, row);
-#pragma unroll
-            for (int i = 0; i < C::MI; i += 2) {
-                float v[2][4], o[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[h][e] = acc[i + h][j][e];
-                trade8(v[0], v[1], o);
-                const int c = c0 + 16 * i + 16 * (quarter / 2) + 8 * (quarter % 2);
-                if (out && c < a.cols) put_out8(a, out, row, c, o);
-            }
-        }
-    });
-}
-
-__global__ __launch_bounds__(256) void out_join_kernel(OutArgs a) {
-    const int64_t per = a.ldacc / 8, all = a.rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int64_t n = i / per;
-        const int c = (int)(i - n * per) * 8;
-        int64_t row;
-        void* out = out_row(a, n, row);
-        if (!out || c >= a.cols) continue;
-        float v[8];
-        sum8(a.acc + n * a.ldacc + c, a.rows * a.ldacc, a.split, v);
-        put_out8(a, out, row, c, v);
+// Products into outputs: one, or dWg | dWu and dWd at once.
+template <int N>
+struct Out {
+    static constexpr int kProducts = N;
+    OutArgs p[N];
+    explicit Out(const OutArgs& a) : p{a} {}
+    Out(const OutArgs& a, const OutArgs& b) : p{a, b} {}
+    template <class C>
+    __device__ __forceinline__ int tiles(int i) const {
+        return (((int)p[i].o.m + C::BM - 1) / C::BM) * (((int)p[i].o.n + C::BN - 1) / C::BN);
     }
-}
+    __device__ __forceinline__ const Operands& operands(int which) const { return p[N == 2 ? which : 0].o; }
+    template <class C>
+    __device__ __forceinline__ bool inside(int which, int m0) const { return m0 + C::BM <= p[N == 2 ? which : 0].cols; }
+    template <class C, bool EDGE>
+    __device__ __forceinline__ void column(int which, int m0, int n0, const Lane& l, const f32x4 (&v)[C::MI]) const {
+        const OutArgs& a = p[N == 2 ? which : 0];
+        const int n = __builtin_amdgcn_readfirstlane(l.row) & ~15;   // the block's first row
+        const Rows to = out_rows(a, n0 + n);
+#pragma unroll
+        for (int i = 0; i < C::MI; i += 2) {
+            float w[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[h][e] = v[i + h][e];
+            put_out<EDGE>(a, to, Spot{l.row - n, m0 + l.xa + 16 * i, l.quarter}, w);
+        }
+    }
+};
 
 __global__ __launch_bounds__(256) void zeros_kernel(uint16_t* p, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
@@ -438,7 +633,7 @@ __global__ __launch_bounds__(256) void zeros_kernel(uint16_t* p, int64_t n) {
 // Launches
 // ---------------------------------------------------------------------------
 template <bool TA, bool TB, bool PAIR> using C256 = mm::Config<256, 256, 2, 4, 2, TA, TB, false, PAIR>;
-template <bool TA, bool TB, bool PAIR> using C128 = mm::Config<128, 128, 2, 2, 4, TA, TB, false, PAIR>;
+template <bool TA, bool TB, bool PAIR> using C128 = mm::Config<128, 128, 2, 2, 2, TA, TB, false, PAIR>;
 template <bool TA, bool TB, bool PAIR> using C64 = mm::Config<64, 64, 2, 2, 8, TA, TB, false, PAIR>;
 template <bool TA, bool TB, bool PAIR> using C32 = mm::Config<128, 32, 4, 1, 4, TA, TB, false, PAIR>;
 
@@ -448,88 +643,84 @@ void of_tile(int tile, F f) {
     else if (tile == TILE_128) f(C128<TA, TB, PAIR>());
     else if (tile == TILE_64) f(C64<TA, TB, PAIR>());
     else if constexpr (!TB) f(C32<TA, TB, PAIR>());
-    else f(C128<TA, TB, PAIR>());
+}
+
+template <class C, class P>
+void launch(const P& p, const Product& r, mm::Segments seg, float* acc, hipStream_t s) {
+    const Cut& c = r.cut;
+    const int64_t items = c.full > (int64_t)c.rem * c.slices ? c.full : (int64_t)c.rem * c.slices;
+    hipLaunchKernelGGL((product_kernel<C, P>), walkers<C>(items), dim3(C::THREADS), 0, s, p, c, seg, acc);
+    if (c.rem) hipLaunchKernelGGL((join_kernel<C, P>), dim3((unsigned)(c.rem * C::NI)), dim3(C::THREADS), 0, s, p, c, acc);
 }
 
 template <bool GRAD>
-void launch_gated(GatedArgs g, const Product& r, int parts, float* acc, hipStream_t s) {
-    g.k = (int)r.k; g.k_per = (int)r.k_per; g.split = (int)r.split;
-    g.acc = r.split > 1 ? acc : nullptr;
+void launch_gated(const GatedArgs& g, const Product& r, int parts, mm::Segments seg, float* acc, hipStream_t s) {
     of_tile<GRAD, false, !GRAD>(r.tile, [&](auto c) {
         using C = decltype(c);
-        const dim3 grid = walkers<C>(ceil_div64(GRAD ? g.fk : 2 * g.fk, C::BM) * ceil_div64(g.rows, C::BN) * r.split);
         if constexpr (GRAD) {
-            if (parts == 1) hipLaunchKernelGGL((dgated_kernel<C, 1>), grid, dim3(C::THREADS), 0, s, g);
-            else hipLaunchKernelGGL((dgated_kernel<C, 3>), grid, dim3(C::THREADS), 0, s, g);
+            if (parts == 1) launch<C>(Dgated<1>(g), r, seg, acc, s);
+            else launch<C>(Dgated<3>(g), r, seg, acc, s);
         } else {
-            if (parts == 1) hipLaunchKernelGGL((gated_kernel<C, 1>), grid, dim3(C::THREADS), 0, s, g);
-            else hipLaunchKernelGGL((gated_kernel<C, 3>), grid, dim3(C::THREADS), 0, s, g);
+            if (parts == 1) launch<C>(Gated<1>(g), r, seg, acc, s);
+            else launch<C>(Gated<3>(g), r, seg, acc, s);
         }
     });
-    if (!g.acc) return;
-    const dim3 grid((unsigned)stride_blocks(ceil_div64(g.rows * (g.fk / 8), 256)));
-    if (parts == 1) hipLaunchKernelGGL((gated_join_kernel<1, GRAD>), grid, dim3(256), 0, s, g);
-    else hipLaunchKernelGGL((gated_join_kernel<3, GRAD>), grid, dim3(256), 0, s, g);
 }
 
-template <bool TA, bool TB>
-void launch_out(OutArgs a, const Product& r, float* acc, hipStream_t s) {
-    a.k = (int)r.k; a.k_per = (int)r.k_per; a.split = (int)r.split;
-    a.acc = r.split > 1 ? acc : nullptr;
-    a.ldacc = (a.cols + 7) / 8 * 8;
-    of_tile<TA, TB, false>(r.tile, [&](auto c) {
-        using C = decltype(c);
-        const dim3 grid = walkers<C>(ceil_div64(a.cols, C::BM) * ceil_div64(a.rows, C::BN) * r.split);
-        hipLaunchKernelGGL((ffn_out_kernel<C>), grid, dim3(C::THREADS), 0, s, a);
-    });
-    if (a.acc)
-        hipLaunchKernelGGL(out_join_kernel, dim3((unsigned)stride_blocks(ceil_div64(a.rows * (a.ldacc / 8), 256))), dim3(256), 0, s, a);
+template <bool TA, bool TB, int N>
+void launch_out(const Out<N>& o, const Product& r, mm::Segments seg, float* acc, hipStream_t s) {
+    of_tile<TA, TB, false>(r.tile, [&](auto c) { launch<decltype(c)>(o, r, seg, acc, s); });
 }
 
-// A matrix as planes in the workspace, or in place.
-mm::Operand operand(const void* in, const float* scale, int kind, bool pack, int parts, int64_t rows, int64_t all, int64_t d,
-                    uint16_t* out, int64_t plane, hipStream_t s) {
+// A matrix in place, or as planes in the workspace that a job fills.
+mm::Operand operand(const void* in, const float* scale, int kind, bool pack, int64_t rows, int64_t all, int64_t d, uint16_t* out,
+                    int64_t plane, PackJobs* jobs) {
     const int64_t kp = ceil_div64(d, 64) * 64;
     if (!pack) return mm::Operand{(const uint16_t*)in, 0, d, (int)rows};
-    const dim3 grid((unsigned)ceil_div64(all, 4));
-    if (parts == 1)
-        hipLaunchKernelGGL((planes_kernel<1>), grid, dim3(256), 0, s, in, scale, kind, rows, all, (int)d, (int)kp, out, plane);
-    else
-        hipLaunchKernelGGL((planes_kernel<3>), grid, dim3(256), 0, s, in, scale, kind, rows, all, (int)d, (int)kp, out, plane);
+    jobs->job[jobs->n++] = PackJob{in, scale, out, rows, all, plane, kind, (int)d, (int)kp, jobs->blocks};
+    jobs->blocks += (unsigned)ceil_div64(all, 4);
     return mm::Operand{out, plane, kp, (int)rows};
 }
 
 struct Inputs {
-    mm::Operand x, w, wd;   // w: Wg's rows and, `pair` elements on, Wu's
+    mm::Operand x, w, wd, dy;   // w: Wg's rows and, `pair` elements on, Wu's
     mm::Segments seg;
 };
 
-Inputs inputs(const FfnArgs& a, const FfnPlan& p, char* ws, bool need_x, hipStream_t s) {
+Inputs inputs(const FfnArgs& a, const FfnPlan& p, char* ws, bool need_x, bool need_w, hipStream_t s) {
     Inputs in{};
+    PackJobs jobs{};
     const int kind = a.bf16 ? 1 : 0;
     in.seg = segments(p.parts, p.parts);
     if (need_x)
-        in.x = operand(a.X, a.x_scale, a.x_scale ? 2 : kind, p.xpack, p.parts, p.t, p.t, p.d, (uint16_t*)(ws + p.x), p.t * p.dk, s);
+        in.x = operand(a.X, a.x_scale, a.x_scale ? 2 : kind, p.xpack, p.t, p.t, p.d, (uint16_t*)(ws + p.x), p.t * p.dk, &jobs);
     uint16_t* w = (uint16_t*)(ws + p.w);
     const int64_t plane = 2 * p.fk * p.dk;
-    in.w = operand(a.Wg, nullptr, kind, p.wpack, p.parts, p.f, p.fk, p.d, w, plane, s);
-    if (p.wpack) {
-        operand(a.Wu, nullptr, kind, true, p.parts, p.f, p.fk, p.d, w + p.fk * p.dk, plane, s);
-        in.w.pair = p.fk * p.dk;
-    } else {
-        in.w.pair = ((intptr_t)a.Wu - (intptr_t)a.Wg) / 2;
+    if (need_w) {
+        in.w = operand(a.Wg, nullptr, kind, p.wpack, p.f, p.fk, p.d, w, plane, &jobs);
+        if (p.wpack) operand(a.Wu, nullptr, kind, true, p.f, p.fk, p.d, w + p.fk * p.dk, plane, &jobs);
+        in.w.pair = p.wpack ? p.fk * p.dk : ((intptr_t)a.Wu - (intptr_t)a.Wg) / 2;
     }
-    in.wd = operand(a.Wd, nullptr, kind, p.dpack, p.parts, p.d, p.d, p.f, (uint16_t*)(ws + p.wd), p.d * p.fk, s);
+    in.wd = operand(a.Wd, nullptr, kind, p.dpack, p.d, p.d, p.f, (uint16_t*)(ws + p.wd), p.d * p.fk, &jobs);
+    if (a.dY) in.dy = operand(a.dY, nullptr, kind, p.ypack, p.t, p.t, p.d, (uint16_t*)(ws + p.dy), p.t * p.dk, &jobs);
+    if (jobs.n > 0) {
+        if (p.parts == 1) hipLaunchKernelGGL((planes_kernel<1>), dim3(jobs.blocks), dim3(256), 0, s, jobs);
+        else hipLaunchKernelGGL((planes_kernel<3>), dim3(jobs.blocks), dim3(256), 0, s, jobs);
+    }
     return in;
 }
 
-GatedArgs gated_args(const FfnArgs& a, const FfnPlan& p, const Inputs& in, char* ws) {
+GatedArgs gated_args(const FfnArgs& a, const FfnPlan& p, const mm::Operand& w, const mm::Operand& x, int64_t m, char* ws) {
     GatedArgs g{};
-    g.w = in.w; g.x = in.x; g.seg = in.seg;
+    g.o = Operands{w, x, m, p.t};
     g.rows = p.t; g.f = (int)p.f; g.fk = (int)p.fk; g.act = a.act;
     g.gate = a.gate; g.up = a.up;
     g.u = (uint16_t*)(ws + p.u);
     return g;
+}
+
+OutArgs out_args(const mm::Operand& x, const mm::Operand& y, int64_t cols, int64_t rows, void* out, int bf16, int accumulate) {
+    return OutArgs{{x, y, cols, rows}, (int)cols, rows, rows, out, nullptr, bf16, accumulate};
 }
 
 }  // namespace
@@ -542,64 +733,50 @@ int run_zeros(void* out, int64_t n, void* stream) {
 
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
-    const Inputs in = inputs(a, p, ws, true, s);
+    const Inputs in = inputs(a, p, ws, true, true, s);
     float* acc = (float*)(ws + p.acc);
-    launch_gated<false>(gated_args(a, p, in, ws), p.gu, p.parts, acc, s);
-    OutArgs o{};
-    o.a = in.wd;
-    o.b = mm::Operand{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
-    o.seg = in.seg; o.cols = (int)p.d; o.rows = o.second = o.valid = p.t; o.out = a.Y; o.out_bf16 = a.bf16;
-    launch_out<false, false>(o, p.y, acc, s);
+    launch_gated<false>(gated_args(a, p, in.w, in.x, 2 * p.fk, ws), p.gu, p.parts, in.seg, acc, s);
+    const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
+    launch_out<false, false>(Out<1>(out_args(in.wd, u, p.d, p.t, a.Y, a.bf16, 0)), p.y, in.seg, acc, s);
     return (int)hipGetLastError();
 }
 
 int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
     FfnArgs a = args;
-    const Inputs in = inputs(a, p, ws, !a.gate || a.dWg, s);
+    const Inputs in = inputs(a, p, ws, !a.gate || a.dWg, !a.gate || a.dX, s);
     float* acc = (float*)(ws + p.acc);
     if (!a.gate) {
         a.gate = ws + p.gate;
         a.up = ws + p.up;
-        GatedArgs g = gated_args(a, p, in, ws);
+        GatedArgs g = gated_args(a, p, in.w, in.x, 2 * p.fk, ws);
         g.u = nullptr;
-        launch_gated<false>(g, p.gu, p.parts, acc, s);
+        launch_gated<false>(g, p.gu, p.parts, in.seg, acc, s);
     }
-    const mm::Operand dy = operand(a.dY, nullptr, a.bf16 ? 1 : 0, p.ypack, p.parts, p.t, p.t, p.d, (uint16_t*)(ws + p.dy), p.t * p.dk, s);
-    GatedArgs g = gated_args(a, p, in, ws);
-    g.w = in.wd; g.x = dy;
+    GatedArgs g = gated_args(a, p, in.wd, in.dy, p.fk, ws);
     g.dab = a.dX || a.dWg ? (uint16_t*)(ws + p.dab) : nullptr;
     if (!a.dWd) g.u = nullptr;
-    launch_gated<true>(g, p.du, p.parts, acc, s);
+    launch_gated<true>(g, p.du, p.parts, in.seg, acc, s);
     const mm::Operand dab{(uint16_t*)(ws + p.dab), p.t * 2 * p.fk, 2 * p.fk, (int)p.t};
-    OutArgs o{};
+    const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
     if (a.dX) {   // over da and Wg, db and Wu: two planes of one part each in place, one matrix of 2 fk rows where packed
-        o.a = in.w; o.b = dab; o.seg = in.seg;
+        OutArgs o = out_args(in.w, dab, p.d, p.t, a.dX, a.bf16, 0);
+        mm::Segments seg = in.seg;
         if (p.wpack) {
-            o.a.rows = (int)(2 * p.fk);
+            o.o.a.rows = (int)(2 * p.fk);
         } else {
-            o.a.plane = in.w.pair;
-            o.b.plane = p.fk;
-            o.seg = mm::Segments{2, 0 | (1 | 1 << 2) << 4};
+            o.o.a.plane = in.w.pair;
+            o.o.b.plane = p.fk;
+            seg = mm::Segments{2, 0 | (1 | 1 << 2) << 4};
         }
-        o.cols = (int)p.d; o.rows = o.second = o.valid = p.t; o.out = a.dX; o.out_bf16 = a.bf16;
-        launch_out<true, false>(o, p.dx, acc, s);
+        launch_out<true, false>(Out<1>(o), p.dx, seg, acc, s);
     }
-    if (a.dWg) {
-        o = OutArgs{};
-        o.a = in.x; o.b = dab; o.seg = in.seg;
-        o.cols = (int)p.d; o.rows = 2 * p.fk; o.second = p.fk; o.valid = p.f; o.out = a.dWg; o.out2 = a.dWu;
-        o.out_bf16 = a.dw_bf16; o.accumulate = a.accumulate;
-        launch_out<true, true>(o, p.dgu, acc, s);
-    }
-    if (a.dWd) {
-        o = OutArgs{};
-        o.a = mm::Operand{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
-        o.b = dy; o.seg = in.seg;
-        o.cols = (int)p.f; o.rows = o.second = o.valid = p.d; o.out = a.dWd;
-        o.out_bf16 = a.dw_bf16; o.accumulate = a.accumulate;
-        launch_out<true, true>(o, p.dd, acc, s);
-    }
+    OutArgs gu = out_args(in.x, dab, p.d, 2 * p.fk, a.dWg, a.dw_bf16, a.accumulate);
+    gu.second = p.fk; gu.valid = p.f; gu.out2 = a.dWu;
+    const OutArgs d = out_args(u, in.dy, p.f, p.d, a.dWd, a.dw_bf16, a.accumulate);
+    if (a.dWg && a.dWd) launch_out<true, true>(Out<2>(gu, d), p.dw, in.seg, acc, s);
+    else if (a.dWg) launch_out<true, true>(Out<1>(gu), p.dgu, in.seg, acc, s);
+    else if (a.dWd) launch_out<true, true>(Out<1>(d), p.dd, in.seg, acc, s);
     return (int)hipGetLastError();
 }
 

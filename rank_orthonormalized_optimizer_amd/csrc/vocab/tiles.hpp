@@ -172,6 +172,17 @@ __device__ __forceinline__ u32x4 trade(const uint32_t (&a)[2], const uint32_t (&
     return w;
 }
 
+// And back: the two blocks' words from eight consecutive rows.
+__device__ __forceinline__ void untrade(const u32x4& w, uint32_t (&a)[2], uint32_t (&b)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const auto x = __builtin_amdgcn_permlane16_swap(w[h], w[2 + h], false, false);
+        const auto z = __builtin_amdgcn_permlane32_swap(x[0], x[1], false, false);
+        a[h] = z[0];
+        b[h] = z[1];
+    }
+}
+
 // Stores such pieces; to: the address for this lane's quarter.
 __device__ __forceinline__ void store_pair(uint16_t* to, const uint32_t (&a)[2], const uint32_t (&b)[2], bool in) {
     const u32x4 w = trade(a, b);

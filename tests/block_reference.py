@@ -83,6 +83,39 @@ def mask(n: int, p: float, seed: int, site: int, device="cpu", start: int = 0):
     return (torch.stack(c, 1).reshape(-1)[:n] >= min(round(p * 2 ** 32), m32))
 
 
+def kept(t):
+    """The values of a gate or up buffer: fp32, or a bf16 buffer's bits in the 16-bit form of dion_block.h."""
+    if t.dtype == torch.float32:
+        return t.to(F64)
+    c = t.view(torch.int16).to(torch.int64) & 0xffff
+    e, f = torch.where(c >> 14 & 1 == 1, (c >> 10 & 15) - 8, (c >> 6 & 255) - 127), \
+        torch.where(c >> 14 & 1 == 1, (c & 1023) / 1024.0, (c & 63) / 64.0).to(F64)
+    v = torch.exp2(e.to(F64)) * (1 + f)
+    v = torch.where(e == -127, torch.exp2(torch.full_like(v, -126)) * f, v)
+    v = torch.where(e == 128, torch.where(f == 0, math.inf, math.nan).to(F64), v)
+    return torch.where(c >> 15 == 1, -v, v)
+
+
+def keep_step(v, dtype):
+    """The most that keeping v rounds away."""
+    if dtype == torch.float32:
+        return U * v.abs()
+    fine = (v.abs() >= 2.0 ** -8) & (v.abs() < 2.0 ** 8)
+    return torch.where(fine, 2.0 ** -11, 2.0 ** -7) * v.abs() + 2.0 ** -132
+
+
+def keep(v, dtype):
+    """v in the form in which gate and up are kept."""
+    if dtype == torch.float32:
+        return v.float()
+    bits = v.float().contiguous().view(torch.int32).to(torch.int64) & 0xffffffff
+    m = bits & 0x7fffffff
+    fine = ((m + 0x1000) >> 13) - (119 << 10)
+    far = ((m + 0x10000) >> 17).clamp(max=0x3fff)
+    c = torch.where((fine >= 0) & (fine < 0x4000), fine | 0x4000, far) | bits >> 16 & 0x8000
+    return torch.where(c >= 0x8000, c - 0x10000, c).to(torch.int16).view(torch.bfloat16)
+
+
 class Norm:
     """h, rstd, y and their bounds (before the outputs' rounding)."""
 
@@ -169,10 +202,11 @@ class Ffn:
         self.gate, self.up, self.gate_bound, self.up_bound = a, b, ea, eb
         if dY is not None:
             if gate is not None:
-                a, b = gate.to(F64).reshape(T, f), up.to(F64).reshape(T, f)
+                a, b = kept(gate).reshape(T, f), kept(up).reshape(T, f)
                 ea, eb = torch.zeros_like(a), torch.zeros_like(b)
             else:
-                ea, eb = ea + half_step(t) * (a.abs() + ea), eb + half_step(t) * (b.abs() + eb)
+                # (a value next to a border of the form may fall on its coarser side)
+                ea, eb = ea + torch.maximum(keep_step(a, t), keep_step(a.abs() + ea, t)), eb + torch.maximum(keep_step(b, t), keep_step(b.abs() + eb, t))
         v, slope, z = activation(act, a)
         rel = 8 * (z + 1) * U
         ev = 1.2 * ea + rel * v.abs()
