@@ -84,8 +84,10 @@ inline NormPlan make_norm_plan(int64_t rows, int64_t width) {
 }
 int run_rms_norm_grad(const NormGradArgs& a, const NormPlan& p, void* stream);
 
-// Layout of a feed-forward call.  parts: bf16 parts of an operand (1 for bf16, 3 for fp32).  The packed planes have rows of
-// a multiple of 64 elements, zeros behind the matrix; Wg's and Wu's are one matrix of 2 fk rows, da and db one of 2 fk columns.
+// Layout of a feed-forward call.  bf16 operands are one part each, in place where rows are a multiple of 64 elements, else
+// in packed planes with rows of a multiple of 64 and zeros behind the matrix.  fp32 operands always go through planes: two
+// fp16 ones (scaled rows) for a, b and du, three bf16 ones for the other products.  Wg's and Wu's planes are one matrix of 2 fk
+// rows, da and db one of 2 fk columns.
 // How a product's tiles go over the chip: `full` of them whole, the `rem` others cut into slices of the reduction.
 struct Cut {
     int full, rem, slices;
@@ -98,21 +100,32 @@ struct Product {
 };
 struct FfnPlan {
     int64_t t, d, f, dk, fk;
-    int parts;
+    int parts;                         // of the operands that are not fp16 planes: 1 or 3
     bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
     Product gu, y, du, dx, dgu, dd, dw;   // (dw: dgu and dd at once)
-    size_t x, w, wd, u, dab, dy, gate, up, acc;
+    size_t x, w, wd, dy;               // their planes
+    size_t x16, w16, wd16, dy16;       // fp16 planes
+    size_t xinv, winv, dinv, yinv;     // inverse scales of their rows
+    size_t u, dab, gate, up, acc;
     size_t total;
 };
+// fp32: inverse scales are read for whole tiles
+inline int64_t scale_rows(int64_t rows) { return ceil_div64(rows, 256) * 256 + 256; }
 
-// Times in microseconds of a tile's slab of 64 k where the chip is full of them, of its start and its epilogue; and the
-// workgroups that a CU holds.
+// Times in microseconds of a tile's slab of 64 k and of its start and epilogue, and the workgroups that a CU holds; `busy` is
+// how many of the chip's CUs have one.  Measured over seven shapes from 64 x 2048 x 5632 to 2000 x 2048 x 5632, each tile
+// and 1, 2, 4 and 8 slices: a slab of 256 x 256 takes 1.1 where few CUs work and 1.6 where all do, one of 128 x 128 0.67 alone on
+// its CU and 1.2 beside another, one of 64 x 64 0.34.
 struct TileCost {
     int tile;
-    double slab, ends;
-    int64_t slots;
+    double few, all, ends;
+    int64_t per_cu;
+    double slab(int64_t workgroups) const {
+        if (per_cu > 1) return workgroups > kCUs ? all : few;
+        return few + (all - few) * (workgroups < kCUs ? (double)workgroups / kCUs : 1.0);
+    }
 };
-constexpr TileCost kTileCosts[] = {{TILE_256, 1.6, 9.0, kCUs}, {TILE_128, 1.2, 6.0, 2 * kCUs}, {TILE_64, 0.5, 4.0, kCUs}};
+constexpr TileCost kTileCosts[] = {{TILE_256, 1.08, 1.6, 9.0, 1}, {TILE_128, 0.67, 1.2, 6.0, 2}, {TILE_64, 0.3, 0.34, 5.0, 1}};
 
 // The tile and the cut of least estimated time for one product of m x n, or two (whose tiles are counted together).
 // narrow: few rows go in tiles of 128 x 32.
@@ -121,17 +134,16 @@ inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms, bool
     double least = 1e300;
     const int64_t slabs = ceil_div64(k, 64);
     for (const TileCost& c : kTileCosts) {
-        TileCost t = c;
-        if (narrow && n <= 32) t = TileCost{TILE_32, 0.5, 4.0, kCUs};
-        const int64_t all = tiles(m, n, t.tile) + (m2 ? tiles(m2, n2, t.tile) : 0);
-        const int64_t rounds = all / t.slots, rest = all % t.slots;
-        const double bytes = 4.0 * tile_m(t.tile) * tile_n(t.tile);
-        for (int64_t s = 1; s <= 16 && (s == 1 || (s <= slabs && rest * s <= t.slots)); ++s) {
+        const TileCost t = narrow && n <= 32 ? TileCost{TILE_32, 0.3, 0.34, 4.0, 1} : c;
+        const int64_t slots = kCUs * t.per_cu, all = tiles(m, n, t.tile) + (m2 ? tiles(m2, n2, t.tile) : 0);
+        const int64_t rounds = all / slots, rest = all % slots;
+        const double bytes = 4.0 * (double)(tile_m(t.tile) * tile_n(t.tile));
+        for (int64_t s = 1; s <= 16 && (s == 1 || (s <= slabs && rest * s <= slots)); ++s) {
             const int64_t per = ceil_div64(slabs, s);
             if (s > 1 && ceil_div64(slabs, per) != s) continue;   // a slice without any k
-            double time = (double)rounds * ((double)(slabs * terms) * t.slab + t.ends);
-            if (rest) time += (double)(per * terms) * t.slab + t.ends;
-            if (rest && s > 1) time += 6.0 + (double)(rest * s) * bytes * 0.5e-6;   // sums written and read at 4 TB/s, a launch
+            double time = (double)rounds * ((double)(slabs * terms) * t.slab(slots) + t.ends);
+            if (rest) time += (double)(per * terms) * t.slab(rest * s) + t.ends;
+            if (rest && s > 1) time += 4.5 + (double)(rest * s) * bytes * 0.4e-6;   // a launch, sums written and read
             if (time >= least) continue;
             least = time;
             best.tile = t.tile;
@@ -153,18 +165,25 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
     q.wpack = !bf16 || width != q.dk;
     q.dpack = !bf16 || hidden != q.fk;
     q.ypack = !bf16 || width != q.dk;
-    const int64_t n = rows < 1 ? 1 : rows, terms = bf16 ? 1 : 6;
+    const int64_t n = rows < 1 ? 1 : rows, terms = bf16 ? 1 : 6, scaled = bf16 ? 1 : 3;
     size_t off = 0, acc = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
     auto plan = [&](Product& r, int64_t m, int64_t n, int64_t k, int64_t t, bool narrow, int64_t m2 = 0, int64_t n2 = 0) {
         r = pick_product(m, n, k, t, narrow, m2, n2);
         if (r.acc > acc) acc = r.acc;
     };
-    if (q.xpack) q.x = take(q.parts * n * q.dk * 2);
-    if (q.wpack) q.w = take(q.parts * 2 * q.fk * q.dk * 2);
-    if (q.dpack) q.wd = take(q.parts * width * q.fk * 2);
+    const bool forms = !for_grad || !saved;   // a and b are formed
+    if (bf16 ? q.xpack : for_grad) q.x = take(q.parts * n * q.dk * 2);
+    if (bf16 ? q.wpack : for_grad) q.w = take(q.parts * 2 * q.fk * q.dk * 2);
+    if (bf16 ? q.dpack : !for_grad) q.wd = take(q.parts * width * q.fk * 2);
+    if (!bf16 && forms) {
+        q.x16 = take(2 * n * q.dk * 2);
+        q.w16 = take(2 * 2 * q.fk * q.dk * 2);
+        q.xinv = take(scale_rows(n) * 4);
+        q.winv = take(2 * scale_rows(q.fk) * 4);
+    }
     q.u = take(q.parts * n * q.fk * 2);
-    plan(q.gu, 2 * q.fk, n, width, terms, true);
+    plan(q.gu, 2 * q.fk, n, width, scaled, true);
     if (!for_grad) {
         plan(q.y, width, n, hidden, terms, true);
     } else {
@@ -173,8 +192,14 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
             q.up = take(n * hidden * (bf16 ? 2 : 4));
         }
         if (q.ypack) q.dy = take(q.parts * n * q.dk * 2);
+        if (!bf16) {
+            q.wd16 = take(2 * width * q.fk * 2);
+            q.dy16 = take(2 * n * q.dk * 2);
+            q.dinv = take(scale_rows(q.dk) * 4);
+            q.yinv = take(scale_rows(n) * 4);
+        }
         q.dab = take(q.parts * n * 2 * q.fk * 2);
-        plan(q.du, q.fk, n, width, terms, true);
+        plan(q.du, q.fk, n, width, scaled, true);
         plan(q.dx, width, n, q.wpack ? 2 * q.fk : hidden, q.wpack ? terms : 2, true);   // (in place: two terms of hidden)
         plan(q.dgu, width, 2 * q.fk, n, terms, false);
         plan(q.dd, hidden, width, n, terms, false);

@@ -8,9 +8,11 @@
 // and u.  Then dX is one product over both, and so are dWg and dWu.  Every product runs along the contiguous dimension of
 // its output in the matrix core's rows, as in cross_entropy.hip.
 //
-// bf16 operands multiply as they are, in place where rows are a multiple of 64 elements; fp32 operands as three bf16 parts
-// in planes in the workspace.  Where the tiles are too few for the chip, the reductions are sliced: the partial sums are
-// stored, and a pass over them takes the epilogue's place.
+// bf16 operands multiply as they are, in place where rows are a multiple of 64 elements.  fp32 operands go through planes in
+// the workspace: a, b and du as two fp16 parts of each row scaled by a power of two (three products; Wd's rows run along du's
+// reduction, so their scales go into dY), the other products as three bf16 parts (six products), since the rows of u, da and db
+// that they would be scaled by are not known when they are formed.  Where tiles are left over that do not fill the chip, their
+// reductions are sliced: the partial sums are stored, and a pass over them takes the epilogue's place.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -60,12 +62,16 @@ __device__ __forceinline__ float activate(int act, float a, float& slope) {
 // ---------------------------------------------------------------------------
 // Planes
 // ---------------------------------------------------------------------------
-// Rows [rows][d] of a matrix to bf16 planes [PARTS][plane] with `all` rows of kp elements, zeros behind the matrix; kind: 0
-// fp32, 1 bf16, 2 e4m3 with a scale per row.
+// Rows [rows][d] of a matrix to planes with `all` rows of kp elements, zeros behind the matrix; kind: 0 fp32, 1 bf16, 2 e4m3
+// with a scale per row.  out: PARTS bf16 planes, or null.  out16: two fp16 ones of the row times a power of two, whose inverse
+// goes to inv, and times fold[column] first where that is given; or null.
 struct PackJob {
     const void* in;
     const float* scale;
+    const float* fold;
     uint16_t* out;
+    uint16_t* out16;
+    float* inv;
     int64_t rows, all, plane;
     int kind, d, kp;
     unsigned first;   // its first workgroup
@@ -77,6 +83,41 @@ struct PackJobs {
     unsigned blocks;
 };
 
+__device__ __forceinline__ void load_any8(const PackJob& job, int64_t row, int c, int d, float s, float (&v)[8]) {
+    if (job.kind == 0) {
+        load8<false>(job.in, row, c, d, v);
+    } else if (job.kind == 1) {
+        load8<true>(job.in, row, c, d, v);
+    } else {
+        const uint8_t* p = (const uint8_t*)job.in + row + c;
+        uint32_t w[2] = {0, 0};
+        if (c + 8 <= d) {
+            const u32x2_bytes q = *(const u32x2_bytes*)p;
+            w[0] = q[0];
+            w[1] = q[1];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < d) w[e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], true);
+            v[4 * h] = lo[0] * s;
+            v[4 * h + 1] = lo[1] * s;
+            v[4 * h + 2] = hi[0] * s;
+            v[4 * h + 3] = hi[1] * s;
+        }
+    }
+}
+
+__device__ __forceinline__ void fold8(const PackJob& job, int c, int d, float (&v)[8]) {
+    if (!job.fold) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c + e < d) v[e] *= job.fold[c + e];
+}
+
 // A wave per row, four of a matrix to a workgroup.
 template <int PARTS>
 __global__ __launch_bounds__(256) void planes_kernel(PackJobs jobs) {
@@ -85,39 +126,35 @@ __global__ __launch_bounds__(256) void planes_kernel(PackJobs jobs) {
     const PackJob& job = jobs.job[at];
     const int64_t r = (int64_t)(blockIdx.x - job.first) * 4 + (threadIdx.x >> 6);
     if (r >= job.all) return;
-    const int d = r < job.rows ? job.d : 0, kp = job.kp, kind = job.kind;
-    const void* in = job.in;
+    const int d = r < job.rows ? job.d : 0, kp = job.kp, lane = threadIdx.x & 63;
     const float s = job.scale && r < job.rows ? job.scale[r] : 1.f;
     const int64_t row = r * job.d;
+    float scale = 1.f;
+    if (PARTS == 3 && job.out16) {
+        float top = 0.f;
 #pragma unroll 4
-    for (int c = (threadIdx.x & 63) * 8; c < kp; c += 512) {
-        float v[8];
-        if (kind == 0) {
-            load8<false>(in, row, c, d, v);
-        } else if (kind == 1) {
-            load8<true>(in, row, c, d, v);
-        } else {
-            const uint8_t* p = (const uint8_t*)in + row + c;
-            uint32_t w[2] = {0, 0};
-            if (c + 8 <= d) {
-                const u32x2_bytes q = *(const u32x2_bytes*)p;
-                w[0] = q[0];
-                w[1] = q[1];
-            } else {
+        for (int c = lane * 8; c < d; c += 512) {
+            float v[8];
+            load_any8(job, row, c, d, s, v);
+            fold8(job, c, d, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < d) w[e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], true);
-                v[4 * h] = lo[0] * s;
-                v[4 * h + 1] = lo[1] * s;
-                v[4 * h + 2] = hi[0] * s;
-                v[4 * h + 3] = hi[1] * s;
-            }
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
         }
-        store8<PARTS>(job.out, job.plane, r * kp + c, v);
+#pragma unroll
+        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        float inverse;
+        scale = row_scale(top, inverse);
+        if (lane == 0) job.inv[r] = inverse;
+    }
+#pragma unroll 4
+    for (int c = lane * 8; c < kp; c += 512) {
+        float v[8];
+        load_any8(job, row, c, d, s, v);
+        if (job.out) store8<PARTS>(job.out, job.plane, r * kp + c, v);
+        if (PARTS == 3 && job.out16) {
+            fold8(job, c, d, v);
+            store8_f16(job.out16, job.plane, r * kp + c, v, scale);
+        }
     }
 }
 
@@ -249,6 +286,9 @@ struct GatedArgs {
     void* up;
     uint16_t* u;           // planes [PARTS][rows][fk], or null (du)
     uint16_t* dab;         // du: planes [PARTS][rows][2 fk], or null
+    const float* xinv;     // fp32: what the sums of a row are multiplied by,
+    const float* winv;     // and those of a column (a, and `winv_b` on b), du: null
+    int winv_b;
 };
 
 // a and b as the gradient is handed them, for bf16 operands: 16 bits, a sign and either, for magnitudes in [2^-8, 2^8), a set
@@ -503,6 +543,7 @@ struct Gated : Single {
         constexpr int H = C::MI % 4 == 0 ? 2 : 1;
         const GatedRows<PARTS> to(g, n0);
         const int c0 = (m0 + l.xa) / 2;
+        const float x = PARTS == 1 ? 1.f : g.xinv[n0 + l.row];
 #pragma unroll
         for (int i = 0; i < C::MI; i += 2 * H) {
             float a[H][4], b[H][4];
@@ -510,6 +551,15 @@ struct Gated : Single {
             for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) { a[h][e] = v[i + 2 * h][e]; b[h][e] = v[i + 2 * h + 1][e]; }
+            if constexpr (PARTS != 1) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const float* w = g.winv + c0 + 8 * i + 16 * h + 4 * l.quarter;
+                    const f32x4 wa = *(const f32x4*)w, wb = *(const f32x4*)(w + g.winv_b);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { a[h][e] = a[h][e] * x * wa[e]; b[h][e] = b[h][e] * x * wb[e]; }
+                }
+            }
             gated<PARTS, H, EDGE>(g, to, Spot{l.row, c0 + 8 * i, l.quarter}, a, b);
         }
     }
@@ -526,6 +576,7 @@ struct Dgated : Single {
     template <class C, bool EDGE>
     __device__ __forceinline__ void column(int, int m0, int n0, const Lane& l, const f32x4 (&v)[C::MI]) const {
         const GatedRows<PARTS> to(g, n0);
+        const float x = PARTS == 1 ? 1.f : g.xinv[n0 + l.row];
         Raw<PARTS> ra[C::MI / 2], rb[C::MI / 2];
 #pragma unroll
         for (int i = 0; i < C::MI; i += 2) {
@@ -541,7 +592,7 @@ struct Dgated : Single {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) du[h][e] = v[i + h][e];
+                for (int e = 0; e < 4; ++e) du[h][e] = PARTS == 1 ? v[i + h][e] : v[i + h][e] * x;
             dgated<PARTS, EDGE>(g, to, Spot{l.row, m0 + l.xa + 16 * i, l.quarter}, du, a, b);
         }
     }
@@ -632,17 +683,12 @@ __global__ __launch_bounds__(256) void zeros_kernel(uint16_t* p, int64_t n) {
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-template <bool TA, bool TB, bool PAIR> using C256 = mm::Config<256, 256, 2, 4, 2, TA, TB, false, PAIR>;
-template <bool TA, bool TB, bool PAIR> using C128 = mm::Config<128, 128, 2, 2, 2, TA, TB, false, PAIR>;
-template <bool TA, bool TB, bool PAIR> using C64 = mm::Config<64, 64, 2, 2, 8, TA, TB, false, PAIR>;
-template <bool TA, bool TB, bool PAIR> using C32 = mm::Config<128, 32, 4, 1, 4, TA, TB, false, PAIR>;
-
-template <bool TA, bool TB, bool PAIR, class F>
+template <bool TA, bool TB, bool F16, bool PAIR, class F>
 void of_tile(int tile, F f) {
-    if (tile == TILE_256) f(C256<TA, TB, PAIR>());
-    else if (tile == TILE_128) f(C128<TA, TB, PAIR>());
-    else if (tile == TILE_64) f(C64<TA, TB, PAIR>());
-    else if constexpr (!TB) f(C32<TA, TB, PAIR>());
+    if (tile == TILE_256) f(mm::Config<256, 256, 2, 4, 2, TA, TB, F16, PAIR>());
+    else if (tile == TILE_128) f(mm::Config<128, 128, 2, 2, 2, TA, TB, F16, PAIR>());   // two workgroups to a CU
+    else if (tile == TILE_64) f(mm::Config<64, 64, 2, 2, 8, TA, TB, F16, PAIR>());
+    else if constexpr (!TB) f(mm::Config<128, 32, 4, 1, 4, TA, TB, F16, PAIR>());
 }
 
 template <class C, class P>
@@ -653,60 +699,98 @@ void launch(const P& p, const Product& r, mm::Segments seg, float* acc, hipStrea
     if (c.rem) hipLaunchKernelGGL((join_kernel<C, P>), dim3((unsigned)(c.rem * C::NI)), dim3(C::THREADS), 0, s, p, c, acc);
 }
 
+template <bool GRAD, int PARTS>
+void launch_gated(const GatedArgs& g, const Product& r, mm::Segments seg, float* acc, hipStream_t s) {
+    using P = typename std::conditional<GRAD, Dgated<PARTS>, Gated<PARTS>>::type;
+    of_tile<GRAD, false, PARTS != 1, !GRAD>(r.tile, [&](auto c) { launch<decltype(c)>(P(g), r, seg, acc, s); });
+}
+
 template <bool GRAD>
-void launch_gated(const GatedArgs& g, const Product& r, int parts, mm::Segments seg, float* acc, hipStream_t s) {
-    of_tile<GRAD, false, !GRAD>(r.tile, [&](auto c) {
-        using C = decltype(c);
-        if constexpr (GRAD) {
-            if (parts == 1) launch<C>(Dgated<1>(g), r, seg, acc, s);
-            else launch<C>(Dgated<3>(g), r, seg, acc, s);
-        } else {
-            if (parts == 1) launch<C>(Gated<1>(g), r, seg, acc, s);
-            else launch<C>(Gated<3>(g), r, seg, acc, s);
-        }
-    });
+void launch_gated(const GatedArgs& g, const Product& r, int parts, float* acc, hipStream_t s) {
+    if (parts == 1) launch_gated<GRAD, 1>(g, r, segments(1, 1), acc, s);
+    else launch_gated<GRAD, 3>(g, r, segments(2, 2), acc, s);
 }
 
 template <bool TA, bool TB, int N>
 void launch_out(const Out<N>& o, const Product& r, mm::Segments seg, float* acc, hipStream_t s) {
-    of_tile<TA, TB, false>(r.tile, [&](auto c) { launch<decltype(c)>(o, r, seg, acc, s); });
+    of_tile<TA, TB, false, false>(r.tile, [&](auto c) { launch<decltype(c)>(o, r, seg, acc, s); });
 }
 
-// A matrix in place, or as planes in the workspace that a job fills.
-mm::Operand operand(const void* in, const float* scale, int kind, bool pack, int64_t rows, int64_t all, int64_t d, uint16_t* out,
-                    int64_t plane, PackJobs* jobs) {
-    const int64_t kp = ceil_div64(d, 64) * 64;
-    if (!pack) return mm::Operand{(const uint16_t*)in, 0, d, (int)rows};
-    jobs->job[jobs->n++] = PackJob{in, scale, out, rows, all, plane, kind, (int)d, (int)kp, jobs->blocks};
-    jobs->blocks += (unsigned)ceil_div64(all, 4);
-    return mm::Operand{out, plane, kp, (int)rows};
+// Planes that a job fills: bf16 ones, fp16 ones, or both.
+void pack(PackJobs& jobs, PackJob job) {
+    if (job.all == 0) job.all = job.rows;
+    job.kp = (job.d + 63) / 64 * 64;
+    job.first = jobs.blocks;
+    jobs.job[jobs.n++] = job;
+    jobs.blocks += (unsigned)ceil_div64(job.all, 4);
+}
+
+void launch_pack(const PackJobs& jobs, int parts, hipStream_t s) {
+    if (jobs.n == 0) return;
+    if (parts == 1) hipLaunchKernelGGL((planes_kernel<1>), dim3(jobs.blocks), dim3(256), 0, s, jobs);
+    else hipLaunchKernelGGL((planes_kernel<3>), dim3(jobs.blocks), dim3(256), 0, s, jobs);
 }
 
 struct Inputs {
-    mm::Operand x, w, wd, dy;   // w: Wg's rows and, `pair` elements on, Wu's
-    mm::Segments seg;
+    mm::Operand x, w, wd, dy;           // parts of X, of Wg and, `pair` elements on, Wu, of Wd, of dY
+    mm::Operand x16, w16, wd16, dy16;   // what a, b and du are formed from: fp16 planes for fp32, else the same
 };
 
-Inputs inputs(const FfnArgs& a, const FfnPlan& p, char* ws, bool need_x, bool need_w, hipStream_t s) {
+// The operands of the products that are asked for: forms: a and b, out: Y, dx, dgu and dd: the gradients.
+Inputs inputs(const FfnArgs& a, const FfnPlan& p, char* ws, bool forms, bool out, hipStream_t s) {
     Inputs in{};
     PackJobs jobs{};
-    const int kind = a.bf16 ? 1 : 0;
-    in.seg = segments(p.parts, p.parts);
-    if (need_x)
-        in.x = operand(a.X, a.x_scale, a.x_scale ? 2 : kind, p.xpack, p.t, p.t, p.d, (uint16_t*)(ws + p.x), p.t * p.dk, &jobs);
-    uint16_t* w = (uint16_t*)(ws + p.w);
-    const int64_t plane = 2 * p.fk * p.dk;
-    if (need_w) {
-        in.w = operand(a.Wg, nullptr, kind, p.wpack, p.f, p.fk, p.d, w, plane, &jobs);
-        if (p.wpack) operand(a.Wu, nullptr, kind, true, p.f, p.fk, p.d, w + p.fk * p.dk, plane, &jobs);
-        in.w.pair = p.wpack ? p.fk * p.dk : ((intptr_t)a.Wu - (intptr_t)a.Wg) / 2;
+    const int kind = a.bf16 ? 1 : 0, t = (int)p.t, d = (int)p.d, f = (int)p.f;
+    auto at = [&](size_t off) { return (uint16_t*)(ws + off); };
+    auto inverse = [&](size_t off) { return (float*)(ws + off); };
+    const int64_t wplane = 2 * p.fk * p.dk, wpair = p.fk * p.dk;
+    const int xkind = a.x_scale ? 2 : kind;
+    if (a.bf16) {
+        in.x = mm::Operand{(const uint16_t*)a.X, 0, p.d, t};
+        if (p.xpack && (forms || a.dWg)) {
+            pack(jobs, {a.X, a.x_scale, nullptr, at(p.x), nullptr, nullptr, t, 0, p.t * p.dk, xkind, d});
+            in.x = mm::Operand{at(p.x), p.t * p.dk, p.dk, t};
+        }
+        in.w = mm::Operand{(const uint16_t*)a.Wg, 0, p.d, f, ((intptr_t)a.Wu - (intptr_t)a.Wg) / 2};
+        if (p.wpack && (forms || a.dX)) {
+            pack(jobs, {a.Wg, nullptr, nullptr, at(p.w), nullptr, nullptr, f, p.fk, wplane, kind, d});
+            pack(jobs, {a.Wu, nullptr, nullptr, at(p.w) + wpair, nullptr, nullptr, f, p.fk, wplane, kind, d});
+            in.w = mm::Operand{at(p.w), wplane, p.dk, f, wpair};
+        }
+        in.wd = mm::Operand{(const uint16_t*)a.Wd, 0, p.f, d};
+        if (p.dpack) {
+            pack(jobs, {a.Wd, nullptr, nullptr, at(p.wd), nullptr, nullptr, d, 0, p.d * p.fk, kind, f});
+            in.wd = mm::Operand{at(p.wd), p.d * p.fk, p.fk, d};
+        }
+        in.dy = mm::Operand{(const uint16_t*)a.dY, 0, p.d, t};
+        if (p.ypack && a.dY) {
+            pack(jobs, {a.dY, nullptr, nullptr, at(p.dy), nullptr, nullptr, t, 0, p.t * p.dk, kind, d});
+            in.dy = mm::Operand{at(p.dy), p.t * p.dk, p.dk, t};
+        }
+        in.x16 = in.x; in.w16 = in.w; in.wd16 = in.wd; in.dy16 = in.dy;
+        launch_pack(jobs, 1, s);
+        return in;
     }
-    in.wd = operand(a.Wd, nullptr, kind, p.dpack, p.d, p.d, p.f, (uint16_t*)(ws + p.wd), p.d * p.fk, &jobs);
-    if (a.dY) in.dy = operand(a.dY, nullptr, kind, p.ypack, p.t, p.t, p.d, (uint16_t*)(ws + p.dy), p.t * p.dk, &jobs);
-    if (jobs.n > 0) {
-        if (p.parts == 1) hipLaunchKernelGGL((planes_kernel<1>), dim3(jobs.blocks), dim3(256), 0, s, jobs);
-        else hipLaunchKernelGGL((planes_kernel<3>), dim3(jobs.blocks), dim3(256), 0, s, jobs);
+    if (forms || a.dWg)
+        pack(jobs, {a.X, a.x_scale, nullptr, a.dWg ? at(p.x) : nullptr, forms ? at(p.x16) : nullptr, inverse(p.xinv), t, 0,
+                    p.t * p.dk, xkind, d});
+    if (forms || a.dX)
+        for (int i = 0; i < 2; ++i)
+            pack(jobs, {i ? a.Wu : a.Wg, nullptr, nullptr, a.dX ? at(p.w) + i * wpair : nullptr, forms ? at(p.w16) + i * wpair : nullptr,
+                        inverse(p.winv) + i * scale_rows(p.fk), f, p.fk, wplane, kind, d});
+    pack(jobs, {a.Wd, nullptr, nullptr, out ? at(p.wd) : nullptr, out ? nullptr : at(p.wd16), inverse(p.dinv), d, 0, p.d * p.fk, kind, f});
+    launch_pack(jobs, 3, s);
+    if (a.dY) {   // du = (dY / scale of Wd's row) (Wd scaled): behind Wd's scales
+        PackJobs last{};
+        pack(last, {a.dY, nullptr, inverse(p.dinv), a.dWd ? at(p.dy) : nullptr, at(p.dy16), inverse(p.yinv), t, 0, p.t * p.dk, kind, d});
+        launch_pack(last, 3, s);
     }
+    in.x = mm::Operand{at(p.x), p.t * p.dk, p.dk, t};
+    in.w = mm::Operand{at(p.w), wplane, p.dk, f, wpair};
+    in.wd = mm::Operand{at(p.wd), p.d * p.fk, p.fk, d};
+    in.dy = mm::Operand{at(p.dy), p.t * p.dk, p.dk, t};
+    in.x16 = in.x; in.w16 = in.w; in.wd16 = in.wd; in.dy16 = in.dy;
+    in.x16.p = at(p.x16); in.w16.p = at(p.w16); in.wd16.p = at(p.wd16); in.dy16.p = at(p.dy16);
     return in;
 }
 
@@ -716,6 +800,8 @@ GatedArgs gated_args(const FfnArgs& a, const FfnPlan& p, const mm::Operand& w, c
     g.rows = p.t; g.f = (int)p.f; g.fk = (int)p.fk; g.act = a.act;
     g.gate = a.gate; g.up = a.up;
     g.u = (uint16_t*)(ws + p.u);
+    g.xinv = (const float*)(ws + p.xinv); g.winv = (const float*)(ws + p.winv);
+    g.winv_b = (int)scale_rows(p.fk);
     return g;
 }
 
@@ -734,49 +820,52 @@ int run_zeros(void* out, int64_t n, void* stream) {
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
     const Inputs in = inputs(a, p, ws, true, true, s);
+    const mm::Segments seg = segments(p.parts, p.parts);
     float* acc = (float*)(ws + p.acc);
-    launch_gated<false>(gated_args(a, p, in.w, in.x, 2 * p.fk, ws), p.gu, p.parts, in.seg, acc, s);
+    launch_gated<false>(gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws), p.gu, p.parts, acc, s);
     const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
-    launch_out<false, false>(Out<1>(out_args(in.wd, u, p.d, p.t, a.Y, a.bf16, 0)), p.y, in.seg, acc, s);
+    launch_out<false, false>(Out<1>(out_args(in.wd, u, p.d, p.t, a.Y, a.bf16, 0)), p.y, seg, acc, s);
     return (int)hipGetLastError();
 }
 
 int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
     FfnArgs a = args;
-    const Inputs in = inputs(a, p, ws, !a.gate || a.dWg, !a.gate || a.dX, s);
+    const Inputs in = inputs(a, p, ws, !a.gate, false, s);
+    const mm::Segments seg = segments(p.parts, p.parts);
     float* acc = (float*)(ws + p.acc);
     if (!a.gate) {
         a.gate = ws + p.gate;
         a.up = ws + p.up;
-        GatedArgs g = gated_args(a, p, in.w, in.x, 2 * p.fk, ws);
+        GatedArgs g = gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws);
         g.u = nullptr;
-        launch_gated<false>(g, p.gu, p.parts, in.seg, acc, s);
+        launch_gated<false>(g, p.gu, p.parts, acc, s);
     }
-    GatedArgs g = gated_args(a, p, in.wd, in.dy, p.fk, ws);
+    GatedArgs g = gated_args(a, p, in.wd16, in.dy16, p.fk, ws);
+    g.xinv = (const float*)(ws + p.yinv);
     g.dab = a.dX || a.dWg ? (uint16_t*)(ws + p.dab) : nullptr;
     if (!a.dWd) g.u = nullptr;
-    launch_gated<true>(g, p.du, p.parts, in.seg, acc, s);
+    launch_gated<true>(g, p.du, p.parts, acc, s);
     const mm::Operand dab{(uint16_t*)(ws + p.dab), p.t * 2 * p.fk, 2 * p.fk, (int)p.t};
     const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
     if (a.dX) {   // over da and Wg, db and Wu: two planes of one part each in place, one matrix of 2 fk rows where packed
         OutArgs o = out_args(in.w, dab, p.d, p.t, a.dX, a.bf16, 0);
-        mm::Segments seg = in.seg;
+        mm::Segments pairs = seg;
         if (p.wpack) {
             o.o.a.rows = (int)(2 * p.fk);
         } else {
             o.o.a.plane = in.w.pair;
             o.o.b.plane = p.fk;
-            seg = mm::Segments{2, 0 | (1 | 1 << 2) << 4};
+            pairs = mm::Segments{2, 0 | (1 | 1 << 2) << 4};
         }
-        launch_out<true, false>(Out<1>(o), p.dx, seg, acc, s);
+        launch_out<true, false>(Out<1>(o), p.dx, pairs, acc, s);
     }
     OutArgs gu = out_args(in.x, dab, p.d, 2 * p.fk, a.dWg, a.dw_bf16, a.accumulate);
     gu.second = p.fk; gu.valid = p.f; gu.out2 = a.dWu;
     const OutArgs d = out_args(u, in.dy, p.f, p.d, a.dWd, a.dw_bf16, a.accumulate);
-    if (a.dWg && a.dWd) launch_out<true, true>(Out<2>(gu, d), p.dw, in.seg, acc, s);
-    else if (a.dWg) launch_out<true, true>(Out<1>(gu), p.dgu, in.seg, acc, s);
-    else if (a.dWd) launch_out<true, true>(Out<1>(d), p.dd, in.seg, acc, s);
+    if (a.dWg && a.dWd) launch_out<true, true>(Out<2>(gu, d), p.dw, seg, acc, s);
+    else if (a.dWg) launch_out<true, true>(Out<1>(gu), p.dgu, seg, acc, s);
+    else if (a.dWd) launch_out<true, true>(Out<1>(d), p.dd, seg, acc, s);
     return (int)hipGetLastError();
 }
 
