@@ -100,6 +100,7 @@ struct Product {
 };
 struct FfnPlan {
     int64_t t, d, f, dk, fk;
+    bool few;                          // forward: few rows, the weights are read in place by run_ffn_few
     int parts;                         // of the operands that are not fp16 planes: 1 or 3
     bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
     Product gu, y, du, dx, dgu, dd, dw;   // (dw: dgu and dd at once)
@@ -154,6 +155,11 @@ inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms, bool
     return best;
 }
 
+// Forward calls of so few rows read the weights in place (run_ffn_few), more go through tiles.  That way and by tiles: bf16
+// 2048 x 5632 1 row 24 us and 28, 4 rows 26 and 28, 16 rows 32 and 29, 8192 x 8192 4 rows 72 and 99, 16 rows 90 and 100; fp32
+// 2048 x 5632 1 row 45 and 110, 32 rows 79 and 111, 48 rows 120 and 123, 64 rows 139 and 124, 8192 x 8192 48 rows 351 and 652.
+constexpr int64_t kFewRows = 8, kFewRowsF32 = 48;
+
 // for_grad: the gradient; saved: gate and up are given to it
 inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16, int x8, int for_grad, int saved, FfnPlan* p) {
     FfnPlan q{};
@@ -172,6 +178,13 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
         r = pick_product(m, n, k, t, narrow, m2, n2);
         if (r.acc > acc) acc = r.acc;
     };
+    q.few = !for_grad && rows <= (bf16 ? kFewRows : kFewRowsF32);
+    if (q.few) {
+        q.u = take(n * q.fk * (bf16 ? 2 : 4));
+        q.total = off;
+        *p = q;
+        return true;
+    }
     const bool forms = !for_grad || !saved;   // a and b are formed
     if (bf16 ? q.xpack : for_grad) q.x = take(q.parts * n * q.dk * 2);
     if (bf16 ? q.wpack : for_grad) q.w = take(q.parts * 2 * q.fk * q.dk * 2);
@@ -228,6 +241,7 @@ struct FfnArgs {
     int act, bf16, dw_bf16, accumulate;
 };
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
+int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 // nothing but zeros, in n 16-bit words
 int run_zeros(void* out, int64_t n, void* stream);

@@ -1,0 +1,271 @@
+// The gated feed-forward block of few rows: a stream of the three weight matrices, read once and in place, whatever their width.
+//
+//   u = act(X Wg^T) (X Wu^T);  Y = u Wd^T
+//
+// Two launches.  A workgroup has 16 output columns (16 rows of a matrix, or of Wg and of Wu); its waves share the reduction,
+// each with loads of its own straight to registers, many of them under way at once, and their sums meet in LDS.  bf16 goes
+// through v_mfma_f32_16x16x32_bf16, fp32 through v_mfma_f32_16x16x4_f32, whose rate (157 TFLOP/s) is enough for the 2 x 16 NT
+// operations that an element of a matrix is worth here.
+//
+// Bound by the latency of two short kernels: one bf16 row, 2048 x 5632: 12.5 and 8.7 us (69 MB of weights, 14 us at the rate of
+// a large copy), where tiles of 128 x 32 with sliced reductions take 26 in four launches.  8192 x 8192 (403 MB): 72 us, 5.6 TB/s.
+// With 8 instead of 12 steps under way the second kernel takes 11.0 us; waves that take every eighth step instead of a
+// piece of the rows, and twice the workgroups on a CU, measured the same.
+//
+// Lane layout of both: A[l % 16][k of the lane's quarter l / 16], B likewise, D element v of lane l is D[4 (l / 16) + v][l % 16].
+// The order of k is free as long as A and B agree: a quarter takes 16 bytes of a row.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "block_plan.h"
+#include "gate.hpp"
+#include "rows.hpp"
+
+namespace dion {
+
+namespace {
+
+struct FewArgs {
+    const void* w[2];     // [cols][k]
+    const void* x;        // [rows][ldx]
+    const float* scale;   // x in 8 bits, or null
+    int rows, cols, k, ldx;
+    int act;
+    void* out;            // u [rows][ldout] (M == 2), or Y
+    int ldout;
+    void* gate;           // [rows][cols], or null
+    void* up;
+};
+
+template <bool BF16> struct Few;
+template <> struct Few<true> {
+    static constexpr int kStep = 32, kPer = 8;   // k of a step, and of a lane
+    // elements c .. c + 7 of a row, zeros from k on
+    static __device__ __forceinline__ u32x4 load(const void* p, int64_t row, int c, int k) {
+        Raw8<true> r;
+        r.load(p, row, c, k);
+        return r.w[0];
+    }
+    static __device__ __forceinline__ u32x4 load8bit(const void* p, int64_t row, int c, int k, float s) {
+        float v[8];
+        load_e4m3<8>(p, row, c, k, s, v);
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = down16(v[2 * e]) | (down16(v[2 * e + 1]) << 16);
+        return w;
+    }
+    static __device__ __forceinline__ f32x4 mma(const u32x4& a, const u32x4& b, const f32x4& c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(mm::bf16x8, a), __builtin_bit_cast(mm::bf16x8, b), c, 0, 0, 0);
+    }
+};
+template <> struct Few<false> {
+    static constexpr int kStep = 16, kPer = 4;
+    static __device__ __forceinline__ u32x4 load(const void* p, int64_t row, int c, int k) {
+        const float* q = (const float*)p + row + c;
+        if (c + 4 <= k) return __builtin_bit_cast(u32x4, (f32x4)*(const f32x4_any*)q);
+        u32x4 w{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < k) w[e] = __float_as_uint(q[e]);
+        return w;
+    }
+    static __device__ __forceinline__ u32x4 load8bit(const void* p, int64_t row, int c, int k, float s) {
+        float v[4];
+        load_e4m3<4>(p, row, c, k, s, v);
+        return u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    }
+    static __device__ __forceinline__ f32x4 mma(const u32x4& a, const u32x4& b, f32x4 c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Four columns of a row of `d` elements at any element's address: bf16 or fp32.
+template <bool BF16>
+__device__ __forceinline__ void put4(void* p, int64_t row, int c, int d, const float (&v)[4]) {
+    if (c + 4 <= d) {
+        if constexpr (BF16)
+            *(u32x2_any*)((uint16_t*)p + row + c) = u32x2{down16(v[0]) | (down16(v[1]) << 16), down16(v[2]) | (down16(v[3]) << 16)};
+        else
+            *(f32x4_any*)((float*)p + row + c) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (c + e >= d) continue;
+            if constexpr (BF16) ((uint16_t*)p)[row + c + e] = (uint16_t)down16(v[e]);
+            else ((float*)p)[row + c + e] = v[e];
+        }
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void keep4(void* p, int64_t row, int c, int d, const float (&v)[4]) {
+    if constexpr (BF16) {
+        const uint32_t w[2] = {keep32(v[0], v[1]), keep32(v[2], v[3])};
+        if (c + 4 <= d) {
+            *(u32x2_any*)((uint16_t*)p + row + c) = u32x2{w[0], w[1]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < d) ((uint16_t*)p)[row + c + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+        }
+    } else {
+        put4<false>(p, row, c, d, v);
+    }
+}
+
+// f(n) of a number that is known when it runs, 1 .. N, or nothing for 0
+template <int N, class F>
+__device__ __forceinline__ void rest(int n, F f) {
+    if constexpr (N > 0) {
+        if (n == N) f(std::integral_constant<int, N>());
+        else rest<N - 1>(n, f);
+    }
+}
+
+// M: matrices (2: Wg and Wu); NT: blocks of 16 rows of x; X8: which has 8 bits; WAVES share the reduction.
+template <bool BF16, int M, int NT, bool X8, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
+    using T = Few<BF16>;
+    constexpr int U = M + NT <= 2 ? 12 : M + NT <= 3 ? 8 : 4;   // steps under way, as many as the registers hold
+    __shared__ __attribute__((aligned(16))) f32x4 sums[WAVES][M * NT][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c0 = blockIdx.x * 16, steps = a.k / T::kStep, per = (steps + WAVES - 1) / WAVES;
+    const int first = wave * per, last = first + per < steps ? first + per : steps;
+    const int col = c0 + lane % 16 < a.cols ? c0 + lane % 16 : a.cols - 1;   // (columns and rows behind the last: any, not stored)
+    const int64_t wrow = (int64_t)col * a.k;
+    int64_t xrow[NT];
+    float s[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int r = 16 * j + lane % 16 < a.rows ? 16 * j + lane % 16 : a.rows - 1;
+        xrow[j] = (int64_t)r * a.ldx;
+        s[j] = X8 ? a.scale[r] : 1.f;
+    }
+    f32x4 sum[M][NT] = {};
+    const auto batch = [&](int at, auto count) {
+        constexpr int N = decltype(count)::value;
+        u32x4 w[N][M], x[N][NT];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (at + i) * T::kStep + lane / 16 * T::kPer;
+#pragma unroll
+            for (int m = 0; m < M; ++m) w[i][m] = T::load(a.w[m], wrow, c, 0x7fffffff);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x[i][j] = X8 ? T::load8bit(a.x, xrow[j], c, 0x7fffffff, s[j]) : T::load(a.x, xrow[j], c, 0x7fffffff);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {   // all of them under way before the first is used
+#pragma unroll
+            for (int m = 0; m < M; ++m) asm volatile("" : "+v"(w[i][m]));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(x[i][j]));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sum[m][j] = T::mma(w[i][m], x[i][j], sum[m][j]);
+    };
+    int at = first;
+    for (; at + U <= last; at += U) batch(at, std::integral_constant<int, U>());
+    rest<U - 1>(last - at, [&](auto count) { batch(at, count); });
+    if (wave == WAVES - 1 && a.k % T::kStep != 0) {   // the step at the rows' end
+        const int c = steps * T::kStep + lane / 16 * T::kPer;
+        u32x4 w[M], x[NT];
+#pragma unroll
+        for (int m = 0; m < M; ++m) w[m] = T::load(a.w[m], wrow, c, a.k);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) x[j] = X8 ? T::load8bit(a.x, xrow[j], c, a.k, s[j]) : T::load(a.x, xrow[j], c, a.k);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) sum[m][j] = T::mma(w[m], x[j], sum[m][j]);
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sums[wave][m * NT + j][lane] = sum[m][j];
+    __syncthreads();
+    if (wave >= NT) return;
+    f32x4 t[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        t[m] = sums[0][m * NT + wave][lane];
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) t[m] += sums[i][m * NT + wave][lane];
+    }
+    const int64_t row = 16 * wave + lane % 16;
+    const int c = c0 + 4 * (lane / 16);
+    if (row >= a.rows) return;
+    float v[4];
+    if constexpr (M == 2) {
+        float p[4], q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float slope;
+            p[e] = t[0][e];
+            q[e] = t[M - 1][e];
+            v[e] = activate<!BF16>(a.act, p[e], slope) * q[e];
+        }
+        if (a.gate) {
+            keep4<BF16>(a.gate, row * a.cols, c, a.cols, p);
+            keep4<BF16>(a.up, row * a.cols, c, a.cols, q);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = t[0][e];
+    }
+    put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
+}
+
+template <bool BF16, int M, int NT>
+void launch_few(const FewArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div64(a.cols, 16));
+    if constexpr (M == 2) {
+        if (a.scale) hipLaunchKernelGGL((few_kernel<BF16, 2, NT, true, 8>), grid, dim3(512), 0, s, a);
+        else hipLaunchKernelGGL((few_kernel<BF16, 2, NT, false, 8>), grid, dim3(512), 0, s, a);
+    } else {   // (twice the waves for each where half the chip's CUs are without a workgroup)
+        if (grid.x < kCUs) hipLaunchKernelGGL((few_kernel<BF16, 1, NT, false, 16>), grid, dim3(1024), 0, s, a);
+        else hipLaunchKernelGGL((few_kernel<BF16, 1, NT, false, 8>), grid, dim3(512), 0, s, a);
+    }
+}
+
+template <bool BF16, int M>
+void launch_few(const FewArgs& a, hipStream_t s) {
+    if (BF16 || a.rows <= 16) launch_few<BF16, M, 1>(a, s);
+    else if constexpr (!BF16) {
+        if (a.rows <= 32) launch_few<false, M, 2>(a, s);
+        else launch_few<false, M, 4>(a, s);
+    }
+}
+
+}  // namespace
+
+int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
+    const hipStream_t s = (hipStream_t)stream;
+    FewArgs g{};
+    g.w[0] = a.Wg; g.w[1] = a.Wu; g.x = a.X; g.scale = a.x_scale;
+    g.rows = (int)p.t; g.cols = (int)p.f; g.k = (int)p.d; g.ldx = (int)p.d; g.act = a.act;
+    g.out = ws + p.u; g.ldout = (int)p.fk; g.gate = a.gate; g.up = a.up;
+    FewArgs d{};
+    d.w[0] = a.Wd; d.x = ws + p.u;
+    d.rows = (int)p.t; d.cols = (int)p.d; d.k = (int)p.f; d.ldx = (int)p.fk;
+    d.out = a.Y; d.ldout = (int)p.d;
+    if (a.bf16) {
+        launch_few<true, 2>(g, s);
+        launch_few<true, 1>(d, s);
+    } else {
+        launch_few<false, 2>(g, s);
+        launch_few<false, 1>(d, s);
+    }
+    return (int)hipGetLastError();
+}
+
+}  // namespace dion

@@ -62,6 +62,34 @@ __device__ __forceinline__ void put8(void* p, int64_t row, int c, int d, const f
     }
 }
 
+// N (4 or 8) 8-bit numbers (e4m3) of a row from column c, times s; zeros from column d on
+template <int N>
+__device__ __forceinline__ void load_e4m3(const void* in, int64_t row, int c, int d, float s, float (&v)[N]) {
+    const uint8_t* p = (const uint8_t*)in + row + c;
+    uint32_t w[2] = {0, 0};
+    if (c + N <= d) {
+        if constexpr (N == 8) {
+            const u32x2_bytes q = *(const u32x2_bytes*)p;
+            w[0] = q[0];
+            w[1] = q[1];
+        } else {
+            __builtin_memcpy(w, p, 4);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (c + e < d) w[e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
+    }
+#pragma unroll
+    for (int h = 0; h < N / 4; ++h) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], true);
+        v[4 * h] = lo[0] * s;
+        v[4 * h + 1] = lo[1] * s;
+        v[4 * h + 2] = hi[0] * s;
+        v[4 * h + 3] = hi[1] * s;
+    }
+}
+
 }  // namespace
 
 }  // namespace dion
