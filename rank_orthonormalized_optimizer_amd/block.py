@@ -24,24 +24,34 @@ E4M3 = torch.float8_e4m3fn
 _ACT = {"silu": _lib.SILU, "gelu": _lib.GELU}
 
 
-def _no_graph(call: str, gradient: str, **tensors) -> None:
+def _no_graph(call: str, gradient: str, *tensors) -> None:
     if torch.is_grad_enabled():
-        for name, t in tensors.items():
+        for name, t in tensors:
             if isinstance(t, torch.Tensor) and t.requires_grad:
                 raise ValueError(f"{call} records no graph, but {name} requires a gradient: call it under torch.no_grad() "
                                  f"or detach {name}, and {gradient} for the gradient")
+
+
+def _check(t, name: str, dtypes, device, shape) -> None:
+    """_need on a tensor that is nearly always right: small calls take as long as their checks."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _need(t, name, dtypes, device, shape)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_I64 = (torch.int64,)
+
+
 def _seed(seed, p: float, device):
-    if seed is None:
-        if p != 0:
-            raise ValueError("dropout needs a seed: an int64 GPU tensor of one element")
+    if p == 0:   # it is not read
         return None
-    _need(seed, "seed", (torch.int64,), device)
+    if seed is None:
+        raise ValueError("dropout needs a seed: an int64 GPU tensor of one element")
+    _need(seed, "seed", _I64, device)
     if seed.numel() != 1:
         raise ValueError(f"seed has shape {tuple(seed.shape)}, expected one element")
     return seed.data_ptr()
@@ -62,16 +72,16 @@ def dropout_(x: torch.Tensor, p: float, seed: torch.Tensor | None = None, site: 
     residual's type, else x's); out may be residual.  The gradient of x is the same call, without residual,
     on the output's gradient.
     """
-    _no_graph("dropout_", "dropout_ of the output's gradient", x=x, residual=residual, out=out)
+    _no_graph("dropout_", "dropout_ of the output's gradient", ("x", x), ("residual", residual), ("out", out))
     _need(x, "x", _DT)
-    device = x.device
+    device, shape = x.device, x.shape
     with _On(device, stream) as handle:
         if residual is not None:
-            _need(residual, "residual", _DT, device, x.shape)
+            _check(residual, "residual", _DT, device, shape)
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype if residual is None else residual.dtype, device=device)
+            out = torch.empty_like(x if residual is None else residual)
         else:
-            _need(out, "out", _DT if residual is None else (residual.dtype,), device, x.shape)
+            _check(out, "out", _DT if residual is None else (residual.dtype,), device, shape)
         st = _lib.load().dion_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), x.numel(), float(p),
                                       _seed(seed, p, device), int(site), _DT[x.dtype], _DT[out.dtype], handle)
     if st != _lib.OK:
@@ -79,37 +89,44 @@ def dropout_(x: torch.Tensor, p: float, seed: torch.Tensor | None = None, site: 
     return out
 
 
+_F32 = (torch.float32,)
+_Q8 = (E4M3,)
+
+
 def _norm(call, x, w, eps, residual, p, seed, site, h, y, scale, rstd, eight, stream):
-    _no_graph(call, "rms_norm_grad_", x=x, w=w, residual=residual)
+    _no_graph(call, "rms_norm_grad_", ("x", x), ("w", w), ("residual", residual))
     _need(x, "x", _DT)
-    device = x.device
+    device, shape = x.device, x.shape
     rows, width = _rows(x, "x")
-    _need(w, "w", _DT, device, (width,))
+    _check(w, "w", _DT, device, shape[-1:])
     with _On(device, stream) as handle:
         if residual is not None:
-            _need(residual, "residual", _DT, device, x.shape)
-        s_dtype = x.dtype if residual is None else residual.dtype
+            _check(residual, "residual", _DT, device, shape)
+        like = x if residual is None else residual   # the stream
         if h is not None:
-            _need(h, "h", _DT if residual is None else (s_dtype,), device, x.shape)
-            s_dtype = h.dtype
+            _check(h, "h", _DT if residual is None else (residual.dtype,), device, shape)
+            like = h
         elif residual is not None or p != 0:
-            h = torch.empty(x.shape, dtype=s_dtype, device=device)
+            h = torch.empty_like(like)
         if y is None:
-            y = torch.empty(x.shape, dtype=E4M3 if eight else x.dtype, device=device)
+            y = torch.empty_like(x, dtype=E4M3) if eight else torch.empty_like(x)
         else:
-            _need(y, "out", (E4M3,) if eight else _DT, device, x.shape)
-        per_row = x.shape[:-1]
-        if eight and scale is None:
-            scale = torch.empty(per_row, dtype=torch.float32, device=device)
-        elif eight:
-            _need(scale, "scale", (torch.float32,), device, per_row)
+            _check(y, "out", _Q8 if eight else _DT, device, shape)
+        per_row = shape[:-1]
+        if eight:
+            if scale is None:
+                scale = x.new_empty(per_row, dtype=torch.float32)
+            else:
+                _check(scale, "scale", _F32, device, per_row)
         if rstd is None:
-            rstd = torch.empty(per_row, dtype=torch.float32, device=device)
+            rstd = x.new_empty(per_row, dtype=torch.float32)
         else:
-            _need(rstd, "rstd", (torch.float32,), device, per_row)
-        st = _lib.load().dion_rms_norm(x.data_ptr(), _ptr(residual), w.data_ptr(), _ptr(h), y.data_ptr(), _ptr(scale),
-                                       rstd.data_ptr(), rows, width, float(eps), float(p), _seed(seed, p, device), int(site),
-                                       _DT[x.dtype], _DT[s_dtype], _DT[w.dtype], _lib.E4M3 if eight else _DT[y.dtype], handle)
+            _check(rstd, "rstd", _F32, device, per_row)
+        st = _lib.load().dion_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(), w.data_ptr(),
+                                       None if h is None else h.data_ptr(), y.data_ptr(),
+                                       scale.data_ptr() if eight else None, rstd.data_ptr(), rows, width, eps, p,
+                                       _seed(seed, p, device), site, _DT[x.dtype], _DT[like.dtype], _DT[w.dtype],
+                                       _lib.E4M3 if eight else _DT[y.dtype], handle)
     if st != _lib.OK:
         raise _lib.DionError(st, "dion_rms_norm")
     return y, scale, x if h is None else h, rstd
@@ -157,24 +174,24 @@ def rms_norm_grad_(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: tor
     or bfloat16, written, or added to with ``accumulate``.
     """
     _need(dY, "dY", _DT)
-    device = dY.device
+    device, shape = dY.device, dY.shape
     rows, width = _rows(dY, "dY")
-    _need(h, "h", _DT, device, dY.shape)
-    _need(w, "w", _DT, device, (width,))
-    _need(rstd, "rstd", (torch.float32,), device, dY.shape[:-1])
+    _check(h, "h", _DT, device, shape)
+    _check(w, "w", _DT, device, shape[-1:])
+    _check(rstd, "rstd", _F32, device, shape[:-1])
     if dsum is not None:
-        _need(dsum, "dsum", (h.dtype,), device, h.shape)
+        _check(dsum, "dsum", (h.dtype,), device, shape)
     if dw is not None:
-        _need(dw, "dw", _DT, device, (width,))
+        _check(dw, "dw", _DT, device, shape[-1:])
     with _On(device, stream) as handle:
         if dh is None:
-            dh = torch.empty(h.shape, dtype=h.dtype, device=device)
+            dh = torch.empty_like(h)
         else:
-            _need(dh, "dh", (h.dtype,), device, h.shape)
+            _check(dh, "dh", (h.dtype,), device, shape)
         if dx is not None:
-            _need(dx, "dx", (dY.dtype,), device, dY.shape)
+            _check(dx, "dx", (dY.dtype,), device, shape)
         elif p != 0:
-            dx = torch.empty(dY.shape, dtype=dY.dtype, device=device)
+            dx = torch.empty_like(dY)
         if dw is None:
             ws = None
         elif workspace is None:
@@ -205,13 +222,13 @@ def _block(X, Wg, Wu, Wd, act, scale):
         raise ValueError(f"Wg must be a matrix [hidden, width], got shape {tuple(Wg.shape)}")
     hidden, width = Wg.shape
     device, dtype = Wg.device, Wg.dtype
-    _need(Wu, "Wu", (dtype,), device, Wg.shape)
-    _need(Wd, "Wd", (dtype,), device, (width, hidden))
-    _need(X, "X", (dtype,) if scale is None else (E4M3,), device)
+    _check(Wu, "Wu", (dtype,), device, Wg.shape)
+    _check(Wd, "Wd", (dtype,), device, (width, hidden))
+    _need(X, "X", (dtype,) if scale is None else _Q8, device)
     if X.dim() < 1 or X.shape[-1] != width:
         raise ValueError(f"X has shape {tuple(X.shape)}, expected [..., {width}]")
     if scale is not None:
-        _need(scale, "scale", (torch.float32,), device, X.shape[:-1])
+        _check(scale, "scale", _F32, device, X.shape[:-1])
     if act not in _ACT:
         raise ValueError(f"act is {act!r}, expected one of {tuple(_ACT)}")
     return X.numel() // width, width, hidden, _DT[dtype], _DT[dtype] if scale is None else _lib.E4M3
@@ -228,19 +245,19 @@ def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Te
     projections (for bfloat16 their bits are a 16-bit form of its own, described in dion_block.h, not bfloat16 numbers).
     Returns (or fills) out, [..., width] of the weights' type.
     """
-    _no_graph("gated_ffn_", "gated_ffn_grad_", X=X, Wg=Wg, Wu=Wu, Wd=Wd, out=out)
+    _no_graph("gated_ffn_", "gated_ffn_grad_", ("X", X), ("Wg", Wg), ("Wu", Wu), ("Wd", Wd), ("out", out))
     rows, width, hidden, dt, xt = _block(X, Wg, Wu, Wd, act, scale)
     device, dtype, inner = Wg.device, Wg.dtype, X.shape[:-1] + (hidden,)
     if (gate is None) != (up is None):
         raise ValueError("gate and up are kept together: give both or neither")
     if gate is not None:
-        _need(gate, "gate", (dtype,), device, inner)
-        _need(up, "up", (dtype,), device, inner)
+        _check(gate, "gate", (dtype,), device, inner)
+        _check(up, "up", (dtype,), device, inner)
     with _On(device, stream) as handle:
         if out is None:
-            out = torch.empty(X.shape, dtype=dtype, device=device)
+            out = torch.empty_like(X, dtype=dtype)
         else:
-            _need(out, "out", (dtype,), device, X.shape)
+            _check(out, "out", (dtype,), device, X.shape)
         ws = gated_ffn_workspace_for(rows, width, hidden, device, dtype, x_dtype=X.dtype) if workspace is None \
             else _given_scratch(workspace, device)
         st = _lib.load().dion_gated_ffn(X.data_ptr(), _ptr(scale), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), _ptr(gate),
@@ -264,12 +281,12 @@ def gated_ffn_grad_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: tor
     """
     rows, width, hidden, dt, xt = _block(X, Wg, Wu, Wd, act, scale)
     device, dtype, inner = Wg.device, Wg.dtype, X.shape[:-1] + (hidden,)
-    _need(dY, "dY", (dtype,), device, X.shape)
+    _check(dY, "dY", (dtype,), device, X.shape)
     if (gate is None) != (up is None):
         raise ValueError("gate and up are kept together: give both or neither")
     if gate is not None:
-        _need(gate, "gate", (dtype,), device, inner)
-        _need(up, "up", (dtype,), device, inner)
+        _check(gate, "gate", (dtype,), device, inner)
+        _check(up, "up", (dtype,), device, inner)
     if dX is not None:
         _need(dX, "dX", (dtype,), device, X.shape)
     if (dWg is None) != (dWu is None):

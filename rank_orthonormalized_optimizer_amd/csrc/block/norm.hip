@@ -147,7 +147,8 @@ __device__ __forceinline__ F team(F v, F* red) {
     return v;
 }
 
-// x to fp32 with the lowest bit set where it is not exact (rounded to odd): rounding that to fewer bits is rounding x once.
+// x to fp32 with the lowest bit set where it is not exact (rounded to odd): rounding that to fewer bits is rounding x once,
+// and it is above or below a number of fewer bits as x is.
 __device__ __forceinline__ float to_odd(double x) {
     const float f = (float)x;
     const double rest = x - (double)f;
@@ -160,7 +161,7 @@ __device__ __forceinline__ float to_odd(double x) {
 template <bool XB, bool SB, int TEAM, int VECS, bool Q8>
 __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs a) {
     using F = typename std::conditional<Q8, double, float>::type;
-    __shared__ F red[2][16];
+    __shared__ F red[2][16];   // (Q8: two times 16 floats in the second)
     const int t = TEAM == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int64_t row = TEAM == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
     if (row >= a.rows) return;   // (a whole team)
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs 
         if (a.h) {
             float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = Q8 && SB ? to_odd(h[i][e]) : (float)h[i][e];
+            for (int e = 0; e < 8; ++e) o[e] = (float)h[i][e];
             put8<SB>(a.h, at, c, a.d, o);
         }
 #pragma unroll
@@ -200,33 +201,42 @@ __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs 
     sum = team<TEAM, Sum>(sum, red[0]);
     const F rstd = (F)1 / sqrt(sum / (F)a.d + (F)a.eps);
     if (a.rstd && t == 0) a.rstd[row] = (float)rstd;
-    F top = 0;
+    float y[VECS][8], top = 0.f;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         float wv[8];
         w[i].get(a.w_bf16, wv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * rstd * (F)wv[e];
-        if constexpr (Q8) {
+        if constexpr (Q8) {   // from here on in fp32, rounded to odd: comparisons with the numbers of fewer bits stay as they are
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const F m = fabs(h[i][e]);
-                top = m > top && m < (F)INFINITY ? m : top;
+                y[i][e] = to_odd(h[i][e] * rstd * (F)wv[e]);
+                top = fmaxf(top, fabsf(y[i][e]));
             }
         } else {
             const int c = (i * TEAM + t) * 8;
-            if (a.y_bf16) put8<true>(a.y, at, c, a.d, h[i]);
-            else put8<false>(a.y, at, c, a.d, h[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[i][e] = h[i][e] * rstd * wv[e];
+            if (a.y_bf16) put8<true>(a.y, at, c, a.d, y[i]);
+            else put8<false>(a.y, at, c, a.d, y[i]);
         }
     }
     if constexpr (Q8) {
-        top = team<TEAM, Max>(top, red[1]);
+        float* red32 = (float*)red[1];
+        top = team<TEAM, Max>(top, red32);
+        if (top == INFINITY) {   // (the same for the team) the largest of the finite ones
+            top = 0.f;
+#pragma unroll
+            for (int i = 0; i < VECS; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fabsf(y[i][e]) < INFINITY ? fmaxf(top, fabsf(y[i][e])) : top;
+            top = team<TEAM, Max>(top, red32 + 16);
+        }
         // top = m 2^e, 1 <= m < 2, and 448 = 1.75 2^8
-        const uint64_t bits = (uint64_t)__double_as_longlong(top);
-        int e = (int)(bits >> 52) - 1023 - 8 + ((bits & 0xfffffffffffffull) > 0xc000000000000ull);
-        e = e < -126 ? -126 : e > 127 ? 127 : e;
-        if (top == 0) e = 0;
-        const double inverse = __longlong_as_double((int64_t)(1023 - e) << 52);
+        const uint32_t bits = __float_as_uint(top);
+        int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
+        e = e < -126 ? -126 : e;
+        if (top == 0.f) e = 0;
+        const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
         if (t == 0) a.scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
@@ -234,18 +244,18 @@ __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs 
             uint32_t q[2] = {0, 0};
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
-                const float v0 = to_odd(h[i][k] * inverse), v1 = to_odd(h[i][k + 1] * inverse);
+                const float v0 = y[i][k] * inverse, v1 = y[i][k + 1] * inverse;
                 const uint32_t p = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v0, v1, 0, false) & 0xffffu;
                 const uint32_t b0 = fabsf(v0) <= 448.f ? p & 0xffu : 0x7fu, b1 = fabsf(v1) <= 448.f ? p >> 8 : 0x7fu;
                 q[k / 4] |= (b0 | (b1 << 8)) << (8 * (k % 4));
             }
-            uint8_t* y = (uint8_t*)a.y + at + c;
+            uint8_t* out = (uint8_t*)a.y + at + c;
             if (c + 8 <= a.d) {
-                *(u32x2_bytes*)y = u32x2_bytes{q[0], q[1]};
+                *(u32x2_bytes*)out = u32x2_bytes{q[0], q[1]};
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (c + k < a.d) y[k] = (uint8_t)(q[k / 4] >> (8 * (k % 4)));
+                    if (c + k < a.d) out[k] = (uint8_t)(q[k / 4] >> (8 * (k % 4)));
             }
         }
     }
