@@ -7,7 +7,7 @@ from functools import reduce
 
 import torch
 
-from . import _lib, vocab
+from . import _lib, block, vocab
 
 _DT = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 
@@ -299,9 +299,10 @@ class MixedDion:
 
     The vocabulary matrices among the parameters (an embedding table, an output head, or one
     [vocab, width] matrix that is both) can be used through the optimizer, which then gathers their
-    gradients itself: ``lookup`` and ``lookup_grad``, ``head_loss``.  All contributions since the last
-    step add up (tied weights, microbatches), in float32 whatever the parameter's type, and ``step``
-    takes them where ``grads`` holds None.
+    gradients itself: ``lookup`` and ``lookup_grad``, ``head_loss``; so can the parameters of the residual
+    blocks between them: ``norm`` and ``norm_grad``, ``feed_forward`` and ``feed_forward_grad``.  All
+    contributions since the last step add up (tied weights, microbatches), in float32 whatever the
+    parameter's type, and ``step`` takes them where ``grads`` holds None.
     """
 
     def __init__(self, params, *, lr: float = 0.01, mu: float = 0.95, rank_fraction: float = 0.25,
@@ -372,6 +373,62 @@ class MixedDion:
         vocab.linear_cross_entropy_grad_(H, W, targets, lse, grad, dH, dW, ignore_index=ignore_index, accumulate=add)
         self.pending.add(i)
         return loss, dH
+
+    @torch.no_grad()
+    def norm(self, i: int, x: torch.Tensor, eps: float = 1e-6, *, eight: bool = False, **kw):
+        """Root-mean-square norm with the weight ``params[i]`` (rms_norm_, or with ``eight`` rms_norm_8bit_; ``kw``: theirs)."""
+        call = block.rms_norm_8bit_ if eight else block.rms_norm_
+        return call(x, self.params[self._index(i)], eps, **kw)
+
+    @torch.no_grad()
+    def norm_grad(self, i: int, dY: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, **kw):
+        """Gradients ``(dh, dx)`` of ``norm`` (rms_norm_grad_; ``kw``: its dsum, p, seed, site, dh and dx); adds the weight's."""
+        i = self._index(i)
+        dw, add = self._gather(i)
+        out = block.rms_norm_grad_(dY, h, self.params[i], rstd, dw, accumulate=add, **kw)
+        self.pending.add(i)
+        return out
+
+    def _gated(self, weights):
+        """The indexes of a feed-forward block's matrices (gate, up, down), three different ones."""
+        idx = [self._index(i) for i in weights]
+        if len(set(idx)) != 3:
+            raise ValueError(f"a feed-forward block has three matrices (gate, up, down), got parameters {idx}")
+        return idx
+
+    @torch.no_grad()
+    def feed_forward(self, weights, X: torch.Tensor, *, act: str = "silu", scale: torch.Tensor | None = None,
+                     keep: bool = True):
+        """Gated feed-forward block of the parameters ``weights`` = (gate, up, down) (gated_ffn_).
+
+        Returns ``(Y, kept)``; ``kept`` goes to ``feed_forward_grad``, which without it (``keep`` False) forms the two
+        projections again.
+        """
+        Wg, Wu, Wd = (self.params[i] for i in self._gated(weights))
+        kept = None
+        if keep:
+            shape = X.shape[:-1] + Wg.shape[:1]
+            kept = tuple(torch.empty(shape, dtype=Wg.dtype, device=Wg.device) for _ in range(2))
+        return block.gated_ffn_(X, Wg, Wu, Wd, act=act, scale=scale, gate=kept and kept[0], up=kept and kept[1]), kept
+
+    @torch.no_grad()
+    def feed_forward_grad(self, weights, X: torch.Tensor, dY: torch.Tensor, kept=None, *, act: str = "silu",
+                          scale: torch.Tensor | None = None) -> torch.Tensor:
+        """Gradient of ``X`` of the block ``feed_forward(weights, X)`` for the output's gradient ``dY`` (gated_ffn_grad_); adds
+        the three matrices'."""
+        idx = self._gated(weights)
+        gathered = [self._gather(i) for i in idx]
+        add = any(a for _, a in gathered)
+        dX = torch.empty_like(dY)
+        gate, up = kept or (None, None)
+        if add:   # one of them has a gradient already: the others start from zero
+            for dW, a in gathered:
+                if not a:
+                    dW.zero_()
+        block.gated_ffn_grad_(X, *(self.params[i] for i in idx), dY, gate, up, dX, *(dW for dW, _ in gathered), act=act,
+                              scale=scale, accumulate=add)
+        self.pending.update(idx)
+        return dX
 
     @torch.no_grad()
     def step(self, grads) -> None:
