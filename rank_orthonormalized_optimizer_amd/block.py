@@ -57,6 +57,11 @@ def _seed(seed, p: float, device):
     return seed.data_ptr()
 
 
+def _space(like, nbytes: int) -> torch.Tensor:
+    """_scratch on a tensor's GPU."""
+    return like.new_empty(max(int(nbytes), 256), dtype=torch.uint8)
+
+
 def _rows(x, name: str):
     """(rows, width) of a tensor [..., width]."""
     if x.dim() < 1 or x.shape[-1] < 1:
@@ -195,7 +200,7 @@ def rms_norm_grad_(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: tor
         if dw is None:
             ws = None
         elif workspace is None:
-            ws = rms_norm_grad_workspace_for(rows, width, device)
+            ws = _space(dY, _lib.load().dion_rms_norm_grad_workspace_size(rows, width))
         else:
             ws = _given_scratch(workspace, device)
         st = _lib.load().dion_rms_norm_grad(dY.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _ptr(dsum),
@@ -258,7 +263,7 @@ def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Te
             out = torch.empty_like(X, dtype=dtype)
         else:
             _check(out, "out", (dtype,), device, X.shape)
-        ws = gated_ffn_workspace_for(rows, width, hidden, device, dtype, x_dtype=X.dtype) if workspace is None \
+        ws = _space(Wg, _lib.load().dion_gated_ffn_workspace_size(rows, width, hidden, dt, xt, 0)) if workspace is None \
             else _given_scratch(workspace, device)
         st = _lib.load().dion_gated_ffn(X.data_ptr(), _ptr(scale), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), _ptr(gate),
                                         _ptr(up), out.data_ptr(), rows, width, hidden, _ACT[act], xt, dt, ws.data_ptr(),
@@ -288,18 +293,18 @@ def gated_ffn_grad_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: tor
         _check(gate, "gate", (dtype,), device, inner)
         _check(up, "up", (dtype,), device, inner)
     if dX is not None:
-        _need(dX, "dX", (dtype,), device, X.shape)
+        _check(dX, "dX", (dtype,), device, X.shape)
     if (dWg is None) != (dWu is None):
         raise ValueError("dWg and dWu come from one product: give both or neither")
     dw = dtype
     for name, t, like in (("dWg", dWg, Wg), ("dWu", dWu, Wu), ("dWd", dWd, Wd)):
         if t is not None:
-            _need(t, name, _DT, device, like.shape)
+            _check(t, name, _DT, device, like.shape)
             dw = t.dtype
     if any(t is not None and t.dtype != dw for t in (dWg, dWu, dWd)):
         raise TypeError("dWg, dWu and dWd must have one dtype")
     with _On(device, stream) as handle:
-        ws = gated_ffn_workspace_for(rows, width, hidden, device, dtype, x_dtype=X.dtype, for_grad=True, saved=gate is not None) \
+        ws = _space(Wg, _lib.load().dion_gated_ffn_workspace_size(rows, width, hidden, dt, xt, 2 if gate is None else 1)) \
             if workspace is None else _given_scratch(workspace, device)
         st = _lib.load().dion_gated_ffn_grad(X.data_ptr(), _ptr(scale), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
                                              dY.data_ptr(), _ptr(gate), _ptr(up), _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(dWd),

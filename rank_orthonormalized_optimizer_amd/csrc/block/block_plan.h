@@ -100,7 +100,7 @@ struct Product {
 };
 struct FfnPlan {
     int64_t t, d, f, dk, fk;
-    bool few;                          // forward: few rows, the weights are read in place by run_ffn_few
+    bool few;                          // few rows: the weights are read in place (run_ffn_few; fp32 gradients: run_ffn_few_grad)
     int parts;                         // of the operands that are not fp16 planes: 1 or 3
     bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
     Product gu, y, du, dx, dgu, dd, dw;   // (dw: dgu and dd at once)
@@ -159,6 +159,15 @@ inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms, bool
 // 2048 x 5632 1 row 24 us and 28, 4 rows 26 and 28, 16 rows 32 and 29, 8192 x 8192 4 rows 72 and 99, 16 rows 90 and 100; fp32
 // 2048 x 5632 1 row 45 and 110, 32 rows 79 and 111, 48 rows 120 and 123, 64 rows 139 and 124, 8192 x 8192 48 rows 351 and 652.
 constexpr int64_t kFewRows = 8, kFewRowsF32 = 48;
+constexpr int64_t kFewGradRowsF32 = 64;
+// Slices of the reduction over k (of `matrices` in a row) for an output of `cols` columns, 64 to a workgroup: two workgroups
+// for every CU, if each of its eight waves has two groups of 16 k.
+inline int64_t few_slices(int64_t cols, int64_t k, int64_t matrices) {
+    const int64_t blocks = ceil_div64(cols, 64), most = ceil_div64(k, 16) * matrices / 16;
+    int64_t s = 2 * kCUs / blocks;
+    if (s > most) s = most;
+    return s < 1 ? 1 : s;
+}
 
 // for_grad: the gradient; saved: gate and up are given to it
 inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16, int x8, int for_grad, int saved, FfnPlan* p) {
@@ -178,9 +187,18 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
         r = pick_product(m, n, k, t, narrow, m2, n2);
         if (r.acc > acc) acc = r.acc;
     };
-    q.few = !for_grad && rows <= (bf16 ? kFewRows : kFewRowsF32);
+    q.few = rows <= (for_grad ? bf16 ? 0 : kFewGradRowsF32 : bf16 ? kFewRows : kFewRowsF32);
     if (q.few) {
         q.u = take(n * q.fk * (bf16 ? 2 : 4));
+        if (for_grad) {
+            q.dab = take(2 * n * q.fk * 4);
+            const int64_t du = few_slices(hidden, width, 1) * q.fk, dx = few_slices(width, hidden, 2) * q.dk;
+            q.acc = take((du > dx ? du : dx) * n * 4);
+            if (!saved) {
+                q.gate = take(n * hidden * 4);
+                q.up = take(n * hidden * 4);
+            }
+        }
         q.total = off;
         *p = q;
         return true;
@@ -242,6 +260,8 @@ struct FfnArgs {
 };
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
+int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, void* stream);   // gate and up alone
+int run_ffn_few_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 // nothing but zeros, in n 16-bit words
 int run_zeros(void* out, int64_t n, void* stream);

@@ -759,6 +759,7 @@ int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
 }
 
 int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) {
+    if (p.few) return run_ffn_few_grad(args, p, ws, stream);
     const hipStream_t s = (hipStream_t)stream;
     FfnArgs a = args;
     const Inputs in = inputs(a, p, ws, !a.gate, false, s);

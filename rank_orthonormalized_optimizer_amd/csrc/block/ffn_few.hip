@@ -34,7 +34,7 @@ struct FewArgs {
     const float* scale;   // x in 8 bits, or null
     int rows, cols, k, ldx;
     int act;
-    void* out;            // u [rows][ldout] (M == 2), or Y
+    void* out;            // u [rows][ldout] (M == 2) or null, or Y
     int ldout;
     void* gate;           // [rows][cols], or null
     void* up;
@@ -84,24 +84,6 @@ template <> struct Few<false> {
         return c;
     }
 };
-
-// Four columns of a row of `d` elements at any element's address: bf16 or fp32.
-template <bool BF16>
-__device__ __forceinline__ void put4(void* p, int64_t row, int c, int d, const float (&v)[4]) {
-    if (c + 4 <= d) {
-        if constexpr (BF16)
-            *(u32x2_any*)((uint16_t*)p + row + c) = u32x2{down16(v[0]) | (down16(v[1]) << 16), down16(v[2]) | (down16(v[3]) << 16)};
-        else
-            *(f32x4_any*)((float*)p + row + c) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (c + e >= d) continue;
-            if constexpr (BF16) ((uint16_t*)p)[row + c + e] = (uint16_t)down16(v[e]);
-            else ((float*)p)[row + c + e] = v[e];
-        }
-    }
-}
 
 template <bool BF16>
 __device__ __forceinline__ void keep4(void* p, int64_t row, int c, int d, const float (&v)[4]) {
@@ -222,7 +204,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = t[0][e];
     }
-    put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
+    if (a.out) put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
 }
 
 template <bool BF16, int M, int NT>
@@ -248,12 +230,29 @@ void launch_few(const FewArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
-    const hipStream_t s = (hipStream_t)stream;
+namespace {
+
+FewArgs gate_args(const FfnArgs& a, const FfnPlan& p) {
     FewArgs g{};
     g.w[0] = a.Wg; g.w[1] = a.Wu; g.x = a.X; g.scale = a.x_scale;
     g.rows = (int)p.t; g.cols = (int)p.f; g.k = (int)p.d; g.ldx = (int)p.d; g.act = a.act;
-    g.out = ws + p.u; g.ldout = (int)p.fk; g.gate = a.gate; g.up = a.up;
+    g.gate = a.gate; g.up = a.up;
+    return g;
+}
+
+}  // namespace
+
+int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, void* stream) {
+    const FewArgs g = gate_args(a, p);
+    if (a.bf16) launch_few<true, 2>(g, (hipStream_t)stream);
+    else launch_few<false, 2>(g, (hipStream_t)stream);
+    return (int)hipGetLastError();
+}
+
+int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
+    const hipStream_t s = (hipStream_t)stream;
+    FewArgs g = gate_args(a, p);
+    g.out = ws + p.u; g.ldout = (int)p.fk;
     FewArgs d{};
     d.w[0] = a.Wd; d.x = ws + p.u;
     d.rows = (int)p.t; d.cols = (int)p.d; d.k = (int)p.f; d.ldx = (int)p.fk;

@@ -62,6 +62,24 @@ __device__ __forceinline__ void put8(void* p, int64_t row, int c, int d, const f
     }
 }
 
+// Four columns of a row of `d` elements at any element's address: bf16 or fp32.
+template <bool BF16>
+__device__ __forceinline__ void put4(void* p, int64_t row, int c, int d, const float (&v)[4]) {
+    if (c + 4 <= d) {
+        if constexpr (BF16)
+            *(u32x2_any*)((uint16_t*)p + row + c) = u32x2{down16(v[0]) | (down16(v[1]) << 16), down16(v[2]) | (down16(v[3]) << 16)};
+        else
+            *(f32x4_any*)((float*)p + row + c) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (c + e >= d) continue;
+            if constexpr (BF16) ((uint16_t*)p)[row + c + e] = (uint16_t)down16(v[e]);
+            else ((float*)p)[row + c + e] = v[e];
+        }
+    }
+}
+
 // N (4 or 8) 8-bit numbers (e4m3) of a row from column c, times s; zeros from column d on
 template <int N>
 __device__ __forceinline__ void load_e4m3(const void* in, int64_t row, int c, int d, float s, float (&v)[N]) {
