@@ -158,7 +158,14 @@ inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms, bool
 // Forward calls of so few rows read the weights in place (run_ffn_few), more go through tiles.  That way and by tiles: bf16
 // 2048 x 5632 1 row 24 us and 28, 4 rows 26 and 28, 16 rows 32 and 29, 8192 x 8192 4 rows 72 and 99, 16 rows 90 and 100; fp32
 // 2048 x 5632 1 row 45 and 110, 32 rows 79 and 111, 48 rows 120 and 123, 64 rows 139 and 124, 8192 x 8192 48 rows 351 and 652.
-constexpr int64_t kFewRows = 8, kFewRowsF32 = 48;
+constexpr int64_t kFewRows = 8, kFewRowsF32 = 64;
+// Slices of the reduction over k for an output of `cols` columns, 16 to a workgroup: where they are fewer than a quarter of the
+// CUs and k is long, a workgroup for every CU (forward, fp32 4 x 65 x 20279: 60 -> 18 us, 22 x 4001 x 75: 40 -> 18).
+inline int64_t few_gate_slices(int64_t cols, int64_t k) {
+    const int64_t blocks = ceil_div64(cols, 16), most = k / 512;
+    if (blocks * 4 > kCUs || most < 2) return 1;
+    return kCUs / blocks < most ? kCUs / blocks : most;
+}
 constexpr int64_t kFewGradRowsF32 = 64;
 // Slices of the reduction over k (of `matrices` in a row) for an output of `cols` columns, 64 to a workgroup: two workgroups
 // for every CU, if each of its eight waves has two groups of 16 k.
@@ -189,16 +196,22 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
     };
     q.few = rows <= (for_grad ? bf16 ? 0 : kFewGradRowsF32 : bf16 ? kFewRows : kFewRowsF32);
     if (q.few) {
+        const int64_t sg = few_gate_slices(hidden, width), sd = few_gate_slices(width, hidden);
+        int64_t sums = !for_grad || !saved ? (sg > 1 ? sg * 2 * q.fk : 0) : 0;
+        auto most = [&](int64_t e) { if (e > sums) sums = e; };
         q.u = take(n * q.fk * (bf16 ? 2 : 4));
         if (for_grad) {
             q.dab = take(2 * n * q.fk * 4);
-            const int64_t du = few_slices(hidden, width, 1) * q.fk, dx = few_slices(width, hidden, 2) * q.dk;
-            q.acc = take((du > dx ? du : dx) * n * 4);
+            most(few_slices(hidden, width, 1) * q.fk);
+            most(few_slices(width, hidden, 2) * q.dk);
             if (!saved) {
                 q.gate = take(n * hidden * 4);
                 q.up = take(n * hidden * 4);
             }
+        } else if (sd > 1) {
+            most(sd * q.dk);
         }
+        q.acc = take(sums * n * 4);
         q.total = off;
         *p = q;
         return true;
@@ -260,7 +273,7 @@ struct FfnArgs {
 };
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
-int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, void* stream);   // gate and up alone
+int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);   // gate and up alone
 int run_ffn_few_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 // nothing but zeros, in n 16-bit words

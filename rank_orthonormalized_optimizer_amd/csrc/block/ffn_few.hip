@@ -33,8 +33,10 @@ struct FewArgs {
     const void* x;        // [rows][ldx]
     const float* scale;   // x in 8 bits, or null
     int rows, cols, k, ldx;
+    int slices;           // of k; several: their sums go to
+    float* acc;           // [slices][M][rows][ldout], for few_join_kernel
     int act;
-    void* out;            // u [rows][ldout] (M == 2) or null, or Y
+    void* out;            // u [rows][ldout] (M == 2) or null, or Y [rows][cols]
     int ldout;
     void* gate;           // [rows][cols], or null
     void* up;
@@ -101,6 +103,26 @@ __device__ __forceinline__ void keep4(void* p, int64_t row, int c, int d, const 
     }
 }
 
+// Four columns of u (p, q: a and b) or of Y (p).
+template <bool BF16, int M>
+__device__ __forceinline__ void few_out(const FewArgs& a, int64_t row, int c, const float (&p)[4], const float (&q)[4]) {
+    if constexpr (M == 2) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float slope;
+            v[e] = activate<!BF16>(a.act, p[e], slope) * q[e];
+        }
+        if (a.gate) {
+            keep4<BF16>(a.gate, row * a.cols, c, a.cols, p);
+            keep4<BF16>(a.up, row * a.cols, c, a.cols, q);
+        }
+        if (a.out) put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
+    } else {
+        put4<BF16>(a.out, row * a.cols, c, a.cols, p);
+    }
+}
+
 // f(n) of a number that is known when it runs, 1 .. N, or nothing for 0
 template <int N, class F>
 __device__ __forceinline__ void rest(int n, F f) {
@@ -117,8 +139,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
     constexpr int U = M + NT <= 2 ? 12 : M + NT <= 3 ? 8 : 4;   // steps under way, as many as the registers hold
     __shared__ __attribute__((aligned(16))) f32x4 sums[WAVES][M * NT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c0 = blockIdx.x * 16, steps = a.k / T::kStep, per = (steps + WAVES - 1) / WAVES;
-    const int first = wave * per, last = first + per < steps ? first + per : steps;
+    const int slice = blockIdx.x % a.slices, c0 = blockIdx.x / a.slices * 16, steps = a.k / T::kStep;
+    const int share = a.slices * WAVES, me = slice * WAVES + wave;
+    const int first = (int)((int64_t)steps * me / share), last = (int)((int64_t)steps * (me + 1) / share);
     const int col = c0 + lane % 16 < a.cols ? c0 + lane % 16 : a.cols - 1;   // (columns and rows behind the last: any, not stored)
     const int64_t wrow = (int64_t)col * a.k;
     int64_t xrow[NT];
@@ -158,7 +181,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
     int at = first;
     for (; at + U <= last; at += U) batch(at, std::integral_constant<int, U>());
     rest<U - 1>(last - at, [&](auto count) { batch(at, count); });
-    if (wave == WAVES - 1 && a.k % T::kStep != 0) {   // the step at the rows' end
+    if (me == share - 1 && a.k % T::kStep != 0) {   // the step at the rows' end
         const int c = steps * T::kStep + lane / 16 * T::kPer;
         u32x4 w[M], x[NT];
 #pragma unroll
@@ -186,30 +209,39 @@ __global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
     const int64_t row = 16 * wave + lane % 16;
     const int c = c0 + 4 * (lane / 16);
     if (row >= a.rows) return;
-    float v[4];
-    if constexpr (M == 2) {
-        float p[4], q[4];
+    if (a.slices > 1) {   // (rows of a multiple of 64)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float slope;
-            p[e] = t[0][e];
-            q[e] = t[M - 1][e];
-            v[e] = activate<!BF16>(a.act, p[e], slope) * q[e];
-        }
-        if (a.gate) {
-            keep4<BF16>(a.gate, row * a.cols, c, a.cols, p);
-            keep4<BF16>(a.up, row * a.cols, c, a.cols, q);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = t[0][e];
+        for (int m = 0; m < M; ++m) *(f32x4*)(a.acc + (((int64_t)slice * M + m) * a.rows + row) * a.ldout + c) = t[m];
+        return;
     }
-    if (a.out) put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
+    float p[4], q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { p[e] = t[0][e]; q[e] = t[M - 1][e]; }
+    few_out<BF16, M>(a, row, c, p, q);
+}
+
+// The slices' sums, four columns a thread.
+template <bool BF16, int M>
+__global__ __launch_bounds__(256) void few_join_kernel(FewArgs a) {
+    const int per = a.ldout / 4, i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.rows * per) return;
+    const int64_t row = i / per;
+    const int c = (i - (int)row * per) * 4;
+    if (c >= a.cols) return;
+    f32x4 t[M] = {};
+#pragma unroll 4
+    for (int s = 0; s < a.slices; ++s)
+#pragma unroll
+        for (int m = 0; m < M; ++m) t[m] += *(const f32x4*)(a.acc + (((int64_t)s * M + m) * a.rows + row) * a.ldout + c);
+    float p[4], q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { p[e] = t[0][e]; q[e] = t[M - 1][e]; }
+    few_out<BF16, M>(a, row, c, p, q);
 }
 
 template <bool BF16, int M, int NT>
 void launch_few(const FewArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)ceil_div64(a.cols, 16));
+    const dim3 grid((unsigned)(ceil_div64(a.cols, 16) * a.slices));
     if constexpr (M == 2) {
         if (a.scale) hipLaunchKernelGGL((few_kernel<BF16, 2, NT, true, 8>), grid, dim3(512), 0, s, a);
         else hipLaunchKernelGGL((few_kernel<BF16, 2, NT, false, 8>), grid, dim3(512), 0, s, a);
@@ -226,14 +258,17 @@ void launch_few(const FewArgs& a, hipStream_t s) {
         if (a.rows <= 32) launch_few<false, M, 2>(a, s);
         else launch_few<false, M, 4>(a, s);
     }
+    if (a.slices > 1)
+        hipLaunchKernelGGL((few_join_kernel<BF16, M>), dim3((unsigned)ceil_div64((int64_t)a.rows * (a.ldout / 4), 256)), dim3(256), 0, s, a);
 }
 
 }  // namespace
 
 namespace {
 
-FewArgs gate_args(const FfnArgs& a, const FfnPlan& p) {
+FewArgs gate_args(const FfnArgs& a, const FfnPlan& p, char* ws) {
     FewArgs g{};
+    g.slices = (int)few_gate_slices(p.f, p.d); g.acc = (float*)(ws + p.acc); g.ldout = (int)p.fk;
     g.w[0] = a.Wg; g.w[1] = a.Wu; g.x = a.X; g.scale = a.x_scale;
     g.rows = (int)p.t; g.cols = (int)p.f; g.k = (int)p.d; g.ldx = (int)p.d; g.act = a.act;
     g.gate = a.gate; g.up = a.up;
@@ -242,8 +277,8 @@ FewArgs gate_args(const FfnArgs& a, const FfnPlan& p) {
 
 }  // namespace
 
-int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, void* stream) {
-    const FewArgs g = gate_args(a, p);
+int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
+    const FewArgs g = gate_args(a, p, ws);
     if (a.bf16) launch_few<true, 2>(g, (hipStream_t)stream);
     else launch_few<false, 2>(g, (hipStream_t)stream);
     return (int)hipGetLastError();
@@ -251,12 +286,13 @@ int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, void* stream) {
 
 int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
-    FewArgs g = gate_args(a, p);
-    g.out = ws + p.u; g.ldout = (int)p.fk;
+    FewArgs g = gate_args(a, p, ws);
+    g.out = ws + p.u;
     FewArgs d{};
     d.w[0] = a.Wd; d.x = ws + p.u;
     d.rows = (int)p.t; d.cols = (int)p.d; d.k = (int)p.f; d.ldx = (int)p.fk;
-    d.out = a.Y; d.ldout = (int)p.d;
+    d.slices = (int)few_gate_slices(p.d, p.f); d.acc = g.acc; d.ldout = (int)p.dk;
+    d.out = a.Y;
     if (a.bf16) {
         launch_few<true, 2>(g, s);
         launch_few<true, 1>(d, s);

@@ -280,7 +280,7 @@ int run_ffn_few_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stre
     if (!a.gate) {
         a.gate = ws + p.gate;
         a.up = ws + p.up;
-        const int e = run_ffn_few_gate(a, p, stream);
+        const int e = run_ffn_few_gate(a, p, ws, stream);
         if (e) return e;
     }
     DownArgs g{};

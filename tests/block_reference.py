@@ -11,7 +11,11 @@ dh      mean(g n): products and sums of at most 64 + 22 terms on a path, 90 u me
         rstd (4 u |g| + |n| e_mean + 6 u |n mean|) + 3 u |dh| + u |dsum|.  dx: two more roundings, times 1 / (1 - p).
 dw      a sum of rows products: at most (rows + 40) u sum(|dY n|).
 a, b    K products of 16-bit parts added in fp32: nseg K additions, doubled for the matrix core's own
-        rounding, and 12 u for fp32 operands' dropped terms: (2 nseg K + 12) u sum |x| |w|.
+        rounding, and 12 u for fp32 operands' dropped terms: (2 nseg K + 12) u sum |x| |w| (nseg 6 covers three
+        products, and single ones in fp32).  Two fp16 parts of a row scaled to [2^13, 2^14) leave 2^-39 of the row's largest
+        besides, where the low part is subnormal: 2^-38 (max|x| sum|w| + max|w| sum|x|).
+du      the same, but Wd's rows k run along the reduction: with m_k = max |Wd_k|, 2^-38 (max_k (|dY_k| m_k)
+        sum_k |Wd_kc| / m_k + sum_k |dY_k| m_k).
 act     |act'| <= 1.2 and |act''| <= 1.2.  The sigmoid's argument z has a rounding of |z| 2 u (gelu's
         polynomial 4 u |z|), which is relative in its exponential, and eight u follow: relative 8 (|z| + 1) u
         of act, and of each of the two terms of act'.
@@ -199,6 +203,9 @@ class Ffn:
             return (2 * nseg * k + 12) * U
         a, b = x @ wg.t(), x @ wu.t()
         ea, eb = grow(d) * (x.abs() @ wg.abs().t()), grow(d) * (x.abs() @ wu.abs().t())
+        if not bf16:
+            for e, w in ((ea, wg), (eb, wu)):
+                e += 2.0 ** -38 * (x.abs().amax(1)[:, None] * w.abs().sum(1) + x.abs().sum(1)[:, None] * w.abs().amax(1))
         self.gate, self.up, self.gate_bound, self.up_bound = a, b, ea, eb
         if dY is not None:
             if gate is not None:
@@ -220,6 +227,9 @@ class Ffn:
         dy = dY.to(F64).reshape(T, d)
         du = dy @ wd
         edu = grow(d) * (dy.abs() @ wd.abs())
+        if not bf16:
+            m = wd.abs().amax(1).clamp(min=2.0 ** -87)
+            edu += 2.0 ** -38 * ((dy.abs() * m).amax(1)[:, None] * (wd.abs() / m[:, None]).sum(0) + (dy.abs() @ m)[:, None])
         es = 1.2 * ea + rel * (slope.abs() + 2 + v.abs())
         e1 = _both(du, edu, b, eb)
         da, db = du * b * slope, du * v
