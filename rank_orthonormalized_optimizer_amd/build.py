@@ -15,7 +15,7 @@ LIB_NAME = "libdion_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["dion_step.hip", "stream16.hip", "elementwise.hip", "spectral.hip", "noalloc.hip", "dion_api.cpp",
            "vocab/embedding.hip", "vocab/cross_entropy.hip", "vocab/vocab_api.cpp",
-           "block/norm.hip", "block/ffn.hip", "block/ffn_few.hip", "block/ffn_few_grad.hip",
+           "block/norm.hip", "block/ffn.hip", "block/ffn_few.hip", "block/ffn_few_grad.hip", "block/ffn_mid.hip",
            "block/block_api.cpp"]
 ARCH = "gfx950"
 

@@ -101,6 +101,8 @@ struct Product {
 struct FfnPlan {
     int64_t t, d, f, dk, fk;
     bool few;                          // few rows: the weights are read in place (run_ffn_few; fp32 gradients: run_ffn_few_grad)
+    bool mid;                          // a moderate number of fp32 rows: the weights are read in place (run_mid_*), rows in planes
+    int mgu, my, mdu, mdx;             // slices of those products' reductions
     int parts;                         // of the operands that are not fp16 planes: 1 or 3
     bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
     Product gu, y, du, dx, dgu, dd, dw;   // (dw: dgu and dd at once)
@@ -155,7 +157,7 @@ inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms, bool
     return best;
 }
 
-// Forward calls of so few rows read the weights in place (run_ffn_few), more go through tiles.  That way and by tiles: bf16
+// Forward calls of so few rows read weights and rows in place (run_ffn_few), more go through tiles.  That way and by tiles: bf16
 // 2048 x 5632 1 row 24 us and 28, 4 rows 26 and 28, 16 rows 32 and 29, 8192 x 8192 4 rows 72 and 99, 16 rows 90 and 100; fp32
 // 2048 x 5632 1 row 45 and 110, 32 rows 79 and 111, 48 rows 120 and 123, 64 rows 139 and 124, 8192 x 8192 48 rows 351 and 652.
 constexpr int64_t kFewRows = 8, kFewRowsF32 = 64;
@@ -176,6 +178,28 @@ inline int64_t few_slices(int64_t cols, int64_t k, int64_t matrices) {
     return s < 1 ? 1 : s;
 }
 
+// fp32 calls that read the weights in place beside planes of the rows (run_mid_*).  That way, and few rows' way or by tiles,
+// width x hidden (us): forward, 2048 x 5632 16 rows 64 and 60, 24 rows 64 and 87, 64 rows 71 and 146, 128 rows 102 and 148, 512 rows
+// 232 and 242; 1024 x 4096 64 rows 45 and 37, 96 rows 55 and 64, 512 rows 101 and 108; 768 x 2048 96 rows 52 and 41; 8192 x 8192 96
+// rows 307 and 683, 640 rows 1657 and 1432.  Gradients, 2048 x 5632 32 rows 121 and 114, 40 rows 124 and 134, 128 rows 188 and 273,
+// 512 rows 424 and 496; 1024 x 4096 48 rows 66 and 63, 64 rows 69 and 83; 768 x 2048 128 rows 77 and 75, 256 rows 90 and 101; 1024 x 1024
+// 256 rows 82 and 78.
+constexpr int64_t kMidRowsF32 = 512;
+inline bool mid_rows(int64_t rows, int64_t elements, int for_grad) {   // elements: of a weight matrix
+    if (rows > kMidRowsF32) return false;
+    if (for_grad) return rows > 64 ? elements >= (3 << 19) : rows > 32 && elements >= (1 << 22);
+    return rows > 64 ? elements >= (1 << 22) : rows > 16 && elements >= (1 << 23);
+}
+// Slices of the reduction's `steps` of 32, four of which are under way, for an output of `cols` columns, `per` to a workgroup:
+// a workgroup for every CU.
+inline int mid_slices(int64_t rows, int64_t cols, int64_t per, int64_t steps) {
+    const int64_t blocks = ceil_div64(cols, per) * ceil_div64(rows, 128), units = ceil_div64(steps, 4);
+    int64_t s = kCUs / blocks;
+    if (s > units) s = units;
+    if (s < 1) s = 1;
+    return (int)ceil_div64(units, ceil_div64(units, s));   // (all slices as long as the longest)
+}
+
 // for_grad: the gradient; saved: gate and up are given to it
 inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16, int x8, int for_grad, int saved, FfnPlan* p) {
     FfnPlan q{};
@@ -194,7 +218,8 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
         r = pick_product(m, n, k, t, narrow, m2, n2);
         if (r.acc > acc) acc = r.acc;
     };
-    q.few = rows <= (for_grad ? bf16 ? 0 : kFewGradRowsF32 : bf16 ? kFewRows : kFewRowsF32);
+    q.mid = !bf16 && mid_rows(rows, width * hidden, for_grad);
+    q.few = !q.mid && rows <= (for_grad ? bf16 ? 0 : kFewGradRowsF32 : bf16 ? kFewRows : kFewRowsF32);
     if (q.few) {
         const int64_t sg = few_gate_slices(hidden, width), sd = few_gate_slices(width, hidden);
         int64_t sums = !for_grad || !saved ? (sg > 1 ? sg * 2 * q.fk : 0) : 0;
@@ -217,6 +242,37 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
         return true;
     }
     const bool forms = !for_grad || !saved;   // a and b are formed
+    if (q.mid) {
+        int64_t sums = 0;
+        auto slice = [&](int64_t cols, int64_t per, int64_t steps, int64_t ld, int64_t outputs) {
+            const int s = mid_slices(n, cols, per, steps);
+            if (s > 1 && s * ld * outputs > sums) sums = s * ld * outputs;
+            return s;
+        };
+        q.x = take(3 * n * q.dk * 2);
+        q.u = take(3 * n * q.fk * 2);
+        if (forms) q.mgu = slice(hidden, 128, q.dk / 32, q.fk, 2);
+        if (!for_grad) {
+            q.my = slice(width, 256, q.fk / 32, q.dk, 1);
+        } else {
+            if (!saved) {
+                q.gate = take(n * hidden * 4);
+                q.up = take(n * hidden * 4);
+            }
+            q.dy = take(3 * n * q.dk * 2);
+            q.dab = take(3 * n * 2 * q.fk * 2);
+            q.mdu = slice(hidden, 256, q.dk / 32, q.fk, 1);
+            q.mdx = slice(width, 256, 2 * q.fk / 32, q.dk, 1);
+            plan(q.dgu, width, 2 * q.fk, n, terms, false);
+            plan(q.dd, hidden, width, n, terms, false);
+            plan(q.dw, width, 2 * q.fk, n, terms, false, hidden, width);
+        }
+        if (acc < (size_t)(sums * n * 4)) acc = (size_t)(sums * n * 4);
+        q.acc = take((int64_t)acc);
+        q.total = off;
+        *p = q;
+        return true;
+    }
     if (bf16 ? q.xpack : for_grad) q.x = take(q.parts * n * q.dk * 2);
     if (bf16 ? q.wpack : for_grad) q.w = take(q.parts * 2 * q.fk * q.dk * 2);
     if (bf16 ? q.dpack : !for_grad) q.wd = take(q.parts * width * q.fk * 2);
@@ -275,6 +331,11 @@ int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);   // gate and up alone
 int run_ffn_few_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
+// a and b (gate and up, planes of u), Y, du (planes of da, db and u), dX from the rows' planes
+int run_mid_gate(const FfnArgs& a, const FfnPlan& p, bool u, char* ws, void* stream);
+int run_mid_out(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
+int run_mid_du(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
+int run_mid_dx(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 // nothing but zeros, in n 16-bit words
 int run_zeros(void* out, int64_t n, void* stream);

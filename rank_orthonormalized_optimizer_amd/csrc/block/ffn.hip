@@ -723,6 +723,19 @@ Inputs inputs(const FfnArgs& a, const FfnPlan& p, char* ws, bool forms, bool out
     return in;
 }
 
+// Planes of the rows alone, of X and of dY.
+Inputs rows_in_planes(const FfnArgs& a, const FfnPlan& p, char* ws, bool x, hipStream_t s) {
+    Inputs in{};
+    PackJobs jobs{};
+    const int t = (int)p.t, d = (int)p.d;
+    in.x = mm::Operand{(uint16_t*)(ws + p.x), p.t * p.dk, p.dk, t};
+    in.dy = mm::Operand{(uint16_t*)(ws + p.dy), p.t * p.dk, p.dk, t};
+    if (x) pack(jobs, {a.X, a.x_scale, nullptr, (uint16_t*)(ws + p.x), nullptr, nullptr, t, 0, p.t * p.dk, a.x_scale ? 2 : 0, d});
+    if (a.dY) pack(jobs, {a.dY, nullptr, nullptr, (uint16_t*)(ws + p.dy), nullptr, nullptr, t, 0, p.t * p.dk, 0, d});
+    launch_pack(jobs, 3, s);
+    return in;
+}
+
 GatedArgs gated_args(const FfnArgs& a, const FfnPlan& p, const mm::Operand& w, const mm::Operand& x, int64_t m, char* ws) {
     GatedArgs g{};
     g.o = Operands{w, x, m, p.t};
@@ -749,6 +762,11 @@ int run_zeros(void* out, int64_t n, void* stream) {
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
     if (p.few) return run_ffn_few(a, p, ws, stream);
     const hipStream_t s = (hipStream_t)stream;
+    if (p.mid) {
+        rows_in_planes(a, p, ws, true, s);
+        const int e = run_mid_gate(a, p, true, ws, stream);
+        return e ? e : run_mid_out(a, p, ws, stream);
+    }
     const Inputs in = inputs(a, p, ws, true, true, s);
     const mm::Segments seg = segments(p.parts, p.parts);
     float* acc = (float*)(ws + p.acc);
@@ -762,34 +780,44 @@ int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) 
     if (p.few) return run_ffn_few_grad(args, p, ws, stream);
     const hipStream_t s = (hipStream_t)stream;
     FfnArgs a = args;
-    const Inputs in = inputs(a, p, ws, !a.gate, false, s);
+    const bool form = !a.gate;
+    const Inputs in = p.mid ? rows_in_planes(a, p, ws, form || a.dWg, s) : inputs(a, p, ws, form, false, s);
     const mm::Segments seg = segments(p.parts, p.parts);
     float* acc = (float*)(ws + p.acc);
-    if (!a.gate) {
+    if (form) {
         a.gate = ws + p.gate;
         a.up = ws + p.up;
-        GatedArgs g = gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws);
-        g.u = nullptr;
-        launch_gated<false>(g, p.gu, p.parts, acc, s);
     }
-    GatedArgs g = gated_args(a, p, in.wd16, in.dy16, p.fk, ws);
-    g.xinv = (const float*)(ws + p.yinv);
-    g.dab = a.dX || a.dWg ? (uint16_t*)(ws + p.dab) : nullptr;
-    if (!a.dWd) g.u = nullptr;
-    launch_gated<true>(g, p.du, p.parts, acc, s);
     const mm::Operand dab{(uint16_t*)(ws + p.dab), p.t * 2 * p.fk, 2 * p.fk, (int)p.t};
     const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
-    if (a.dX) {   // over da and Wg, db and Wu: two planes of one part each in place, one matrix of 2 fk rows where packed
-        OutArgs o = out_args(in.w, dab, p.d, p.t, a.dX, a.bf16, 0);
-        mm::Segments pairs = seg;
-        if (p.wpack) {
-            o.o.a.rows = (int)(2 * p.fk);
-        } else {
-            o.o.a.plane = in.w.pair;
-            o.o.b.plane = p.fk;
-            pairs = mm::Segments{2, 0 | (1 | 1 << 2) << 4};
+    if (p.mid) {
+        int e = form ? run_mid_gate(a, p, false, ws, stream) : 0;
+        if (!e) e = run_mid_du(a, p, ws, stream);
+        if (!e && a.dX) e = run_mid_dx(a, p, ws, stream);
+        if (e) return e;
+    } else {
+        if (form) {
+            GatedArgs g = gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws);
+            g.u = nullptr;
+            launch_gated<false>(g, p.gu, p.parts, acc, s);
         }
-        launch_out<true, false>(Out<1>(o), p.dx, pairs, acc, s);
+        GatedArgs g = gated_args(a, p, in.wd16, in.dy16, p.fk, ws);
+        g.xinv = (const float*)(ws + p.yinv);
+        g.dab = a.dX || a.dWg ? (uint16_t*)(ws + p.dab) : nullptr;
+        if (!a.dWd) g.u = nullptr;
+        launch_gated<true>(g, p.du, p.parts, acc, s);
+        if (a.dX) {   // over da and Wg, db and Wu: two planes of one part each in place, one matrix of 2 fk rows where packed
+            OutArgs o = out_args(in.w, dab, p.d, p.t, a.dX, a.bf16, 0);
+            mm::Segments pairs = seg;
+            if (p.wpack) {
+                o.o.a.rows = (int)(2 * p.fk);
+            } else {
+                o.o.a.plane = in.w.pair;
+                o.o.b.plane = p.fk;
+                pairs = mm::Segments{2, 0 | (1 | 1 << 2) << 4};
+            }
+            launch_out<true, false>(Out<1>(o), p.dx, pairs, acc, s);
+        }
     }
     OutArgs gu = out_args(in.x, dab, p.d, 2 * p.fk, a.dWg, a.dw_bf16, a.accumulate);
     gu.second = p.fk; gu.valid = p.f; gu.out2 = a.dWu;

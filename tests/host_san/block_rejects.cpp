@@ -104,6 +104,25 @@ int main() {
                     const int64_t rows = 2 * p.fk + 2 * d + 2 * t;   // of the packing, four to a workgroup
                     if ((rows / 4 + 5) * 256 >= (int64_t)1 << 32) { fprintf(stderr, "FAIL packing\n"); ++failures; }
                     const size_t acc = p.total - p.acc;
+                    if (p.mid) {
+                        // slices: of the reductions, none without a step; their sums; offsets in the rows' planes in 32 bits
+                        auto slices = [&](const char* what, int n, int64_t steps, int64_t sums, int64_t planes) {
+                            if (n < 1 || n > (steps + 3) / 4 || (n > 1 && (size_t)(n * sums * t * 4) > acc) || planes * t * 2 >= (int64_t)1 << 31) {
+                                fprintf(stderr, "FAIL slices of %s: %ld x %ld x %ld\n", what, (long)t, (long)d, (long)f);
+                                ++failures;
+                            }
+                        };
+                        if (!saved) slices("a, b", p.mgu, p.dk / 32, 2 * p.fk, 3 * p.dk);
+                        if (!g) slices("Y", p.my, p.fk / 32, p.dk, 3 * p.fk);
+                        if (g) {
+                            slices("du", p.mdu, p.dk / 32, p.fk, 3 * p.dk);
+                            slices("dX", p.mdx, p.fk / 16, p.dk, 6 * p.fk);
+                            product("dWg, dWu", p.dgu, d, 2 * p.fk, t, 0, 0, acc);
+                            product("dWd", p.dd, f, d, t, 0, 0, acc);
+                            product("dW", p.dw, d, 2 * p.fk, t, f, d, acc);
+                        }
+                        continue;
+                    }
                     product("a, b", p.gu, 2 * p.fk, t, d, 0, 0, acc);
                     if (!g) {
                         product("Y", p.y, d, t, f, 0, 0, acc);

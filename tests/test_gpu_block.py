@@ -247,7 +247,10 @@ def test_norm_gradient_by_differences(cuda):
 # ---------------------------------------------------------------------------- gated feed-forward block
 SIZES = [(1, 1, 1), (1, 64, 64), (1, 2048, 640), (2, 8, 200), (3, 7, 5), (16, 1032, 72), (17, 65, 33), (31, 320, 1024),
          (33, 64, 128), (48, 72, 200), (5, 130, 4104), (4, 65, 9000), (9, 1500, 90), (6, 5001, 40), (64, 2048, 512), (129, 255, 130), (130, 128, 129), (257, 255, 1013), (300, 512, 384), (520, 1024, 640),
-         (700, 40, 1500), (2050, 136, 2056), (1500, 704, 1400)]
+         (700, 40, 1500), (2050, 136, 2056), (1500, 704, 1400),
+         # a moderate number of fp32 rows whose weights are read in place
+         (17, 1029, 8200), (24, 8193, 1027), (33, 4099, 1032), (64, 2051, 4099), (65, 1001, 4203), (129, 16390, 257), (130, 257, 16500),
+         (300, 1300, 1250), (512, 8200, 513)]
 TYPES = [("f32", 16), ("bf16", 16), ("bf16", 8), ("f32", 8)]
 
 
