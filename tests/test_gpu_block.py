@@ -377,3 +377,82 @@ def test_feed_forward_far_out(cuda, t, act):
     for k, v in zip(("dX", "dWg", "dWu", "dWd"), out):
         w, e = getattr(want, k), getattr(want, k + "_bound")
         close(v, w, e + half_step(t) * (w.abs() + e), k)
+
+
+PATHS = [("f32", 3, 100, 4000), ("f32", 20, 1030, 8200), ("f32", 40, 2100, 2003), ("f32", 40, 70, 300), ("f32", 100, 1100, 4000),
+         ("f32", 200, 255, 1013), ("f32", 520, 300, 500), ("bf16", 3, 100, 4000), ("bf16", 100, 320, 1000), ("bf16", 257, 255, 130)]
+
+
+@pytest.mark.parametrize("dt,rows,width,hidden", PATHS)
+def test_feed_forward_in_graphs(cuda, dt, rows, width, hidden):
+    """Every way through the block, captured twice over one workspace: each replay as the eager call, bit for bit, whatever the
+    workspace holds before."""
+    import rank_orthonormalized_optimizer_amd as dion
+    t = DT[dt]
+    X, _, Wg, Wu, Wd, dY = ffn_inputs(cuda, rows, width, hidden, dt, 16)
+    ws = dirty(max((dion.gated_ffn_workspace_for(rows, width, hidden, cuda, t, for_grad=g, saved=s) for g, s in
+                    ((False, True), (True, True), (True, False))), key=lambda w: w.numel()))
+    gate, up = (torch.empty(rows, hidden, device=cuda, dtype=t) for _ in range(2))
+    Y = torch.empty_like(X)
+    out = [torch.empty_like(v) for v in (X, Wg, Wu, Wd)]
+    again = [torch.empty_like(v) for v in out]
+
+    def forward(ws=None):
+        dion.gated_ffn_(X, Wg, Wu, Wd, gate=gate, up=up, out=Y, workspace=ws)
+
+    def backward(ws=None):
+        dion.gated_ffn_grad_(X, Wg, Wu, Wd, dY, gate, up, *out, workspace=ws)
+        dion.gated_ffn_grad_(X, Wg, Wu, Wd, dY, None, None, *again, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        forward()
+        backward()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for f in (forward, backward):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f(ws)
+    for i in range(3):
+        X.copy_(X.roll(1, 0))
+        dY.mul_(-1)
+        dirty(ws)
+        for g in graphs:
+            g.replay()
+        got = [v.clone() for v in (gate, up, Y, *out, *again)]
+        forward()
+        backward()
+        for a, b in zip(got, (gate, up, Y, *out, *again)):
+            assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("dt,rows,width,hidden", PATHS)
+def test_feed_forward_keeps_what_is_not_finite_apart(cuda, dt, rows, width, hidden):
+    """A row that is not finite reaches its own row of Y and dX, a weight's row its own column of gate; everything else stays as
+    it was, bit for bit."""
+    import rank_orthonormalized_optimizer_amd as dion
+    t = DT[dt]
+    X, _, Wg, Wu, Wd, dY = ffn_inputs(cuda, rows, width, hidden, dt, 16)
+
+    def run():
+        gate, up = (torch.empty(rows, hidden, device=cuda, dtype=t) for _ in range(2))
+        Y, dX = dion.gated_ffn_(X, Wg, Wu, Wd, gate=gate, up=up), torch.empty_like(X)
+        dion.gated_ffn_grad_(X, Wg, Wu, Wd, dY, gate, up, dX)
+        return gate, up, Y, dX
+    clean = run()
+    bad = rows - 2
+    X[bad, width - 1], dY[bad, 0] = float("inf"), float("nan")
+    rest = torch.arange(rows, device=cuda) != bad
+    for name, a, b in zip(("gate", "up", "Y", "dX"), run(), clean):
+        assert torch.equal(a[rest], b[rest]), name
+    assert torch.isnan(run()[3][bad]).any()
+    X[bad, width - 1], dY[bad, 0] = 0, 0
+    clean = run()
+    for j, c in ((1, 0), (hidden - 1, width - 1)):   # the ends of a row, whose neighbours are other rows
+        Wg[j, c] = float("nan")
+    gate, up, _, _ = run()
+    other = torch.ones(hidden, dtype=torch.bool, device=cuda)
+    other[1] = other[hidden - 1] = False
+    assert torch.equal(gate[:, other], clean[0][:, other]) and torch.equal(up, clean[1])
+    assert torch.isnan(kept(gate) if t == BF16 else gate)[:, ~other].all()
