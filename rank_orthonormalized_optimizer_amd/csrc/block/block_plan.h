@@ -65,6 +65,8 @@ struct NormGradArgs {
 // its sums, and a narrow team leaves a CU more rows at a time.  2^26 elements, norm, to 8 bits and gradient (us): bf16 rows of
 // 1024 by a wave 92, 86, 81, by four 100, 182, 95; of 2048 by a wave 94, 94, 75, by four 92, 101, 73; of 8192 by four 96, 95, 75,
 // by sixteen 108, 161, 78; of 16384 by four 96, 98, 94, by sixteen 94, 134, 92, in fp32 210, 201, 153 and 199, 198, 198.
+// (bf16 rows of 1025 to 2048 that go to 8 bits are a wave's: with dropout 16384 rows of 2048 69 -> 56, of 1536 70 -> 62; in fp32 81 -> 86,
+// its gradient 104 -> 111.)
 struct NormPlan {
     int team, vecs;
     int64_t per_block;   // rows of a workgroup at a time

@@ -11,8 +11,8 @@
 // The mask is Philox4x32-10 over the elements' numbers: a call yields the words of four elements in a row, so the eight of
 // a vector take two calls, or three where the row does not start at a multiple of four.
 //
-// Bound by HBM: dropout of 65536 x 4096 bf16 with a residual 312 us (5.2 TB/s), norm of 16384 x 2048 bf16 to 8 bits with dropout 80 us
-// (2.9 TB/s: fp64 arithmetic), gradient of 65536 x 4096 with an fp32 stream 839 us (5.1 TB/s); small ones by the launch (one row
+// Bound by HBM: dropout of 65536 x 4096 bf16 with a residual 312 us (5.2 TB/s), norm of 16384 x 2048 bf16 to 8 bits with dropout 71 us
+// (3.3 TB/s: fp64 arithmetic and the mask), gradient of 65536 x 4096 with an fp32 stream 839 us (5.1 TB/s); small ones by the launch (one row
 // of 2048: 2.7 us).
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -463,6 +463,12 @@ int run_dropout(const DropoutArgs& a, void* stream) {
 }
 
 int run_rms_norm(const NormArgs& a, void* stream) {
+    if (a.scale && a.x_bf16 && a.d > 1024 && a.d <= 2048) {   // by a wave, which needs no barrier for the row's sum and largest
+        const dim3 grid((unsigned)ceil_div64(a.rows, 4));
+        if (a.s_bf16) hipLaunchKernelGGL((norm_kernel<true, true, 64, 4, true>), grid, dim3(256), 0, (hipStream_t)stream, a);
+        else hipLaunchKernelGGL((norm_kernel<true, false, 64, 4, true>), grid, dim3(256), 0, (hipStream_t)stream, a);
+        return (int)hipGetLastError();
+    }
     of_plan(make_norm_plan(a.rows, a.d), [&](auto t, auto v) {
         launch_norm<decltype(t)::value, decltype(v)::value>(a, (hipStream_t)stream);
     });
