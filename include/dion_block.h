@@ -101,11 +101,11 @@ int dion_rms_norm_grad(const void* dY, const void* h, const void* w, const float
  *   Y         device, [rows][width], dtype, written
  *   act       dion_activation
  * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores; u is rounded to bf16 for the second
- * product.  fp32 operands give fp32-accurate products: a, b and du from two fp16 parts of each row scaled by a power of two
+ * product, or for up to 64 rows to two bf16 parts.  fp32 operands give fp32-accurate products: a, b and du from two fp16 parts of each row scaled by a power of two
  * (2^-23 of an element and 2^-38 of its row's largest left out, three part products, terms below 2^-22 dropped; rows up to
  * 2^100), the others from three bf16 parts (an exact split, six part products, terms below 2^-24 dropped), and all of few
- * rows in fp32 (how many rows are few is a matter of the sizes).  8-bit rows go as bf16, which holds x scale exactly where scale is a power of two, as dion_rms_norm leaves
- * it, and is rounded else.  Operands are taken to be finite; others make what they reach NaN or infinite.
+ * rows in fp32 (how many rows are few is a matter of the sizes).  8-bit rows go as bf16, which holds x scale exactly where
+ * scale is a power of two, as dion_rms_norm leaves it, and is rounded else.  Operands are taken to be finite; others make what they reach NaN or infinite.
  * Workspace size: for_grad 0 for dion_gated_ffn, 1 for dion_gated_ffn_grad given gate and up, 2 without them; 0 for invalid
  * sizes.
  */
@@ -121,7 +121,7 @@ int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const vo
  *   dX             device, [rows][width], dtype, written (of the values that X stands for), or NULL
  *   dWg, dWu, dWd  device, shaped as the weights, dw_dtype, written, or added to with accumulate 1; dWg and dWu both or
  *                  neither NULL, dWd or NULL.  One output at least is given
- * Arithmetic: as above; da, db and u are rounded to bf16 where dtype is bf16, and a and b to the form in which they are kept.
+ * Arithmetic: as above; da, db and u are rounded to bf16 where dtype is bf16 (for up to 16 rows to two bf16 parts), and a and b to the form in which they are kept.
  */
 int dion_gated_ffn_grad(const void* X, const float* x_scale, const void* Wg, const void* Wu, const void* Wd, const void* dY,
                         const void* gate, const void* up, void* dX, void* dWg, void* dWu, void* dWd, int64_t rows,

@@ -108,6 +108,7 @@ struct FfnPlan {
     bool mid;                          // a moderate number of fp32 rows: the weights are read in place (run_mid_*), rows in planes
     int mgu, my, mdu, mdx;             // slices of those products' reductions
     int parts;                         // of the operands that are not fp16 planes: 1 or 3
+    int uparts;                        // of u, da and db: 1, 2 or 3
     bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
     Product gu, y, du, dx, dgu, dd, dw;   // (dw: dgu and dd at once)
     size_t x, w, wd, dy;               // their planes
@@ -204,6 +205,11 @@ inline int mid_slices(int64_t rows, int64_t cols, int64_t per, int64_t steps) {
     return (int)ceil_div64(units, ceil_div64(units, s));   // (all slices as long as the longest)
 }
 
+// bf16 calls of so few rows take two bf16 parts of u, da and db, whose rounding adds as much to the outputs' errors as the
+// outputs' own does.  That way and with one part (us): forward, 2048 x 5632 16 rows 28.0 and 26.7, 64 rows 29.7 and 26.7, 8192 x 8192 16
+// rows 99.4 and 99.1, 64 rows 107 and 97; gradients, 2048 x 5632 16 rows 63.6 and 55.5, 64 rows 75.2 and 64.0.
+constexpr int64_t kTwoPartRows = 64, kTwoPartGradRows = 16;
+
 // for_grad: the gradient; saved: gate and up are given to it
 inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16, int x8, int for_grad, int saved, FfnPlan* p) {
     FfnPlan q{};
@@ -211,11 +217,12 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
     q.dk = ceil_div64(width, 64) * 64;
     q.fk = ceil_div64(hidden, 64) * 64;
     q.parts = bf16 ? 1 : 3;
+    q.uparts = bf16 ? rows <= (for_grad ? kTwoPartGradRows : kTwoPartRows) ? 2 : 1 : 3;
     q.xpack = !bf16 || x8 || width != q.dk;
     q.wpack = !bf16 || width != q.dk;
     q.dpack = !bf16 || hidden != q.fk;
     q.ypack = !bf16 || width != q.dk;
-    const int64_t n = rows < 1 ? 1 : rows, terms = bf16 ? 1 : 6, scaled = bf16 ? 1 : 3;
+    const int64_t n = rows < 1 ? 1 : rows, terms = bf16 ? q.uparts : 6, scaled = bf16 ? 1 : 3;
     size_t off = 0, acc = 0;
     auto take = [&](int64_t bytes) { const size_t at = off; off += align256((size_t)bytes); return at; };
     auto plan = [&](Product& r, int64_t m, int64_t n, int64_t k, int64_t t, bool narrow, int64_t m2 = 0, int64_t n2 = 0) {
@@ -228,7 +235,7 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
         const int64_t sg = few_gate_slices(hidden, width), sd = few_gate_slices(width, hidden);
         int64_t sums = !for_grad || !saved ? (sg > 1 ? sg * 2 * q.fk : 0) : 0;
         auto most = [&](int64_t e) { if (e > sums) sums = e; };
-        q.u = take(n * q.fk * (bf16 ? 2 : 4));
+        q.u = take(n * q.fk * 4);   // (fp32, or two bf16 parts)
         if (for_grad) {
             q.dab = take(2 * n * q.fk * 4);
             most(few_slices(hidden, width, 1) * q.fk);
@@ -286,7 +293,7 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
         q.xinv = take(scale_rows(n) * 4);
         q.winv = take(2 * scale_rows(q.fk) * 4);
     }
-    q.u = take(q.parts * n * q.fk * 2);
+    q.u = take(q.uparts * n * q.fk * 2);
     plan(q.gu, 2 * q.fk, n, width, scaled, true);
     if (!for_grad) {
         plan(q.y, width, n, hidden, terms, true);
@@ -302,9 +309,9 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
             q.dinv = take(scale_rows(q.dk) * 4);
             q.yinv = take(scale_rows(n) * 4);
         }
-        q.dab = take(q.parts * n * 2 * q.fk * 2);
+        q.dab = take(q.uparts * n * 2 * q.fk * 2);
         plan(q.du, q.fk, n, width, scaled, true);
-        plan(q.dx, width, n, q.wpack ? 2 * q.fk : hidden, q.wpack ? terms : 2, true);   // (in place: two terms of hidden)
+        plan(q.dx, width, n, q.wpack ? 2 * q.fk : hidden, q.wpack ? terms : 2 * terms, true);   // (in place: twice the terms, of hidden)
         plan(q.dgu, width, 2 * q.fk, n, terms, false);
         plan(q.dd, hidden, width, n, terms, false);
         plan(q.dw, width, 2 * q.fk, n, terms, false, hidden, width);

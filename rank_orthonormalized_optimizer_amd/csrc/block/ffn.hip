@@ -241,7 +241,7 @@ struct GatedArgs {
     void* gate;            // [rows][f], or null
     void* up;
     uint16_t* u;           // planes [PARTS][rows][fk], or null (du)
-    uint16_t* dab;         // du: planes [PARTS][rows][2 fk], or null
+    uint16_t* dab;         // du: planes [PARTS][rows][2 fk], or for two parts [rows][2][2 fk], or null
     const float* xinv;     // fp32: what the sums of a row are multiplied by,
     const float* winv;     // and those of a column (a, and `winv_b` on b), du: null
     int winv_b;
@@ -352,7 +352,7 @@ __device__ __forceinline__ void put_parts(const Rows (&to)[PARTS], const Spot& s
 // a or b to its buffer, rows of d elements
 template <int PARTS, int H, bool EDGE>
 __device__ __forceinline__ void put_kept(const Rows& to, const Spot& s, int d, const float (&v)[H][4]) {
-    if constexpr (PARTS == 1) {
+    if constexpr (PARTS != 3) {
         uint32_t w[H][2];
 #pragma unroll
         for (int h = 0; h < H; ++h)
@@ -368,10 +368,10 @@ __device__ __forceinline__ void put_kept(const Rows& to, const Spot& s, int d, c
 // Two blocks of a or b as they are in memory.
 template <int PARTS>
 struct Raw {
-    u32x4 w[PARTS == 1 ? 1 : 2];
+    u32x4 w[PARTS != 3 ? 1 : 2];
     template <bool EDGE>
     __device__ __forceinline__ void load(const Rows& from, const Spot& s, int d) {
-        if constexpr (PARTS == 1) {
+        if constexpr (PARTS != 3) {
             w[0] = load_words<EDGE>(from, s, d);
         } else {
 #pragma unroll
@@ -380,7 +380,7 @@ struct Raw {
         }
     }
     __device__ __forceinline__ void get(float (&v)[2][4]) const {
-        if constexpr (PARTS == 1) {
+        if constexpr (PARTS != 3) {
             uint32_t t[2][2];
             untrade(w[0], t[0], t[1]);
 #pragma unroll
@@ -401,15 +401,17 @@ template <int PARTS>
 struct GatedRows {
     Rows gate, up, u[PARTS], da[PARTS], db[PARTS];
     __device__ __forceinline__ GatedRows(const GatedArgs& g, int64_t n) {
-        constexpr int B = PARTS == 1 ? 2 : 4;
+        constexpr int B = PARTS != 3 ? 2 : 4;
         gate = Rows::of<B>(g.gate, n, g.gate ? g.rows : 0, g.f);
         up = Rows::of<B>(g.up, n, g.up ? g.rows : 0, g.f);
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
             u[q] = Rows::of<2>(g.u + q * g.rows * g.fk, n, g.u ? g.rows : 0, g.fk);
-            da[q] = Rows::of<2>(g.dab + q * g.rows * 2 * g.fk, n, g.dab ? g.rows : 0, 2 * g.fk);
+            const int64_t at = PARTS == 2 ? (int64_t)q * 2 * g.fk : q * g.rows * 2 * g.fk;
+            constexpr int WIDE = PARTS == 2 ? 4 : 2;
+            da[q] = Rows::of<2>(g.dab + at, n, g.dab ? g.rows : 0, WIDE * g.fk);
             db[q] = da[q];
-            db[q].to = Rows::of<2>(g.dab + q * g.rows * 2 * g.fk + g.fk, n, g.dab ? g.rows : 0, 2 * g.fk).to;
+            db[q].to = Rows::of<2>(g.dab + at + g.fk, n, g.dab ? g.rows : 0, WIDE * g.fk).to;
         }
     }
 };
@@ -429,7 +431,7 @@ __device__ __forceinline__ void gated(const GatedArgs& g, const GatedRows<PARTS>
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float slope;
-            u[h][e] = activate<PARTS != 1>(g.act, a[h][e], slope) * b[h][e];
+            u[h][e] = activate<PARTS == 3>(g.act, a[h][e], slope) * b[h][e];
             if (EDGE && s.own(h) + e >= g.f) u[h][e] = 0.f;
         }
     put_parts<PARTS, H, EDGE>(to.u, s, g.fk, u);
@@ -445,7 +447,7 @@ __device__ __forceinline__ void dgated(const GatedArgs& g, const GatedRows<PARTS
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float slope;
-            const float v = activate<PARTS != 1>(g.act, a[h][e], slope);
+            const float v = activate<PARTS == 3>(g.act, a[h][e], slope);
             da[h][e] = du[h][e] * b[h][e] * slope;
             db[h][e] = du[h][e] * v;
             u[h][e] = v * b[h][e];
@@ -477,7 +479,7 @@ struct Gated : Single {
         constexpr int H = C::MI % 4 == 0 ? 2 : 1;
         const GatedRows<PARTS> to(g, n0);
         const int c0 = (m0 + l.xa) / 2;
-        const float x = PARTS == 1 ? 1.f : g.xinv[n0 + l.row];
+        const float x = PARTS != 3 ? 1.f : g.xinv[n0 + l.row];
 #pragma unroll
         for (int i = 0; i < C::MI; i += 2 * H) {
             float a[H][4], b[H][4];
@@ -485,7 +487,7 @@ struct Gated : Single {
             for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) { a[h][e] = v[i + 2 * h][e]; b[h][e] = v[i + 2 * h + 1][e]; }
-            if constexpr (PARTS != 1) {
+            if constexpr (PARTS == 3) {
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
                     const float* w = g.winv + c0 + 8 * i + 16 * h + 4 * l.quarter;
@@ -510,7 +512,7 @@ struct Dgated : Single {
     template <class C, bool EDGE>
     __device__ __forceinline__ void column(int, int m0, int n0, const Lane& l, const f32x4 (&v)[C::MI]) const {
         const GatedRows<PARTS> to(g, n0);
-        const float x = PARTS == 1 ? 1.f : g.xinv[n0 + l.row];
+        const float x = PARTS != 3 ? 1.f : g.xinv[n0 + l.row];
         Raw<PARTS> ra[C::MI / 2], rb[C::MI / 2];
 #pragma unroll
         for (int i = 0; i < C::MI; i += 2) {
@@ -526,7 +528,7 @@ struct Dgated : Single {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) du[h][e] = PARTS == 1 ? v[i + h][e] : v[i + h][e] * x;
+                for (int e = 0; e < 4; ++e) du[h][e] = PARTS != 3 ? v[i + h][e] : v[i + h][e] * x;
             dgated<PARTS, EDGE>(g, to, Spot{l.row, m0 + l.xa + 16 * i, l.quarter}, du, a, b);
         }
     }
@@ -636,12 +638,13 @@ void launch(const P& p, const Product& r, mm::Segments seg, float* acc, hipStrea
 template <bool GRAD, int PARTS>
 void launch_gated(const GatedArgs& g, const Product& r, mm::Segments seg, float* acc, hipStream_t s) {
     using P = typename std::conditional<GRAD, Dgated<PARTS>, Gated<PARTS>>::type;
-    of_tile<GRAD, false, PARTS != 1, !GRAD>(r.tile, [&](auto c) { launch<decltype(c)>(P(g), r, seg, acc, s); });
+    of_tile<GRAD, false, PARTS == 3, !GRAD>(r.tile, [&](auto c) { launch<decltype(c)>(P(g), r, seg, acc, s); });
 }
 
 template <bool GRAD>
 void launch_gated(const GatedArgs& g, const Product& r, int parts, float* acc, hipStream_t s) {
     if (parts == 1) launch_gated<GRAD, 1>(g, r, segments(1, 1), acc, s);
+    else if (parts == 2) launch_gated<GRAD, 2>(g, r, segments(1, 1), acc, s);
     else launch_gated<GRAD, 3>(g, r, segments(2, 2), acc, s);
 }
 
@@ -683,23 +686,23 @@ Inputs inputs(const FfnArgs& a, const FfnPlan& p, char* ws, bool forms, bool out
         in.x = mm::Operand{(const uint16_t*)a.X, 0, p.d, t};
         if (p.xpack && (forms || a.dWg)) {
             pack(jobs, {a.X, a.x_scale, nullptr, at(p.x), nullptr, nullptr, t, 0, p.t * p.dk, xkind, d});
-            in.x = mm::Operand{at(p.x), p.t * p.dk, p.dk, t};
+            in.x = mm::Operand{at(p.x), 0, p.dk, t};
         }
         in.w = mm::Operand{(const uint16_t*)a.Wg, 0, p.d, f, ((intptr_t)a.Wu - (intptr_t)a.Wg) / 2};
         if (p.wpack && (forms || a.dX)) {
             pack(jobs, {a.Wg, nullptr, nullptr, at(p.w), nullptr, nullptr, f, p.fk, wplane, kind, d});
             pack(jobs, {a.Wu, nullptr, nullptr, at(p.w) + wpair, nullptr, nullptr, f, p.fk, wplane, kind, d});
-            in.w = mm::Operand{at(p.w), wplane, p.dk, f, wpair};
+            in.w = mm::Operand{at(p.w), 0, p.dk, f, wpair};
         }
         in.wd = mm::Operand{(const uint16_t*)a.Wd, 0, p.f, d};
         if (p.dpack) {
             pack(jobs, {a.Wd, nullptr, nullptr, at(p.wd), nullptr, nullptr, d, 0, p.d * p.fk, kind, f});
-            in.wd = mm::Operand{at(p.wd), p.d * p.fk, p.fk, d};
+            in.wd = mm::Operand{at(p.wd), 0, p.fk, d};
         }
         in.dy = mm::Operand{(const uint16_t*)a.dY, 0, p.d, t};
         if (p.ypack && a.dY) {
             pack(jobs, {a.dY, nullptr, nullptr, at(p.dy), nullptr, nullptr, t, 0, p.t * p.dk, kind, d});
-            in.dy = mm::Operand{at(p.dy), p.t * p.dk, p.dk, t};
+            in.dy = mm::Operand{at(p.dy), 0, p.dk, t};
         }
         in.x16 = in.x; in.w16 = in.w; in.wd16 = in.wd; in.dy16 = in.dy;
         launch_pack(jobs, 1, s);
@@ -741,6 +744,12 @@ Inputs rows_in_planes(const FfnArgs& a, const FfnPlan& p, char* ws, bool x, hipS
     return in;
 }
 
+// The products of u, da and db: of bf16 operands, whose planes are all the same, with one part or two of them.
+mm::Segments part_products(const FfnPlan& p) {
+    if (p.parts == 3) return segments(3, 3);
+    return p.uparts == 2 ? mm::Segments{2, 1 | 1 << 2} : segments(1, 1);   // the second parts first
+}
+
 GatedArgs gated_args(const FfnArgs& a, const FfnPlan& p, const mm::Operand& w, const mm::Operand& x, int64_t m, char* ws) {
     GatedArgs g{};
     g.o = Operands{w, x, m, p.t};
@@ -773,9 +782,9 @@ int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
         return e ? e : run_mid_out(a, p, ws, stream);
     }
     const Inputs in = inputs(a, p, ws, true, true, s);
-    const mm::Segments seg = segments(p.parts, p.parts);
+    const mm::Segments seg = part_products(p);
     float* acc = (float*)(ws + p.acc);
-    launch_gated<false>(gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws), p.gu, p.parts, acc, s);
+    launch_gated<false>(gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws), p.gu, p.uparts, acc, s);
     const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
     launch_out<false, false>(Out<1>(out_args(in.wd, u, p.d, p.t, a.Y, a.bf16, 0)), p.y, seg, acc, s);
     return (int)hipGetLastError();
@@ -787,13 +796,13 @@ int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) 
     FfnArgs a = args;
     const bool form = !a.gate;
     const Inputs in = p.mid ? rows_in_planes(a, p, ws, form || a.dWg, s) : inputs(a, p, ws, form, false, s);
-    const mm::Segments seg = segments(p.parts, p.parts);
+    const mm::Segments seg = part_products(p);
     float* acc = (float*)(ws + p.acc);
     if (form) {
         a.gate = ws + p.gate;
         a.up = ws + p.up;
     }
-    const mm::Operand dab{(uint16_t*)(ws + p.dab), p.t * 2 * p.fk, 2 * p.fk, (int)p.t};
+    const mm::Operand dab{(uint16_t*)(ws + p.dab), p.uparts == 2 ? 2 * p.fk : p.t * 2 * p.fk, (p.uparts == 2 ? 4 : 2) * p.fk, (int)p.t};
     const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
     if (p.mid) {
         int e = form ? run_mid_gate(a, p, false, ws, stream) : 0;
@@ -804,13 +813,13 @@ int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) 
         if (form) {
             GatedArgs g = gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws);
             g.u = nullptr;
-            launch_gated<false>(g, p.gu, p.parts, acc, s);
+            launch_gated<false>(g, p.gu, p.uparts, acc, s);
         }
         GatedArgs g = gated_args(a, p, in.wd16, in.dy16, p.fk, ws);
         g.xinv = (const float*)(ws + p.yinv);
         g.dab = a.dX || a.dWg ? (uint16_t*)(ws + p.dab) : nullptr;
         if (!a.dWd) g.u = nullptr;
-        launch_gated<true>(g, p.du, p.parts, acc, s);
+        launch_gated<true>(g, p.du, p.uparts, acc, s);
         if (a.dX) {   // over da and Wg, db and Wu: two planes of one part each in place, one matrix of 2 fk rows where packed
             OutArgs o = out_args(in.w, dab, p.d, p.t, a.dX, a.bf16, 0);
             mm::Segments pairs = seg;
@@ -819,7 +828,8 @@ int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) 
             } else {
                 o.o.a.plane = in.w.pair;
                 o.o.b.plane = p.fk;
-                pairs = mm::Segments{2, 0 | (1 | 1 << 2) << 4};
+                pairs = p.uparts == 2 ? mm::Segments{4, 2 << 2 | (1 | 3 << 2) << 4 | 0 << 8 | (1 | 1 << 2) << 12}
+                                      : mm::Segments{2, 0 | (1 | 1 << 2) << 4};
             }
             launch_out<true, false>(Out<1>(o), p.dx, pairs, acc, s);
         }

@@ -36,7 +36,7 @@ struct FewArgs {
     int slices;           // of k; several: their sums go to
     float* acc;           // [slices][M][rows][ldout], for few_join_kernel
     int act;
-    void* out;            // u [rows][ldout] (M == 2) or null, or Y [rows][cols]
+    void* out;            // u (M == 2) or null, fp32 [rows][ldout] or bf16 parts [2][rows][ldout]; or Y [rows][cols]
     int ldout;
     void* gate;           // [rows][cols], or null
     void* up;
@@ -117,7 +117,14 @@ __device__ __forceinline__ void few_out(const FewArgs& a, int64_t row, int c, co
             keep4<BF16>(a.gate, row * a.cols, c, a.cols, p);
             keep4<BF16>(a.up, row * a.cols, c, a.cols, q);
         }
-        if (a.out) put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
+        if (a.out) {
+            put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
+            if constexpr (BF16) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] -= up16(down16(v[e]));
+                put4<BF16>(a.out, (a.rows + row) * a.ldout, c, a.cols, v);
+            }
+        }
     } else {
         put4<BF16>(a.out, row * a.cols, c, a.cols, p);
     }
@@ -133,9 +140,13 @@ __device__ __forceinline__ void rest(int n, F f) {
 }
 
 // M: matrices (2: Wg and Wu); NT: blocks of 16 rows of x; X8: which has 8 bits; WAVES share the reduction.
+// bf16 with one matrix: x is u in two parts, the second ones of row r in the place of row r + 8, so that u's rounding, which
+// would add as much to Y's error as Y's own, costs nothing.
 template <bool BF16, int M, int NT, bool X8, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
     using T = Few<BF16>;
+    constexpr bool SPLIT = BF16 && M == 1;
+    static_assert(!SPLIT || NT == 1, "rows r and r + 8");
     constexpr int U = M + NT <= 2 ? 12 : M + NT <= 3 ? 8 : 4;   // steps under way, as many as the registers hold
     __shared__ __attribute__((aligned(16))) f32x4 sums[WAVES][M * NT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -148,8 +159,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
     float s[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int r = 16 * j + lane % 16 < a.rows ? 16 * j + lane % 16 : a.rows - 1;
-        xrow[j] = (int64_t)r * a.ldx;
+        const int own = SPLIT ? lane % 8 : 16 * j + lane % 16, r = own < a.rows ? own : a.rows - 1;
+        xrow[j] = (int64_t)(SPLIT && lane % 16 >= 8 ? a.rows + r : r) * a.ldx;
         s[j] = X8 ? a.scale[r] : 1.f;
     }
     f32x4 sum[M][NT] = {};
@@ -209,6 +220,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void few_kernel(FewArgs a) {
     const int64_t row = 16 * wave + lane % 16;
     const int c = c0 + 4 * (lane / 16);
     if (row >= a.rows) return;
+    if constexpr (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) t[0] += sums[i][0][lane + 8];
+    }
     if (a.slices > 1) {   // (rows of a multiple of 64)
 #pragma unroll
         for (int m = 0; m < M; ++m) *(f32x4*)(a.acc + (((int64_t)slice * M + m) * a.rows + row) * a.ldout + c) = t[m];

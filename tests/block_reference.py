@@ -197,7 +197,9 @@ class Ffn:
             x = x * scale.to(F64).reshape(-1, 1)
         T, d, f = x.shape[0], x.shape[1], wg.shape[0]
         bf16 = t == torch.bfloat16
-        nseg, part = (1, half_step(t)) if bf16 else (6, U)
+        nseg, part = (1, half_step(t)) if bf16 else (6, U)   # products of parts, and what is left out of u, da and db
+        if bf16 and T <= (64 if dY is None else 16):   # two parts: the second one's rounding is left
+            nseg, part = 2, half_step(t) ** 2
 
         def grow(k):
             return (2 * nseg * k + 12) * U
