@@ -208,7 +208,7 @@ inline int mid_slices(int64_t rows, int64_t cols, int64_t per, int64_t steps) {
 // bf16 calls of so few rows take two bf16 parts of u, da and db, whose rounding adds as much to the outputs' errors as the
 // outputs' own does.  That way and with one part (us): forward, 2048 x 5632 16 rows 28.0 and 26.7, 64 rows 29.7 and 26.7, 8192 x 8192 16
 // rows 99.4 and 99.1, 64 rows 107 and 97; gradients, 2048 x 5632 16 rows 63.6 and 55.5, 64 rows 75.2 and 64.0.
-constexpr int64_t kTwoPartRows = 64, kTwoPartGradRows = 16;
+constexpr int64_t kTwoPartRows = 64, kTwoPartGradRows = 16;   // (narrow tiles for gradients)
 
 // for_grad: the gradient; saved: gate and up are given to it
 inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16, int x8, int for_grad, int saved, FfnPlan* p) {

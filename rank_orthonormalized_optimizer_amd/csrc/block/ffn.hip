@@ -17,7 +17,7 @@
 // Bound by the matrix cores, whose clocks fall under this load.  8192 x 2048 x 5632 bf16 (rows, width, hidden): a, b and u 362 us
 // (1.04 PFLOP/s, a library product of that shape 1.07), Y 156 (1.21), du, da, db and u 283 (0.67; a and b are read and three
 // outputs written), dX 297 (1.27), the three weights' gradients 485 (1.17).  4096 x 1024 x 4096 fp32, part products: a, b and u 197
-// us (1.05 PFLOP/s), Y 154 and 16 (1.21), du 240, dX 317 and 15 (1.25), gradients 569 (1.09), planes 3 x 30.
+// us (1.05 PFLOP/s), Y 154 and 16 (1.21), du 188 (0.55), dX 317 and 15 (1.25), gradients 569 (1.09), planes 3 x 30.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -513,23 +513,29 @@ struct Dgated : Single {
     __device__ __forceinline__ void column(int, int m0, int n0, const Lane& l, const f32x4 (&v)[C::MI]) const {
         const GatedRows<PARTS> to(g, n0);
         const float x = PARTS != 3 ? 1.f : g.xinv[n0 + l.row];
-        Raw<PARTS> ra[C::MI / 2], rb[C::MI / 2];
+        // fp32 ones, which are twice as wide, half a column at a time: a whole one spills (4096 x 1024 x 4096: 234 us, so 188)
+        constexpr int N = PARTS == 3 && C::MI >= 8 ? C::MI / 2 : C::MI;
 #pragma unroll
-        for (int i = 0; i < C::MI; i += 2) {
-            const Spot s{l.row, m0 + l.xa + 16 * i, l.quarter};
-            ra[i / 2].template load<EDGE>(to.gate, s, g.f);
-            rb[i / 2].template load<EDGE>(to.up, s, g.f);
-        }
+        for (int i0 = 0; i0 < C::MI; i0 += N) {
+            Raw<PARTS> ra[N / 2], rb[N / 2];
 #pragma unroll
-        for (int i = 0; i < C::MI; i += 2) {
-            float du[2][4], a[2][4], b[2][4];
-            ra[i / 2].get(a);
-            rb[i / 2].get(b);
+            for (int i = 0; i < N; i += 2) {
+                const Spot s{l.row, m0 + l.xa + 16 * (i0 + i), l.quarter};
+                ra[i / 2].template load<EDGE>(to.gate, s, g.f);
+                rb[i / 2].template load<EDGE>(to.up, s, g.f);
+            }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < N; i += 2) {
+                float du[2][4], a[2][4], b[2][4];
+                ra[i / 2].get(a);
+                rb[i / 2].get(b);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) du[h][e] = PARTS != 3 ? v[i + h][e] : v[i + h][e] * x;
-            dgated<PARTS, EDGE>(g, to, Spot{l.row, m0 + l.xa + 16 * i, l.quarter}, du, a, b);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) du[h][e] = PARTS != 3 ? v[i0 + i + h][e] : v[i0 + i + h][e] * x;
+                dgated<PARTS, EDGE>(g, to, Spot{l.row, m0 + l.xa + 16 * (i0 + i), l.quarter}, du, a, b);
+            }
+            if (N < C::MI) __builtin_amdgcn_sched_barrier(0);
         }
     }
 };
@@ -644,7 +650,8 @@ void launch_gated(const GatedArgs& g, const Product& r, mm::Segments seg, float*
 template <bool GRAD>
 void launch_gated(const GatedArgs& g, const Product& r, int parts, float* acc, hipStream_t s) {
     if (parts == 1) launch_gated<GRAD, 1>(g, r, segments(1, 1), acc, s);
-    else if (parts == 2) launch_gated<GRAD, 2>(g, r, segments(1, 1), acc, s);
+    else if (parts == 2 && GRAD) launch<mm::Config<128, 32, 4, 1, 4, true, false, false, false>>(Dgated<2>(g), r, segments(1, 1), acc, s);   // so few rows
+    else if (parts == 2) launch_gated<false, 2>(g, r, segments(1, 1), acc, s);
     else launch_gated<GRAD, 3>(g, r, segments(2, 2), acc, s);
 }
 
