@@ -7,7 +7,7 @@
 // through v_mfma_f32_16x16x32_bf16, fp32 through v_mfma_f32_16x16x4_f32, whose rate (157 TFLOP/s) is enough for the 2 x 16 NT
 // operations that an element of a matrix is worth here.
 //
-// Bound by the latency of two short kernels: one bf16 row, 2048 x 5632: 12.4 and 8.4 us (69 MB of weights, 14 us at the rate of
+// Bound by the latency of two short kernels: one bf16 row, 2048 x 5632: 12.2 and 8.7 us (69 MB of weights, 14 us at the rate of
 // a large copy), where tiles of 128 x 32 with sliced reductions take 26 in four launches.  8192 x 8192 (403 MB): 72 us, 5.6 TB/s.
 // With 8 instead of 12 steps under way the second kernel takes 11.0 us; waves that take every eighth step instead of a
 // piece of the rows, and twice the workgroups on a CU, measured the same.
