@@ -107,7 +107,8 @@ int dion_rms_norm_grad(const void* dY, const void* h, const void* w, const float
  * rows in fp32 (how many rows are few is a matter of the sizes).  8-bit rows go as bf16, which holds x scale exactly where
  * scale is a power of two, as dion_rms_norm leaves it, and is rounded else.  Operands are taken to be finite; others make what they reach NaN or infinite.
  * Workspace size: for_grad 0 for dion_gated_ffn, 1 for dion_gated_ffn_grad given gate and up, 2 without them; 0 for invalid
- * sizes.
+ * sizes.  It does not only grow with the rows, since few and many go different ways: a workspace for several numbers of rows
+ * has the largest of their sizes.
  */
 size_t dion_gated_ffn_workspace_size(int64_t rows, int64_t width, int64_t hidden, int dtype, int x_dtype, int for_grad);
 int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const void* Wu, const void* Wd, void* gate, void* up,

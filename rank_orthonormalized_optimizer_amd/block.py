@@ -215,7 +215,8 @@ def rms_norm_grad_(dY: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: tor
 
 def gated_ffn_workspace_for(rows: int, width: int, hidden: int, device, dtype=torch.bfloat16, *, x_dtype=None,
                             for_grad: bool = False, saved: bool = True) -> torch.Tensor:
-    """Scratch for one gated_ffn_ call, or with ``for_grad`` one gated_ffn_grad_ call (``saved``: given gate and up)."""
+    """Scratch for one gated_ffn_ call, or with ``for_grad`` one gated_ffn_grad_ call (``saved``: given gate and up), of these
+    sizes: fewer rows may need more."""
     x = _lib.E4M3 if x_dtype == E4M3 else _DT[dtype]
     return _scratch(int(_lib.load().dion_gated_ffn_workspace_size(rows, width, hidden, _DT[dtype], x,
                                                                   (1 if saved else 2) if for_grad else 0)), device)
