@@ -185,8 +185,8 @@ inline int64_t few_slices(int64_t cols, int64_t k, int64_t matrices) {
 
 // fp32 calls that read the weights in place beside planes of the rows (run_mid_*).  That way, and few rows' way or by tiles,
 // width x hidden (us): forward, 2048 x 5632 16 rows 64 and 60, 24 rows 64 and 87, 64 rows 71 and 146, 128 rows 102 and 148, 512 rows
-// 232 and 242; 1024 x 4096 64 rows 45 and 37, 96 rows 55 and 64, 512 rows 101 and 108; 768 x 2048 96 rows 52 and 41; 8192 x 8192 96
-// rows 307 and 683, 640 rows 1657 and 1432.  Gradients, 2048 x 5632 32 rows 121 and 114, 40 rows 124 and 134, 128 rows 188 and 273,
+// 232 and 242; 1024 x 4096 64 rows 45 and 37, 96 rows 53 and 64, 512 rows 102 and 108; 768 x 2048 96 rows 52 and 41; 8192 x 8192 96
+// rows 278 and 683, 640 rows 1657 and 1432.  Gradients, 2048 x 5632 32 rows 121 and 114, 40 rows 124 and 134, 128 rows 188 and 273,
 // 512 rows 424 and 496; 1024 x 4096 48 rows 66 and 63, 64 rows 69 and 83; 768 x 2048 128 rows 77 and 75, 256 rows 90 and 101; 1024 x 1024
 // 256 rows 82 and 78.
 constexpr int64_t kMidRowsF32 = 512;

@@ -308,10 +308,14 @@ __global__ __launch_bounds__(256) void mid_join_kernel(MidArgs a) {
 
 template <int KIND, bool TRANS>
 void launch_mid(MidArgs a, hipStream_t s) {
-    const int nt = a.rows <= 64 ? 4 : 8;
-    a.groups = (int)ceil_div64(a.rows, 16 * nt);
+    // as few groups as can be, of 64, 96 or 128 rows (96 instead of 128: forward, 8192 x 8192, 96 rows 307 us, so 278,
+    // 192 rows 539 and 464)
+    const int blocks = (int)ceil_div64(a.rows, 16);
+    a.groups = (blocks + 7) / 8;
+    const int nt = (blocks + a.groups - 1) / a.groups;
     const dim3 grid((unsigned)(ceil_div64(a.cols, kCols<KIND>) * a.slices * a.groups)), block(64 * kWaves);
-    if (nt == 4) hipLaunchKernelGGL((mid_kernel<KIND, TRANS, 4>), grid, block, 0, s, a);
+    if (nt <= 4) hipLaunchKernelGGL((mid_kernel<KIND, TRANS, 4>), grid, block, 0, s, a);
+    else if (nt <= 6) hipLaunchKernelGGL((mid_kernel<KIND, TRANS, 6>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((mid_kernel<KIND, TRANS, 8>), grid, block, 0, s, a);
     if (a.slices > 1)
         hipLaunchKernelGGL((mid_join_kernel<KIND>), dim3((unsigned)ceil_div64((int64_t)a.rows * (a.ldacc / 4), 256)), dim3(256), 0, s, a);
