@@ -180,10 +180,10 @@ def _plain_norm(s):
         return out
     top = y.abs().amax(1)
     m, e = torch.frexp(top)   # top = m 2^e, 0.5 <= m < 1; 448 = 0.875 2^9
-    scale = torch.where(top > 0, torch.exp2((e - 9 + (m > 0.875)).to(real)), 1.0)[:, None]
+    scale = torch.where(top > 0, torch.ldexp(torch.ones_like(top), e - 9 + (m > 0.875)), 1.0)[:, None]
     y /= scale
     _, e = torch.frexp(y.abs().clamp(min=2.0 ** -6))   # e4m3: four significant bits, steps of 2^-9 below 2^-6
-    step = torch.exp2((e - 4).to(real))
+    step = torch.ldexp(torch.ones_like(y), e - 4)
     out["y"] = (torch.round(y / step) * step * scale).float()
     out["scale"] = scale[:, 0].float()
     return out
