@@ -42,6 +42,8 @@ extern "C" {
 #define DION_E4M3 2
 
 typedef enum { DION_SILU = 0, DION_GELU = 1 } dion_activation;   /* a / (1 + exp(-a)); the tanh form of gelu */
+/* added to the activation, in both calls of a block: bf16's gate and up are kept in the even form */
+#define DION_KEEP_EVEN 16
 
 #define DION_BLOCK_MAX_ROWS ((int64_t)1 << 20)
 
@@ -95,11 +97,15 @@ int dion_rms_norm_grad(const void* dY, const void* h, const void* w, const float
  *   Wg, Wu    device, [hidden][width], dtype (DION_F32 or DION_BF16)
  *   Wd        device, [width][hidden], dtype
  *   gate, up  device, [rows][hidden], elements of dtype's size: a and b, written for the gradient; both or neither NULL.  In
- *             fp32 for fp32.  For bf16 in 16 bits of their own, more exact than bf16 where it counts: bit 15 the sign; bit 14
- *             set for magnitudes in [2^-8, 2^8), with 4 bits of exponent (from 2^-8) and 10 of fraction below it; else clear,
- *             with the upper 14 bits of the magnitude's fp32 form (8 of exponent, 6 of fraction).  Rounded to nearest, ties away from zero
+ *             fp32 for fp32.  For bf16 in 16 bits of their own, more exact than bf16 at the usual sizes: bit 15 the sign; bit 14
+ *             set for magnitudes in [2^-8, 2^8), with 4 bits of exponent (from 2^-8) and 10 of fraction below it; else clear.
+ *             Then with DION_KEEP_EVEN 7 bits of exponent n (2^(n - 80) below 72, else 2^(n - 64)) and 7 of fraction, as exact as
+ *             bf16; all zeros is 0, for what rounds to 2^-80 or less, and all ones NaN, for what rounds to 2^64 - 2^56 or more
+ *             and what is not finite.  Without it the upper 14 bits of the magnitude's fp32 form (8 of exponent, 6 of fraction):
+ *             any magnitude, at half of bf16's exactness, so twice its rounding in the gradients of blocks whose projections are
+ *             far from 1.  Rounded to nearest, ties away from zero
  *   Y         device, [rows][width], dtype, written
- *   act       dion_activation
+ *   act       dion_activation, and for bf16 DION_KEEP_EVEN or not (which counts where gate and up are given)
  * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores; u is rounded to bf16 for the second
  * product, or for up to 64 rows to two bf16 parts.  fp32 operands give fp32-accurate products: a, b and du from two fp16 parts of each row scaled by a power of two
  * (2^-23 of an element and 2^-38 of its row's largest left out, three part products, terms below 2^-22 dropped; rows up to
@@ -118,7 +124,8 @@ int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const vo
 /*
  * Its gradients.
  *   dY             device, [rows][width], dtype
- *   gate, up       from dion_gated_ffn on the same X, Wg, Wu, read only; or both NULL: formed again
+ *   gate, up       from dion_gated_ffn on the same X, Wg, Wu, with the same act, read only; or both NULL: formed again (for bf16
+ *                  in the even form)
  *   dX             device, [rows][width], dtype, written (of the values that X stands for), or NULL
  *   dWg, dWu, dWd  device, shaped as the weights, dw_dtype, written, or added to with accumulate 1; dWg and dWu both or
  *                  neither NULL, dWd or NULL.  One output at least is given

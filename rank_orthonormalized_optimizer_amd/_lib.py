@@ -53,6 +53,7 @@ VOCAB_EXPORTS = ("dion_embedding", "dion_embedding_grad_workspace_size", "dion_e
 # include/dion_block.h
 E4M3 = 2
 SILU, GELU = 0, 1
+KEEP_EVEN = 16
 BLOCK_MAX_ROWS = 1 << 20
 BLOCK_EXPORTS = ("dion_dropout", "dion_rms_norm", "dion_rms_norm_grad_workspace_size", "dion_rms_norm_grad",
                  "dion_gated_ffn_workspace_size", "dion_gated_ffn", "dion_gated_ffn_grad")

@@ -408,7 +408,8 @@ class MixedDion:
         kept = None
         if keep:
             shape = X.shape[:-1] + Wg.shape[:1]
-            kept = tuple(torch.empty(shape, dtype=Wg.dtype, device=Wg.device) for _ in range(2))
+            form = torch.int16 if Wg.dtype == torch.bfloat16 else Wg.dtype   # (16 bits as exact as bfloat16 at any scale)
+            kept = tuple(torch.empty(shape, dtype=form, device=Wg.device) for _ in range(2))
         return block.gated_ffn_(X, Wg, Wu, Wd, act=act, scale=scale, gate=kept and kept[0], up=kept and kept[1]), kept
 
     @torch.no_grad()

@@ -240,6 +240,17 @@ def _block(X, Wg, Wu, Wd, act, scale):
     return X.numel() // width, width, hidden, _DT[dtype], _DT[dtype] if scale is None else _lib.E4M3
 
 
+def _kept(gate, up, dtype, device, shape) -> int:
+    """Checks gate and up; what their form adds to the activation."""
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are kept together: give both or neither")
+    if gate is None:
+        return 0
+    _check(gate, "gate", (dtype, torch.int16) if dtype == torch.bfloat16 else (dtype,), device, shape)
+    _check(up, "up", (gate.dtype,), device, shape)
+    return _lib.KEEP_EVEN if gate.dtype == torch.int16 else 0
+
+
 def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor, *, act: str = "silu",
                scale: torch.Tensor | None = None, gate: torch.Tensor | None = None, up: torch.Tensor | None = None,
                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -247,18 +258,16 @@ def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Te
 
     X: [..., width]; Wg, Wu: [hidden, width]; Wd: [width, hidden]; all float32 or all bfloat16.  With ``scale`` (float32 per
     row) X is float8_e4m3fn and stands for ``X * scale``, as rms_norm_8bit_ leaves it.  act: "silu" or "gelu" (its tanh form).
-    gate, up: [..., hidden] of the weights' type, both or neither: filled with what gated_ffn_grad_ needs of the two
-    projections (for bfloat16 their bits are a 16-bit form of its own, described in dion_block.h, not bfloat16 numbers).
+    gate, up: [..., hidden], both or neither: filled with what gated_ffn_grad_ needs of the two projections, float32 for
+    float32 weights and int16 for bfloat16 ones, whose bits are a form described in dion_block.h: at least as exact as
+    bfloat16 from 2^-80 to 2^64 and three bits more so in [2^-8, 2^8).  (bfloat16 tensors are taken too.  Their bits are no
+    bfloat16 numbers either, but a form that has one bit less than those outside [2^-8, 2^8).)
     Returns (or fills) out, [..., width] of the weights' type.
     """
     _no_graph("gated_ffn_", "gated_ffn_grad_", ("X", X), ("Wg", Wg), ("Wu", Wu), ("Wd", Wd), ("out", out))
     rows, width, hidden, dt, xt = _block(X, Wg, Wu, Wd, act, scale)
     device, dtype, inner = Wg.device, Wg.dtype, X.shape[:-1] + (hidden,)
-    if (gate is None) != (up is None):
-        raise ValueError("gate and up are kept together: give both or neither")
-    if gate is not None:
-        _check(gate, "gate", (dtype,), device, inner)
-        _check(up, "up", (dtype,), device, inner)
+    act = _ACT[act] | _kept(gate, up, dtype, device, inner)
     with _On(device, stream) as handle:
         if out is None:
             out = torch.empty_like(X, dtype=dtype)
@@ -267,7 +276,7 @@ def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Te
         ws = _space(Wg, _lib.load().dion_gated_ffn_workspace_size(rows, width, hidden, dt, xt, 0)) if workspace is None \
             else _given_scratch(workspace, device)
         st = _lib.load().dion_gated_ffn(X.data_ptr(), _ptr(scale), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), _ptr(gate),
-                                        _ptr(up), out.data_ptr(), rows, width, hidden, _ACT[act], xt, dt, ws.data_ptr(),
+                                        _ptr(up), out.data_ptr(), rows, width, hidden, act, xt, dt, ws.data_ptr(),
                                         ws.numel(), handle)
     if st != _lib.OK:
         raise _lib.DionError(st, "dion_gated_ffn")
@@ -288,11 +297,7 @@ def gated_ffn_grad_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: tor
     rows, width, hidden, dt, xt = _block(X, Wg, Wu, Wd, act, scale)
     device, dtype, inner = Wg.device, Wg.dtype, X.shape[:-1] + (hidden,)
     _check(dY, "dY", (dtype,), device, X.shape)
-    if (gate is None) != (up is None):
-        raise ValueError("gate and up are kept together: give both or neither")
-    if gate is not None:
-        _check(gate, "gate", (dtype,), device, inner)
-        _check(up, "up", (dtype,), device, inner)
+    act = _ACT[act] | _kept(gate, up, dtype, device, inner)
     if dX is not None:
         _check(dX, "dX", (dtype,), device, X.shape)
     if (dWg is None) != (dWu is None):
@@ -309,7 +314,7 @@ def gated_ffn_grad_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: tor
             if workspace is None else _given_scratch(workspace, device)
         st = _lib.load().dion_gated_ffn_grad(X.data_ptr(), _ptr(scale), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(),
                                              dY.data_ptr(), _ptr(gate), _ptr(up), _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(dWd),
-                                             rows, width, hidden, _ACT[act], xt, dt, _DT[dw], int(bool(accumulate)),
+                                             rows, width, hidden, act, xt, dt, _DT[dw], int(bool(accumulate)),
                                              ws.data_ptr(), ws.numel(), handle)
     if st != _lib.OK:
         raise _lib.DionError(st, "dion_gated_ffn_grad")

@@ -41,6 +41,13 @@ bool is_dtype(int t) { return t == DION_F32 || t == DION_BF16; }
 int64_t size_of(int t) { return t == DION_E4M3 ? 1 : t == DION_BF16 ? 2 : 4; }
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
+// false: no activation, or a form of gate and up that the type does not have
+bool split_act(int& act, int dtype, int* even) {
+    *even = (act & DION_KEEP_EVEN) != 0;
+    act &= ~DION_KEEP_EVEN;
+    return (act == DION_SILU || act == DION_GELU) && (!*even || dtype == DION_BF16);
+}
+
 // false: p is no probability of dropping
 bool make_mask(double p, const int64_t* seed, int64_t site, dion::Mask* m) {
     if (!(p >= 0 && p < 1)) return false;
@@ -142,7 +149,8 @@ int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const vo
     if (!is_dtype(dtype) || (x_dtype != dtype && x_dtype != DION_E4M3)) return DION_ERR_DTYPE;
     dion::FfnPlan p;
     if (!make_plan(rows, width, hidden, dtype, x_dtype, 0, 0, &p)) return DION_ERR_SHAPE;
-    if (act != DION_SILU && act != DION_GELU) return DION_ERR_OPTION;
+    int even;
+    if (!split_act(act, dtype, &even)) return DION_ERR_OPTION;
     if (rows == 0) return DION_OK;
     if (!X || !Wg || !Wu || !Wd || !Y || !workspace || !gate != !up || (x_dtype == DION_E4M3) != (x_scale != nullptr))
         return DION_ERR_NULL;
@@ -157,7 +165,7 @@ int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const vo
     if (any_overlap(rs, 4, 9)) return DION_ERR_OVERLAP;
     dion::FfnArgs a{};
     a.X = X; a.x_scale = x_scale; a.Wg = Wg; a.Wu = Wu; a.Wd = Wd; a.Y = Y; a.gate = gate; a.up = up;
-    a.act = act; a.bf16 = dtype == DION_BF16;
+    a.act = act; a.bf16 = dtype == DION_BF16; a.even = even;
     const int e = dion::run_ffn(a, p, (char*)workspace, stream);
     return e ? DION_ERR_HIP - e : DION_OK;
 }
@@ -169,7 +177,8 @@ int dion_gated_ffn_grad(const void* X, const float* x_scale, const void* Wg, con
     if (!is_dtype(dtype) || !is_dtype(dw_dtype) || (x_dtype != dtype && x_dtype != DION_E4M3)) return DION_ERR_DTYPE;
     dion::FfnPlan p;
     if (!make_plan(rows, width, hidden, dtype, x_dtype, 1, gate != nullptr, &p)) return DION_ERR_SHAPE;
-    if ((act != DION_SILU && act != DION_GELU) || (accumulate != 0 && accumulate != 1)) return DION_ERR_OPTION;
+    int even;
+    if (!split_act(act, dtype, &even) || (accumulate != 0 && accumulate != 1)) return DION_ERR_OPTION;
     if ((!dX && !dWg && !dWd) || !dWg != !dWu || !gate != !up) return DION_ERR_NULL;
     if (rows == 0 && (accumulate || (!dWg && !dWd))) return DION_OK;
     if (rows > 0 && (!X || !Wg || !Wu || !Wd || !dY || !workspace || (x_dtype == DION_E4M3) != (x_scale != nullptr)))
@@ -196,7 +205,7 @@ int dion_gated_ffn_grad(const void* X, const float* x_scale, const void* Wg, con
     dion::FfnArgs a{};
     a.X = X; a.x_scale = x_scale; a.Wg = Wg; a.Wu = Wu; a.Wd = Wd; a.dY = dY; a.gate = (void*)gate; a.up = (void*)up;
     a.dX = dX; a.dWg = dWg; a.dWu = dWu; a.dWd = dWd;
-    a.act = act; a.bf16 = dtype == DION_BF16; a.dw_bf16 = dw_dtype == DION_BF16; a.accumulate = accumulate;
+    a.act = act; a.bf16 = dtype == DION_BF16; a.dw_bf16 = dw_dtype == DION_BF16; a.accumulate = accumulate; a.even = even;
     e = dion::run_ffn_grad(a, p, (char*)workspace, stream);
     return e ? DION_ERR_HIP - e : DION_OK;
 }

@@ -337,6 +337,7 @@ struct FfnArgs {
     void* dWu;
     void* dWd;
     int act, bf16, dw_bf16, accumulate;
+    int even;               // the form of gate and up, for bf16 operands
 };
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);

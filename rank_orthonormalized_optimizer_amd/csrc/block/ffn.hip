@@ -350,14 +350,14 @@ __device__ __forceinline__ void put_parts(const Rows (&to)[PARTS], const Spot& s
 }
 
 // a or b to its buffer, rows of d elements
-template <int PARTS, int H, bool EDGE>
+template <int PARTS, bool EVEN, int H, bool EDGE>
 __device__ __forceinline__ void put_kept(const Rows& to, const Spot& s, int d, const float (&v)[H][4]) {
     if constexpr (PARTS != 3) {
         uint32_t w[H][2];
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) w[h][e / 2] = keep32(v[h][e], v[h][e + 1]);
+            for (int e = 0; e < 4; e += 2) w[h][e / 2] = keep32<EVEN>(v[h][e], v[h][e + 1]);
         put_words<H, EDGE, false>(to, s, d, w);
     } else {
 #pragma unroll
@@ -366,7 +366,7 @@ __device__ __forceinline__ void put_kept(const Rows& to, const Spot& s, int d, c
 }
 
 // Two blocks of a or b as they are in memory.
-template <int PARTS>
+template <int PARTS, bool EVEN>
 struct Raw {
     u32x4 w[PARTS != 3 ? 1 : 2];
     template <bool EDGE>
@@ -386,7 +386,7 @@ struct Raw {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[h][e] = kept16(t[h][e / 2] >> (16 * (e % 2)) & 0xffffu);
+                for (int e = 0; e < 4; ++e) v[h][e] = kept16<EVEN>(t[h][e / 2] >> (16 * (e % 2)) & 0xffffu);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -417,12 +417,12 @@ struct GatedRows {
 };
 
 // u of H blocks from a and b, which are kept where asked for.
-template <int PARTS, int H, bool EDGE>
+template <int PARTS, bool EVEN, int H, bool EDGE>
 __device__ __forceinline__ void gated(const GatedArgs& g, const GatedRows<PARTS>& to, const Spot& s, const float (&a)[H][4],
                                       const float (&b)[H][4]) {
     if (g.gate) {
-        put_kept<PARTS, H, EDGE>(to.gate, s, g.f, a);
-        put_kept<PARTS, H, EDGE>(to.up, s, g.f, b);
+        put_kept<PARTS, EVEN, H, EDGE>(to.gate, s, g.f, a);
+        put_kept<PARTS, EVEN, H, EDGE>(to.up, s, g.f, b);
     }
     if (!g.u) return;
     float u[H][4];
@@ -467,7 +467,7 @@ struct Single {
 };
 
 // a and b: blocks 2 i and 2 i + 1 of a tile are a and b of the same 16 columns
-template <int PARTS>
+template <int PARTS, bool EVEN>
 struct Gated : Single {
     GatedArgs g;
     explicit Gated(const GatedArgs& a) : g(a) {}
@@ -496,13 +496,13 @@ struct Gated : Single {
                     for (int e = 0; e < 4; ++e) { a[h][e] = a[h][e] * x * wa[e]; b[h][e] = b[h][e] * x * wb[e]; }
                 }
             }
-            gated<PARTS, H, EDGE>(g, to, Spot{l.row, c0 + 8 * i, l.quarter}, a, b);
+            gated<PARTS, EVEN, H, EDGE>(g, to, Spot{l.row, c0 + 8 * i, l.quarter}, a, b);
         }
     }
 };
 
 // du.  A column's a and b are all on their way before the first is used.
-template <int PARTS>
+template <int PARTS, bool EVEN>
 struct Dgated : Single {
     GatedArgs g;
     explicit Dgated(const GatedArgs& a) : g(a) {}
@@ -517,7 +517,7 @@ struct Dgated : Single {
         constexpr int N = PARTS == 3 && C::MI >= 8 ? C::MI / 2 : C::MI;
 #pragma unroll
         for (int i0 = 0; i0 < C::MI; i0 += N) {
-            Raw<PARTS> ra[N / 2], rb[N / 2];
+            Raw<PARTS, EVEN> ra[N / 2], rb[N / 2];
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
                 const Spot s{l.row, m0 + l.xa + 16 * (i0 + i), l.quarter};
@@ -641,18 +641,21 @@ void launch(const P& p, const Product& r, mm::Segments seg, float* acc, hipStrea
     if (c.rem) hipLaunchKernelGGL((join_kernel<C, P>), dim3((unsigned)(c.rem * C::NI)), dim3(C::THREADS), 0, s, p, c, acc);
 }
 
-template <bool GRAD, int PARTS>
+template <bool GRAD, int PARTS, bool EVEN>
 void launch_gated(const GatedArgs& g, const Product& r, mm::Segments seg, float* acc, hipStream_t s) {
-    using P = typename std::conditional<GRAD, Dgated<PARTS>, Gated<PARTS>>::type;
-    of_tile<GRAD, false, PARTS == 3, !GRAD>(r.tile, [&](auto c) { launch<decltype(c)>(P(g), r, seg, acc, s); });
+    using P = typename std::conditional<GRAD, Dgated<PARTS, EVEN>, Gated<PARTS, EVEN>>::type;
+    if constexpr (GRAD && PARTS == 2) launch<mm::Config<128, 32, 4, 1, 4, true, false, false, false>>(P(g), r, seg, acc, s);   // so few rows
+    else of_tile<GRAD, false, PARTS == 3, !GRAD>(r.tile, [&](auto c) { launch<decltype(c)>(P(g), r, seg, acc, s); });
 }
 
+// even: the form of gate and up, for bf16 operands.  (One that is known when the kernel runs cost du of 8192 x 2048 x 5632 30 us.)
 template <bool GRAD>
-void launch_gated(const GatedArgs& g, const Product& r, int parts, float* acc, hipStream_t s) {
-    if (parts == 1) launch_gated<GRAD, 1>(g, r, segments(1, 1), acc, s);
-    else if (parts == 2 && GRAD) launch<mm::Config<128, 32, 4, 1, 4, true, false, false, false>>(Dgated<2>(g), r, segments(1, 1), acc, s);   // so few rows
-    else if (parts == 2) launch_gated<false, 2>(g, r, segments(1, 1), acc, s);
-    else launch_gated<GRAD, 3>(g, r, segments(2, 2), acc, s);
+void launch_gated(const GatedArgs& g, const Product& r, int parts, int even, float* acc, hipStream_t s) {
+    if (parts == 3) launch_gated<GRAD, 3, false>(g, r, segments(2, 2), acc, s);
+    else if (parts == 1 && even) launch_gated<GRAD, 1, true>(g, r, segments(1, 1), acc, s);
+    else if (parts == 1) launch_gated<GRAD, 1, false>(g, r, segments(1, 1), acc, s);
+    else if (even) launch_gated<GRAD, 2, true>(g, r, segments(1, 1), acc, s);
+    else launch_gated<GRAD, 2, false>(g, r, segments(1, 1), acc, s);
 }
 
 template <bool TA, bool TB, int N>
@@ -791,7 +794,7 @@ int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
     const Inputs in = inputs(a, p, ws, true, true, s);
     const mm::Segments seg = part_products(p);
     float* acc = (float*)(ws + p.acc);
-    launch_gated<false>(gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws), p.gu, p.uparts, acc, s);
+    launch_gated<false>(gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws), p.gu, p.uparts, a.even, acc, s);
     const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
     launch_out<false, false>(Out<1>(out_args(in.wd, u, p.d, p.t, a.Y, a.bf16, 0)), p.y, seg, acc, s);
     return (int)hipGetLastError();
@@ -808,6 +811,7 @@ int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) 
     if (form) {
         a.gate = ws + p.gate;
         a.up = ws + p.up;
+        a.even = 1;
     }
     const mm::Operand dab{(uint16_t*)(ws + p.dab), p.uparts == 2 ? 2 * p.fk : p.t * 2 * p.fk, (p.uparts == 2 ? 4 : 2) * p.fk, (int)p.t};
     const mm::Operand u{(uint16_t*)(ws + p.u), p.t * p.fk, p.fk, (int)p.t};
@@ -820,13 +824,13 @@ int run_ffn_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stream) 
         if (form) {
             GatedArgs g = gated_args(a, p, in.w16, in.x16, 2 * p.fk, ws);
             g.u = nullptr;
-            launch_gated<false>(g, p.gu, p.uparts, acc, s);
+            launch_gated<false>(g, p.gu, p.uparts, a.even, acc, s);
         }
         GatedArgs g = gated_args(a, p, in.wd16, in.dy16, p.fk, ws);
         g.xinv = (const float*)(ws + p.yinv);
         g.dab = a.dX || a.dWg ? (uint16_t*)(ws + p.dab) : nullptr;
         if (!a.dWd) g.u = nullptr;
-        launch_gated<true>(g, p.du, p.uparts, acc, s);
+        launch_gated<true>(g, p.du, p.uparts, a.even, acc, s);
         if (a.dX) {   // over da and Wg, db and Wu: two planes of one part each in place, one matrix of 2 fk rows where packed
             OutArgs o = out_args(in.w, dab, p.d, p.t, a.dX, a.bf16, 0);
             mm::Segments pairs = seg;

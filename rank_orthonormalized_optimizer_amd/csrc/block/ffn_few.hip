@@ -35,7 +35,7 @@ struct FewArgs {
     int rows, cols, k, ldx;
     int slices;           // of k; several: their sums go to
     float* acc;           // [slices][M][rows][ldout], for few_join_kernel
-    int act;
+    int act, even;
     void* out;            // u (M == 2) or null, fp32 [rows][ldout] or bf16 parts [2][rows][ldout]; or Y [rows][cols]
     int ldout;
     void* gate;           // [rows][cols], or null
@@ -88,9 +88,16 @@ template <> struct Few<false> {
 };
 
 template <bool BF16>
-__device__ __forceinline__ void keep4(void* p, int64_t row, int c, int d, const float (&v)[4]) {
+__device__ __forceinline__ void keep4(void* p, int64_t row, int c, int d, int even, const float (&v)[4]) {
     if constexpr (BF16) {
-        const uint32_t w[2] = {keep32(v[0], v[1]), keep32(v[2], v[3])};
+        uint32_t w[2];
+        if (even) {
+            w[0] = keep32<true>(v[0], v[1]);
+            w[1] = keep32<true>(v[2], v[3]);
+        } else {
+            w[0] = keep32<false>(v[0], v[1]);
+            w[1] = keep32<false>(v[2], v[3]);
+        }
         if (c + 4 <= d) {
             *(u32x2_any*)((uint16_t*)p + row + c) = u32x2{w[0], w[1]};
         } else {
@@ -114,8 +121,8 @@ __device__ __forceinline__ void few_out(const FewArgs& a, int64_t row, int c, co
             v[e] = activate<!BF16>(a.act, p[e], slope) * q[e];
         }
         if (a.gate) {
-            keep4<BF16>(a.gate, row * a.cols, c, a.cols, p);
-            keep4<BF16>(a.up, row * a.cols, c, a.cols, q);
+            keep4<BF16>(a.gate, row * a.cols, c, a.cols, a.even, p);
+            keep4<BF16>(a.up, row * a.cols, c, a.cols, a.even, q);
         }
         if (a.out) {
             put4<BF16>(a.out, row * a.ldout, c, a.cols, v);
@@ -285,7 +292,7 @@ FewArgs gate_args(const FfnArgs& a, const FfnPlan& p, char* ws) {
     FewArgs g{};
     g.slices = (int)few_gate_slices(p.f, p.d); g.acc = (float*)(ws + p.acc); g.ldout = (int)p.fk;
     g.w[0] = a.Wg; g.w[1] = a.Wu; g.x = a.X; g.scale = a.x_scale;
-    g.rows = (int)p.t; g.cols = (int)p.f; g.k = (int)p.d; g.ldx = (int)p.d; g.act = a.act;
+    g.rows = (int)p.t; g.cols = (int)p.f; g.k = (int)p.d; g.ldx = (int)p.d; g.act = a.act; g.even = a.even;
     g.gate = a.gate; g.up = a.up;
     return g;
 }
