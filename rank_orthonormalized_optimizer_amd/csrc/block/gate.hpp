@@ -28,7 +28,7 @@ template <bool EXACT>
 __device__ __forceinline__ float activate(int act, float a, float& slope) {
     float x = a, z = a, dz = 1.f;
     if (act != DION_SILU) {
-        x = fminf(fmaxf(a, -30.f), 30.f);
+        x = a < -30.f ? -30.f : a > 30.f ? 30.f : a;   // (a NaN stays one)
         const float q = x * x;
         z = 1.59576912f * x * fmaf(0.044715f, q, 1.f);
         dz = 1.59576912f * fmaf(0.134145f, q, 1.f);
