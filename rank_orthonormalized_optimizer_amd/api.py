@@ -302,7 +302,8 @@ class MixedDion:
     gradients itself: ``lookup`` and ``lookup_grad``, ``head_loss``; so can the parameters of the residual
     blocks between them: ``norm`` and ``norm_grad``, ``feed_forward`` and ``feed_forward_grad``.  All
     contributions since the last step add up (tied weights, microbatches), in float32 whatever the
-    parameter's type, and ``step`` takes them where ``grads`` holds None.
+    parameter's type, and ``step`` takes them where ``grads`` holds None.  Calls that gather, and ``step``, run on
+    torch's current stream; a program that changes it between them orders the streams.
     """
 
     def __init__(self, params, *, lr: float = 0.01, mu: float = 0.95, rank_fraction: float = 0.25,
@@ -381,11 +382,15 @@ class MixedDion:
         return call(x, self.params[self._index(i)], eps, **kw)
 
     @torch.no_grad()
-    def norm_grad(self, i: int, dY: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, **kw):
-        """Gradients ``(dh, dx)`` of ``norm`` (rms_norm_grad_; ``kw``: its dsum, p, seed, site, dh and dx); adds the weight's."""
+    def norm_grad(self, i: int, dY: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, *, dsum: torch.Tensor | None = None,
+                  p: float = 0.0, seed: torch.Tensor | None = None, site: int = 0, dh: torch.Tensor | None = None,
+                  dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+        """Gradients ``(dh, dx)`` of ``norm`` (rms_norm_grad_, with its arguments but for a stream: what is gathered belongs to
+        the current one, as in every call that gathers); adds the weight's."""
         i = self._index(i)
         dw, add = self._gather(i)
-        out = block.rms_norm_grad_(dY, h, self.params[i], rstd, dw, accumulate=add, **kw)
+        out = block.rms_norm_grad_(dY, h, self.params[i], rstd, dw, dsum=dsum, p=p, seed=seed, site=site, dh=dh, dx=dx,
+                                   accumulate=add, workspace=workspace)
         self.pending.add(i)
         return out
 
