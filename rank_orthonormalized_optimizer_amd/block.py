@@ -99,7 +99,7 @@ _Q8 = (E4M3,)
 
 
 def _norm(call, x, w, eps, residual, p, seed, site, h, y, scale, rstd, eight, stream):
-    _no_graph(call, "rms_norm_grad_", ("x", x), ("w", w), ("residual", residual))
+    _no_graph(call, "rms_norm_grad_", ("x", x), ("w", w), ("residual", residual), ("h", h), ("out", y), ("scale", scale), ("rstd", rstd))
     _need(x, "x", _DT)
     device, shape = x.device, x.shape
     rows, width = _rows(x, "x")
@@ -264,7 +264,8 @@ def gated_ffn_(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Te
     bfloat16 numbers either, but a form that has one bit less than those outside [2^-8, 2^8).)
     Returns (or fills) out, [..., width] of the weights' type.
     """
-    _no_graph("gated_ffn_", "gated_ffn_grad_", ("X", X), ("Wg", Wg), ("Wu", Wu), ("Wd", Wd), ("out", out))
+    _no_graph("gated_ffn_", "gated_ffn_grad_", ("X", X), ("Wg", Wg), ("Wu", Wu), ("Wd", Wd), ("scale", scale), ("gate", gate), ("up", up),
+              ("out", out))
     rows, width, hidden, dt, xt = _block(X, Wg, Wu, Wd, act, scale)
     device, dtype, inner = Wg.device, Wg.dtype, X.shape[:-1] + (hidden,)
     act = _ACT[act] | _kept(gate, up, dtype, device, inner)
