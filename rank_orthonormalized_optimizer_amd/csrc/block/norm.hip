@@ -161,6 +161,15 @@ __device__ __forceinline__ float to_odd(double x) {
     return __uint_as_float((rest > 0.0) == (x > 0.0) ? b + 1 : b - 1);
 }
 
+// The same to 20 bits of fraction in two instructions and the conversion, for bf16's seven (subnormal numbers of fp32 may still be
+// rounded twice).  16384 rows of 2048, the stream rounded to fp32 first 45 us, so 46, with to_odd 51.
+__device__ __forceinline__ float to_20_odd(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    const uint32_t low = (uint32_t)b;
+    return (float)__longlong_as_double((long long)((b & 0xffffffff00000000u) | (uint64_t)(low != 0 ? 1u : 0u) << 32));
+}
+__device__ __forceinline__ float to_20_odd(float x) { return x; }
+
 // Q8: in fp64, y in 8 bits.
 template <bool XB, bool SB, int TEAM, int VECS, bool Q8>
 __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs a) {
@@ -196,7 +205,7 @@ __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs 
         if (a.h) {
             float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = (float)h[i][e];
+            for (int e = 0; e < 8; ++e) o[e] = SB ? to_20_odd(h[i][e]) : (float)h[i][e];   // (rounded once)
             put8<SB>(a.h, at, c, a.d, o);
         }
 #pragma unroll
