@@ -128,7 +128,7 @@ int dion_gated_ffn(const void* X, const float* x_scale, const void* Wg, const vo
  *                  in the even form)
  *   dX             device, [rows][width], dtype, written (of the values that X stands for), or NULL
  *   dWg, dWu, dWd  device, shaped as the weights, dw_dtype, written, or added to with accumulate 1; dWg and dWu both or
- *                  neither NULL, dWd or NULL.  One output at least is given
+ *                  neither NULL, dWd or NULL.  One output at least is given, where there are rows
  * Arithmetic: as above; da, db and u are rounded to bf16 where dtype is bf16 (for up to 16 rows to two bf16 parts), and a and b to the form in which they are kept.
  */
 int dion_gated_ffn_grad(const void* X, const float* x_scale, const void* Wg, const void* Wu, const void* Wd, const void* dY,

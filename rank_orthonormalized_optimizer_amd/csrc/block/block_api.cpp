@@ -179,7 +179,8 @@ int dion_gated_ffn_grad(const void* X, const float* x_scale, const void* Wg, con
     if (!make_plan(rows, width, hidden, dtype, x_dtype, 1, gate != nullptr, &p)) return DION_ERR_SHAPE;
     int even;
     if (!split_act(act, dtype, &even) || (accumulate != 0 && accumulate != 1)) return DION_ERR_OPTION;
-    if ((!dX && !dWg && !dWd) || !dWg != !dWu || !gate != !up) return DION_ERR_NULL;
+    // (no rows: dX has no elements, and an array without any may be NULL)
+    if ((rows > 0 && !dX && !dWg && !dWd) || !dWg != !dWu || !gate != !up) return DION_ERR_NULL;
     if (rows == 0 && (accumulate || (!dWg && !dWd))) return DION_OK;
     if (rows > 0 && (!X || !Wg || !Wu || !Wd || !dY || !workspace || (x_dtype == DION_E4M3) != (x_scale != nullptr)))
         return DION_ERR_NULL;
