@@ -68,7 +68,8 @@ int dion_dropout(const void* x, const void* residual, void* out, int64_t n, doub
  *   scale     device fp32 [rows], written where y_dtype is DION_E4M3 (1 for a row of zeros), else NULL
  *   rstd      device fp32 [rows], written, or NULL
  *   eps       >= 0, finite.  p, seed, site as above, over rows x width elements
- * Arithmetic: in fp32; y is formed from h before its rounding.  With DION_E4M3 in fp64, so that no rounding on the way moves
+ * Arithmetic: in fp32; y is formed from h before its rounding; rows whose squares leave fp32's range are scaled first (rstd
+ * itself may then be subnormal, or infinite above 2^128).  With DION_E4M3 in fp64, so that no rounding on the way moves
  * a value across a border of its 8-bit numbers.  Elements that are not finite become NaN in 8 bits and do not count for scale.
  */
 int dion_rms_norm(const void* x, const void* residual, const void* w, void* h, void* y, float* scale, float* rstd,

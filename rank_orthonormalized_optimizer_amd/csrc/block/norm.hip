@@ -212,8 +212,28 @@ __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs 
         for (int e = 0; e < 8; ++e) sum += h[i][e] * h[i][e];   // zeros behind column d (where a mask may keep them)
     }
     sum = team<TEAM, Sum>(sum, red[0]);
-    const F rstd = (F)1 / sqrt(sum / (F)a.d + (F)a.eps);
-    if (a.rstd && t == 0) a.rstd[row] = (float)rstd;
+    F rstd = (F)1 / sqrt(sum / (F)a.d + (F)a.eps), seen = rstd;
+    if constexpr (!Q8) {
+        // Squares that leave fp32's range: the row again, times a power of two that brings them back (the same for the team).
+        // With eps at least 2^-100 nothing that underflows counts.  (The code alone costs rows of 65536 174 -> 181 us, others nothing.)
+        if (sum == INFINITY || (sum < 0x1p-70f && a.eps < 0x1p-100)) {
+            const bool large = sum == INFINITY;
+            const float f = large ? 0x1p-80f : 0x1p90f;
+            sum = 0;
+#pragma unroll
+            for (int i = 0; i < VECS; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    h[i][e] *= f;
+                    sum += h[i][e] * h[i][e];
+                }
+            sum = team<TEAM, Sum>(sum, red[1]);
+            const double exact = 1.0 / sqrt((double)sum / a.d * (large ? 0x1p160 : 0x1p-180) + a.eps);
+            seen = (float)exact;
+            rstd = (float)(exact * (large ? 0x1p80 : 0x1p-90));
+        }
+    }
+    if (a.rstd && t == 0) a.rstd[row] = (float)seen;
     float y[VECS][8], top = 0.f;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
