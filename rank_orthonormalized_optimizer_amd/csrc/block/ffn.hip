@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void planes_kernel(PackJobs jobs) {
             load_any8(job, row, c, d, s, v);
             fold8(job, c, d, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+            for (int e = 0; e < 8; ++e) top = fabsf(v[e]) < INFINITY ? fmaxf(top, fabsf(v[e])) : top;   // (others reach no scale)
         }
 #pragma unroll
         for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
