@@ -106,7 +106,8 @@ struct FfnPlan {
     int64_t t, d, f, dk, fk;
     bool few;                          // few rows: the weights are read in place (run_ffn_few; fp32 gradients: run_ffn_few_grad)
     bool mid;                          // a moderate number of fp32 rows: the weights are read in place (run_mid_*), rows in planes
-    int mgu, my, mdu, mdx;             // slices of those products' reductions
+    int fgu, fy, fdu, fdx;             // slices of few rows' reductions: of a and b, Y, du, dX
+    int mgu, my, mdu, mdx;             // of a moderate number's
     int parts;                         // of the operands that are not fp16 planes: 1 or 3
     int uparts;                        // of u, da and db: 1, 2 or 3
     bool xpack, wpack, dpack, ypack;   // X, Wg and Wu, Wd, dY go through planes in the workspace
@@ -232,20 +233,26 @@ inline bool make_ffn_plan(int64_t rows, int64_t width, int64_t hidden, int bf16,
     q.mid = !bf16 && mid_rows(rows, width * hidden, for_grad);
     q.few = !q.mid && rows <= (for_grad ? bf16 ? 0 : kFewGradRowsF32 : bf16 ? kFewRows : kFewRowsF32);
     if (q.few) {
-        const int64_t sg = few_gate_slices(hidden, width), sd = few_gate_slices(width, hidden);
-        int64_t sums = !for_grad || !saved ? (sg > 1 ? sg * 2 * q.fk : 0) : 0;
+        int64_t sums = 0;
         auto most = [&](int64_t e) { if (e > sums) sums = e; };
+        if (!for_grad || !saved) {
+            q.fgu = (int)few_gate_slices(hidden, width);
+            if (q.fgu > 1) most(q.fgu * 2 * q.fk);
+        }
         q.u = take(n * q.fk * 4);   // (fp32, or two bf16 parts)
         if (for_grad) {
             q.dab = take(2 * n * q.fk * 4);
-            most(few_slices(hidden, width, 1) * q.fk);
-            most(few_slices(width, hidden, 2) * q.dk);
+            q.fdu = (int)few_slices(hidden, width, 1);
+            q.fdx = (int)few_slices(width, hidden, 2);
+            most(q.fdu * q.fk);
+            most(q.fdx * q.dk);
             if (!saved) {
                 q.gate = take(n * hidden * 4);
                 q.up = take(n * hidden * 4);
             }
-        } else if (sd > 1) {
-            most(sd * q.dk);
+        } else {
+            q.fy = (int)few_gate_slices(width, hidden);
+            if (q.fy > 1) most(q.fy * q.dk);
         }
         q.acc = take(sums * n * 4);
         q.total = off;

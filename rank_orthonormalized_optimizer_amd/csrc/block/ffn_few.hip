@@ -290,7 +290,7 @@ namespace {
 
 FewArgs gate_args(const FfnArgs& a, const FfnPlan& p, char* ws) {
     FewArgs g{};
-    g.slices = (int)few_gate_slices(p.f, p.d); g.acc = (float*)(ws + p.acc); g.ldout = (int)p.fk;
+    g.slices = p.fgu; g.acc = (float*)(ws + p.acc); g.ldout = (int)p.fk;
     g.w[0] = a.Wg; g.w[1] = a.Wu; g.x = a.X; g.scale = a.x_scale;
     g.rows = (int)p.t; g.cols = (int)p.f; g.k = (int)p.d; g.ldx = (int)p.d; g.act = a.act; g.even = a.even;
     g.gate = a.gate; g.up = a.up;
@@ -313,7 +313,7 @@ int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
     FewArgs d{};
     d.w[0] = a.Wd; d.x = ws + p.u;
     d.rows = (int)p.t; d.cols = (int)p.d; d.k = (int)p.f; d.ldx = (int)p.fk;
-    d.slices = (int)few_gate_slices(p.d, p.f); d.acc = g.acc; d.ldout = (int)p.dk;
+    d.slices = p.fy; d.acc = g.acc; d.ldout = (int)p.dk;
     d.out = a.Y;
     if (a.bf16) {
         launch_few<true, 2>(g, s);

@@ -286,7 +286,7 @@ int run_ffn_few_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stre
     DownArgs g{};
     g.w[0] = (const float*)a.Wd; g.x[0] = (const float*)a.dY;
     g.rows = (int)p.t; g.cols = (int)p.f; g.k = (int)p.d; g.ldx = (int)p.d; g.act = a.act;
-    g.slices = (int)few_slices(p.f, p.d, 1); g.ldacc = (int)p.fk; g.acc = (float*)(ws + p.acc);
+    g.slices = p.fdu; g.ldacc = (int)p.fk; g.acc = (float*)(ws + p.acc);
     g.gate = (const float*)a.gate; g.up = (const float*)a.up;
     g.da = (float*)(ws + p.dab); g.db = g.da + p.t * p.fk; g.u = (float*)(ws + p.u); g.ldout = (int)p.fk;
     launch_down<1>(g, s);
@@ -294,7 +294,7 @@ int run_ffn_few_grad(const FfnArgs& args, const FfnPlan& p, char* ws, void* stre
         DownArgs x{};
         x.w[0] = (const float*)a.Wg; x.w[1] = (const float*)a.Wu; x.x[0] = g.da; x.x[1] = g.db;
         x.rows = (int)p.t; x.cols = (int)p.d; x.k = (int)p.f; x.ldx = (int)p.fk;
-        x.slices = (int)few_slices(p.d, p.f, 2); x.ldacc = (int)p.dk; x.acc = g.acc;
+        x.slices = p.fdx; x.ldacc = (int)p.dk; x.acc = g.acc;
         x.out = (float*)a.dX;
         launch_down<2>(x, s);
     }
