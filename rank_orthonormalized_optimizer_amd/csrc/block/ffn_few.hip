@@ -300,9 +300,7 @@ FewArgs gate_args(const FfnArgs& a, const FfnPlan& p, char* ws) {
 }  // namespace
 
 int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream) {
-    const FewArgs g = gate_args(a, p, ws);
-    if (a.bf16) launch_few<true, 2>(g, (hipStream_t)stream);
-    else launch_few<false, 2>(g, (hipStream_t)stream);
+    launch_few<false, 2>(gate_args(a, p, ws), (hipStream_t)stream);
     return (int)hipGetLastError();
 }
 
