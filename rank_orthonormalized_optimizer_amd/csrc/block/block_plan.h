@@ -65,8 +65,9 @@ struct NormGradArgs {
 // its sums, and a narrow team leaves a CU more rows at a time.  2^26 elements, norm, to 8 bits and gradient (us): bf16 rows of
 // 1024 by a wave 92, 86, 81, by four 100, 182, 95; of 2048 by a wave 94, 94, 75, by four 92, 101, 73; of 8192 by four 96, 95, 75,
 // by sixteen 108, 161, 78; of 16384 by four 96, 98, 94, by sixteen 94, 134, 92, in fp32 210, 201, 153 and 199, 198, 198.
-// (bf16 rows of 1025 to 2048 that go to 8 bits are a wave's: with dropout 16384 rows of 2048 69 -> 56, of 1536 70 -> 62; in fp32 81 -> 86,
-// its gradient 104 -> 111.)
+// bf16 rows of 1025 to 2048 that go to 8 bits are a wave's too: 16384 rows of 2048 with dropout, calls in a row over buffers that no
+// cache holds, by a wave 61, by four 72, of 1536 64 and 69, 32768 rows of 2048 without dropout 93 and 105; in fp32 by a wave 86, by
+// four 81, its gradient 111 and 104.
 struct NormPlan {
     int team, vecs;
     int64_t per_block;   // rows of a workgroup at a time
@@ -74,10 +75,11 @@ struct NormPlan {
     size_t total;        // bytes of the partial sums
 };
 
-inline NormPlan make_norm_plan(int64_t rows, int64_t width) {
+// wave: of bf16 rows that go to 8 bits, which a wave holds twice as much of
+inline NormPlan make_norm_plan(int64_t rows, int64_t width, bool wave = false) {
     NormPlan p{};
     const int64_t v = ceil_div64(width, 8);   // vectors of a row
-    p.team = v <= 128 ? 64 : v <= 2048 ? 256 : 1024;
+    p.team = v <= (wave ? 256 : 128) ? 64 : v <= 2048 ? 256 : 1024;
     p.vecs = 1;
     while ((int64_t)p.team * p.vecs < v) p.vecs *= 2;
     p.per_block = p.team == 64 ? 4 : 1;
@@ -348,7 +350,7 @@ struct FfnArgs {
 };
 int run_ffn(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 int run_ffn_few(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
-int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);   // gate and up alone
+int run_ffn_few_gate(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);   // gate and up alone, fp32
 int run_ffn_few_grad(const FfnArgs& a, const FfnPlan& p, char* ws, void* stream);
 // a and b (gate and up, planes of u), Y, du (planes of da, db and u), dX from the rows' planes
 int run_mid_gate(const FfnArgs& a, const FfnPlan& p, bool u, char* ws, void* stream);

@@ -492,15 +492,14 @@ int run_dropout(const DropoutArgs& a, void* stream) {
 }
 
 int run_rms_norm(const NormArgs& a, void* stream) {
-    if (a.scale && a.x_bf16 && a.d > 1024 && a.d <= 2048) {   // by a wave, which needs no barrier for the row's sum and largest
+    const NormPlan p = make_norm_plan(a.rows, a.d, a.scale && a.x_bf16);
+    if (p.team == 64 && p.vecs == 4) {   // (bf16 rows to 8 bits alone)
         const dim3 grid((unsigned)ceil_div64(a.rows, 4));
         if (a.s_bf16) hipLaunchKernelGGL((norm_kernel<true, true, 64, 4, true>), grid, dim3(256), 0, (hipStream_t)stream, a);
         else hipLaunchKernelGGL((norm_kernel<true, false, 64, 4, true>), grid, dim3(256), 0, (hipStream_t)stream, a);
         return (int)hipGetLastError();
     }
-    of_plan(make_norm_plan(a.rows, a.d), [&](auto t, auto v) {
-        launch_norm<decltype(t)::value, decltype(v)::value>(a, (hipStream_t)stream);
-    });
+    of_plan(p, [&](auto t, auto v) { launch_norm<decltype(t)::value, decltype(v)::value>(a, (hipStream_t)stream); });
     return (int)hipGetLastError();
 }
 
