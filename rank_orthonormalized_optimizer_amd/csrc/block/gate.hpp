@@ -22,20 +22,21 @@ __device__ __forceinline__ float sigmoid(float z) {
     return z < -87.f ? 0.f : fmaf(r, fmaf(-e, r, 1.f), r);
 }
 
-// act(a) and its derivative: a r and r + x r (1 - r) z' with r = 1 / (1 + exp(-z)) and
+// act(a) and its derivative: a r and r + a r (1 - r) z' with r = 1 / (1 + exp(-z)) and
 //   silu  z = a;  gelu  z = 2 sqrt(2 / pi) (x + 0.044715 x^3), as (1 + tanh(z / 2)) / 2 = r, and z is past every border at |a| = 30
 template <bool EXACT>
 __device__ __forceinline__ float activate(int act, float a, float& slope) {
     float x = a, z = a, dz = 1.f;
     if (act != DION_SILU) {
-        x = a < -30.f ? -30.f : a > 30.f ? 30.f : a;   // (a NaN stays one)
+        x = fminf(fmaxf(a, -30.f), 30.f);   // (of a NaN: -30)
         const float q = x * x;
         z = 1.59576912f * x * fmaf(0.044715f, q, 1.f);
         dz = 1.59576912f * fmaf(0.134145f, q, 1.f);
     }
     const float r = sigmoid<EXACT>(z);
-    slope = fmaf(x * r * (1.f - r), dz, r);
-    return a * r;
+    const float v = a * r;   // (where x is not a, r (1 - r) is zero; a NaN is one again)
+    slope = fmaf(v * (1.f - r), dz, r);
+    return v;
 }
 
 // a and b as the gradient is handed them, for bf16 operands: 16 bits, a sign and either, for magnitudes in [2^-8, 2^8), a set
