@@ -109,8 +109,8 @@ int dion_rms_norm_grad(const void* dY, const void* h, const void* w, const float
  *   act       dion_activation, and for bf16 DION_KEEP_EVEN or not (which counts where gate and up are given)
  * Arithmetic: bf16 operands multiply exactly and add up in fp32 on the matrix cores; u is rounded to bf16 for the second
  * product, or for up to 64 rows to two bf16 parts.  fp32 operands give fp32-accurate products: a, b and du from two fp16 parts of each row scaled by a power of two
- * (2^-23 of an element and 2^-38 of its row's largest left out, three part products, terms below 2^-22 dropped; rows up to
- * 2^100), the others from three bf16 parts (an exact split, six part products, terms below 2^-24 dropped), and all of few
+ * (2^-23 of an element and 2^-38 of its row's largest left out, or 2^-125 where that is more, three part products, terms below
+ * 2^-22 dropped; rows up to 2^100; for du dY's elements count times 2^-13 of the largest of Wd's row that they meet), the others from three bf16 parts (an exact split, six part products, terms below 2^-24 dropped), and all of few
  * rows in fp32 (how many rows are few is a matter of the sizes).  8-bit rows go as bf16, which holds x scale exactly where
  * scale is a power of two, as dion_rms_norm leaves it, and is rounded else.  Operands are taken to be finite; others make what they reach NaN or infinite.
  * Workspace size: for_grad 0 for dion_gated_ffn, 1 for dion_gated_ffn_grad given gate and up, 2 without them; 0 for invalid

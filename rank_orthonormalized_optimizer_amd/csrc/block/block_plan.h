@@ -170,7 +170,9 @@ inline Product pick_product(int64_t m, int64_t n, int64_t k, int64_t terms, bool
 // 2048 x 5632 1 row 45 and 110, 32 rows 79 and 111, 48 rows 120 and 123, 64 rows 139 and 124, 8192 x 8192 48 rows 351 and 652.
 constexpr int64_t kFewRows = 8, kFewRowsF32 = 64;
 // Slices of the reduction over k for an output of `cols` columns, 16 to a workgroup: where they are fewer than a quarter of the
-// CUs and k is long, a workgroup for every CU (forward, fp32 4 x 65 x 20279: 60 -> 18 us, 22 x 4001 x 75: 40 -> 18).
+// CUs and k is long, a workgroup for every CU (forward, fp32 4 x 65 x 20279: 60 -> 18 us, 22 x 4001 x 75: 40 -> 18).  More columns
+// are left uncut, though a quarter of the CUs has little to stream with: width 1024, whose 64 blocks are cut, and 1040, whose 65 are
+// not, hidden 28672: one bf16 row 40 us and 67, 16 fp32 rows 96 and 194; hidden 5632: 16 and 19, 32 and 45.
 inline int64_t few_gate_slices(int64_t cols, int64_t k) {
     const int64_t blocks = ceil_div64(cols, 16), most = k / 512;
     if (blocks * 4 > kCUs || most < 2) return 1;

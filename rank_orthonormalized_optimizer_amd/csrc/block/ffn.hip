@@ -16,7 +16,7 @@
 //
 // Bound by the matrix cores, whose clocks fall under this load.  8192 x 2048 x 5632 bf16 (rows, width, hidden): a, b and u 362 us
 // (1.04 PFLOP/s, a library product of that shape 1.07), Y 156 (1.21), du, da, db and u 283 (0.67; a and b are read and three
-// outputs written), dX 297 (1.27), the three weights' gradients 485 (1.17).  4096 x 1024 x 4096 fp32, part products: a, b and u 197
+// outputs written; in the even form 294), dX 297 (1.27), the three weights' gradients 485 (1.17).  4096 x 1024 x 4096 fp32, part products: a, b and u 197
 // us (1.05 PFLOP/s), Y 154 and 16 (1.21), du 188 (0.55), dX 317 and 15 (1.25), gradients 569 (1.09), planes 3 x 30.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -513,7 +513,8 @@ struct Dgated : Single {
     __device__ __forceinline__ void column(int, int m0, int n0, const Lane& l, const f32x4 (&v)[C::MI]) const {
         const GatedRows<PARTS> to(g, n0);
         const float x = PARTS != 3 ? 1.f : g.xinv[n0 + l.row];
-        // fp32 ones, which are twice as wide, half a column at a time: a whole one spills (4096 x 1024 x 4096: 234 us, so 188)
+        // fp32 ones, which are twice as wide, half a column at a time: 4096 x 1024 x 4096 234 us, so 188.  (25 vector registers still
+        // spill, and 30 of the bf16 ones, which go by whole columns; both spill scalar ones, mostly the rows' descriptors.)
         constexpr int N = PARTS == 3 && C::MI >= 8 ? C::MI / 2 : C::MI;
 #pragma unroll
         for (int i0 = 0; i0 < C::MI; i0 += N) {

@@ -12,7 +12,8 @@
 // Bound by HBM up to 64 rows, then by both: 8192 x 8192 fp32, a and b 32 rows 140 us (3.8 TB/s; without the products 125),
 // 128 rows 199 (2.7 TB/s, 650 TFLOP/s of part products; 161), dX 130 and 188 (93 and 130).  With workgroups of four waves,
 // which read the rows' planes twice as often, 238 and 222 for 128 rows; with the next loads all started before the products 222
-// and 212, for a wave whose loads are held up starts no product; with two steps under way as with four waves.
+// and 212, for a wave whose loads are held up starts no product; with two steps under way as with four waves.  (Each the least of
+// several runs on one card; on others a and b of 128 rows took 188 to 209 at least and 210 to 225 in the median.)
 //
 // Lane layout of v_mfma_f32_16x16x32_bf16: A[l % 16][8 values of k of the quarter l / 16], B likewise, D element v of lane l is
 // D[4 (l / 16) + v][l % 16].  The order of k is free as long as A and B agree: a quarter has k of 4 q .. 4 q + 3 and 16 behind

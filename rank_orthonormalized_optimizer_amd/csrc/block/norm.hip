@@ -5,14 +5,15 @@
 //   n = h rstd;  g = dY w;  dh = rstd (g - n mean(g n)) + dsum;  dx = keep dh / (1 - p);  dw = sum over the rows of dY n
 //
 // One pass over the data: a team of threads (a wave, four or sixteen) holds a row in registers between the row's sum and
-// its output.  dw is summed per thread over the rows that its workgroup strides over, then over the workgroups in a fixed
+// its output.  (Above 16384 elements a row outgrows them in part: 10 to 450 vector registers spill, and the gradient reads its
+// rows twice.  2^26 elements in rows of 65536: norm 181 us, to 8 bits 400.)  dw is summed per thread over the rows that its workgroup strides over, then over the workgroups in a fixed
 // order.
 //
 // The mask is Philox4x32-10 over the elements' numbers: a call yields the words of four elements in a row, so the eight of
 // a vector take two calls, or three where the row does not start at a multiple of four.
 //
 // Bound by HBM: dropout of 65536 x 4096 bf16 with a residual 312 us (5.2 TB/s), norm of 16384 x 2048 bf16 to 8 bits with dropout 71 us
-// (3.3 TB/s: fp64 arithmetic and the mask), gradient of 65536 x 4096 with an fp32 stream 839 us (5.1 TB/s); small ones by the launch (one row
+// (3.3 TB/s: fp64 arithmetic and the mask; 61 where calls follow one another), gradient of 65536 x 4096 with an fp32 stream 839 us (5.1 TB/s); small ones by the launch (one row
 // of 2048: 2.7 us).
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -215,7 +216,8 @@ __global__ __launch_bounds__(TEAM == 64 ? 256 : TEAM) void norm_kernel(NormArgs 
     F rstd = (F)1 / sqrt(sum / (F)a.d + (F)a.eps), seen = rstd;
     if constexpr (!Q8) {
         // Squares that leave fp32's range: the row again, times a power of two that brings them back (the same for the team).
-        // With eps at least 2^-100 nothing that underflows counts.  (The code alone costs rows of 65536 174 -> 181 us, others nothing.)
+        // With eps at least 2^-100 nothing that underflows counts.  (The code alone costs 2^26 elements in
+        // rows of 65536, bf16, 174 -> 181 us and of 32768, fp32, 228 -> 240; shorter rows nothing.)
         if (sum == INFINITY || (sum < 0x1p-70f && a.eps < 0x1p-100)) {
             const bool large = sum == INFINITY;
             const float f = large ? 0x1p-80f : 0x1p90f;
