@@ -5,10 +5,11 @@ A "step" is one Dion update of every matrix of a workload (all its stacks), with
 inputs already resident in HBM.  The headline workload is the rank-fraction-1/4
 attention stack: 24 fp32 matrices of 1024 x 1024 at r = 256 with low-rank-plus-noise
 gradients (see workloads/).  The default run also measures every other workload and
-reports them in a "configs" array.  Prints one JSON line.
+reports them in a "configs" array.  Prints one JSON line of a few KB: the headline workload's
+figures, and the main ones of each other.  --details FILE keeps the whole record of every workload.
 
   python bench.py [--steps K] [--warmup W] [--workload 1..5] [--configs 1,2,3,4,5 | none]
-                  [--no-cpu-baseline] [--eager]
+                  [--no-cpu-baseline] [--eager] [--details FILE]
 
 Inputs are drawn on the device with the workloads' recipes (workloads.make_state_device and
 make_grad_device: same distributions as the host generators the parity tests use, drawn by a
@@ -21,7 +22,7 @@ resident gradient).  The replays set the value; both times are reported ("eager_
 
 Metric: updates/s (steps per second over the whole workload), with the effective parameter
 bandwidth (algorithmic bytes / step time) and its share of the 8 TB/s HBM peak alongside.
-Every phase of the step is priced against the roofline that bounds it ("phase_roofline"; the
+Every phase of the step is priced against the roofline that bounds it ("phase_roofline", among the details; the
 phase times come from HIP events the library records at its phase boundaries, on the stream
 the kernels run on), the dominant single-kernel phase is the "roofline" entry, and the
 multi-kernel QR phase has its own "qr_roofline".  "cpu_baseline" times the fp64 oracle on
@@ -510,6 +511,37 @@ def measure(wl, dev, stream, args, cpu_s: float, host_inputs: bool) -> dict:
     return ent
 
 
+def line(out: dict) -> dict:
+    """The record as it is printed: without the phases' rooflines, each other workload by its main figures, all but
+    the headline's value and time in six digits."""
+    def some(d, *keys):
+        return {k: d[k] for k in keys if k in d}
+
+    def roofline(d):
+        return some(d, "bound", "kernel", "dtype", "achieved", "peak", "unit", "frac", "ms")
+
+    def digits(v):
+        if isinstance(v, float):
+            return float(f"{v:.6g}")
+        if isinstance(v, dict):
+            return {k: digits(x) for k, x in v.items()}
+        return [digits(x) for x in v] if isinstance(v, list) else v
+
+    brief = {k: v for k, v in out.items() if k not in ("phase_roofline", "configs", "elementwise", "spectral")}
+    if "configs" in out:
+        brief["configs"] = [dict(some(c, "wid", "workload", "value", "ms_per_step", "eager_ms_per_step", "dtype", "effective_param_GBps",
+                                      "fp64_chain_matrices"),
+                                 roofline=some(c["roofline"], "kernel", "dtype", "frac"),
+                                 **({"cpu_baseline": some(c["cpu_baseline"], "value")} if "cpu_baseline" in c else {}))
+                            for c in out["configs"]]
+    if "elementwise" in out:
+        brief["elementwise"] = {k: dict(some(out["elementwise"][k], "ms_per_step", "effective_GBps"),
+                                        roofline=some(out["elementwise"][k]["roofline"], "bound", "frac")) for k in ("adamw", "lion")}
+    if "spectral" in out:
+        brief["spectral"] = [dict(some(c, "workload", "ms_per_call"), roofline=roofline(c["roofline"])) for c in out["spectral"]["cases"]]
+    return dict(digits(brief), **some(out, "value", "ms_per_step"))
+
+
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
@@ -541,6 +573,8 @@ def main() -> int:
                     help="only the lambda_max estimate measurement, printed as one JSON line")
     ap.add_argument("--calibrate-copy", action="store_true",
                     help="also run one 256 MiB device-to-device copy (reference for HBM byte counters)")
+    ap.add_argument("--details", metavar="FILE",
+                    help="also write the whole record (phase rooflines, every workload in full) to FILE as JSON")
     ap.add_argument("--cpu-seconds", type=float, default=12.0, help="oracle budget of the headline workload")
     ap.add_argument("--config-cpu-seconds", type=float, default=4.0, help="oracle budget of each other workload")
     args = ap.parse_args()
@@ -612,7 +646,10 @@ def main() -> int:
     if not args.no_spectral:
         print("[bench] multi-power-iteration lambda_max estimate", file=sys.stderr, flush=True)
         out["spectral"] = spectral_block(dev, stream, with_cpu=not args.no_cpu_baseline)
-    print(json.dumps(out), flush=True)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(out, f)
+    print(json.dumps(line(out)), flush=True)
     return 0
 
 
